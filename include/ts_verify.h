@@ -311,6 +311,165 @@ ts_status ts_verify_chain_greedy_static(const void* target_logits, ts_dtype dt, 
                                         int32_t* accept_length, int32_t* accept_index,
                                         float* logprobs, cudaStream_t stream);
 
+/* ---- Around the verify step: the target's window over an 8-bit paged KV cache ------------
+ *
+ * A window is what a verify call checks: the rows of the last emitted token and of its
+ * drafts. The calls below run the target's attention on exactly those windows, store the K
+ * and V of exactly the rows a verify call accepted, read prefixes back, and verify drafted
+ * trees. K and V of a window stay in 16 bits until its rows are accepted, so rejected drafts
+ * never reach the cache.
+ *
+ * The cache holds e4m3 codes in pages of page_size tokens with one fp32 scale for each block
+ * (a page of one head): value = code * scale. Page ids outside [0, num_pages) are never
+ * accessed: their tokens count as absent (attention), read back as 0 and are not stored.
+ * seq_lens[b] is taken as clamped to [0, max_pages * page_size].
+ * Base addresses and strides (in bytes) must be multiples of 16, head_dim must be 64 or 128,
+ * page_size 16, 32, 64 or 128 (else TS_ERR_INVALID_ARG). */
+#define TS_F16 2 /* a dtype of the calls below only */
+#define TS_MAX_WINDOW (TS_MAX_DRAFT + 1)
+
+typedef struct ts_kv_cache {
+  void* k;                    /* token t, head h of page p at k + p*k_page_stride +
+                                 h*k_head_stride + t*k_token_stride: head_dim codes */
+  void* v;
+  int64_t k_page_stride, k_head_stride, k_token_stride;
+  int64_t v_page_stride, v_head_stride, v_token_stride;
+  float* k_scale;             /* [num_pages, heads] */
+  float* v_scale;
+  int64_t num_pages;
+  int32_t heads;              /* KV heads */
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t max_pages;          /* pages a request can have (>= 0) */
+  const int32_t* page_table;  /* [batch, ld_table]; token t of request b is in page
+                                 page_table[b*ld_table + t/page_size] */
+  int64_t ld_table;           /* >= max_pages */
+  const int32_t* seq_lens;    /* [batch] tokens in the cache */
+  int64_t batch;
+} ts_kv_cache;
+
+typedef struct ts_attn_args {
+  const ts_kv_cache* cache;  /* host struct */
+  const void* q;             /* row r, head h at q + r*q_row_stride + h*q_head_stride
+                                (bytes, multiples of 16): head_dim values of `dtype` */
+  int64_t q_row_stride, q_head_stride;
+  int32_t dtype;             /* TS_BF16 or TS_F16: q, k_new, v_new and out */
+  int32_t heads_q;           /* a multiple of cache->heads; head h reads KV head
+                                h / (heads_q / heads) */
+  const void* k_new;         /* the window's own K and V, one row for each row of q, laid out
+                                like q with `heads` heads; both NULL: cached tokens only */
+  const void* v_new;
+  int64_t k_row_stride, k_head_stride, v_row_stride, v_head_stride;
+  int64_t total_rows;
+  const int32_t* qo_indptr;  /* [batch + 1]: request b owns rows qo_indptr[b] ..
+                                qo_indptr[b+1] - 1, at most TS_MAX_WINDOW; NULL: total_rows /
+                                batch rows each. A window that does not fit is skipped (its
+                                outputs are left as they were), as are rows that no window
+                                owns */
+  const int32_t* parents;    /* [total_rows] or NULL. NULL: row t of a window sees its own
+                                rows 0..t. Else the window is a tree: row t sees itself and
+                                its ancestors; parents[r] is the window row of r's parent,
+                                below r's own (any other value: no parent) */
+  float sm_scale;            /* scores are sm_scale * q.k */
+  float reserved0;
+  void* out;                 /* [total_rows, heads_q, head_dim] contiguous, 16-byte aligned */
+  float* lse;                /* [total_rows, heads_q] ln(sum exp(score)), or NULL */
+} ts_attn_args;
+
+/* Attention of each window over its request's cached tokens and over itself:
+ * out = sum_i softmax(score)_i v_i. A row that sees no token gives 0 and lse -inf. Tokens
+ * that a row does not see have no effect on it, whatever they hold.
+ * Scores, softmax statistics and sums are fp32; cached K and V enter the products as they
+ * are, q relative to its row's largest value and the probabilities in 11 significant bits.
+ * Scales of V below 2^-100 count as 2^-100. Workspace: ts_attention_workspace_size bytes
+ * of scratch (no zero fill needed). */
+ts_status ts_window_attention(const ts_attn_args* args, void* workspace, size_t ws_bytes,
+                              cudaStream_t stream);
+size_t ts_attention_workspace_size(int32_t head_dim);
+
+typedef struct ts_kv_append_args {
+  const ts_kv_cache* cache;  /* host struct; seq_lens: tokens before the call (not updated) */
+  const void* k;             /* row r, head h at k + r*k_row_stride + h*k_head_stride (bytes,
+                                multiples of 16): head_dim values of `dtype` */
+  const void* v;
+  int64_t k_row_stride, k_head_stride, v_row_stride, v_head_stride;
+  int32_t dtype;             /* TS_F32, TS_BF16 or TS_F16 */
+  int32_t reserved0;
+  int64_t total_rows;
+  /* Which rows: src_index and src_len (the accept_index and accept_length of a verify call:
+   * the rows src_index[b*ld_src + j], j < src_len[b]), or qo_indptr (rows qo_indptr[b] ..
+   * qo_indptr[b+1] - 1), or neither (total_rows / batch each). */
+  const int32_t* src_index;  /* [batch, ld_src] or NULL */
+  const int32_t* src_len;    /* [batch], taken as clamped to [0, ld_src] */
+  int64_t ld_src;
+  const int32_t* qo_indptr;  /* [batch + 1] or NULL */
+} ts_kv_append_args;
+
+/* Quantises rows into the cache: row j of request b becomes token seq_lens[b] + j. Over the
+ * new tokens of a block let A be the largest finite magnitude and 2^e, e the least integer
+ * in [-60, 60], the least scale with A <= 448 * 2^e. The block's scale becomes 2^e, or, if
+ * the block holds earlier tokens, the larger of its scale and 2^e; when that raises it, the
+ * earlier tokens' codes are rounded again to the new scale. Codes are code = e4m3(x / scale),
+ * to nearest, ties to even, saturating (infinities too; NaN stays NaN). Row numbers outside
+ * [0, total_rows) and a qo_indptr pair that does not fit store nothing (their positions are
+ * left as they were), nor does a position past the page table. No two requests may store to
+ * the same page in one call, and a page that is stored to must not be read meanwhile. */
+ts_status ts_kv_append(const ts_kv_append_args* args, cudaStream_t stream);
+
+typedef struct ts_kv_read_args {
+  const ts_kv_cache* cache;   /* host struct */
+  const int32_t* out_indptr;  /* [batch + 1]: tokens start[b] .. of request b go to output
+                                 rows out_indptr[b] .. out_indptr[b+1] - 1 */
+  const int32_t* start;       /* [batch] or NULL (0) */
+  int64_t total_rows;         /* rows of the outputs */
+  int32_t dtype;              /* TS_F32, TS_BF16 or TS_F16 */
+  int32_t reserved0;
+  void* k_out;                /* [total_rows, heads, head_dim] contiguous, 16-byte aligned */
+  void* v_out;
+} ts_kv_read_args;
+
+/* Reads tokens back: code * scale in fp32, rounded to `dtype`. Positions outside
+ * [0, seq_lens[b]) give 0. out_indptr must not decrease; a pair that does not fit in
+ * [0, total_rows] is skipped. Rows that no request owns are left as they were. */
+ts_status ts_kv_read(const ts_kv_read_args* args, cudaStream_t stream);
+
+typedef struct ts_tree_args {
+  const float* target_probs; /* [total_rows, ld] fp32: p of each node */
+  int64_t vocab, ld;
+  int64_t batch;
+  int64_t total_rows;
+  const int32_t* qo_indptr;  /* [batch + 1]: request b's nodes are rows qo_indptr[b] ..
+                                qo_indptr[b+1] - 1, 1 to TS_MAX_WINDOW of them; NULL:
+                                total_rows / batch each */
+  const int32_t* tokens;     /* [total_rows] token of each node (its first node, the root,
+                                holds the last emitted token: not read) */
+  const int32_t* parents;    /* [total_rows] as for ts_attn_args; a node other than the root
+                                whose parent is not a node before it is never accepted */
+  const float* uniforms;     /* [total_rows] coins in (0, 1): a node's own test; the root's
+                                is the coin of the last draw */
+  int32_t D;                 /* most drafts accepted; outputs are [batch, D+1] */
+  int32_t reserved0;
+  int32_t* accepted_tokens;  /* [batch, D+1] out */
+  int32_t* accept_length;    /* [batch] out */
+  int32_t* accept_index;     /* [batch, D+1] out, or NULL: the row of each node kept (the row
+                                whose p emitted the token; the rows to store with
+                                ts_kv_append) */
+  float* logprobs;           /* [batch, D+1] out, or NULL: ln p(token); 0 after the last */
+} ts_tree_args;
+
+/* Verification of drafted trees against the target's probabilities with given coins
+ * (target-only, as ts_chain_spec_sampling without draft probabilities; a tree that is a
+ * chain gives the same tokens). From the root on, the children of the current node are
+ * tried in row order: child x with coin u is accepted iff u * (1 - r) < p(x), r the sum of
+ * p over the siblings rejected before it (in double); a token that an earlier sibling holds,
+ * or outside [0, vocab), has p(x) = 0. After D drafts, or when no child is accepted, the
+ * last token is drawn from the current node's p without the children rejected there, or
+ * from p itself if that leaves no mass: the smallest id whose inclusive prefix mass exceeds
+ * the root's coin times the total. This emits tokens with the distribution p.
+ * A window outside [1, TS_MAX_WINDOW] rows or past total_rows gives accept_length 0.
+ * Outputs past the emitted tokens are -1 (logprobs 0). No workspace. */
+ts_status ts_tree_spec_sampling(const ts_tree_args* args, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -9,8 +9,13 @@ from .tsverify import (  # noqa: F401
     chain_spec_sampling,
     gather_logprobs,
     gumbel_max_sample,
+    kv_append,
+    kv_read,
+    make_attention_workspace,
     make_workspace,
     softmax_temp,
     topk_topp_renorm,
+    tree_spec_sampling,
     verify_chain_greedy,
+    window_attention,
 )

@@ -1,6 +1,6 @@
 // The C ABI of libtsverify.so: argument validation, workspace carve-up, launch geometry
 // and dispatch to the kernels. Host code only; every step of the computation runs in
-// the kernels of ts_stream.cu, ts_sample.cu and ts_staged.cu.
+// the kernels of the other translation units.
 #include <stdarg.h>
 #include <stdio.h>
 
@@ -84,6 +84,46 @@ ts_status take_workspace(int64_t batch, int32_t R, int64_t vocab, void* ws, size
     return fail(TS_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   if (ws_bytes < need)
     return fail(TS_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+  return TS_OK;
+}
+
+bool multiple16(const void* p, int64_t a, int64_t b) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && a % 16 == 0 && b % 16 == 0;
+}
+
+// The calls on a KV cache.
+ts_status check_cache(const ts_kv_cache* c) {
+  if (!c) return fail(TS_ERR_INVALID_ARG, "cache is NULL");
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale || !c->seq_lens || (c->max_pages > 0 && !c->page_table))
+    return fail(TS_ERR_INVALID_ARG, "k, v, k_scale, v_scale, page_table and seq_lens of the cache are required");
+  if (c->head_dim != 64 && c->head_dim != 128)
+    return fail(TS_ERR_INVALID_ARG, "head_dim must be 64 or 128 (got %d)", c->head_dim);
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+    return fail(TS_ERR_INVALID_ARG, "page_size must be 16, 32, 64 or 128 (got %d)", c->page_size);
+  if (c->heads < 1 || c->heads > 1024) return fail(TS_ERR_INVALID_ARG, "heads must be in [1, 1024]");
+  if (c->batch < 1 || c->batch > 1 << 16) return fail(TS_ERR_INVALID_ARG, "batch must be in [1, 65536]");
+  if (c->num_pages < 0 || c->num_pages > INT32_MAX) return fail(TS_ERR_INVALID_ARG, "num_pages must be in [0, 2^31)");
+  if (c->max_pages < 0 || (int64_t)c->max_pages * c->page_size > (int64_t)1 << 30)
+    return fail(TS_ERR_INVALID_ARG, "max_pages * page_size must be in [0, 2^30]");
+  if (c->ld_table < c->max_pages) return fail(TS_ERR_INVALID_ARG, "ld_table must be >= max_pages");
+  if (!multiple16(c->k, c->k_page_stride, c->k_head_stride) || c->k_token_stride % 16 ||
+      !multiple16(c->v, c->v_page_stride, c->v_head_stride) || c->v_token_stride % 16)
+    return fail(TS_ERR_INVALID_ARG, "the cache needs 16-byte aligned addresses and strides");
+  return TS_OK;
+}
+
+ts_status check_kv_dtype(int dt) {
+  if (dt != TS_F32 && dt != TS_BF16 && dt != TS_F16)
+    return fail(TS_ERR_UNSUPPORTED_DTYPE, "unsupported dtype %d", dt);
+  return TS_OK;
+}
+
+// Packed (qo_indptr) or equal windows.
+ts_status check_window(const int32_t* qo_indptr, int64_t total_rows, int64_t batch) {
+  if (total_rows < 1 || total_rows > batch * (int64_t)TS_MAX_WINDOW)
+    return fail(TS_ERR_INVALID_ARG, "total_rows must be in [1, batch * %d]", TS_MAX_WINDOW);
+  if (!qo_indptr && total_rows % batch)
+    return fail(TS_ERR_INVALID_ARG, "total_rows must be a multiple of batch without qo_indptr");
   return TS_OK;
 }
 
@@ -604,6 +644,86 @@ ts_status ts_gather_logprobs(const void* x, ts_dtype dt, int32_t is_probs, int64
   a.lp_tokens = tokens;
   a.lp_out = out;
   return launched(tsv::launch_rowstat(a, dt == TS_BF16, stream), "logprobs launch");
+}
+
+// ---- around the verify step
+
+ts_status ts_window_attention(const ts_attn_args* p, void* workspace, size_t ws_bytes,
+                              cudaStream_t stream) {
+  if (!p) return fail(TS_ERR_INVALID_ARG, "args is NULL");
+  ts_status st;
+  if ((st = check_cache(p->cache)) != TS_OK) return st;
+  const ts_kv_cache& c = *p->cache;
+  if (p->dtype != TS_BF16 && p->dtype != TS_F16)
+    return fail(TS_ERR_UNSUPPORTED_DTYPE, "attention takes bf16 or fp16, not dtype %d", p->dtype);
+  if (p->heads_q < 1 || p->heads_q % c.heads)
+    return fail(TS_ERR_INVALID_ARG, "heads_q (%d) must be a multiple of the cache's %d heads", p->heads_q, c.heads);
+  if ((st = check_window(p->qo_indptr, p->total_rows, c.batch)) != TS_OK) return st;
+  if (p->total_rows * (int64_t)p->heads_q > (int64_t)1 << 31)
+    return fail(TS_ERR_INVALID_ARG, "total_rows * heads_q is above 2^31");
+  if (!p->q || !p->out || (p->k_new == nullptr) != (p->v_new == nullptr))
+    return fail(TS_ERR_INVALID_ARG, "q and out are required, k_new and v_new come together");
+  if (p->parents && !p->k_new)
+    return fail(TS_ERR_INVALID_ARG, "parents describe the window's own rows: k_new and v_new are required");
+  if (!multiple16(p->q, p->q_row_stride, p->q_head_stride) ||
+      !multiple16(p->k_new, p->k_row_stride, p->k_head_stride) ||
+      !multiple16(p->v_new, p->v_row_stride, p->v_head_stride) || !multiple16(p->out, 0, 0))
+    return fail(TS_ERR_INVALID_ARG, "q, k_new, v_new and out need 16-byte aligned addresses and strides");
+  const size_t need = tsv::window_workspace(c.head_dim, sm_count());
+  if (!workspace || ws_bytes < need || !multiple16(workspace, 0, 0))
+    return fail(TS_ERR_INVALID_ARG, "workspace must have %zu 16-byte aligned bytes (got %zu)", need, ws_bytes);
+  return launched(tsv::launch_window(c, *p, workspace, sm_count(), stream), "window attention launch");
+}
+
+size_t ts_attention_workspace_size(int32_t head_dim) {
+  return head_dim == 64 || head_dim == 128 ? tsv::window_workspace(head_dim, sm_count()) : 0;
+}
+
+ts_status ts_kv_append(const ts_kv_append_args* p, cudaStream_t stream) {
+  if (!p) return fail(TS_ERR_INVALID_ARG, "args is NULL");
+  ts_status st;
+  if ((st = check_cache(p->cache)) != TS_OK) return st;
+  const ts_kv_cache& c = *p->cache;
+  if ((st = check_kv_dtype(p->dtype)) != TS_OK) return st;
+  if (!p->k || !p->v) return fail(TS_ERR_INVALID_ARG, "k and v are required");
+  if ((p->src_index == nullptr) != (p->src_len == nullptr) || (p->src_index && p->qo_indptr))
+    return fail(TS_ERR_INVALID_ARG, "src_index and src_len come together, and not with qo_indptr");
+  if (p->total_rows < 1 || p->total_rows > (int64_t)1 << 30)
+    return fail(TS_ERR_INVALID_ARG, "total_rows must be in [1, 2^30]");
+  if (p->src_index && (p->ld_src < 1 || p->ld_src > (int64_t)1 << 30))
+    return fail(TS_ERR_INVALID_ARG, "ld_src must be in [1, 2^30]");
+  if (!p->src_index && !p->qo_indptr && p->total_rows % c.batch)
+    return fail(TS_ERR_INVALID_ARG, "total_rows must be a multiple of batch without src_index and qo_indptr");
+  if (!multiple16(p->k, p->k_row_stride, p->k_head_stride) || !multiple16(p->v, p->v_row_stride, p->v_head_stride))
+    return fail(TS_ERR_INVALID_ARG, "k and v need 16-byte aligned addresses and strides");
+  return launched(tsv::launch_kv_append(c, *p, sm_count(), stream), "cache append launch");
+}
+
+ts_status ts_kv_read(const ts_kv_read_args* p, cudaStream_t stream) {
+  if (!p) return fail(TS_ERR_INVALID_ARG, "args is NULL");
+  ts_status st;
+  if ((st = check_cache(p->cache)) != TS_OK) return st;
+  if ((st = check_kv_dtype(p->dtype)) != TS_OK) return st;
+  if (!p->out_indptr || !p->k_out || !p->v_out)
+    return fail(TS_ERR_INVALID_ARG, "out_indptr, k_out and v_out are required");
+  if (p->total_rows < 1 || p->total_rows > (int64_t)1 << 30)
+    return fail(TS_ERR_INVALID_ARG, "total_rows must be in [1, 2^30]");
+  if (!multiple16(p->k_out, 0, 0) || !multiple16(p->v_out, 0, 0))
+    return fail(TS_ERR_INVALID_ARG, "k_out and v_out must be 16-byte aligned");
+  return launched(tsv::launch_kv_read(*p->cache, *p, stream), "cache read launch");
+}
+
+ts_status ts_tree_spec_sampling(const ts_tree_args* p, cudaStream_t stream) {
+  if (!p) return fail(TS_ERR_INVALID_ARG, "args is NULL");
+  ts_status st;
+  if (p->D < 0 || p->D > TS_MAX_DRAFT) return fail(TS_ERR_INVALID_ARG, "D must be in [0, %d]", TS_MAX_DRAFT);
+  if ((st = check_common(p->batch, p->vocab, p->ld)) != TS_OK) return st;
+  if (p->batch > (int64_t)1 << 24) return fail(TS_ERR_INVALID_ARG, "batch must be at most 2^24");
+  if ((st = check_window(p->qo_indptr, p->total_rows, p->batch)) != TS_OK) return st;
+  if (!p->target_probs || !p->tokens || !p->parents || !p->uniforms || !p->accepted_tokens || !p->accept_length)
+    return fail(TS_ERR_INVALID_ARG,
+                "target_probs, tokens, parents, uniforms, accepted_tokens and accept_length are required");
+  return launched(tsv::launch_tree(*p, sm_count(), stream), "tree verification launch");
 }
 
 }  // extern "C"

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/ts_verify.h"
+
 namespace tsv {
 
 constexpr int kMaxSplits = 64;  // row splits of the streaming kernels
@@ -255,5 +257,14 @@ struct StagedArgs {
 cudaError_t launch_staged(const StagedArgs& a, cudaStream_t s, const char** why);
 cudaError_t staged_read_error(uint32_t* word, int clear);
 int staged_max_vocab(int bf16);
+
+// ---------------------------------------------------------------------------------
+// Around the verify step (ts_window.cu, ts_kvcache.cu, ts_tree.cu): arguments checked by
+// the ABI.
+cudaError_t launch_window(const ts_kv_cache& c, const ts_attn_args& a, void* ws, int sms, cudaStream_t s);
+size_t window_workspace(int head_dim, int sms);
+cudaError_t launch_kv_append(const ts_kv_cache& c, const ts_kv_append_args& a, int sms, cudaStream_t s);
+cudaError_t launch_kv_read(const ts_kv_cache& c, const ts_kv_read_args& a, cudaStream_t s);
+cudaError_t launch_tree(const ts_tree_args& a, int sms, cudaStream_t s);
 
 }  // namespace tsv

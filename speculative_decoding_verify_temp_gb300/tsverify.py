@@ -15,9 +15,10 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtsverify.so")
 
-TS_F32, TS_BF16 = 0, 1
+TS_F32, TS_BF16, TS_F16 = 0, 1, 2
 GREEDY_T = 1e-5
 MAX_DRAFT = 64
+MAX_WINDOW = MAX_DRAFT + 1
 _lib = None
 
 
@@ -88,6 +89,111 @@ class SampleArgs(ctypes.Structure):
     ]
 
 
+class KvCache(ctypes.Structure):
+    """ts_kv_cache of include/ts_verify.h."""
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_page_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("k_token_stride", ctypes.c_int64),
+        ("v_page_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+        ("v_token_stride", ctypes.c_int64),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int64),
+        ("heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("page_table", ctypes.c_void_p),
+        ("ld_table", ctypes.c_int64),
+        ("seq_lens", ctypes.c_void_p),
+        ("batch", ctypes.c_int64),
+    ]
+
+
+class AttnArgs(ctypes.Structure):
+    """ts_attn_args of include/ts_verify.h."""
+    _fields_ = [
+        ("cache", ctypes.POINTER(KvCache)),
+        ("q", ctypes.c_void_p),
+        ("q_row_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("heads_q", ctypes.c_int32),
+        ("k_new", ctypes.c_void_p),
+        ("v_new", ctypes.c_void_p),
+        ("k_row_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("v_row_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+        ("total_rows", ctypes.c_int64),
+        ("qo_indptr", ctypes.c_void_p),
+        ("parents", ctypes.c_void_p),
+        ("sm_scale", ctypes.c_float),
+        ("reserved0", ctypes.c_float),
+        ("out", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p),
+    ]
+
+
+class KvAppendArgs(ctypes.Structure):
+    """ts_kv_append_args of include/ts_verify.h."""
+    _fields_ = [
+        ("cache", ctypes.POINTER(KvCache)),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_row_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("v_row_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("reserved0", ctypes.c_int32),
+        ("total_rows", ctypes.c_int64),
+        ("src_index", ctypes.c_void_p),
+        ("src_len", ctypes.c_void_p),
+        ("ld_src", ctypes.c_int64),
+        ("qo_indptr", ctypes.c_void_p),
+    ]
+
+
+class KvReadArgs(ctypes.Structure):
+    """ts_kv_read_args of include/ts_verify.h."""
+    _fields_ = [
+        ("cache", ctypes.POINTER(KvCache)),
+        ("out_indptr", ctypes.c_void_p),
+        ("start", ctypes.c_void_p),
+        ("total_rows", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("reserved0", ctypes.c_int32),
+        ("k_out", ctypes.c_void_p),
+        ("v_out", ctypes.c_void_p),
+    ]
+
+
+class TreeArgs(ctypes.Structure):
+    """ts_tree_args of include/ts_verify.h."""
+    _fields_ = [
+        ("target_probs", ctypes.c_void_p),
+        ("vocab", ctypes.c_int64),
+        ("ld", ctypes.c_int64),
+        ("batch", ctypes.c_int64),
+        ("total_rows", ctypes.c_int64),
+        ("qo_indptr", ctypes.c_void_p),
+        ("tokens", ctypes.c_void_p),
+        ("parents", ctypes.c_void_p),
+        ("uniforms", ctypes.c_void_p),
+        ("D", ctypes.c_int32),
+        ("reserved0", ctypes.c_int32),
+        ("accepted_tokens", ctypes.c_void_p),
+        ("accept_length", ctypes.c_void_p),
+        ("accept_index", ctypes.c_void_p),
+        ("logprobs", ctypes.c_void_p),
+    ]
+
+
 def load():
     """Loads libtsverify.so (raises if it has not been built)."""
     global _lib
@@ -128,6 +234,14 @@ def load():
                                                 P, P, P, P, P, ctypes.c_size_t, P]
     L.ts_verify_chain_greedy_ragged.restype = st
     L.ts_sample_from_logits.restype = st
+    L.ts_attention_workspace_size.argtypes = [i32]
+    L.ts_attention_workspace_size.restype = ctypes.c_size_t
+    L.ts_window_attention.argtypes = [ctypes.POINTER(AttnArgs), P, ctypes.c_size_t, P]
+    L.ts_window_attention.restype = st
+    for name, args in (("ts_kv_append", KvAppendArgs), ("ts_kv_read", KvReadArgs),
+                       ("ts_tree_spec_sampling", TreeArgs)):
+        getattr(L, name).argtypes = [ctypes.POINTER(args), P]
+        getattr(L, name).restype = st
     _lib = L
     return L
 
@@ -361,3 +475,210 @@ def gather_logprobs(x, tokens, is_probs: bool = False, workspace=None, out=None,
         _p(x), _dtype(x), int(bool(is_probs)), rows, V, ld, _p(tokens), _p(out), _p(workspace),
         nbytes, _stream(stream)))
     return out
+
+
+# ---- around the verify step: a window's attention over the 8-bit cache, the cache, trees ----
+
+_KV_DTYPES = {torch.float32: TS_F32, torch.bfloat16: TS_BF16, torch.float16: TS_F16}
+
+
+def _kv_dtype(dtype) -> int:
+    if dtype not in _KV_DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return _KV_DTYPES[dtype]
+
+
+class _On:
+    """The device and stream of a call: its outputs and scratch come from that stream's pool,
+    its kernels go to that stream."""
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            raise ValueError("expected CUDA tensors")
+        same = device.index is None or device.index == torch.cuda.current_device()
+        self.contexts = [] if same else [torch.cuda.device(device)]
+        if stream is not None:
+            self.contexts.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.contexts:
+            c.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _int32(name, t, shape):
+    """A contiguous int32 tensor of this shape (None: not given)."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens):
+    """The ts_kv_cache of the tensors (pages, heads, page_size, head_dim)."""
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must be [pages, heads, page_size, head_dim]")
+    for t in (k_cache, v_cache):
+        if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            raise TypeError("the cache holds float8_e4m3fn (or its bytes as uint8)")
+        if t.stride(3) != 1:
+            raise ValueError("the cache needs unit stride in the last dimension")
+    n, H, size, D = k_cache.shape
+    for t in (k_scale, v_scale):
+        if t.dtype != torch.float32 or tuple(t.shape) != (n, H) or not t.is_contiguous():
+            raise ValueError(f"scales must be contiguous fp32 tensors of shape ({n}, {H})")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or \
+            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be a 2-D int32 tensor with unit stride in the last dimension")
+    B, P = page_table.shape
+    _same_device(k_cache.device, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+                 page_table=page_table, seq_lens=seq_lens)
+    ks, vs = k_cache.stride(), v_cache.stride()
+    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
+                   k_scale.data_ptr(), v_scale.data_ptr(), n, H, D, size, P, page_table.data_ptr(),
+                   max(page_table.stride(0), P) if B > 1 else P, _int32("seq_lens", seq_lens, (B,)), B)
+
+
+def _heads(name, t, heads, D):
+    """(rows, row stride, head stride) in bytes of a [rows, heads, D] tensor."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [rows, {heads}, {D}] with unit stride in the last dimension")
+    size = t.element_size()
+    return t.shape[0], t.stride(0) * size, t.stride(1) * size
+
+
+def attention_workspace_size(head_dim: int) -> int:
+    return int(load().ts_attention_workspace_size(head_dim))
+
+
+def make_attention_workspace(head_dim: int, device=None):
+    """Scratch for window_attention calls with this head_dim that do not overlap."""
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        return torch.empty(attention_workspace_size(head_dim), dtype=torch.uint8, device="cuda")
+
+
+def window_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, *, k_new=None,
+                     v_new=None, qo_indptr=None, parents=None, sm_scale=None, lse: bool = False,
+                     out=None, workspace=None, stream=None):
+    """Attention of each request's window over its cached tokens and itself.
+
+    q [rows, Hq, D] and the window's own k_new, v_new [rows, H, D] (bf16 or fp16; without them:
+    the cached tokens only); k_cache, v_cache [pages, H, page_size, D] e4m3 with k_scale,
+    v_scale fp32 [pages, H]; page_table int32 [B, max_pages], seq_lens int32 [B]. Rows are
+    packed by qo_indptr (int32 [B+1]) or rows / B a request; parents (int32 [rows], window
+    row numbers) makes each window a tree. sm_scale: 1/sqrt(D) by default. Returns
+    dict(out=[rows, Hq, D], lse=[rows, Hq] fp32 or None)."""
+    c = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)
+    D, dev = c.head_dim, k_cache.device
+    if q.dim() != 3:
+        raise ValueError("q must be [rows, heads, head_dim]")
+    rows, qr, qh = _heads("q", q, q.shape[1], D)
+    _same_device(dev, q=q, k_new=k_new, v_new=v_new, qo_indptr=qo_indptr, parents=parents, out=out,
+                 workspace=workspace)
+    kr = kh = vr = vh = 0
+    if k_new is not None and v_new is not None:
+        nk, kr, kh = _heads("k_new", k_new, c.heads, D)
+        nv, vr, vh = _heads("v_new", v_new, c.heads, D)
+        if nk != rows or nv != rows or k_new.dtype != q.dtype or v_new.dtype != q.dtype:
+            raise ValueError("k_new and v_new must have the rows and the dtype of q")
+    with _On(dev, stream) as s:
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
+            raise ValueError("out must be contiguous, with the shape and dtype of q")
+        z = torch.empty(q.shape[:2], dtype=torch.float32, device=dev) if lse else None
+        if workspace is None:
+            workspace = torch.empty(attention_workspace_size(D), dtype=torch.uint8, device=dev)
+        a = AttnArgs(ctypes.pointer(c), q.data_ptr(), qr, qh, _kv_dtype(q.dtype), q.shape[1],
+                     None if k_new is None else k_new.data_ptr(),
+                     None if v_new is None else v_new.data_ptr(), kr, kh, vr, vh, rows,
+                     _int32("qo_indptr", qo_indptr, (c.batch + 1,)),
+                     _int32("parents", parents, (rows,)),
+                     D ** -0.5 if sm_scale is None else sm_scale, 0.0, out.data_ptr(),
+                     None if z is None else z.data_ptr())
+        _check("ts_window_attention", load().ts_window_attention(
+            ctypes.byref(a), _p(workspace), workspace.numel() * workspace.element_size(), s))
+    return dict(out=out, lse=z)
+
+
+def kv_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, *, qo_indptr=None,
+              src_index=None, src_len=None, stream=None):
+    """Quantises rows of k, v [rows, H, D] (bf16, fp16 or fp32) into the cache, in place, behind
+    each request's seq_lens tokens (which it does not update): the rows src_index[b, :src_len[b]]
+    (a verify call's accept_index and accept_length), or the packed rows of qo_indptr, or
+    rows / B a request."""
+    c = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)
+    rows, kr, kh = _heads("k", k, c.heads, c.head_dim)
+    nv, vr, vh = _heads("v", v, c.heads, c.head_dim)
+    if nv != rows or v.dtype != k.dtype:
+        raise ValueError("v must have the rows and the dtype of k")
+    _same_device(k_cache.device, k=k, v=v, qo_indptr=qo_indptr, src_index=src_index, src_len=src_len)
+    n = 0
+    if src_index is not None:
+        if src_index.dim() != 2:
+            raise ValueError("src_index must be [B, n]")
+        n = src_index.shape[1]
+    with _On(k_cache.device, stream) as s:
+        a = KvAppendArgs(ctypes.pointer(c), k.data_ptr(), v.data_ptr(), kr, kh, vr, vh,
+                         _kv_dtype(k.dtype), 0, rows, _int32("src_index", src_index, (c.batch, n)),
+                         _int32("src_len", src_len, (c.batch,)), n,
+                         _int32("qo_indptr", qo_indptr, (c.batch + 1,)))
+        _check("ts_kv_append", load().ts_kv_append(ctypes.byref(a), s))
+
+
+def kv_read(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, *, out_indptr, total_rows: int,
+            start=None, dtype=torch.bfloat16, out=None, stream=None):
+    """Reads tokens back: request b's tokens from start[b] (0) on into rows out_indptr[b] ..
+    out_indptr[b+1] - 1 of k and v [total_rows, H, D] (out: a pair of such tensors)."""
+    c = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)
+    dev, shape = k_cache.device, (total_rows, c.heads, c.head_dim)
+    with _On(dev, stream) as s:
+        k, v = out or (torch.empty(shape, dtype=dtype, device=dev) for _ in range(2))
+        for t in (k, v):
+            if t.dtype != k.dtype or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"outputs must be contiguous tensors of shape {shape} and one dtype")
+        _same_device(dev, out_indptr=out_indptr, start=start, k=k, v=v)
+        a = KvReadArgs(ctypes.pointer(c), _int32("out_indptr", out_indptr, (c.batch + 1,)),
+                       _int32("start", start, (c.batch,)), total_rows, _kv_dtype(k.dtype), 0,
+                       k.data_ptr(), v.data_ptr())
+        _check("ts_kv_read", load().ts_kv_read(ctypes.byref(a), s))
+    return dict(k=k, v=v)
+
+
+def tree_spec_sampling(target_probs, D: int, tokens, parents, uniforms, *, qo_indptr=None,
+                       accept_index: bool = True, logprobs: bool = True, outputs=None, stream=None):
+    """Verifies drafted trees against fp32 probability rows [rows, V] (one a node) with given
+    coins: tokens, parents (int32) and uniforms (fp32) are [B, N], or [rows] packed by
+    qo_indptr (int32 [B+1]). At most D drafts are accepted; outputs [B, D+1]."""
+    rows, V, ld = _rows(target_probs)
+    if target_probs.dtype != torch.float32:
+        raise TypeError("target_probs must be fp32")
+    if qo_indptr is None and tokens.dim() != 2:
+        raise ValueError("tokens must be [B, N] without qo_indptr")
+    B = tokens.shape[0] if qo_indptr is None else qo_indptr.numel() - 1
+    if tokens.numel() != rows:
+        raise ValueError("target_probs must have one row for each token")
+    if uniforms.dtype != torch.float32 or uniforms.numel() != rows or not uniforms.is_contiguous():
+        raise ValueError("uniforms must be a contiguous fp32 tensor with one coin for each token")
+    dev = target_probs.device
+    _same_device(dev, tokens=tokens, parents=parents, uniforms=uniforms, qo_indptr=qo_indptr)
+    with _On(dev, stream) as s:
+        acc, alen, aidx, lp = outputs or _chain_outputs(B, D + 1, dev, accept_index, logprobs)
+        a = TreeArgs(target_probs.data_ptr(), V, ld, B, rows,
+                     _int32("qo_indptr", qo_indptr, (B + 1,)),
+                     _int32("tokens", tokens, tokens.shape), _int32("parents", parents, tokens.shape),
+                     uniforms.data_ptr(), D, 0, acc.data_ptr(), alen.data_ptr(),
+                     None if aidx is None else aidx.data_ptr(), None if lp is None else lp.data_ptr())
+        _check("ts_tree_spec_sampling", load().ts_tree_spec_sampling(ctypes.byref(a), s))
+    return dict(accepted_tokens=acc, accept_length=alen, accept_index=aidx, logprobs=lp)
