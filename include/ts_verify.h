@@ -80,7 +80,8 @@ const char* ts_last_error_message(void);
  * library's device error word: 0 if no bounded wait ever gave up; otherwise bits 0-7
  * come from the cluster-staged kernels, bits 8-15 from the renorm row kernel, bits
  * 16-23 from the staged softmax and bits 24-31 from the chain kernel (bit 24: a stage
- * wait gave up; bit 25: a CTA's wait for its own copies in flight ran out). The word is
+ * wait gave up; bit 25: a CTA's wait for its own copies in flight ran out) and window
+ * attention (bit 27: a wait gave up; that call's outputs are unspecified). The word is
  * sticky until cleared, but it only reports: a later call is not affected by it.
  * Returns TS_ERR_TIMEOUT if a wait gave up, TS_ERR_CUDA if the read failed. A
  * diagnostic, not part of the hot path. */
@@ -385,7 +386,8 @@ typedef struct ts_attn_args {
  * of scratch (no zero fill needed). */
 ts_status ts_window_attention(const ts_attn_args* args, void* workspace, size_t ws_bytes,
                               cudaStream_t stream);
-size_t ts_attention_workspace_size(int32_t head_dim);
+size_t ts_attention_workspace_size(int64_t batch, int64_t total_rows, int32_t heads_q,
+                                   int32_t heads, int32_t head_dim);
 
 typedef struct ts_kv_append_args {
   const ts_kv_cache* cache;  /* host struct; seq_lens: tokens before the call (not updated) */

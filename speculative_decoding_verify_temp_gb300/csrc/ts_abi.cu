@@ -200,12 +200,13 @@ ts_status ts_device_error(uint32_t* word_host, int clear) {
   if (!word_host) return fail(TS_ERR_INVALID_ARG, "word_host is NULL");
   uint32_t w = 0;
   cudaError_t e = tsv::staged_read_error(&w, clear);
-  uint32_t w2 = 0, w3 = 0, w4 = 0;
+  uint32_t w2 = 0, w3 = 0, w4 = 0, w5 = 0;
   if (e == cudaSuccess) e = tsv::row_read_error(&w2, clear);
   if (e == cudaSuccess) e = tsv::softmax_read_error(&w3, clear);
   if (e == cudaSuccess) e = tsv::chain_read_error(&w4, clear);
+  if (e == cudaSuccess) e = tsv::window_read_error(&w5, clear);
   if (e != cudaSuccess) return cuda_fail(e, "reading the device error word");
-  w |= (w2 << 8) | (w3 << 16) | (w4 << 24);
+  w |= (w2 << 8) | (w3 << 16) | (w4 << 24) | (w5 << 27);
   *word_host = w;
   if (w) return fail(TS_ERR_TIMEOUT, "a bounded device wait gave up (word 0x%x)", w);
   g_msg[0] = 0;
@@ -669,14 +670,18 @@ ts_status ts_window_attention(const ts_attn_args* p, void* workspace, size_t ws_
       !multiple16(p->k_new, p->k_row_stride, p->k_head_stride) ||
       !multiple16(p->v_new, p->v_row_stride, p->v_head_stride) || !multiple16(p->out, 0, 0))
     return fail(TS_ERR_INVALID_ARG, "q, k_new, v_new and out need 16-byte aligned addresses and strides");
-  const size_t need = tsv::window_workspace(c.head_dim, sm_count());
+  const size_t need = tsv::window_workspace(c.batch, p->total_rows, p->heads_q, c.heads, c.head_dim, sm_count());
   if (!workspace || ws_bytes < need || !multiple16(workspace, 0, 0))
     return fail(TS_ERR_INVALID_ARG, "workspace must have %zu 16-byte aligned bytes (got %zu)", need, ws_bytes);
   return launched(tsv::launch_window(c, *p, workspace, sm_count(), stream), "window attention launch");
 }
 
-size_t ts_attention_workspace_size(int32_t head_dim) {
-  return head_dim == 64 || head_dim == 128 ? tsv::window_workspace(head_dim, sm_count()) : 0;
+size_t ts_attention_workspace_size(int64_t batch, int64_t total_rows, int32_t heads_q,
+                                   int32_t heads, int32_t head_dim) {
+  if (batch < 1 || batch > 1 << 16 || total_rows < 1 || total_rows > batch * TS_MAX_WINDOW || heads < 1 ||
+      heads_q < 1 || heads_q % heads || (head_dim != 64 && head_dim != 128))
+    return 0;
+  return tsv::window_workspace(batch, total_rows, heads_q, heads, head_dim, sm_count());
 }
 
 ts_status ts_kv_append(const ts_kv_append_args* p, cudaStream_t stream) {

@@ -22,13 +22,8 @@
 
 #include <algorithm>
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "../../include/ts_verify.h"
-#include "ts_common.cuh"
-#include "ts_internal.h"
-#include "ts_kv.cuh"
+#include "ts_window.cuh"
+#include "ts_window_prep.cuh"
 
 namespace tsv {
 
@@ -37,100 +32,10 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16 * kWarps;
-constexpr int window_ctas_per_sm(int) { return 2; }
+constexpr int kCtasPerSm = 2;
 constexpr int kMinTiles = 4;      // least tiles a CTA takes: pieces of 256 tokens or more
-constexpr float kNone = -1e30f;   // the reference before any token
-constexpr float kSlack = 8.f;
 
-struct Params {
-  ts_kv_cache c;
-  ts_attn_args a;
-  int32_t page_shift;
-  int32_t group;
-  float scale_log2;
-  float* part;      // [2 * CTAs][rows][D + 2] pieces: output, reference, sum
-  int4* desc;       // [CTAs] {tail unit's request, its head and row block, rows, 0 | 1: the
-                    // CTA's first piece ends its unit}
-};
-
-template <typename T>
-__device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1);
-template <>
-__device__ __forceinline__ void mma16816<__half>(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-template <>
-__device__ __forceinline__ void mma16816<__nv_bfloat16>(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <typename T>
-__device__ __forceinline__ uint32_t pack(float lo, float hi);
-template <>
-__device__ __forceinline__ uint32_t pack<__half>(float lo, float hi) { return f16x2(lo, hi); }
-template <>
-__device__ __forceinline__ uint32_t pack<__nv_bfloat16>(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <typename T>
-__device__ __forceinline__ float2 unpack(uint32_t w);
-template <>
-__device__ __forceinline__ float2 unpack<__half>(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
-template <>
-__device__ __forceinline__ float2 unpack<__nv_bfloat16>(uint32_t w) {
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-}
-template <typename T>
-__device__ __forceinline__ bool not_finite(uint32_t half_word);  // one 16-bit value
-template <>
-__device__ __forceinline__ bool not_finite<__half>(uint32_t w) { return (w & 0x7C00u) == 0x7C00u; }
-template <>
-__device__ __forceinline__ bool not_finite<__nv_bfloat16>(uint32_t w) { return (w & 0x7F80u) == 0x7F80u; }
-
-// What the line of tiles needs of a request.
-struct Req {
-  int64_t row0;
-  int32_t rows;    // window rows (0: skipped)
-  int32_t len;     // cached tokens
-  int32_t blocks;  // row blocks
-  int32_t ctx;     // tiles of cached tokens
-  int32_t tiles;   // all tiles of a unit (>= 1)
-  __device__ __forceinline__ int64_t weight(int heads) const {
-    return rows ? (int64_t)heads * blocks * tiles : 0;
-  }
-};
-
-template <int ROWS>
-__device__ __forceinline__ Req request(const Params& p, int64_t b) {
-  Req r;
-  if (p.a.qo_indptr) {
-    r.row0 = p.a.qo_indptr[b];
-    const int64_t r1 = p.a.qo_indptr[b + 1];
-    r.rows = r.row0 >= 0 && r1 <= p.a.total_rows && r1 > r.row0 && r1 - r.row0 <= TS_MAX_WINDOW ? (int)(r1 - r.row0) : 0;
-  } else {
-    r.rows = (int)(p.a.total_rows / p.c.batch);
-    r.row0 = b * r.rows;
-  }
-  const int64_t cap = (int64_t)p.c.max_pages << p.page_shift;
-  r.len = (int32_t)min((int64_t)max(p.c.seq_lens[b], 0), cap);
-  r.blocks = (r.rows * p.group + ROWS - 1) / ROWS;
-  r.ctx = (int)(((int64_t)r.len + kTile - 1) / kTile);
-  r.tiles = r.ctx + (p.a.k_new ? (r.rows + kTile - 1) / kTile : 0);
-  r.tiles = max(r.tiles, 1);
-  return r;
-}
-
-// A piece's slot: [rows][D] outputs, then [rows] references, then [rows] sums.
-__host__ __device__ constexpr int slot_floats(int rows, int D) { return rows * (D + 2); }
+using Params = WindowParams;
 
 template <int D, int MT, typename T>
 __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Params p) {
@@ -146,67 +51,22 @@ __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Par
   float* s_o = s_fac + ROWS;
   float* s_m = s_o + kWarps * ROWS * (D + 4);
   float* s_l = s_m + kWarps * ROWS;
-  __shared__ uint64_t s_sees[TS_MAX_WINDOW][2];  // bit j: the row sees window token j
-  __shared__ int64_t s_scan[kWarps], s_start;
-  __shared__ int32_t s_b;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-  const int64_t cta = blockIdx.x, ctas = gridDim.x;
-
-  // ---- this CTA's share of the line
-  int64_t mine = 0;
-  const int64_t each = (p.c.batch + kThreads - 1) / kThreads;
-  const int64_t b_lo = min(p.c.batch, tid * each), b_hi = min(p.c.batch, b_lo + each);
-  for (int64_t b = b_lo; b < b_hi; ++b) mine += request<ROWS>(p, b).weight(p.c.heads);
-  int64_t upto = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t t = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += t;
-  }
-  if (lane == 31) s_scan[warp] = upto;
-  if (tid == 0) s_b = -1;
-  __syncthreads();
-  int64_t all = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) upto += s_scan[w];
-    all += s_scan[w];
-  }
-  const int64_t share = max((all + ctas - 1) / ctas, (int64_t)kMinTiles);
-  const int64_t begin = min(all, cta * share), end = min(all, begin + share);
+  const int64_t cta = blockIdx.x;
   int4 desc = make_int4(-1, 0, 0, 0);
-  if (begin < end && upto - mine <= begin && begin < upto) {  // one thread
-    int64_t at = upto - mine;
-    for (int64_t b = b_lo; b < b_hi; ++b) {
-      const int64_t w = request<ROWS>(p, b).weight(p.c.heads);
-      if (begin < at + w) {
-        s_b = (int32_t)b;
-        s_start = begin - at;
-        break;
-      }
-      at += w;
-    }
-  }
-  __syncthreads();
-  if (begin >= end) {
+  grid_launch();
+  Line<ROWS, kTile> line;
+  if (!line_begin<ROWS, kTile, kThreads>(p, kMinTiles, line)) {
     if (tid == 0) p.desc[cta] = desc;
+    grid_wait();  // so that this kernel's end is the end of the one before too
     return;
   }
-  int64_t b = s_b;
-  Req r = request<ROWS>(p, b);
-  int32_t unit = (int32_t)(s_start / r.tiles), tile = (int32_t)(s_start % r.tiles);
-  int64_t left = end - begin;
-
-  while (left > 0) {
-    while (r.rows == 0 || unit >= p.c.heads * r.blocks) {
-      r = request<ROWS>(p, ++b);
-      unit = 0;
-    }
-    const int kvh = unit / r.blocks, block = unit % r.blocks;
-    const int t0 = tile, t1 = (int)min((int64_t)r.tiles, t0 + left);
-    const int rows = min(ROWS, r.rows * p.group - block * ROWS);  // of this block
-    const bool window = p.a.k_new != nullptr && t1 > r.ctx;
+  bool waited = false;
+  Segment sg;
+  while (line.next(p, sg)) {
+    const Req& r = sg.r;
+    const int kvh = sg.kvh, block = sg.block, t0 = sg.t0, t1 = sg.t1, rows = sg.rows;
 
     // ---- Q: row i of the unit is window row (block*ROWS + i) / group of head kvh*group +
     // the remainder. Each row's factor, then the fragments.
@@ -251,26 +111,6 @@ __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Par
         w[2 + half] = f16x2(v.x * inv, v.y * inv);
       }
       s_q[i] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    if (window) {
-      // what each window row sees; ancestors lie before a row, so the walks end
-      for (int i = tid; i < r.rows; i += kThreads) {
-        uint64_t lo = 0, hi = 0;
-        if (p.a.parents) {
-          int at = i;
-          while (at >= 0) {
-            if (at < 64) lo |= 1ull << at;
-            else hi |= 1ull << (at - 64);
-            const int up = p.a.parents[r.row0 + at];
-            at = up < at ? up : -1;
-          }
-        } else {
-          lo = i >= 63 ? ~0ull : (2ull << i) - 1;
-          hi = i >= 64 ? (2ull << (i - 64)) - 1 : 0;
-        }
-        s_sees[i][0] = lo;
-        s_sees[i][1] = hi;
-      }
     }
     __syncthreads();
 
@@ -341,8 +181,7 @@ __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Par
     // ---- cached tokens
     const char* kc = static_cast<const char*>(p.c.k) + kvh * p.c.k_head_stride;
     const char* vc = static_cast<const char*>(p.c.v) + kvh * p.c.v_head_stride;
-    const int32_t* table = p.c.page_table + b * p.c.ld_table;
-    const int ctx_end = min(t1, r.ctx);
+    const int32_t* table = p.c.page_table + sg.b * p.c.ld_table;
     struct Loaded {
       uint4 k[2][D / 64];
       uint32_t v[4][VW];
@@ -350,7 +189,7 @@ __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Par
     };
     auto page_of = [&](int t) -> int32_t {  // page of this warp's tokens of tile t, or -1
       const int64_t tok = (int64_t)t * kTile + warp * 16;
-      if (t >= ctx_end || tok >= r.len) return -1;
+      if (t >= t1 || tok >= r.len) return -1;
       const int32_t id = table[tok >> p.page_shift];
       return id >= 0 && id < p.c.num_pages ? id : -1;
     };
@@ -385,13 +224,13 @@ __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Par
     };
     Loaded next;
     int32_t page = page_of(t0), page2 = page_of(t0 + 1);
-    if (t0 < ctx_end) fetch(t0, page, next);
-    for (int t = t0; t < ctx_end; ++t) {
+    if (t0 < t1) fetch(t0, page, next);
+    for (int t = t0; t < t1; ++t) {
       Loaded now = next;
       const int32_t page_now = page;
       page = page2;
       page2 = page_of(t + 2);
-      if (t + 1 < ctx_end) fetch(t + 1, page, next);
+      if (t + 1 < t1) fetch(t + 1, page, next);
       if (page_now < 0) continue;
       const int tok = t * kTile + warp * 16;
       float x[MT][2][4];
@@ -455,120 +294,6 @@ __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Par
         }
     }
 
-    // ---- the window's own tokens, in their own type; probabilities in two parts of it
-    for (int t = max(t0, r.ctx); window && t < t1; ++t) {
-      const int tok = (t - r.ctx) * kTile + warp * 16;
-      if (tok >= r.rows) continue;
-      const char* kn = static_cast<const char*>(p.a.k_new) + (r.row0 + tok) * p.a.k_row_stride + kvh * p.a.k_head_stride;
-      const char* vn = static_cast<const char*>(p.a.v_new) + (r.row0 + tok) * p.a.v_row_stride + kvh * p.a.v_head_stride;
-      float x[MT][2][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[mt][n][e] = 0.f;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const int dim = (ks / 4) * 64 + c * 16 + (ks % 4) * 4;
-        uint2 kb[2];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          kb[n] = make_uint2(0, 0);
-          if (tok + n * 8 + g < r.rows)
-            kb[n] = *reinterpret_cast<const uint2*>(kn + (n * 8 + g) * p.a.k_row_stride + dim * 2);
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          uint32_t qa[4];
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int row = mt * 16 + half * 8 + g;
-            uint2 w = make_uint2(0, 0);
-            if (row < rows) w = *reinterpret_cast<const uint2*>(q_row(row) + dim * 2);
-            qa[half] = w.x;
-            qa[2 + half] = w.y;
-          }
-          mma16816<T>(x[mt][0], qa, kb[0].x, kb[0].y);
-          mma16816<T>(x[mt][1], qa, kb[1].x, kb[1].y);
-        }
-      }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int i = mt * 16 + (e >> 1) * 8 + g, j = tok + n * 8 + 2 * c + (e & 1);
-            const bool seen = i < rows && j < r.rows && (s_sees[(block * ROWS + i) / p.group][j >> 6] >> (j & 63) & 1);
-            x[mt][n][e] = seen ? x[mt][n][e] * p.scale_log2 : -INFINITY;
-          }
-      softmax(x, 1.f);
-      uint32_t pa[MT][4], pb[MT][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float u = x[mt][n][2 * h], v = x[mt][n][2 * h + 1];
-            const uint32_t w = pack<T>(u, v);
-            const float2 f = unpack<T>(w);
-            pa[mt][n * 2 + h] = w;
-            pb[mt][n * 2 + h] = pack<T>(u - f.x, v - f.y);
-          }
-      // a value that is not finite must reach only the rows that see it: 0 in the product,
-      // added row by row below
-      bool odd = false;
-      auto v_at = [&](int i, int dim) -> uint32_t {
-        if (tok + i >= r.rows) return 0;
-        return *reinterpret_cast<const uint16_t*>(vn + i * p.a.v_row_stride + dim * 2);
-      };
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int dim = g * (D / 8) + j;
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[i] = v_at(2 * c + (i & 1) + (i >> 1) * 8, dim);
-          if (not_finite<T>(w[i])) {
-            odd = true;
-            w[i] = 0;
-          }
-        }
-        const uint32_t b0 = w[0] | (w[1] << 16), b1 = w[2] | (w[3] << 16);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma16816<T>(o[mt][j], pa[mt], b0, b1);
-          mma16816<T>(o[mt][j], pb[mt], b0, b1);
-        }
-      }
-      if (__any_sync(0xffffffffu, odd)) {
-        for (int i = 0; i < 16; ++i) {
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              // p of (row h*8 + g, token i) lies in lane i % 8 / 2 of the quad
-              const int from = (lane & ~3) | ((i & 7) >> 1);
-              const float p0 = __shfl_sync(0xffffffffu, i < 8 ? x[mt][0][2 * h] : x[mt][1][2 * h], from);
-              const float p1 = __shfl_sync(0xffffffffu, i < 8 ? x[mt][0][2 * h + 1] : x[mt][1][2 * h + 1], from);
-              const int row = mt * 16 + h * 8 + g;
-              if (row >= rows || tok + i >= r.rows) continue;
-              const int j = tok + i;
-              if (!(s_sees[(block * ROWS + row) / p.group][j >> 6] >> (j & 63) & 1)) continue;
-#pragma unroll
-              for (int d = 0; d < NT; ++d)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const uint32_t w = v_at(i, (2 * c + e) * (D / 8) + d);
-                  if (not_finite<T>(w)) o[mt][d][2 * h + e] += (i & 1 ? p1 : p0) * unpack<T>(w).x;
-                }
-            }
-        }
-      }
-    }
-
     // ---- the warps meet: lane (g, c) holds dims (2c + e) * D/8 + j of rows g and g + 8
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -590,8 +315,12 @@ __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Par
             *reinterpret_cast<float4*>(at + (2 * c + e) * (D / 8) + j) =
                 make_float4(o[mt][j][2 * h + e], o[mt][j + 1][2 * h + e], o[mt][j + 2][2 * h + e], o[mt][j + 3][2 * h + e]);
       }
+    if (!waited) {  // for the window's own part
+      grid_wait();
+      waited = true;
+    }
     __syncthreads();
-    const bool whole = t0 == 0 && t1 == r.tiles;
+    const bool whole = sg.whole();
     const int slot = (int)(2 * cta) + (t0 == 0 ? 1 : 0);
     float* part = p.part + (int64_t)slot * slot_floats(ROWS, D);
     for (int i = tid; i < rows * (D / 4); i += kThreads) {
@@ -610,12 +339,14 @@ __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Par
         acc.z = fmaf(by, v.z, acc.z), acc.w = fmaf(by, v.w, acc.w);
       }
       if (whole) {
-        const int j = block * ROWS + row;
-        const int64_t at = (r.row0 + j / p.group) * p.a.heads_q + kvh * p.group + j % p.group;
-        const float inv = sum != 0.f ? 1.f / sum : 0.f;  // a row that saw nothing: 0
-        const uint2 w = make_uint2(pack<T>(acc.x * inv, acc.y * inv), pack<T>(acc.z * inv, acc.w * inv));
+        const int64_t at = sg.at(p, ROWS, row);
+        float own;
+        const float by = finish_row(p, at, top, sum, own);  // the row's threads write the same lse
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.own_ml) v = *reinterpret_cast<const float4*>(p.own_o + at * D + d);
+        const uint2 w = make_uint2(pack<T>(fmaf(acc.x, by, v.x * own), fmaf(acc.y, by, v.y * own)),
+                                   pack<T>(fmaf(acc.z, by, v.z * own), fmaf(acc.w, by, v.w * own)));
         *reinterpret_cast<uint2*>(static_cast<char*>(p.a.out) + (at * D + d) * 2) = w;
-        if (d == 0 && p.a.lse) p.a.lse[at] = sum != 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
       } else {
         *reinterpret_cast<float4*>(part + row * D + d) = acc;
         if (d == 0) {
@@ -626,53 +357,15 @@ __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Par
     }
     if (!whole) {
       if (t0 == 0) {
-        desc.x = (int)b;
-        desc.y = unit;
+        desc.x = (int)sg.b;
+        desc.y = kvh * r.blocks + block;
         desc.z = rows;
       } else {
         desc.w = t1 == r.tiles ? 1 : 0;
       }
     }
-    left -= t1 - t0;
-    tile = 0;
-    ++unit;
   }
   if (tid == 0) p.desc[cta] = desc;
-}
-
-// One warp a row of a unit that spans CTAs: the piece of the CTA where it begins (slot
-// 2i + 1), then the first pieces (slots 2j) of the CTAs after it up to the one that ends it.
-template <int D, int ROWS, typename T>
-__global__ void __launch_bounds__(kThreads) k_join(const __grid_constant__ Params p) {
-  const int first = blockIdx.x, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * kWarps + (threadIdx.x >> 5);
-  const int4 d = p.desc[first];
-  if (d.x < 0 || row >= d.z) return;
-  int pieces = 1;
-  while (first + pieces < (int)gridDim.x && p.desc[first + pieces].w == 0) ++pieces;
-  ++pieces;
-  auto piece = [&](int i) { return p.part + (int64_t)(i ? 2 * (first + i) : 2 * first + 1) * slot_floats(ROWS, D); };
-  float top = kNone;
-  for (int i = lane; i < pieces; i += 32) top = fmaxf(top, piece(i)[ROWS * D + row]);
-  top = warp_max(top);
-  constexpr int PER = D / 32;
-  float acc[PER] = {}, sum = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < pieces; ++i) {
-    const float* x = piece(i);
-    const float by = ex2(x[ROWS * D + row] - top);
-    sum = fmaf(by, x[ROWS * D + ROWS + row], sum);
-#pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] = fmaf(by, x[row * D + lane * PER + e], acc[e]);
-  }
-  const Req r = request<ROWS>(p, d.x);
-  const int kvh = d.y / r.blocks, j = d.y % r.blocks * ROWS + row;
-  const int64_t at = (r.row0 + j / p.group) * p.a.heads_q + kvh * p.group + j % p.group;
-  const float inv = sum != 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-  for (int e = 0; e < PER; e += 2)
-    *reinterpret_cast<uint32_t*>(static_cast<char*>(p.a.out) + (at * D + lane * PER + e) * 2) = pack<T>(acc[e] * inv, acc[e + 1] * inv);
-  if (lane == 0 && p.a.lse) p.a.lse[at] = sum != 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 constexpr int smem_bytes(int D, int rows) {
@@ -684,10 +377,16 @@ cudaError_t launch(const Params& p, int sms, cudaStream_t s) {
   constexpr int ROWS = 16 * MT, bytes = smem_bytes(D, ROWS);
   cudaError_t e = cudaFuncSetAttribute(k_window<D, MT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  const int grid = sms * window_ctas_per_sm(MT);
-  k_window<D, MT, T><<<grid, kThreads, bytes, s>>>(p);
-  k_join<D, ROWS, T><<<dim3(grid, ROWS / kWarps), kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  const int grid = sms * kCtasPerSm;
+  if (p.a.k_new) {
+    if ((e = launch_prep<D, ROWS, 0, T>(p, s)) != cudaSuccess) return e;
+    e = launch_after(k_window<D, MT, T>, dim3(grid), kThreads, bytes, s, p);
+  } else {
+    k_window<D, MT, T><<<grid, kThreads, bytes, s>>>(p);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) return e;
+  return launch_after(k_join<D, ROWS, kTile, T>, dim3(grid, ROWS / 4), 128, 0, s, p);
 }
 
 template <int MT>
@@ -698,16 +397,46 @@ cudaError_t launch_mt(const Params& p, int sms, cudaStream_t s) {
   return bf16 ? launch<64, MT, __nv_bfloat16>(p, sms, s) : launch<64, MT, __half>(p, sms, s);
 }
 
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// The rows of a block: by the average window.
+int block_rows(const WindowParams& p) {
+  const int64_t rows = (p.a.total_rows * p.group + p.c.batch - 1) / p.c.batch;
+  if (p.c.head_dim == 128) return rows <= 32 ? 32 : 64;
+  return rows <= 16 ? 16 : 32;
+}
+
+// Lays the workspace out; returns its bytes.
+size_t lay_out(WindowParams& p, void* ws, int sms) {
+  const int rows = block_rows(p), D = p.c.head_dim;
+  const size_t ctas = (size_t)sms * kCtasPerSm;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    char* at = static_cast<char*>(ws) + off;
+    off += up256(bytes);
+    return at;
+  };
+  p.desc = reinterpret_cast<int4*>(take(ctas * sizeof(int4)));
+  p.part = reinterpret_cast<float*>(take(2 * ctas * slot_floats(rows, D) * sizeof(float)));
+  const size_t n = (size_t)p.a.total_rows * p.a.heads_q;
+  p.own_o = reinterpret_cast<float*>(take(n * D * sizeof(float)));
+  p.own_ml = reinterpret_cast<float2*>(take(n * sizeof(float2)));
+  const size_t blocks = (size_t)block_count(p, rows) * p.c.heads;
+  p.q_parts = reinterpret_cast<uint8_t*>(take(D == 128 ? blocks * q_block_bytes(rows, 3) : 0));
+  return off;
+}
+
 }  // namespace
 
-size_t window_workspace(int head_dim, int sms) {
-  size_t most = 0;
-  for (int mt = 1; mt <= 2; ++mt) {
-    const size_t ctas = (size_t)sms * window_ctas_per_sm(mt);
-    const size_t n = ctas * sizeof(int4) + 2 * ctas * slot_floats(16 * mt, head_dim) * sizeof(float);
-    most = std::max(most, n);
-  }
-  return (most + 255) & ~(size_t)255;
+size_t window_workspace(int64_t batch, int64_t total_rows, int heads_q, int heads, int head_dim, int sms) {
+  WindowParams p{};
+  p.c.batch = batch;
+  p.c.heads = heads;
+  p.c.head_dim = head_dim;
+  p.a.total_rows = total_rows;
+  p.a.heads_q = heads_q;
+  p.group = heads_q / heads;
+  return lay_out(p, nullptr, sms);
 }
 
 cudaError_t launch_window(const ts_kv_cache& c, const ts_attn_args& a, void* ws, int sms, cudaStream_t s) {
@@ -717,13 +446,15 @@ cudaError_t launch_window(const ts_kv_cache& c, const ts_attn_args& a, void* ws,
   p.page_shift = __builtin_ctz((unsigned)c.page_size);
   p.group = a.heads_q / c.heads;
   p.scale_log2 = a.sm_scale * kLog2e;
-  // blocks of 16 rows where the average window has no more, else of 32: the cached codes are
-  // converted and read once a block
-  const int64_t rows = (a.total_rows * p.group + c.batch - 1) / c.batch;
-  const int mt = rows <= 16 ? 1 : 2;
-  p.desc = static_cast<int4*>(ws);
-  p.part = reinterpret_cast<float*>(p.desc + (size_t)sms * window_ctas_per_sm(mt));
-  return mt == 1 ? launch_mt<1>(p, sms, s) : launch_mt<2>(p, sms, s);
+  lay_out(p, ws, sms);
+  if (!a.k_new) p.own_ml = nullptr;
+  if (c.head_dim == 128) {
+    bool done = false;
+    const cudaError_t e = launch_window_tc(p, block_rows(p), sms, s, &done);
+    if (done || e != cudaSuccess) return e;
+    return launch_mt<2>(p, sms, s);
+  }
+  return block_rows(p) == 16 ? launch_mt<1>(p, sms, s) : launch_mt<2>(p, sms, s);
 }
 
 }  // namespace tsv

@@ -234,7 +234,7 @@ def load():
                                                 P, P, P, P, P, ctypes.c_size_t, P]
     L.ts_verify_chain_greedy_ragged.restype = st
     L.ts_sample_from_logits.restype = st
-    L.ts_attention_workspace_size.argtypes = [i32]
+    L.ts_attention_workspace_size.argtypes = [i64, i64, i32, i32, i32]
     L.ts_attention_workspace_size.restype = ctypes.c_size_t
     L.ts_window_attention.argtypes = [ctypes.POINTER(AttnArgs), P, ctypes.c_size_t, P]
     L.ts_window_attention.restype = st
@@ -558,14 +558,15 @@ def _heads(name, t, heads, D):
     return t.shape[0], t.stride(0) * size, t.stride(1) * size
 
 
-def attention_workspace_size(head_dim: int) -> int:
-    return int(load().ts_attention_workspace_size(head_dim))
+def attention_workspace_size(batch: int, rows: int, heads_q: int, heads: int, head_dim: int) -> int:
+    return int(load().ts_attention_workspace_size(batch, rows, heads_q, heads, head_dim))
 
 
-def make_attention_workspace(head_dim: int, device=None):
-    """Scratch for window_attention calls with this head_dim that do not overlap."""
+def make_attention_workspace(batch: int, rows: int, heads_q: int, heads: int, head_dim: int, device=None):
+    """Scratch for window_attention calls of this size that do not overlap."""
     with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
-        return torch.empty(attention_workspace_size(head_dim), dtype=torch.uint8, device="cuda")
+        return torch.empty(attention_workspace_size(batch, rows, heads_q, heads, head_dim),
+                           dtype=torch.uint8, device="cuda")
 
 
 def window_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, *, k_new=None,
@@ -599,7 +600,8 @@ def window_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens
             raise ValueError("out must be contiguous, with the shape and dtype of q")
         z = torch.empty(q.shape[:2], dtype=torch.float32, device=dev) if lse else None
         if workspace is None:
-            workspace = torch.empty(attention_workspace_size(D), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(attention_workspace_size(c.batch, rows, q.shape[1], c.heads, D),
+                                    dtype=torch.uint8, device=dev)
         a = AttnArgs(ctypes.pointer(c), q.data_ptr(), qr, qh, _kv_dtype(q.dtype), q.shape[1],
                      None if k_new is None else k_new.data_ptr(),
                      None if v_new is None else v_new.data_ptr(), kr, kh, vr, vh, rows,

@@ -224,7 +224,7 @@ def test_graph_streams_and_two_calls_at_once():
     b = make(17, [3, 9], [11, 1500], 8, 2, 128, 32, torch.bfloat16)
     want = [tv.window_attention(**x, lse=True) for x in (a, b)]
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
-    ws = [tv.make_attention_workspace(128) for _ in streams]
+    ws = [tv.make_attention_workspace(2, n, 8, 2, 128) for n in (7, 12)]
     torch.cuda.synchronize()
     got = [[], []]
     for _ in range(10):

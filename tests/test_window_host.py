@@ -95,9 +95,12 @@ def test_attention_refusals(lib, kw, word, status):
 
 
 def test_attention_workspace(lib):
-    need = lib.ts_attention_workspace_size(128)
-    assert need > lib.ts_attention_workspace_size(64) > 0 and need % 256 == 0
-    assert lib.ts_attention_workspace_size(96) == 0
+    need = lib.ts_attention_workspace_size(2, 6, 32, 8, 128)
+    assert need > lib.ts_attention_workspace_size(2, 6, 32, 8, 64) > 0 and need % 256 == 0
+    assert lib.ts_attention_workspace_size(2, 130, 32, 8, 128) > need
+    for bad in ((2, 6, 32, 8, 96), (0, 6, 32, 8, 128), (2, 131, 32, 8, 128), (2, 0, 32, 8, 128), (2, 6, 32, 7, 128),
+                (2, 6, 32, 0, 128), (1 << 17, 6, 32, 8, 128)):
+        assert lib.ts_attention_workspace_size(*bad) == 0
     for ws, n in ((None, need), (FAKE, need - 1), (FAKE + 4, need)):
         a = attn()
         assert lib.ts_window_attention(ctypes.byref(a), ctypes.c_void_p(ws), n, None) == 1

@@ -44,8 +44,9 @@ def sees(t, parents=None):
 def attention(q, k_cache, v_cache, k_scale, v_scale, table, lens, windows, k_new=None, v_new=None,
               parents=None, sm_scale=None):
     """out, lse and, per output element, what its error bound is made of: the weighted mean of
-    |v| and, per row, the largest sum of |q k| and the number of tokens. windows: (first row,
-    rows) of each request."""
+    |v| and, per row, the largest sum of |q k|, the number of tokens, and the largest |q| of the
+    request's rows of a KV head times the largest sum of |k|. windows: (first row, rows) of
+    each request."""
     rows, Hq, D = q.shape
     H = k_cache.shape[1]
     G = Hq // H
@@ -56,6 +57,7 @@ def attention(q, k_cache, v_cache, k_scale, v_scale, table, lens, windows, k_new
     lse = torch.full((rows, Hq), -math.inf, dtype=torch.float64)
     big = torch.zeros_like(lse)
     count = torch.zeros_like(lse)
+    floor = torch.zeros_like(lse)
     table = table.cpu()
     for b, (r0, t) in enumerate(windows):
         n = min(max(int(lens[b]), 0), table.shape[1] * k_cache.shape[2])
@@ -81,17 +83,21 @@ def attention(q, k_cache, v_cache, k_scale, v_scale, table, lens, windows, k_new
                 lse[r0 + i, h] = m + torch.log(z)
                 big[r0 + i, h] = (kk.abs() @ q[r0 + i, h].abs()).max() * abs(scale)
                 count[r0 + i, h] = len(idx)
-    return out, lse, absv, big, count
+                heads = q[r0:r0 + t, h // G * G:(h // G + 1) * G].abs()
+                floor[r0 + i, h] = heads.max() * kk.abs().sum(1).max() * abs(scale)
+    return out, lse, absv, big, count, floor
 
 
-def attention_bounds(out, lse, absv, big, count, dtype, D):
+def attention_bounds(out, lse, absv, big, count, floor, dtype, D):
     """How far the kernel may be off, from its roundings.
-    Scores: D + 4 fp32 roundings or truncations of partial sums no larger than sum |q k|
-    (2^-23 each), and q's 2^-25 of its row's largest: d = (D + 6) 2^-23 sum |q k|; the exponent's
+    Scores: D + 8 fp32 roundings or truncations of partial sums no larger than sum |q k|
+    (2^-23 each), and an error of each q of 2^-17 of the largest of its row block (e4m3 parts: the
+    largest lies in [2^7, 2^8), the last part is rounded to a multiple of 2^-9 or better):
+    d = (D + 8) 2^-23 sum |q k| + 2^-17 max |q| sum |k|; the exponent's
     argument is rounded in log2 units, at most as large (2^-23 of it) and the hardware 2^x is
     good to 2^-22. Probabilities: 2^-11 (fp16). Sums over n tokens: n 2^-23. The quotient of two
     such sums doubles what they share. The output is rounded by eps / 2 of its value."""
-    d = (D + 8) * 2.0 ** -23 * big + 2.0 ** -21
+    d = (D + 8) * 2.0 ** -23 * big + 2.0 ** -17 * floor + 2.0 ** -21
     share = 2.0 ** -11 + 2 * d + 2 * count * 2.0 ** -23
     half = torch.finfo(dtype).eps / 2
     tiny = torch.finfo(dtype).tiny
