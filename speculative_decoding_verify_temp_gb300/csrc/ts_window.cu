@@ -23,7 +23,7 @@
 #include <algorithm>
 
 #include "ts_window.cuh"
-#include "ts_window_prep.cuh"
+#include "ts_window_own.cuh"
 
 namespace tsv {
 
@@ -379,7 +379,7 @@ cudaError_t launch(const Params& p, int sms, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int grid = sms * kCtasPerSm;
   if (p.a.k_new) {
-    if ((e = launch_prep<D, ROWS, 0, T>(p, s)) != cudaSuccess) return e;
+    if ((e = launch_own<D, ROWS, T>(p, s)) != cudaSuccess) return e;
     e = launch_after(k_window<D, MT, T>, dim3(grid), kThreads, bytes, s, p);
   } else {
     k_window<D, MT, T><<<grid, kThreads, bytes, s>>>(p);
@@ -421,8 +421,6 @@ size_t lay_out(WindowParams& p, void* ws, int sms) {
   const size_t n = (size_t)p.a.total_rows * p.a.heads_q;
   p.own_o = reinterpret_cast<float*>(take(n * D * sizeof(float)));
   p.own_ml = reinterpret_cast<float2*>(take(n * sizeof(float2)));
-  const size_t blocks = (size_t)block_count(p, rows) * p.c.heads;
-  p.q_parts = reinterpret_cast<uint8_t*>(take(D == 128 ? blocks * q_block_bytes(rows, 3) : 0));
   return off;
 }
 

@@ -24,9 +24,6 @@ struct WindowParams {
   float* part;      // [2 * CTAs][rows * (D + 2)] pieces: outputs, references, sums
   int4* desc;       // [CTAs] {tail unit's request, its head and row block, rows, 0 | 1: the
                     // CTA's first piece ends its unit}
-  // ts_window_tc.cu: what the first kernel prepares
-  uint8_t* q_parts;  // [blocks][heads]: [parts][rows][D] codes as they lie in shared memory, and
-                     // in 16 bytes more the scale that they stand for
   float* own_o;      // [total_rows * heads_q][D] the window's own part: outputs,
   float2* own_ml;    // [total_rows * heads_q] references and sums
 };
@@ -69,12 +66,13 @@ template <>
 __device__ __forceinline__ float2 unpack<__nv_bfloat16>(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
+// Bits 15 and 31: the low and the high value are not finite (all exponent bits set).
 template <typename T>
-__device__ __forceinline__ bool not_finite(uint32_t half_word);  // one 16-bit value
+__device__ __forceinline__ uint32_t not_finite(uint32_t w);
 template <>
-__device__ __forceinline__ bool not_finite<__half>(uint32_t w) { return (w & 0x7C00u) == 0x7C00u; }
+__device__ __forceinline__ uint32_t not_finite<__half>(uint32_t w) { return ((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u; }
 template <>
-__device__ __forceinline__ bool not_finite<__nv_bfloat16>(uint32_t w) { return (w & 0x7F80u) == 0x7F80u; }
+__device__ __forceinline__ uint32_t not_finite<__nv_bfloat16>(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
 
 // What the line of tiles needs of a request.
 struct Req {
@@ -115,16 +113,15 @@ __device__ __forceinline__ Req request(const WindowParams& p, const RawReq& raw)
   const bool fits = raw.row0 >= 0 && raw.row1 <= p.a.total_rows && raw.row1 > raw.row0 && raw.row1 - raw.row0 <= TS_MAX_WINDOW;
   r.rows = fits ? raw.row1 - raw.row0 : 0;
   r.len = min(max(raw.len, 0), p.c.max_pages << p.page_shift);  // at most 2^30
-  r.blocks = (r.rows * p.group + ROWS - 1) / ROWS;
-  r.tiles = max((r.len + TILE - 1) / TILE, 1);
+  r.blocks = (int)((unsigned)(r.rows * p.group + ROWS - 1) / ROWS);
+  r.tiles = max((int)((unsigned)(r.len + TILE - 1) / TILE), 1);
   return r;
 }
 
 // A CTA's share of the line of all units' tiles: segments, each of one unit.
 struct Segment {
   Req r;
-  int64_t b;
-  int32_t kvh, block, rows;  // rows of this block
+  int32_t b, kvh, block, rows;  // rows of this block
   int32_t t0, t1;
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == r.tiles; }
   // window row and head of the block's row i, as an index of [total_rows][heads_q]
@@ -138,25 +135,30 @@ template <int ROWS, int TILE>
 struct Line {
   Req r;
   RawReq after;  // the request behind it
-  int64_t b, left;
-  int32_t unit, tile;
+  int64_t left;
+  int32_t b, kvh, block, tile;
   __device__ __forceinline__ bool next(const WindowParams& p, Segment& s) {
     if (left <= 0) return false;
-    while (r.rows == 0 || unit >= p.c.heads * r.blocks) {
+    if (block >= r.blocks) {
+      block = 0;
+      ++kvh;
+    }
+#pragma unroll 1
+    while (r.rows == 0 || kvh >= p.c.heads) {
       r = request<ROWS, TILE>(p, after);
       after = raw_request(p, ++b + 1);
-      unit = 0;
+      kvh = block = 0;
     }
     s.r = r;
     s.b = b;
-    s.kvh = unit / r.blocks;
-    s.block = unit % r.blocks;
-    s.rows = min(ROWS, r.rows * p.group - s.block * ROWS);
+    s.kvh = kvh;
+    s.block = block;
+    s.rows = min(ROWS, r.rows * p.group - block * ROWS);
     s.t0 = tile;
     s.t1 = (int)min((int64_t)r.tiles, tile + left);
     left -= s.t1 - s.t0;
     tile = 0;
-    ++unit;
+    ++block;
     return true;
   }
 };
@@ -173,6 +175,7 @@ __device__ __forceinline__ bool line_begin(const WindowParams& p, int least, Lin
   int64_t mine = 0;
   const int64_t each = (p.c.batch + THREADS - 1) / THREADS;
   const int64_t b_lo = min(p.c.batch, tid * each), b_hi = min(p.c.batch, b_lo + each);
+#pragma unroll 1
   for (int64_t b = b_lo; b < b_hi; ++b) mine += request<ROWS, TILE>(p, raw_request(p, b)).weight(p.c.heads);
   int64_t upto = mine;
 #pragma unroll
@@ -192,6 +195,7 @@ __device__ __forceinline__ bool line_begin(const WindowParams& p, int least, Lin
   const int64_t begin = min(all, blockIdx.x * share), end = min(all, begin + share);
   if (begin < end && upto - mine <= begin && begin < upto) {  // one thread
     int64_t at = upto - mine;
+#pragma unroll 1
     for (int64_t b = b_lo; b < b_hi; ++b) {
       const int64_t w = request<ROWS, TILE>(p, raw_request(p, b)).weight(p.c.heads);
       if (begin < at + w) {
@@ -207,8 +211,10 @@ __device__ __forceinline__ bool line_begin(const WindowParams& p, int least, Lin
   line.b = s_b;
   line.r = request<ROWS, TILE>(p, raw_request(p, line.b));
   line.after = raw_request(p, line.b + 1);
-  line.unit = (int32_t)(s_start / line.r.tiles);
+  const int32_t unit = (int32_t)(s_start / line.r.tiles);
   line.tile = (int32_t)(s_start % line.r.tiles);
+  line.kvh = unit / line.r.blocks;
+  line.block = unit % line.r.blocks;
   line.left = end - begin;
   return true;
 }
@@ -222,22 +228,22 @@ __host__ __device__ inline int64_t block_base(int64_t row0, int group, int rows,
 }
 inline int64_t block_count(const WindowParams& p, int rows) { return p.a.total_rows * p.group / rows + p.c.batch; }
 
-// The final scale and lse of a row: reference top and sum of the cached tokens; joined with
-// the window's own part, whose factor comes back in own. The factor of the cached part is
-// returned.
+// The final scale of a row (1 / sum) and its lse, from its reference and sum; 0 for a row that
+// saw nothing.
+__device__ __forceinline__ float finish_row(const WindowParams& p, int64_t at, float top, float sum) {
+  if (p.a.lse) p.a.lse[at] = sum != 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+  return sum != 0.f ? 1.f / sum : 0.f;
+}
+
+// The same, joined with the window's own part if there is one in own_ml: its factor comes back
+// in own.
 __device__ __forceinline__ float finish_row(const WindowParams& p, int64_t at, float top, float sum, float& own) {
   own = 0.f;
-  float by = 1.f;
-  if (p.own_ml) {
-    const float2 ml = p.own_ml[at];
-    const float to = fmaxf(top, ml.x);
-    by = ex2(top - to);
-    own = ex2(ml.x - to);
-    sum = fmaf(sum, by, ml.y * own);
-    top = to;
-  }
-  const float inv = sum != 0.f ? 1.f / sum : 0.f;  // a row that saw nothing: 0
-  if (p.a.lse) p.a.lse[at] = sum != 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+  if (!p.own_ml) return finish_row(p, at, top, sum);
+  const float2 ml = p.own_ml[at];
+  const float to = fmaxf(top, ml.x), by = ex2(top - to);
+  own = ex2(ml.x - to);
+  const float inv = finish_row(p, at, to, fmaf(sum, by, ml.y * own));
   own *= inv;
   return by * inv;
 }

@@ -1,7 +1,6 @@
 // Window attention over the 8-bit cache on the tensor cores, head_dim 128.
 //
-//   k_window_prep  (ts_window_prep.cuh) Q in e4m3 parts, and the window's own part
-//   k_window_tc    the cached tokens: one persistent CTA an SM
+//   k_window_tc    one persistent CTA an SM: the cached tokens, and the window's own
 //   k_join         joins the pieces of units that more than one CTA worked on
 //
 // The cache is read once and its bytes go to the tensor cores as they are: TMA brings pages
@@ -13,29 +12,31 @@
 //   S^T [128 tokens x ROWS] = K [128 x D] (Q_hi + Q_lo (+ Q_lo2))^T      one accumulator
 //   O^T [D x 3 ROWS]       += V^T [D x 128 tokens] [P_hi | P_lo | P_lo2]  one accumulator a part
 //
-// A thread of a softmax group is a token: it reads its row of S^T from TMEM, the scales of its
-// block and its validity are its own, and it writes its row of P. P = 2^(x - m) with a
-// reference m a row (x in log2 units, V's scale in the exponent as in ts_window.cu); a
-// reference follows only when a score exceeds it by 2^8 (one vote a tile), and then O is scaled
-// in TMEM. Parts of P: the fp16 rounding of p in three codes, the second and third scaled by
-// 2^5 and 2^10, so that all 11 bits are kept down to 2^-20 where the row's largest p is between
-// 2^7 and 2^8.
+// P = 2^(x - m) with a reference m a row (x in log2 units, V's scale in the exponent as in
+// ts_window.cu); a reference follows only when a score exceeds it by 2^8 (one vote a tile), and
+// then O is scaled in TMEM. Parts of P: the fp16 rounding of p in three codes, the second and
+// third scaled by 2^5 and 2^10, so that all 11 bits are kept down to 2^-9, and values down to
+// 2^-20, where the row's largest p is between 2^4 and 2^8.
 //
-// Two softmax groups of four warps take turns at the tiles, each with its own S, O, m and
-// sums in TMEM and registers, so that one's arithmetic overlaps the other's products; they
-// meet at the end of a unit. One warp loads (a ring of four tiles of 32 KB, 128 KB in flight
-// an SM), one lane issues the products.
+// A softmax thread is a token: it reads its row of S^T from TMEM, the scales of its block and
+// its validity are its own, and it writes its row of P. Its work on a tile is a chain of waits
+// and short bursts, so four groups of four warps work on different parts of the line: with
+// blocks of 32 rows each group takes every fourth tile, with blocks of 64 two groups share a
+// tile (32 rows each) and two pairs take turns. Tiles of one turn have their own S, P and O; the
+// turns meet at the end of a unit, where the window's own tokens come in (ts_window_own.cuh) and
+// the result is written. One warp each loads K (with the blocks' scales) and V, rings of four
+// tiles or 64 KB; a lane each of two warps issues the first and the second products. The first
+// of them also splits Q, the second looks up what the rows of a tree see.
 //
 // Every wait on a barrier is bounded; after one ran out no wait waits and nothing more is
 // issued, so that the CTA runs to its end (results unspecified, reported by ts_device_error).
-#include <cuda.h>
 #include <stddef.h>
 #include <stdint.h>
 
 #include <algorithm>
 
 #include "ts_window.cuh"
-#include "ts_window_prep.cuh"
+#include "ts_window_own.cuh"
 
 namespace tsv {
 
@@ -46,68 +47,90 @@ constexpr int kD = 128;
 constexpr int kStages = 4;         // tiles of K, and as many of V, in shared memory
 constexpr int kStageBytes = kTile * kD;
 constexpr int kMeta = 8;           // tiles whose scales are in shared memory
-constexpr int kAhead = 2;          // tiles that K and its products run ahead of V and its: a unit's
-                                   // scores are ready when its group comes to them
 constexpr int kParts = 3;          // of a probability
+constexpr int kGroups = 4;         // of softmax threads
 constexpr int kGroupThreads = 128;
-constexpr int kThreads = 3 * kGroupThreads;  // two softmax groups; the third's first two warps load and issue
-// registers a thread: 2 * 208 + 88 = 3 * 168, what the block is launched with
-constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
-static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "the groups' registers");
+constexpr int kSoftmaxThreads = kGroups * kGroupThreads;
+constexpr int kThreads = kSoftmaxThreads + 128;
+constexpr int kCols = 32;          // rows of a block that a softmax thread has scores of
 constexpr int kMinTiles = 2;       // least tiles a CTA takes: pieces of 256 tokens or more
 constexpr float kHead = 4.f;       // a reference is set this far below the largest score
-constexpr uint64_t kWaitCycles = (uint64_t)1 << 32;
+constexpr int kOwnLd = kD + 4;     // floats between rows of the window's own part
+constexpr int kBarAll = kGroups + 1;  // named barrier of all softmax threads; 1 .. kGroups: a group's
 
 __device__ uint32_t g_window_error;
 
 template <int ROWS, int QP>
 struct Layout {
   static constexpr int q_bytes = QP * ROWS * kD;
-  static constexpr int q_buffers = ROWS == 64 && QP == 3 ? 1 : 2;  // what shared memory has room for
   static constexpr int p_part = ROWS * kTile;
+  static constexpr bool split = ROWS == 2 * kCols;        // two groups share a tile's rows
+  static constexpr int turns = split ? kGroups / 2 : kGroups;  // tiles in work at a time
   static constexpr int off_v = kStages * kStageBytes;
   static constexpr int off_q = 2 * kStages * kStageBytes;
-  static constexpr int off_p = off_q + q_buffers * q_bytes;
-  static constexpr int off_x = off_p + 2 * kParts * p_part;
-  static constexpr int group_cols = (1 + kParts) * ROWS;  // TMEM columns of a group: S, O parts
+  static constexpr int off_p = off_q + q_bytes;
+  static constexpr int off_x = off_p + turns * kParts * p_part;
+  // TMEM columns: the turns' S, then their O, a part after the other
+  static constexpr int col_o = turns * ROWS, o_cols = kParts * ROWS;
+  static constexpr int tmem_cols = 512;
+  static_assert(col_o + turns * o_cols <= tmem_cols, "TMEM");
+  static_assert(ROWS * kOwnLd * 4 <= turns * kParts * p_part, "the own part lies in P's place");
 };
 
 template <int ROWS>
 struct Shared {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], meta_full[kMeta];
-  uint64_t q_full[2], q_empty[2], s_full[2], s_free[2], p_full[2], o_done[2], o_free;
-  alignas(16) float q_scale[2][4];         // what Q's codes stand for
-  float ks[kMeta][8], vs[kMeta][8];        // scales of a tile's pages (vs 0: no such page)
-  alignas(16) float m[2][ROWS];            // read as float4
-  alignas(16) float delta[2][ROWS];
-  float red[2][4][ROWS];
-  float4 w[ROWS];  // a row's factors: the groups' and the window's own part
-  int32_t at[2][ROWS];  // a row's index in [total_rows][heads_q], a copy for each group
-  int32_t live[2];
+  uint64_t s_full[kGroups], s_free[kGroups], p_full[kGroups], o_done[kGroups];  // a turn's
+  uint64_t q_full, q_empty, o_free, trees_full;
+  float q_scale;                            // what Q's codes stand for
+  float ks[kMeta][8], vs[kMeta][8];         // scales of a tile's pages (vs 0: no such page)
+  alignas(16) float neg_m[kGroups][kCols];  // a group's references, negated; read as vectors
+  alignas(16) float delta[kGroups][kCols];
+  float red[kGroups][4][kCols];
+  float w[kGroups + 1][ROWS];  // a row's factors: the turns', and the window's own part
+  float2 own[ROWS];            // the own part's references and sums
+  int32_t at[ROWS];            // a row's index in [total_rows][heads_q]
+  int32_t parents[TS_MAX_WINDOW];
+  Sees trees[TS_MAX_WINDOW];
+  int32_t live[kGroups];
   uint32_t tmem;
   int32_t stop;
 };
 
-static_assert(offsetof(Shared<32>, m) % 16 == 0 && offsetof(Shared<64>, m) % 16 == 0 && offsetof(Shared<32>, w) % 16 == 0 &&
-                  offsetof(Shared<64>, w) % 16 == 0 && Layout<32, 2>::off_x % 16 == 0,
+static_assert(offsetof(Shared<32>, neg_m) % 16 == 0 && offsetof(Shared<64>, neg_m) % 16 == 0 &&
+                  offsetof(Shared<32>, delta) % 16 == 0 && offsetof(Shared<64>, delta) % 16 == 0 &&
+                  Layout<32, 2>::off_x % 16 == 0 && Layout<64, 3>::off_x % 16 == 0,
               "vector loads");
 
 template <int ROWS, int QP>
 constexpr int smem_bytes() { return Layout<ROWS, QP>::off_x + (int)sizeof(Shared<ROWS>) + 1024; }
+static_assert(smem_bytes<64, 3>() <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ bool stopped(const int32_t* stop) { return *reinterpret_cast<const volatile int32_t*>(stop) != 0; }
 
+// Waits for a phase; gives up after two to three turns of the clock's upper word (4 to 7 s) and
+// sets *stop, or when that is set. Written out for size: it stands in every loop, and the loops
+// of the six roles have to stay in the instruction caches.
 __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, int32_t* stop) {
-  if (mbar_try_wait(bar, parity)) return;
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (stopped(stop)) return;
-    if ((uint64_t)(clock64() - t0) > kWaitCycles) {
-      *reinterpret_cast<volatile int32_t*>(stop) = 1;
-      atomicOr(&g_window_error, 1u);
-      return;
-    }
-  }
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .u32 t0, t1, f;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n"
+      " @p bra.uni DONE_%=;\n"
+      " mov.u32 t0, %%clock_hi;\n"
+      "AGAIN_%=:\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n"
+      " @p bra.uni DONE_%=;\n"
+      " ld.volatile.shared.u32 f, [%2];\n"
+      " setp.ne.u32 p, f, 0;\n"
+      " @p bra.uni DONE_%=;\n"
+      " mov.u32 t1, %%clock_hi;\n"
+      " sub.u32 t1, t1, t0;\n"
+      " setp.lt.u32 p, t1, 3;\n"
+      " @p bra.uni AGAIN_%=;\n"
+      " st.volatile.shared.u32 [%2], 1;\n"
+      "DONE_%=:\n}\n" ::"r"(smem_u32(bar)),
+      "r"(parity), "r"(smem_u32(stop))
+      : "memory");
 }
 
 __device__ __forceinline__ void bar_sync(int id, int threads) {
@@ -124,7 +147,7 @@ __device__ __forceinline__ bool bar_or(int id, int threads, bool x) {
   return r != 0;
 }
 
-// Of the lanes' 32 columns x: lane l gets the reduction of column l over the lanes. 31 shuffles.
+// Of the lanes' 16 columns x: lane l gets the reduction of column l % 16 over the lanes. 16 shuffles.
 template <int O, typename F>
 __device__ __forceinline__ void halve(float* y, int lane, F f) {
   const bool up = lane & O;
@@ -136,25 +159,29 @@ __device__ __forceinline__ void halve(float* y, int lane, F f) {
   if constexpr (O > 1) halve<O / 2>(y, lane, f);
 }
 template <typename F>
-__device__ __forceinline__ float reduce_columns(const float* x, int lane, F f) {
-  float y[16];
-  const bool up = lane & 16;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float keep = up ? x[i + 16] : x[i], give = up ? x[i] : x[i + 16];
-    y[i] = f(keep, __shfl_xor_sync(0xffffffffu, give, 16));
-  }
-  halve<8>(y, lane, f);
-  return y[0];
+__device__ __forceinline__ float reduce_columns(float* x, int lane, F f) {
+  halve<8>(x, lane, f);
+  return f(x[0], __shfl_xor_sync(0xffffffffu, x[0], 16));
 }
 
-// The next part of two values: its codes; the values become the rest, times 2^5 (exact).
-__device__ __forceinline__ uint16_t next_part(__half2& h) {
-  uint16_t codes;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(codes) : "r"(*reinterpret_cast<const uint32_t*>(&h)));
-  const uint32_t back = e4m3x2_to_f16x2(codes);
-  h = __hmul2(__hsub2(h, *reinterpret_cast<const __half2*>(&back)), __float2half2_rn(32.f));
+// The next part of four values: its codes; the values become the rest, times 2^5 (exact).
+__device__ __forceinline__ uint32_t next_part(__half2& a, __half2& b) {
+  uint32_t codes, back_a, back_b;
+  asm("{\n .reg .b16 u, v;\n cvt.rn.satfinite.e4m3x2.f16x2 u, %3;\n cvt.rn.satfinite.e4m3x2.f16x2 v, %4;\n"
+      " mov.b32 %0, {u, v};\n cvt.rn.f16x2.e4m3x2 %1, u;\n cvt.rn.f16x2.e4m3x2 %2, v;\n}\n"
+      : "=r"(codes), "=r"(back_a), "=r"(back_b)
+      : "r"(*reinterpret_cast<const uint32_t*>(&a)), "r"(*reinterpret_cast<const uint32_t*>(&b)));
+  const __half2 by = __float2half2_rn(32.f);
+  a = __hmul2(__hsub2(a, *reinterpret_cast<const __half2*>(&back_a)), by);
+  b = __hmul2(__hsub2(b, *reinterpret_cast<const __half2*>(&back_b)), by);
   return codes;
+}
+
+// A value that the compiler knows nothing about: branches on it are not merged into copies of
+// the code between them (the loops have to stay in the instruction caches).
+__device__ __forceinline__ int apart(int v) {
+  asm volatile("" : "+r"(v));
+  return v;
 }
 
 template <int ROWS, int QP, typename T>
@@ -168,16 +195,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* s_p = sm + L::off_p;
   Shared<ROWS>& x = *reinterpret_cast<Shared<ROWS>*>(sm + L::off_x);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kFirst = kSoftmaxThreads / 32;  // the warps behind the softmax groups
   int4 desc = make_int4(-1, 0, 0, 0);
   grid_launch();
   Line<ROWS, kTile> line;
   if (!line_begin<ROWS, kTile, kThreads>(p, kMinTiles, line)) {
     if (tid == 0) p.desc[blockIdx.x] = desc;
-    grid_wait();  // so that this kernel's end is the end of the one before too
     return;
   }
-  constexpr uint32_t kTmemCols = 2 * L::group_cols;  // 256 or 512
-  if (warp == 9) tmem_alloc(&x.tmem, kTmemCols);
+  if (warp == kFirst) tmem_alloc(&x.tmem, L::tmem_cols);
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&x.k_full[i], 1);
@@ -186,15 +212,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&x.v_empty[i], 1);
     }
     for (int i = 0; i < kMeta; ++i) mbar_init(&x.meta_full[i], 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&x.q_full[i], 1);
-      mbar_init(&x.q_empty[i], 3);  // the products, and both groups have read the scale
+    for (int i = 0; i < L::turns; ++i) {
       mbar_init(&x.s_full[i], 1);
-      mbar_init(&x.s_free[i], 4);
-      mbar_init(&x.p_full[i], 4);
+      mbar_init(&x.s_free[i], L::split ? 8 : 4);
+      mbar_init(&x.p_full[i], L::split ? 8 : 4);
       mbar_init(&x.o_done[i], 1);
     }
-    mbar_init(&x.o_free, 8);
+    mbar_init(&x.q_full, 1);
+    mbar_init(&x.q_empty, 1 + kGroups);  // the products, and the groups have read the scale
+    mbar_init(&x.o_free, kSoftmaxThreads / 32);
+    mbar_init(&x.trees_full, 1);
     x.stop = 0;
     fence_mbar_init();
   }
@@ -204,277 +231,319 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = x.tmem;
   Segment s{};
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 8) {
-      // ---- loads: lane i brings page i of a tile. K runs kAhead tiles ahead of V, across
-      // units.
-      const int pages = kTile >> p.page_shift;
+  if (warp >= kFirst) {
+    if (warp < kFirst + 2) {
+      // ---- loads: one warp K and the scales, one V. Page numbers come 32 a round, one a lane,
+      // two rounds ahead, and the scales one round ahead (they are scattered reads of DRAM, two
+      // of them in a row before a tile's scores can be formed; the same goes for the unit
+      // ahead). The lanes that hold a tile's pages bring them.
+      const bool is_k = warp == kFirst;
+      const CUtensorMap* map = is_k ? &k_map : &v_map;
+      unsigned char* ring = sm + (is_k ? 0 : L::off_v);
+      uint64_t *full = is_k ? x.k_full : x.v_full, *empty = is_k ? x.k_empty : x.v_empty;
+      const int per_tile = kTile >> p.page_shift, per_round = 32 / per_tile;  // pages, tiles
       const int page_bytes = p.c.page_size * kD;
-      uint32_t ik = 0, iv = 0, u = 0;
-      int32_t page_a = -1, head_a = 0, page_b = -1, head_b = 0;  // of the last two tiles, V not loaded yet
-      auto load = [&](uint32_t i, unsigned char* base, const CUtensorMap* map, int32_t page, int32_t head, uint64_t* full, uint64_t* empty) {
-        const int st = i % kStages;
-        wait(&empty[st], (i / kStages & 1) ^ 1, &x.stop);
-        __syncwarp();
-        if (stopped(&x.stop)) return;
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], kStageBytes);
-        __syncwarp();
-        // a page outside the tensor reads as zeros
-        if (lane < pages)
-          tma_load_4d(base + st * kStageBytes + lane * page_bytes, map, 0, 0, head, page >= 0 ? page : (int32_t)p.c.num_pages, &full[st]);
+      // the lane's page of round r of a segment, or -1
+      auto page_of = [&](const Segment& g, int r) -> int32_t {
+        const int i = g.t0 * per_tile + r * 32 + lane;
+        if (i >= g.t1 * per_tile || (int64_t)i << p.page_shift >= g.r.len) return -1;
+        const int32_t id = p.c.page_table[g.b * p.c.ld_table + i];
+        return id >= 0 && id < p.c.num_pages ? id : -1;
       };
-      auto load_v = [&]() {
-        const bool two = ik - iv == 2;
-        load(iv, sm + L::off_v, &v_map, two ? page_a : page_b, two ? head_a : head_b, x.v_full, x.v_empty);
-        ++iv;
+      auto scales_of = [&](const Segment& g, int32_t page, float& ks, float& vs) {
+        ks = vs = 0.f;
+        if (page < 0 || !is_k) return;
+        const int64_t at = (int64_t)page * p.c.heads + g.kvh;
+        ks = __ldg(p.c.k_scale + at);
+        vs = fmaxf(__ldg(p.c.v_scale + at), 0x1p-100f);
       };
-      auto load_q = [&]() {
-        const int qb = u % L::q_buffers;
-        wait(&x.q_empty[qb], (u / L::q_buffers & 1) ^ 1, &x.stop);
-        __syncwarp();
-        if (lane == 0 && !stopped(&x.stop)) {
-          const int64_t blk = block_base(s.r.row0, p.group, ROWS, s.b) + s.block;
-          const uint8_t* q = p.q_parts + (blk * p.c.heads + s.kvh) * q_block_bytes(ROWS, QP);
-          mbar_arrive_expect_tx(&x.q_full[qb], L::q_bytes + 16);
-          bulk_g2s(s_q + qb * L::q_bytes, q, L::q_bytes, &x.q_full[qb]);
-          bulk_g2s(x.q_scale[qb], q + L::q_bytes, 16, &x.q_full[qb]);
-        }
-        __syncwarp();
-        ++u;
-      };
-      bool waited = false;
-      while (line.next(p, s)) {
-        const int32_t* table = p.c.page_table + s.b * p.c.ld_table;
-        auto page_of = [&](int t) -> int32_t {
-          const int32_t tok = t * kTile + (lane << p.page_shift);
-          if (lane >= pages || t >= s.t1 || tok >= s.r.len) return -1;
-          const int32_t id = table[tok >> p.page_shift];
-          return id >= 0 && id < p.c.num_pages ? id : -1;
-        };
-        auto scales_of = [&](int32_t page, float& ks, float& vs) {
-          ks = vs = 0.f;
-          if (page < 0) return;
-          ks = __ldg(p.c.k_scale + (int64_t)page * p.c.heads + s.kvh);
-          vs = fmaxf(__ldg(p.c.v_scale + (int64_t)page * p.c.heads + s.kvh), 0x1p-100f);
-        };
-        int32_t page = page_of(s.t0), page1 = page_of(s.t0 + 1);
-        // Q comes from the kernel before; the first tiles of the cache need not wait for it
-        bool q_due = true;
-        if (waited) {
-          // with one buffer, Q waits for the unit before, and that for the rest of its V
-          if (L::q_buffers == 1)
-            while (iv < ik) load_v();
-          load_q();
-          q_due = false;
-        }
-        float ks, vs;
-        scales_of(page, ks, vs);
-        for (int t = s.t0; t < s.t1; ++t) {
-          const int32_t page2 = page_of(t + 2);
+      Segment ahead;
+      bool more = line.next(p, s);
+      int32_t page = page_of(s, 0), page1 = page_of(s, 1);
+      float ks, vs, next_ks, next_vs;
+      scales_of(s, page, ks, vs);
+      uint32_t i = 0;
+#pragma unroll 1
+      while (more) {
+        const bool next = line.next(p, ahead);
+        const int32_t next0 = next ? page_of(ahead, 0) : -1, next1 = next ? page_of(ahead, 1) : -1;
+        const int n = s.t1 - s.t0;
+#pragma unroll 1
+        for (int r = 0; r * per_round < n; ++r) {
+          const int32_t page2 = page_of(s, r + 2);
           float ks1, vs1;
-          scales_of(page1, ks1, vs1);
-          if (q_due && ik == kAhead) {
-            grid_wait();
-            waited = true;
-            load_q();
-            q_due = false;
+          scales_of(s, page1, ks1, vs1);
+          const int end = min(n - r * per_round, per_round);
+#pragma unroll 1
+          for (int j = 0; j < end; ++j, ++i) {
+            const int at = lane - j * per_tile, st = i % kStages;
+            wait(&empty[st], (i / kStages & 1) ^ 1, &x.stop);
+            __syncwarp();
+            if (!stopped(&x.stop)) {
+              if (lane == 0) mbar_arrive_expect_tx(&full[st], kStageBytes);
+              __syncwarp();
+              // a page outside the tensor reads as zeros
+              if (at >= 0 && at < per_tile)
+                tma_load_4d(ring + st * kStageBytes + at * page_bytes, map, 0, 0, s.kvh, page >= 0 ? page : (int32_t)p.c.num_pages, &full[st]);
+            }
+            if (is_k) {
+              // the place of tile i - kMeta: its groups have freed S of a later tile since
+              if (at >= 0 && at < per_tile) {
+                x.ks[i % kMeta][at] = ks;
+                x.vs[i % kMeta][at] = vs;
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&x.meta_full[i % kMeta]);
+            }
           }
-          load(ik, sm, &k_map, page, s.kvh, x.k_full, x.k_empty);
-          // the slot of tile ik - kMeta: its group has freed S of a later tile since
-          if (lane < pages) {
-            x.ks[ik % kMeta][lane] = ks;
-            x.vs[ik % kMeta][lane] = vs;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&x.meta_full[ik % kMeta]);
-          if (ik - iv == kAhead) load_v();
-          page_a = page_b, head_a = head_b;
-          page_b = page, head_b = s.kvh;
-          ++ik;
+          if (r == 0) scales_of(ahead, next0, next_ks, next_vs);
           page = page1;
           page1 = page2;
           ks = ks1;
           vs = vs1;
         }
-        if (q_due) {
-          grid_wait();
-          waited = true;
-          load_q();
-        }
+        s = ahead;
+        more = next;
+        page = next0;
+        page1 = next1;
+        ks = next_ks;
+        vs = next_vs;
       }
-      while (iv < ik) load_v();
-    } else if (warp == 9 && lane == 0) {
-      // ---- the first products, S of tile after tile. Tiles are counted through the CTA's
-      // units; tile i belongs to group i % 2.
+    } else if (warp == kFirst + 2) {
+      // ---- Q of a unit, by the warp, and the first products, by a lane. Tiles are counted
+      // through the CTA's units; tile i has turn i % turns.
       const uint32_t k_lo = desc_lo(smem_u32(sm), 16), q_lo = desc_lo(smem_u32(s_q), 16), hi = desc_hi(8 * kD, kSwizzle128);
       uint32_t i = 0, u = 0;
+#pragma unroll 1
       while (line.next(p, s)) {
-        const int n = s.t1 - s.t0, qb = u % L::q_buffers;
-        wait(&x.q_full[qb], u / L::q_buffers & 1, &x.stop);
-        for (int j = 0; j < n; ++j, ++i) {
-          const int w = i & 1, st = i % kStages;
-          wait(&x.k_full[st], i / kStages & 1, &x.stop);
-          if (i >= 2) wait(&x.s_free[w], (i / 2 - 1) & 1, &x.stop);
-          if (stopped(&x.stop)) continue;
-          tc_fence_after();
-          const uint32_t d = tmem + w * L::group_cols, a = k_lo + st * (kStageBytes / 16), b = q_lo + qb * (L::q_bytes / 16);
+        wait(&x.q_empty, (u & 1) ^ 1, &x.stop);
+        __syncwarp();
+        const float scale = split_q<ROWS, QP, T>(p, s, s_q);
+        if (lane == 0) x.q_scale = scale;
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x.q_full);
+        const int n = s.t1 - s.t0;
+        if (lane == 0) {
+#pragma unroll 1
+          for (int j = 0; j < n; ++j, ++i) {
+            const int w = i % L::turns, st = i % kStages;
+            wait(&x.k_full[st], i / kStages & 1, &x.stop);
+            if (i >= L::turns) wait(&x.s_free[w], (i / L::turns - 1) & 1, &x.stop);
+            if (stopped(&x.stop)) continue;
+            tc_fence_after();
+            const uint32_t d = tmem + w * ROWS, a = k_lo + st * (kStageBytes / 16);
 #pragma unroll
-          for (int part = 0; part < QP; ++part)
+            for (int part = 0; part < QP; ++part)
 #pragma unroll
-            for (int k = 0; k < kD / 32; ++k)
-              mma_f8(d, a + k * 2, hi, b + part * (ROWS * kD / 16) + k * 2, hi, f8_idesc(kTile, ROWS, false, false), part > 0 || k > 0);
-          mma_commit(&x.s_full[w]);
-          mma_commit(&x.k_empty[st]);
-          if (j == n - 1) mma_commit(&x.q_empty[qb]);
+              for (int k = 0; k < kD / 32; ++k)
+                mma_f8(d, a + k * 2, hi, q_lo + part * (ROWS * kD / 16) + k * 2, hi, f8_idesc(kTile, ROWS, false, false), part > 0 || k > 0);
+            mma_commit(&x.s_full[w]);
+            mma_commit(&x.k_empty[st]);
+          }
+          mma_commit(&x.q_empty);
         }
+        __syncwarp();
         ++u;
       }
-    } else if (warp == 10 && lane == 0) {
-      // ---- the second products, O
+    } else {
+      // ---- what the rows of a tree see, by the warp, and the second products, by a lane
       const uint32_t v_lo = desc_lo(smem_u32(sm) + L::off_v, 16), v_hi = desc_hi(8 * kD, kSwizzle128);
       const uint32_t p_lo = desc_lo(smem_u32(s_p), L::p_part), p_hi = desc_hi(8 * ROWS, ROWS == 64 ? kSwizzle64 : kSwizzle32);
       uint32_t i = 0, u = 0;
+#pragma unroll 1
       while (line.next(p, s)) {
         const int n = s.t1 - s.t0;
-        for (int j = 0; j < n; ++j, ++i) {
-          const int w = i & 1, st = i % kStages;
-          wait(&x.v_full[st], i / kStages & 1, &x.stop);
-          if (j == 0 && u > 0) wait(&x.o_free, (u - 1) & 1, &x.stop);
-          wait(&x.p_full[w], i / 2 & 1, &x.stop);
-          if (stopped(&x.stop)) continue;
-          tc_fence_after();
-          const uint32_t d = tmem + w * L::group_cols + ROWS, a = v_lo + st * (kStageBytes / 16), b = p_lo + w * (kParts * L::p_part / 16);
-#pragma unroll
-          for (int k = 0; k < kTile / 32; ++k)
-            mma_f8(d, a + k * (32 * kD / 16), v_hi, b + k * (32 * ROWS / 16), p_hi, f8_idesc(kD, kParts * ROWS, true, true), j >= 2 || k > 0);
-          mma_commit(&x.o_done[w]);
-          mma_commit(&x.v_empty[st]);
+        if (u > 0) wait(&x.o_free, (u - 1) & 1, &x.stop);  // the unit before is written
+        __syncwarp();
+        if (p.a.k_new && s.t0 == 0) {
+          // the window's rows on their way to L1: 256 bytes each of K and V
+#pragma unroll 1
+          for (int k = lane; k < s.r.rows * 4; k += 32) {
+            const int64_t row = s.r.row0 + (k >> 2);
+            const char* at = k & 2 ? static_cast<const char*>(p.a.v_new) + row * p.a.v_row_stride + s.kvh * p.a.v_head_stride
+                                   : static_cast<const char*>(p.a.k_new) + row * p.a.k_row_stride + s.kvh * p.a.k_head_stride;
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(at + (k & 1) * 128));
+          }
+          if (p.a.parents) {
+#pragma unroll 1
+            for (int k = lane; k < s.r.rows; k += 32) x.parents[k] = p.a.parents[s.r.row0 + k];
+            __syncwarp();
+#pragma unroll 1
+            for (int k = lane; k < s.r.rows; k += 32) x.trees[k] = tree_sees(x.parents, k);
+          }
         }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&x.trees_full);
+#pragma unroll 1
+          for (int j = 0; j < n; ++j, ++i) {
+            const int w = i % L::turns, st = i % kStages;
+            wait(&x.v_full[st], i / kStages & 1, &x.stop);
+            wait(&x.p_full[w], i / L::turns & 1, &x.stop);
+            if (stopped(&x.stop)) continue;
+            tc_fence_after();
+            const uint32_t d = tmem + L::col_o + w * L::o_cols, a = v_lo + st * (kStageBytes / 16), b = p_lo + w * (kParts * L::p_part / 16);
+#pragma unroll
+            for (int k = 0; k < kTile / 32; ++k)
+              mma_f8(d, a + k * (32 * kD / 16), v_hi, b + k * (32 * ROWS / 16), p_hi, f8_idesc(kD, kParts * ROWS, true, true), j >= L::turns || k > 0);
+            mma_commit(&x.o_done[w]);
+            mma_commit(&x.v_empty[st]);
+          }
+        }
+        __syncwarp();
         ++u;
       }
     }
     __syncwarp();
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    // ---- softmax: group w takes tiles t0 + w, t0 + w + 2, ...; a thread is a token
-    const int w = warp >> 2, token = tid & (kGroupThreads - 1);
-    const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21) + w * L::group_cols;  // this warp's lanes
-    unsigned char* my_p = s_p + w * kParts * L::p_part + token * ROWS;
-    const int turn = ROWS == 64 ? token >> 1 & 3 : token >> 2 & 1;  // the swizzle of its row
+    // ---- softmax: a thread is a token. A group's turn, and its first row.
+    const int group = warp >> 2, token = tid & (kGroupThreads - 1);
+    const int turn = L::split ? group >> 1 : group, col0 = L::split ? (group & 1) * kCols : 0;
+    const uint32_t quarter = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's lanes
+    const uint32_t my_s = quarter + turn * ROWS + col0, my_o = quarter + L::col_o + turn * L::o_cols + col0;
+    const int flip = ROWS == 64 ? token >> 1 & 3 : token >> 2 & 1;  // the swizzle of a token's row of P
+    unsigned char* my_p = s_p + turn * kParts * L::p_part + token * ROWS;
     uint32_t i0 = 0, u = 0;  // tiles and units of the CTA before this one
-    float l[ROWS];
-    bool waited = false;
+    f32x2 l[kCols / 2];
+#pragma unroll 1
     while (line.next(p, s)) {
-      const int n = s.t1 - s.t0, j0 = (w ^ i0) & 1;
-      const int last = n - 1 - ((n - 1 - j0) & 1);  // this group's last tile (< j0: none)
-      wait(&x.q_full[u % L::q_buffers], u / L::q_buffers & 1, &x.stop);
-      const float q_scale = x.q_scale[u % L::q_buffers][0] * p.scale_log2;
+      const int n = s.t1 - s.t0;
+      const int rows = min(kCols, s.rows - col0);  // of this group (< 1: none)
+      const int j0 = (turn - (int)(i0 % L::turns) + L::turns) % L::turns;  // its first tile
+      wait(&x.q_full, u & 1, &x.stop);
+      const float q_scale = x.q_scale * p.scale_log2;
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r) l[r] = 0.f;
-      if (token < ROWS) x.m[w][token] = 0.f;
-      if (token < ROWS) x.at[w][token] = (int32_t)s.at(p, ROWS, min(token, s.rows - 1));
+      for (int r = 0; r < kCols / 2; ++r) l[r] = 0;
+      if (token < kCols) x.neg_m[group][token] = 0.f;
+      if (tid < s.rows) x.at[tid] = (int32_t)s.at(p, ROWS, tid);
       bool fresh = true;  // no token of this unit seen yet: the references are not set
-      bar_sync(1 + w, kGroupThreads);
-      if (token == 0) mbar_arrive(&x.q_empty[u % L::q_buffers]);
-      for (int j = j0; j < n; j += 2) {
-        const uint32_t i = i0 + j, slot = i % kMeta;
+      bar_sync(1 + group, kGroupThreads);
+      if (token == 0) mbar_arrive(&x.q_empty);
+      int j = j0;
+#pragma unroll 1
+      for (; j < n; j += L::turns) {
+        const uint32_t i = i0 + j, slot = i % kMeta, phase = i / L::turns & 1;
         wait(&x.meta_full[slot], i / kMeta & 1, &x.stop);
         const float ks = x.ks[slot][token >> p.page_shift], vs = x.vs[slot][token >> p.page_shift];
         const bool valid = vs > 0.f && (s.t0 + j) * kTile + token < s.r.len;
         const float f = ks * q_scale, lv = __log2f(vs), inv_v = valid ? 1.f / vs : 0.f;
-        wait(&x.s_full[w], i / 2 & 1, &x.stop);
+        wait(&x.s_full[turn], phase, &x.stop);
         __syncwarp();
         tc_fence_after();
-        float t[ROWS];
+        // 16 rows a step (registers); rows behind the block's last are skipped. First whether a
+        // score is too far above its reference, then, from TMEM again, P.
+        const bool all_valid = __all_sync(0xffffffffu, valid);
+        const f32x2 f2 = pair(f, f), lv2 = pair(lv, lv);
+        // scores less references of rows c .. c + 15
+        auto scores = [&](int c, float* y) {
+          tmem_ld16(my_s + c, y);
+          tmem_wait_ld();
+          tmem_tie16(y);
 #pragma unroll
-        for (int r = 0; r < ROWS; r += 32) tmem_ld32(mine + r, t + r);
-        tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&x.s_free[w]);
+          for (int r = 0; r < 16; r += 4) {
+            const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(&x.neg_m[group][c + r]);
+            const float2 a = unpair(fma2(pair(y[r], y[r + 1]), f2, add2(lv2, m.x)));
+            const float2 b = unpair(fma2(pair(y[r + 2], y[r + 3]), f2, add2(lv2, m.y)));
+            y[r] = a.x, y[r + 1] = a.y, y[r + 2] = b.x, y[r + 3] = b.y;
+          }
+          if (!all_valid) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) y[r] = valid ? y[r] : -INFINITY;
+          }
+        };
         float top = -INFINITY;
+        if (!fresh) {
+#pragma unroll 1
+          for (int c = 0; c < rows; c += 16) {
+            float y[16];
+            scores(c, y);
 #pragma unroll
-        for (int r = 0; r < ROWS; r += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(&x.m[w][r]);
-          t[r] = fmaf(t[r], f, lv) - m.x;
-          t[r + 1] = fmaf(t[r + 1], f, lv) - m.y;
-          t[r + 2] = fmaf(t[r + 2], f, lv) - m.z;
-          t[r + 3] = fmaf(t[r + 3], f, lv) - m.w;
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, y[r]);
+          }
         }
-        if (!__all_sync(0xffffffffu, valid)) {
-#pragma unroll
-          for (int r = 0; r < ROWS; ++r) t[r] = valid ? t[r] : -INFINITY;
-        }
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) top = fmaxf(top, t[r]);
-        if (bar_or(1 + w, kGroupThreads, fresh || top > kSlack)) {
+        if (bar_or(1 + group, kGroupThreads, fresh || top > kSlack)) {
           // rows whose largest score is that far up get a new reference
-#pragma unroll
-          for (int h = 0; h < ROWS; h += 32) {
-            x.red[w][warp & 3][h + lane] = reduce_columns(t + h, lane, [](float a, float b) { return fmaxf(a, b); });
-            __syncwarp();  // one half after the other: fewer registers
+#pragma unroll 1
+          for (int c = 0; c < rows; c += 16) {
+            float y[16];
+            scores(c, y);
+            const float v = reduce_columns(y, lane, [](float a, float b) { return fmaxf(a, b); });
+            if (lane < 16) x.red[group][warp & 3][c + lane] = v;
           }
-          const bool any_valid = bar_or(1 + w, kGroupThreads, valid);
-          if (token < ROWS) {
-            float d = x.red[w][0][token];
+          const bool any_valid = bar_or(1 + group, kGroupThreads, valid);
+          if (token < kCols) {
+            float d = -INFINITY;
+            if (token < rows) {
 #pragma unroll
-            for (int k = 1; k < 4; ++k) d = fmaxf(d, x.red[w][k][token]);
+              for (int k = 0; k < 4; ++k) d = fmaxf(d, x.red[group][k][token]);
+            }
             d = (fresh ? d > -INFINITY : d > kSlack) ? d - kHead : 0.f;
-            x.delta[w][token] = d;
-            x.m[w][token] += d;
+            x.delta[group][token] = -d;
+            x.neg_m[group][token] -= d;
           }
-          bar_sync(1 + w, kGroupThreads);
-#pragma unroll
-          for (int r = 0; r < ROWS; r += 4) {
-            const float4 d = *reinterpret_cast<const float4*>(&x.delta[w][r]);
-            t[r] -= d.x, t[r + 1] -= d.y, t[r + 2] -= d.z, t[r + 3] -= d.w;
-            l[r] *= ex2(-d.x), l[r + 1] *= ex2(-d.y), l[r + 2] *= ex2(-d.z), l[r + 3] *= ex2(-d.w);
-            asm volatile("" ::: "memory");  // no loads ahead of their turn: registers
-          }
+          bar_sync(1 + group, kGroupThreads);
           if (!fresh) {
-            wait(&x.o_done[w], (i / 2 - 1) & 1, &x.stop);
+#pragma unroll
+            for (int r = 0; r < kCols / 2; r += 2) {
+              const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(&x.delta[group][2 * r]);
+              const float2 a = unpair(d.x), b = unpair(d.y);
+              l[r] = mul2(l[r], pair(ex2(a.x), ex2(a.y)));
+              l[r + 1] = mul2(l[r + 1], pair(ex2(b.x), ex2(b.y)));
+            }
+            wait(&x.o_done[turn], phase ^ 1, &x.stop);
             __syncwarp();
             tc_fence_after();
-            for (int c0 = 0; c0 < kParts * ROWS; c0 += 8) {
-              float o[8];
-              tmem_ld8(mine + ROWS + c0, o);
-              tmem_wait_ld();
+#pragma unroll 1
+            for (int c = 0; c < rows; c += 8) {
+              const float4 a = *reinterpret_cast<const float4*>(&x.delta[group][c]), b = *reinterpret_cast<const float4*>(&x.delta[group][c + 4]);
+              if (a.x == 0.f && a.y == 0.f && a.z == 0.f && a.w == 0.f && b.x == 0.f && b.y == 0.f && b.z == 0.f && b.w == 0.f)
+                continue;  // the same for every thread
+              const float by[8] = {ex2(a.x), ex2(a.y), ex2(a.z), ex2(a.w), ex2(b.x), ex2(b.y), ex2(b.z), ex2(b.w)};
+#pragma unroll 1
+              for (int part = 0; part < kParts; ++part) {
+                float o[8];
+                tmem_ld8(my_o + part * ROWS + c, o);
+                tmem_wait_ld();
+                tmem_tie8(o);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] *= ex2(-x.delta[w][(c0 + e) % ROWS]);
-              tmem_st8(mine + ROWS + c0, o);
+                for (int e = 0; e < 8; ++e) o[e] *= by[e];
+                tmem_st8(my_o + part * ROWS + c, o);
+              }
             }
             tmem_wait_st();
           }
           if (any_valid) fresh = false;
         }
-        // P's shared memory: the product of this group's tile before is done
-        if (j >= 2) wait(&x.o_done[w], (i / 2 - 1) & 1, &x.stop);
+        // P's place: the product that read it is done (one of an earlier unit was awaited there)
+        if (j >= L::turns) wait(&x.o_done[turn], phase ^ 1, &x.stop);
         __syncwarp();
+        const f32x2 inv2 = pair(inv_v, inv_v);
 #pragma unroll
-        for (int r = 0; r < ROWS; r += 16) {
+        for (int c = 0; c < kCols; c += 16) {
+          if (c >= apart(rows)) continue;
+          float y[16];
+          scores(c, y);
           uint32_t codes[kParts][4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            float e[4];
+            const int r = c / 2 + 2 * k;
+            const float e0 = ex2(y[4 * k]), e1 = ex2(y[4 * k + 1]), e2 = ex2(y[4 * k + 2]), e3 = ex2(y[4 * k + 3]);
+            l[r] = fma2(pair(e0, e1), inv2, l[r]);
+            l[r + 1] = fma2(pair(e2, e3), inv2, l[r + 1]);
+            __half2 u0 = __floats2half2_rn(e0, e1), u1 = __floats2half2_rn(e2, e3);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              e[q] = ex2(t[r + 4 * k + q]);
-              l[r + 4 * k + q] = fmaf(e[q], inv_v, l[r + 4 * k + q]);
-            }
-            __half2 a = __floats2half2_rn(e[0], e[1]), b = __floats2half2_rn(e[2], e[3]);
-#pragma unroll
-            for (int part = 0; part < kParts; ++part) {
-              const uint16_t ca = next_part(a), cb = next_part(b);
-              codes[part][k] = (uint32_t)ca | ((uint32_t)cb << 16);
-            }
+            for (int part = 0; part < kParts; ++part) codes[part][k] = next_part(u0, u1);
           }
 #pragma unroll
           for (int part = 0; part < kParts; ++part)
-            *reinterpret_cast<uint4*>(my_p + part * L::p_part + ((r / 16) ^ turn) * 16) =
+            *reinterpret_cast<uint4*>(my_p + part * L::p_part + (((col0 + c) / 16) ^ flip) * 16) =
                 make_uint4(codes[part][0], codes[part][1], codes[part][2], codes[part][3]);
         }
-        if (!valid) {  // whatever lies behind the last token: 0 times it must be 0
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x.s_free[turn]);
+        if (!valid && col0 == 0) {  // whatever lies behind the last token: 0 times it must be 0
           wait(&x.v_full[i % kStages], i / kStages & 1, &x.stop);
           uint4* v = reinterpret_cast<uint4*>(sm + L::off_v + (i % kStages) * kStageBytes + token * kD);
 #pragma unroll
@@ -483,93 +552,115 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_async_shared();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&x.p_full[w]);
+        if (lane == 0) mbar_arrive(&x.p_full[turn]);
       }
-      // ---- the end of the unit: sums over the tokens, then the groups meet. Group w finishes
-      // half of the rows; a thread is a dim there.
-      const bool whole = s.whole();
-      if (!waited) {  // for the window's own part
-        grid_wait();
-        waited = true;
+      // ---- the end of the unit: sums over the tokens, then the turns meet
+#pragma unroll
+      for (int c = 0; c < kCols; c += 16) {
+        float y[16];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const float2 v = unpair(l[c / 2 + r]);
+          y[2 * r] = v.x;
+          y[2 * r + 1] = v.y;
+        }
+        const float v = reduce_columns(y, lane, [](float a, float b) { return a + b; });
+        if (lane < 16) x.red[group][warp & 3][c + lane] = v;
       }
-      constexpr int HALF = ROWS / 2;
-      const int d = token, c_lo = w * HALF;
-      const bool own_part = whole && p.own_ml != nullptr;
-#pragma unroll
-      for (int h = 0; h < ROWS; h += 32)
-        x.red[w][warp & 3][h + lane] = reduce_columns(l + h, lane, [](float a, float b) { return a + b; });
-      float own[HALF];
-#pragma unroll
-      for (int e = 0; e < HALF; ++e)
-        own[e] = own_part && c_lo + e < s.rows ? p.own_o[(int64_t)x.at[w][c_lo + e] * kD + d] : 0.f;
-      if (token == 0) x.live[w] = !fresh;
-      if (last >= j0) wait(&x.o_done[w], (i0 + last) / 2 & 1, &x.stop);
+      if (token == 0) x.live[group] = !fresh;
+      if (j > j0) wait(&x.o_done[turn], (i0 + j - L::turns) / L::turns & 1, &x.stop);  // its last product
+      wait(&x.trees_full, u & 1, &x.stop);
       __syncwarp();
-      bar_sync(3, 2 * kGroupThreads);
+      bar_sync(kBarAll, kSoftmaxThreads);
       tc_fence_after();
-      const int slot = 2 * (int)blockIdx.x + (s.t0 == 0 ? 1 : 0);
-      float* part = p.part + (int64_t)slot * slot_floats(ROWS, kD);
-      const bool live0 = x.live[0], live1 = x.live[1];
-      if (tid < ROWS) {
-        const int r = tid;
-        float sum[2];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) sum[g] = (x.red[g][0][r] + x.red[g][1][r]) + (x.red[g][2][r] + x.red[g][3][r]);
-        const float m0 = live0 ? x.m[0][r] : kNone, m1 = live1 ? x.m[1][r] : kNone;
-        const float to = fmaxf(m0, m1);
-        float w0 = live0 ? ex2(m0 - to) : 0.f, w1 = live1 ? ex2(m1 - to) : 0.f, wo = 0.f;
-        const float all = w0 * sum[0] + w1 * sum[1];
-        if (whole) {
-          if (r < s.rows) {
-            const float by = finish_row(p, x.at[w][r], to, all, wo);
-            w0 *= by;
-            w1 *= by;
+      // the window's own part, into P's place (every product is done with it): 16 rows a warp,
+      // and a share of the dims
+      const bool own = p.a.k_new != nullptr && s.t0 == 0;  // the first piece takes the window in
+      float* s_own = reinterpret_cast<float*>(s_p);
+      if (own) {
+        constexpr int kSlices = 16 / (ROWS / 16);  // of the dims
+        const int i16 = warp / kSlices * 16, j1 = (warp % kSlices + 1) * (kD / 8 / kSlices);
+        if (i16 < s.rows) {
+          const Sees* trees = p.a.parents ? x.trees : nullptr;
+          const bool odd = own_part<kD, ROWS, T>(p, s, i16, j1 - kD / 8 / kSlices, j1, trees, s_own, kOwnLd, x.own);
+          if (odd) {
+            // this warp's dims, from its own references (they are the same in every slice)
+            __syncwarp();
+#pragma unroll 1
+            for (int i = i16; i < min(s.rows, i16 + 16); ++i)
+              own_odd<kD, ROWS, T>(p, s, i, (j1 - kD / 8 / kSlices) * 8, j1 * 8, trees, x.own[i].x, s_own + i * kOwnLd);
           }
+        }
+        bar_sync(kBarAll, kSoftmaxThreads);
+      }
+      const bool whole = s.whole();
+      float* part = p.part + (2 * (int64_t)blockIdx.x + (s.t0 == 0 ? 1 : 0)) * slot_floats(ROWS, kD);
+      if (tid < s.rows) {
+        const int r = tid, c = r % kCols;
+        float m[L::turns], sum[L::turns];
+        const float2 ml = own ? x.own[r] : make_float2(kNone, 0.f);
+        float to = ml.x;
+#pragma unroll
+        for (int k = 0; k < L::turns; ++k) {
+          const int g = L::split ? 2 * k + r / kCols : k;
+          const bool live = x.live[g];
+          const float (&v)[4][kCols] = x.red[g];
+          sum[k] = live ? (v[0][c] + v[1][c]) + (v[2][c] + v[3][c]) : 0.f;
+          m[k] = live ? -x.neg_m[g][c] : kNone;
+          to = fmaxf(to, m[k]);
+        }
+        float by = ex2(ml.x - to), all = by * ml.y;
+        x.w[L::turns][r] = by;
+#pragma unroll
+        for (int k = 0; k < L::turns; ++k) {
+          m[k] = ex2(m[k] - to);
+          all = fmaf(m[k], sum[k], all);
+        }
+        by = 1.f;
+        if (whole) {
+          by = finish_row(p, x.at[r], to, all);
         } else {
           part[ROWS * kD + r] = to;
           part[ROWS * kD + ROWS + r] = all;
         }
-        x.w[r] = make_float4(w0, w1, wo, 0.f);
+        x.w[L::turns][r] *= by;
+#pragma unroll
+        for (int k = 0; k < L::turns; ++k) x.w[k][r] = m[k] * by;
       }
-      bar_sync(3, 2 * kGroupThreads);
-      const uint32_t quarter = tmem + ((uint32_t)(warp & 3) << 21);
+      bar_sync(kBarAll, kSoftmaxThreads);
+      // a group finishes 8 rows at a time; a thread is a dim
+      const int d = token;
+#pragma unroll 1
+      for (int c = group * 8; c < s.rows; c += 8 * kGroups) {
+        float o[8];
 #pragma unroll
-      for (int c0 = 0; c0 < HALF; c0 += 8) {
-        if (c_lo + c0 < s.rows) {
-          float o[8] = {};
+        for (int e = 0; e < 8; ++e) o[e] = own ? x.w[L::turns][c + e] * s_own[(c + e) * kOwnLd + d] : 0.f;
+#pragma unroll 1
+        for (int k = 0; k < L::turns; ++k) {
+          if (!x.live[L::split ? 2 * k : k]) continue;  // both groups of a turn see the same tokens
+          float y[kParts][8];
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            if (g ? !live1 : !live0) continue;
-            float y[kParts][8];
+          for (int part_ = 0; part_ < kParts; ++part_) tmem_ld8(quarter + L::col_o + k * L::o_cols + part_ * ROWS + c, y[part_]);
+          tmem_wait_ld();
 #pragma unroll
-            for (int part_ = 0; part_ < kParts; ++part_)
-              tmem_ld8(quarter + g * L::group_cols + (1 + part_) * ROWS + c_lo + c0, y[part_]);
-            tmem_wait_ld();
+          for (int part_ = 0; part_ < kParts; ++part_) tmem_tie8(y[part_]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 by = x.w[c_lo + c0 + e];
-              o[e] = fmaf(g ? by.y : by.x, fmaf(fmaf(y[2][e], 0x1p-5f, y[1][e]), 0x1p-5f, y[0][e]), o[e]);
-            }
-          }
+          for (int e = 0; e < 8; ++e) o[e] = fmaf(x.w[k][c + e], fmaf(fmaf(y[2][e], 0x1p-5f, y[1][e]), 0x1p-5f, y[0][e]), o[e]);
+        }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int r = c_lo + c0 + e;
-            if (r < s.rows) {
-              if (whole)
-                reinterpret_cast<T*>(p.a.out)[(int64_t)x.at[w][r] * kD + d] = T(fmaf(x.w[r].z, own[c0 + e], o[e]));
-              else
-                part[r * kD + d] = o[e];
-            }
-          }
+        for (int e = 0; e < 8; ++e) {
+          if (c + e >= s.rows) break;
+          if (whole) reinterpret_cast<T*>(p.a.out)[(int64_t)x.at[c + e] * kD + d] = T(o[e]);
+          else part[(c + e) * kD + d] = o[e];
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&x.o_free);
-      bar_sync(1 + w, kGroupThreads);  // the group's references and indexes have been read
+      bar_sync(kBarAll, kSoftmaxThreads);  // what the groups share has been read
       if (!whole) {
         if (s.t0 == 0) {
-          desc.x = (int)s.b;
+          desc.x = s.b;
           desc.y = s.kvh * s.r.blocks + s.block;
           desc.z = s.rows;
         } else {
@@ -581,16 +672,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (tid == 0) p.desc[blockIdx.x] = desc;
   }
-  if (stopped(&x.stop)) {  // copies in flight land before the CTA leaves its shared memory
+  if (stopped(&x.stop)) {
+    if (tid == 0) atomicOr(&g_window_error, 1u);
+    // copies in flight land before the CTA leaves its shared memory
     const long long t0 = clock64();
     while (clock64() - t0 < (1ll << 26)) {
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kFirst) {
     tc_fence_after();
-    tmem_free(tmem, kTmemCols);
+    tmem_free(tmem, L::tmem_cols);
   }
 }
 
@@ -627,18 +720,8 @@ cudaError_t launch(const WindowParams& p, const CUtensorMap& k, const CUtensorMa
   constexpr int bytes = smem_bytes<ROWS, QP>();
   cudaError_t e = cudaFuncSetAttribute(k_window_tc<ROWS, QP, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  if ((e = launch_prep<kD, ROWS, QP, T>(p, s)) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sms);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, k_window_tc<ROWS, QP, T>, p, k, v)) != cudaSuccess) return e;
+  k_window_tc<ROWS, QP, T><<<sms, kThreads, bytes, s>>>(p, k, v);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_after(k_join<kD, ROWS, kTile, T>, dim3(sms, ROWS / 4), 128, 0, s, p);
 }
 
@@ -653,7 +736,9 @@ cudaError_t window_read_error(uint32_t* word, int clear) {
   return e;
 }
 
-cudaError_t launch_window_tc(const WindowParams& p, int rows, int sms, cudaStream_t s, bool* done) {
+cudaError_t launch_window_tc(const WindowParams& params, int rows, int sms, cudaStream_t s, bool* done) {
+  WindowParams p = params;
+  p.own_ml = nullptr;  // the window's own part is in the pieces
   CUtensorMap k, v;
   const ts_kv_cache& c = p.c;
   *done = encoder() != nullptr && c.num_pages > 0 && c.num_pages < INT32_MAX &&
