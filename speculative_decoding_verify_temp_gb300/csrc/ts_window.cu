@@ -419,7 +419,8 @@ size_t lay_out(WindowParams& p, void* ws, int sms) {
   p.desc = reinterpret_cast<int4*>(take(ctas * sizeof(int4)));
   p.part = reinterpret_cast<float*>(take(2 * ctas * slot_floats(rows, D) * sizeof(float)));
   const size_t n = (size_t)p.a.total_rows * p.a.heads_q;
-  p.own_o = reinterpret_cast<float*>(take(n * D * sizeof(float)));
+  // the window's own part: of every row, or (ts_window_tc.cu) of a block a CTA
+  p.own_o = reinterpret_cast<float*>(take(std::max(n, (size_t)sms * rows) * D * sizeof(float)));
   p.own_ml = reinterpret_cast<float2*>(take(n * sizeof(float2)));
   return off;
 }

@@ -257,22 +257,32 @@ __global__ void __launch_bounds__(128) k_join(const __grid_constant__ WindowPara
   const int row = blockIdx.y * 4 + (threadIdx.x >> 5);
   const int4 d = p.desc[first];
   if (d.x < 0 || row >= d.z) return;
-  int pieces = 1;
-  while (first + pieces < (int)gridDim.x && p.desc[first + pieces].w == 0) ++pieces;
-  ++pieces;
+  int pieces = 1;  // the CTAs after this one up to the first that ends the unit, 32 a look
+  for (;; pieces += 32) {
+    const int i = first + pieces + lane;
+    const unsigned ends = __ballot_sync(0xffffffffu, i >= (int)gridDim.x || p.desc[i].w != 0);
+    if (ends) {
+      pieces += __ffs(ends);
+      break;
+    }
+  }
   auto piece = [&](int i) { return p.part + (int64_t)(i ? 2 * (first + i) : 2 * first + 1) * slot_floats(ROWS, D); };
   float top = kNone;
   for (int i = lane; i < pieces; i += 32) top = fmaxf(top, piece(i)[ROWS * D + row]);
   top = warp_max(top);
   constexpr int PER = D / 32;
   float acc[PER] = {}, sum = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = 0; i < pieces; ++i) {
     const float* x = piece(i);
     const float by = ex2(x[ROWS * D + row] - top);
     sum = fmaf(by, x[ROWS * D + ROWS + row], sum);
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] = fmaf(by, x[row * D + lane * PER + e], acc[e]);
+    for (int e = 0; e < PER; e += 2) {
+      const float2 v = *reinterpret_cast<const float2*>(x + row * D + lane * PER + e);
+      acc[e] = fmaf(by, v.x, acc[e]);
+      acc[e + 1] = fmaf(by, v.y, acc[e + 1]);
+    }
   }
   Segment s;
   s.r = request<ROWS, TILE>(p, raw_request(p, d.x));

@@ -70,21 +70,22 @@ __device__ __forceinline__ bool own_part(const WindowParams& p, const Segment& s
     const char* vn = static_cast<const char*>(p.a.v_new) + (s.r.row0 + tok) * p.a.v_row_stride + s.kvh * p.a.v_head_stride;
     float x[2][4] = {};
 #pragma unroll 2
-    for (int ks = 0; ks < D / 16; ++ks) {
-      // lane c's four dims of step ks: any order serves, as Q's and K's agree
-      const int dim = ks * 16 + c * 4;
-      uint32_t qa[4];
+    for (int ks = 0; ks < D / 32; ++ks) {
+      // lane c's eight dims, two steps of four: any order serves, as Q's and K's agree
+      const int dim = ks * 32 + c * 8;
+      uint4 qw[2], kw[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint2 w = q[h] ? __ldg(reinterpret_cast<const uint2*>(q[h] + dim * 2)) : make_uint2(0, 0);
-        qa[h] = w.x;
-        qa[2 + h] = w.y;
-      }
+      for (int h = 0; h < 2; ++h) qw[h] = q[h] ? __ldg(reinterpret_cast<const uint4*>(q[h] + dim * 2)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
-        uint2 kb = make_uint2(0, 0);
-        if (tok + n * 8 + g < s.r.rows) kb = __ldg(reinterpret_cast<const uint2*>(kn + (n * 8 + g) * p.a.k_row_stride + dim * 2));
-        mma16816<T>(x[n], qa, kb.x, kb.y);
+        kw[n] = make_uint4(0, 0, 0, 0);
+        if (tok + n * 8 + g < s.r.rows) kw[n] = __ldg(reinterpret_cast<const uint4*>(kn + (n * 8 + g) * p.a.k_row_stride + dim * 2));
+      }
+      const uint32_t q0[4] = {qw[0].x, qw[1].x, qw[0].y, qw[1].y}, q1[4] = {qw[0].z, qw[1].z, qw[0].w, qw[1].w};
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        mma16816<T>(x[n], q0, kw[n].x, kw[n].y);
+        mma16816<T>(x[n], q1, kw[n].z, kw[n].w);
       }
     }
     float by[2];
@@ -115,7 +116,7 @@ __device__ __forceinline__ bool own_part(const WindowParams& p, const Segment& s
         pb[n * 2 + h] = pack<T>(a - f.x, b - f.y);
       }
     }
-#pragma unroll 1
+#pragma unroll 2
     for (int j = j0; j < j1; ++j) {
       // V: dim 8j + g of tokens 2c, 2c + 1, 2c + 8, 2c + 9
       uint32_t v[2];

@@ -23,8 +23,8 @@
 // and short bursts, so four groups of four warps work on different parts of the line: with
 // blocks of 32 rows each group takes every fourth tile, with blocks of 64 two groups share a
 // tile (32 rows each) and two pairs take turns. Tiles of one turn have their own S, P and O; the
-// turns meet at the end of a unit, where the window's own tokens come in (ts_window_own.cuh) and
-// the result is written. One warp each loads K (with the blocks' scales) and V, rings of four
+// turns meet at the end of a unit and the result is written. The window's own tokens
+// (ts_window_own.cuh) are worked on at a unit's beginning, while Q is split. One warp each loads K (with the blocks' scales) and V, rings of four
 // tiles or 64 KB; a lane each of two warps issues the first and the second products. The first
 // of them also splits Q, the second looks up what the rows of a tree see.
 //
@@ -55,7 +55,6 @@ constexpr int kThreads = kSoftmaxThreads + 128;
 constexpr int kCols = 32;          // rows of a block that a softmax thread has scores of
 constexpr int kMinTiles = 2;       // least tiles a CTA takes: pieces of 256 tokens or more
 constexpr float kHead = 4.f;       // a reference is set this far below the largest score
-constexpr int kOwnLd = kD + 4;     // floats between rows of the window's own part
 constexpr int kBarAll = kGroups + 1;  // named barrier of all softmax threads; 1 .. kGroups: a group's
 
 __device__ uint32_t g_window_error;
@@ -74,7 +73,6 @@ struct Layout {
   static constexpr int col_o = turns * ROWS, o_cols = kParts * ROWS;
   static constexpr int tmem_cols = 512;
   static_assert(col_o + turns * o_cols <= tmem_cols, "TMEM");
-  static_assert(ROWS * kOwnLd * 4 <= turns * kParts * p_part, "the own part lies in P's place");
 };
 
 template <int ROWS>
@@ -411,6 +409,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = s.t1 - s.t0;
       const int rows = min(kCols, s.rows - col0);  // of this group (< 1: none)
       const int j0 = (turn - (int)(i0 % L::turns) + L::turns) % L::turns;  // its first tile
+      // the window's own part, while Q is split and the first scores are formed: 16 rows a warp,
+      // and a share of the dims
+      const bool own = p.a.k_new != nullptr && s.t0 == 0;  // the first piece takes the window in
+      float* own_o = p.own_o + (int64_t)blockIdx.x * ROWS * kD;
+      if (own) {
+        constexpr int kSlices = 16 / (ROWS / 16);  // of the dims
+        const int i16 = warp / kSlices * 16, j1 = (warp % kSlices + 1) * (kD / 8 / kSlices), jn = kD / 8 / kSlices;
+        if (p.a.parents) wait(&x.trees_full, u & 1, &x.stop);
+        __syncwarp();
+        if (i16 < s.rows) {
+          const Sees* trees = p.a.parents ? x.trees : nullptr;
+          const bool odd = own_part<kD, ROWS, T>(p, s, i16, j1 - jn, j1, trees, own_o, kD, x.own);
+          if (odd) {
+            // this warp's dims, from its own references (they are the same in every slice)
+            __syncwarp();
+#pragma unroll 1
+            for (int i = i16; i < min(s.rows, i16 + 16); ++i)
+              own_odd<kD, ROWS, T>(p, s, i, (j1 - jn) * 8, j1 * 8, trees, x.own[i].x, own_o + i * kD);
+          }
+        }
+      }
       wait(&x.q_full, u & 1, &x.stop);
       const float q_scale = x.q_scale * p.scale_log2;
 #pragma unroll
@@ -569,30 +588,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (token == 0) x.live[group] = !fresh;
       if (j > j0) wait(&x.o_done[turn], (i0 + j - L::turns) / L::turns & 1, &x.stop);  // its last product
-      wait(&x.trees_full, u & 1, &x.stop);
+      if (!own || !p.a.parents) wait(&x.trees_full, u & 1, &x.stop);  // every phase has to be seen
       __syncwarp();
       bar_sync(kBarAll, kSoftmaxThreads);
       tc_fence_after();
-      // the window's own part, into P's place (every product is done with it): 16 rows a warp,
-      // and a share of the dims
-      const bool own = p.a.k_new != nullptr && s.t0 == 0;  // the first piece takes the window in
-      float* s_own = reinterpret_cast<float*>(s_p);
-      if (own) {
-        constexpr int kSlices = 16 / (ROWS / 16);  // of the dims
-        const int i16 = warp / kSlices * 16, j1 = (warp % kSlices + 1) * (kD / 8 / kSlices);
-        if (i16 < s.rows) {
-          const Sees* trees = p.a.parents ? x.trees : nullptr;
-          const bool odd = own_part<kD, ROWS, T>(p, s, i16, j1 - kD / 8 / kSlices, j1, trees, s_own, kOwnLd, x.own);
-          if (odd) {
-            // this warp's dims, from its own references (they are the same in every slice)
-            __syncwarp();
-#pragma unroll 1
-            for (int i = i16; i < min(s.rows, i16 + 16); ++i)
-              own_odd<kD, ROWS, T>(p, s, i, (j1 - kD / 8 / kSlices) * 8, j1 * 8, trees, x.own[i].x, s_own + i * kOwnLd);
-          }
-        }
-        bar_sync(kBarAll, kSoftmaxThreads);
-      }
       const bool whole = s.whole();
       float* part = p.part + (2 * (int64_t)blockIdx.x + (s.t0 == 0 ? 1 : 0)) * slot_floats(ROWS, kD);
       if (tid < s.rows) {
@@ -634,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = group * 8; c < s.rows; c += 8 * kGroups) {
         float o[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = own ? x.w[L::turns][c + e] * s_own[(c + e) * kOwnLd + d] : 0.f;
+        for (int e = 0; e < 8; ++e) o[e] = own && c + e < s.rows ? x.w[L::turns][c + e] * own_o[(c + e) * kD + d] : 0.f;
 #pragma unroll 1
         for (int k = 0; k < L::turns; ++k) {
           if (!x.live[L::split ? 2 * k : k]) continue;  // both groups of a turn see the same tokens
@@ -738,7 +737,7 @@ cudaError_t window_read_error(uint32_t* word, int clear) {
 
 cudaError_t launch_window_tc(const WindowParams& params, int rows, int sms, cudaStream_t s, bool* done) {
   WindowParams p = params;
-  p.own_ml = nullptr;  // the window's own part is in the pieces
+  p.own_ml = nullptr;  // the window's own part is in the pieces; own_o: a block a CTA
   CUtensorMap k, v;
   const ts_kv_cache& c = p.c;
   *done = encoder() != nullptr && c.num_pages > 0 && c.num_pages < INT32_MAX &&
