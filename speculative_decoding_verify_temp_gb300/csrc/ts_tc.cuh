@@ -20,10 +20,10 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t leading) {
   return ((addr >> 4) & 0x3FFF) | (((leading >> 4) & 0x3FFF) << 16);
 }
 
-// Instruction descriptor of kind::f8f6f4: e4m3 operands, fp32 accumulators. a_mn, b_mn: the
-// operand's rows (A) or columns (B) lie along contiguous memory instead of k.
-__host__ __device__ constexpr uint32_t f8_idesc(int m, int n, bool a_mn, bool b_mn) {
-  return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+// Instruction descriptor of kind::f8f6f4: e4m3 operands (B: e5m2 if b_e5m2), fp32 accumulators.
+// a_mn, b_mn: the operand's rows (A) or columns (B) lie along contiguous memory instead of k.
+__host__ __device__ constexpr uint32_t f8_idesc(int m, int n, bool a_mn, bool b_mn, bool b_e5m2 = false) {
+  return (1u << 4) | (b_e5m2 ? 1u << 10 : 0u) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(m >> 4) << 24);
 }
 

@@ -10,13 +10,18 @@
 // is the M = 128 of the instruction and the window's rows, few as they are, its N:
 //
 //   S^T [128 tokens x ROWS] = K [128 x D] (Q_hi + Q_lo (+ Q_lo2))^T      one accumulator
-//   O^T [D x 3 ROWS]       += V^T [D x 128 tokens] [P_hi | P_lo | P_lo2]  one accumulator a part
+//   O^T [D x 2, 3 ROWS]    += V^T [D x 128 tokens] [P_hi | P_lo (| P_lo2)] one accumulator a part
 //
 // P = 2^(x - m) with a reference m a row (x in log2 units, V's scale in the exponent as in
 // ts_window.cu); a reference follows only when a score exceeds it by 2^8 (one vote a tile), and
 // then O is scaled in TMEM. Parts of P: the fp16 rounding of p in three codes, the second and
 // third scaled by 2^5 and 2^10, so that all 11 bits are kept down to 2^-9, and values down to
-// 2^-20, where the row's largest p is between 2^4 and 2^8.
+// 2^-20, where the row's largest p is between 2^4 and 2^8. bf16 calls with blocks of 64 rows take
+// two parts (their output has 8 bits): e4m3, and e5m2 for the rest times 2^12: 7 bits and half a
+// step, down to 2^-24. The columns of TMEM that this leaves are second buffers of S, so that the
+// first products run a whole round of turns ahead: 330 us against 392 for 16 trees of 32 nodes
+// over 8191 tokens. Blocks of 32 rows have four turns, and the three parts of one type go
+// through one instruction (222 clocks a tile against 384 for two types).
 //
 // A softmax thread is a token: it reads its row of S^T from TMEM, the scales of its block and
 // its validity are its own, and it writes its row of P. Its work on a tile is a chain of waits
@@ -46,8 +51,7 @@ constexpr int kTile = 128;
 constexpr int kD = 128;
 constexpr int kStages = 4;         // tiles of K, and as many of V, in shared memory
 constexpr int kStageBytes = kTile * kD;
-constexpr int kMeta = 8;           // tiles whose scales are in shared memory
-constexpr int kParts = 3;          // of a probability
+constexpr int kMeta = 16;          // tiles whose scales are in shared memory
 constexpr int kGroups = 4;         // of softmax threads
 constexpr int kGroupThreads = 128;
 constexpr int kSoftmaxThreads = kGroups * kGroupThreads;
@@ -62,6 +66,7 @@ __device__ uint32_t g_window_error;
 template <int ROWS, int QP>
 struct Layout {
   static constexpr int q_bytes = QP * ROWS * kD;
+  static constexpr int kParts = ROWS == 64 && QP == 2 ? 2 : 3;  // of a probability
   static constexpr int p_part = ROWS * kTile;
   static constexpr bool split = ROWS == 2 * kCols;        // two groups share a tile's rows
   static constexpr int turns = split ? kGroups / 2 : kGroups;  // tiles in work at a time
@@ -69,16 +74,21 @@ struct Layout {
   static constexpr int off_q = 2 * kStages * kStageBytes;
   static constexpr int off_p = off_q + q_bytes;
   static constexpr int off_x = off_p + turns * kParts * p_part;
-  // TMEM columns: the turns' S, then their O, a part after the other
-  static constexpr int col_o = turns * ROWS, o_cols = kParts * ROWS;
+  // TMEM columns: the buffers of S, then the turns' O, a part after the other
+  static constexpr int s_bufs = kParts == 2 ? 2 * turns : turns;
+  static constexpr int col_o = s_bufs * ROWS, o_cols = kParts * ROWS;
   static constexpr int tmem_cols = 512;
+  // a tile's scales are overwritten kMeta tiles later, when the first product of the tile kStages
+  // before that one is done, and with it the groups' reading of the scores s_bufs before that
+  static_assert(kMeta >= s_bufs + kStages, "scales");
   static_assert(col_o + turns * o_cols <= tmem_cols, "TMEM");
 };
 
 template <int ROWS>
 struct Shared {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], meta_full[kMeta];
-  uint64_t s_full[kGroups], s_free[kGroups], p_full[kGroups], o_done[kGroups];  // a turn's
+  uint64_t s_full[2 * kGroups], s_free[2 * kGroups];  // a buffer's
+  uint64_t p_full[kGroups], o_done[kGroups];          // a turn's
   uint64_t q_full, q_empty, o_free, trees_full;
   float q_scale;                            // what Q's codes stand for
   float ks[kMeta][8], vs[kMeta][8];         // scales of a tile's pages (vs 0: no such page)
@@ -162,17 +172,26 @@ __device__ __forceinline__ float reduce_columns(float* x, int lane, F f) {
   return f(x[0], __shfl_xor_sync(0xffffffffu, x[0], 16));
 }
 
-// The next part of four values: its codes; the values become the rest, times 2^5 (exact).
-__device__ __forceinline__ uint32_t next_part(__half2& a, __half2& b) {
-  uint32_t codes, back_a, back_b;
-  asm("{\n .reg .b16 u, v;\n cvt.rn.satfinite.e4m3x2.f16x2 u, %3;\n cvt.rn.satfinite.e4m3x2.f16x2 v, %4;\n"
-      " mov.b32 %0, {u, v};\n cvt.rn.f16x2.e4m3x2 %1, u;\n cvt.rn.f16x2.e4m3x2 %2, v;\n}\n"
-      : "=r"(codes), "=r"(back_a), "=r"(back_b)
-      : "r"(*reinterpret_cast<const uint32_t*>(&a)), "r"(*reinterpret_cast<const uint32_t*>(&b)));
-  const __half2 by = __float2half2_rn(32.f);
-  a = __hmul2(__hsub2(a, *reinterpret_cast<const __half2*>(&back_a)), by);
-  b = __hmul2(__hsub2(b, *reinterpret_cast<const __half2*>(&back_b)), by);
-  return codes;
+// Four probabilities (two fp16 pairs) in parts: codes[0 .. N-1].
+template <int N>
+__device__ __forceinline__ void split_p(__half2 a, __half2 b, uint32_t* codes) {
+#pragma unroll
+  for (int part = 0; part < N; ++part) {
+    if (N == 2 && part == 1) {
+      asm("{\n .reg .b16 u, v;\n cvt.rn.satfinite.e5m2x2.f16x2 u, %1;\n cvt.rn.satfinite.e5m2x2.f16x2 v, %2;\n mov.b32 %0, {u, v};\n}\n"
+          : "=r"(codes[part])
+          : "r"(*reinterpret_cast<const uint32_t*>(&a)), "r"(*reinterpret_cast<const uint32_t*>(&b)));
+      return;
+    }
+    uint32_t back_a, back_b;
+    asm("{\n .reg .b16 u, v;\n cvt.rn.satfinite.e4m3x2.f16x2 u, %3;\n cvt.rn.satfinite.e4m3x2.f16x2 v, %4;\n"
+        " mov.b32 %0, {u, v};\n cvt.rn.f16x2.e4m3x2 %1, u;\n cvt.rn.f16x2.e4m3x2 %2, v;\n}\n"
+        : "=r"(codes[part]), "=r"(back_a), "=r"(back_b)
+        : "r"(*reinterpret_cast<const uint32_t*>(&a)), "r"(*reinterpret_cast<const uint32_t*>(&b)));
+    const __half2 by = __float2half2_rn(N == 2 ? 4096.f : 32.f);
+    a = __hmul2(__hsub2(a, *reinterpret_cast<const __half2*>(&back_a)), by);
+    b = __hmul2(__hsub2(b, *reinterpret_cast<const __half2*>(&back_b)), by);
+  }
 }
 
 // A value that the compiler knows nothing about: branches on it are not merged into copies of
@@ -193,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* s_p = sm + L::off_p;
   Shared<ROWS>& x = *reinterpret_cast<Shared<ROWS>*>(sm + L::off_x);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kFirst = kSoftmaxThreads / 32;  // the warps behind the softmax groups
+  constexpr int kParts = L::kParts, kFirst = kSoftmaxThreads / 32;  // the warps behind the softmax groups
   int4 desc = make_int4(-1, 0, 0, 0);
   grid_launch();
   Line<ROWS, kTile> line;
@@ -210,9 +229,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&x.v_empty[i], 1);
     }
     for (int i = 0; i < kMeta; ++i) mbar_init(&x.meta_full[i], 1);
-    for (int i = 0; i < L::turns; ++i) {
+    for (int i = 0; i < L::s_bufs; ++i) {
       mbar_init(&x.s_full[i], 1);
       mbar_init(&x.s_free[i], L::split ? 8 : 4);
+    }
+    for (int i = 0; i < L::turns; ++i) {
       mbar_init(&x.p_full[i], L::split ? 8 : 4);
       mbar_init(&x.o_done[i], 1);
     }
@@ -285,7 +306,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_4d(ring + st * kStageBytes + at * page_bytes, map, 0, 0, s.kvh, page >= 0 ? page : (int32_t)p.c.num_pages, &full[st]);
             }
             if (is_k) {
-              // the place of tile i - kMeta: its groups have freed S of a later tile since
               if (at >= 0 && at < per_tile) {
                 x.ks[i % kMeta][at] = ks;
                 x.vs[i % kMeta][at] = vs;
@@ -309,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kFirst + 2) {
       // ---- Q of a unit, by the warp, and the first products, by a lane. Tiles are counted
-      // through the CTA's units; tile i has turn i % turns.
+      // through the CTA's units; tile i has turn i % turns and buffer i % s_bufs.
       const uint32_t k_lo = desc_lo(smem_u32(sm), 16), q_lo = desc_lo(smem_u32(s_q), 16), hi = desc_hi(8 * kD, kSwizzle128);
       uint32_t i = 0, u = 0;
 #pragma unroll 1
@@ -325,9 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
 #pragma unroll 1
           for (int j = 0; j < n; ++j, ++i) {
-            const int w = i % L::turns, st = i % kStages;
+            const int w = i % L::s_bufs, st = i % kStages;
             wait(&x.k_full[st], i / kStages & 1, &x.stop);
-            if (i >= L::turns) wait(&x.s_free[w], (i / L::turns - 1) & 1, &x.stop);
+            if (i >= L::s_bufs) wait(&x.s_free[w], (i / L::s_bufs - 1) & 1, &x.stop);
             if (stopped(&x.stop)) continue;
             tc_fence_after();
             const uint32_t d = tmem + w * ROWS, a = k_lo + st * (kStageBytes / 16);
@@ -382,9 +402,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (stopped(&x.stop)) continue;
             tc_fence_after();
             const uint32_t d = tmem + L::col_o + w * L::o_cols, a = v_lo + st * (kStageBytes / 16), b = p_lo + w * (kParts * L::p_part / 16);
+            // three parts of one type: columns side by side in one instruction; two of different
+            // types: one after the other
+            constexpr int kAtOnce = kParts == 3 ? 3 : 1;
 #pragma unroll
-            for (int k = 0; k < kTile / 32; ++k)
-              mma_f8(d, a + k * (32 * kD / 16), v_hi, b + k * (32 * ROWS / 16), p_hi, f8_idesc(kD, kParts * ROWS, true, true), j >= L::turns || k > 0);
+            for (int part = 0; part < kParts; part += kAtOnce)
+#pragma unroll
+              for (int k = 0; k < kTile / 32; ++k)
+                mma_f8(d + part * ROWS, a + k * (32 * kD / 16), v_hi, b + part * (L::p_part / 16) + k * (32 * ROWS / 16), p_hi,
+                       f8_idesc(kD, kAtOnce * ROWS, true, true, kParts == 2 && part == 1), j >= L::turns || k > 0);
             mma_commit(&x.o_done[w]);
             mma_commit(&x.v_empty[st]);
           }
@@ -399,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int group = warp >> 2, token = tid & (kGroupThreads - 1);
     const int turn = L::split ? group >> 1 : group, col0 = L::split ? (group & 1) * kCols : 0;
     const uint32_t quarter = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's lanes
-    const uint32_t my_s = quarter + turn * ROWS + col0, my_o = quarter + L::col_o + turn * L::o_cols + col0;
+    const uint32_t my_o = quarter + L::col_o + turn * L::o_cols + col0;
     const int flip = ROWS == 64 ? token >> 1 & 3 : token >> 2 & 1;  // the swizzle of a token's row of P
     unsigned char* my_p = s_p + turn * kParts * L::p_part + token * ROWS;
     uint32_t i0 = 0, u = 0;  // tiles and units of the CTA before this one
@@ -442,12 +468,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       int j = j0;
 #pragma unroll 1
       for (; j < n; j += L::turns) {
-        const uint32_t i = i0 + j, slot = i % kMeta, phase = i / L::turns & 1;
+        const uint32_t i = i0 + j, slot = i % kMeta, phase = i / L::turns & 1, buf = i % L::s_bufs;
+        const uint32_t my_s = quarter + buf * ROWS + col0;
         wait(&x.meta_full[slot], i / kMeta & 1, &x.stop);
         const float ks = x.ks[slot][token >> p.page_shift], vs = x.vs[slot][token >> p.page_shift];
         const bool valid = vs > 0.f && (s.t0 + j) * kTile + token < s.r.len;
         const float f = ks * q_scale, lv = __log2f(vs), inv_v = valid ? 1.f / vs : 0.f;
-        wait(&x.s_full[turn], phase, &x.stop);
+        wait(&x.s_full[buf], i / L::s_bufs & 1, &x.stop);
         __syncwarp();
         tc_fence_after();
         // 16 rows a step (registers); rows behind the block's last are skipped. First whether a
@@ -543,25 +570,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (c >= apart(rows)) continue;
           float y[16];
           scores(c, y);
-          uint32_t codes[kParts][4];
+          uint32_t codes[4][kParts];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int r = c / 2 + 2 * k;
             const float e0 = ex2(y[4 * k]), e1 = ex2(y[4 * k + 1]), e2 = ex2(y[4 * k + 2]), e3 = ex2(y[4 * k + 3]);
             l[r] = fma2(pair(e0, e1), inv2, l[r]);
             l[r + 1] = fma2(pair(e2, e3), inv2, l[r + 1]);
-            __half2 u0 = __floats2half2_rn(e0, e1), u1 = __floats2half2_rn(e2, e3);
-#pragma unroll
-            for (int part = 0; part < kParts; ++part) codes[part][k] = next_part(u0, u1);
+            split_p<kParts>(__floats2half2_rn(e0, e1), __floats2half2_rn(e2, e3), codes[k]);
           }
 #pragma unroll
           for (int part = 0; part < kParts; ++part)
             *reinterpret_cast<uint4*>(my_p + part * L::p_part + (((col0 + c) / 16) ^ flip) * 16) =
-                make_uint4(codes[part][0], codes[part][1], codes[part][2], codes[part][3]);
+                make_uint4(codes[0][part], codes[1][part], codes[2][part], codes[3][part]);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&x.s_free[turn]);
+        if (lane == 0) mbar_arrive(&x.s_free[buf]);
         if (!valid && col0 == 0) {  // whatever lies behind the last token: 0 times it must be 0
           wait(&x.v_full[i % kStages], i / kStages & 1, &x.stop);
           uint4* v = reinterpret_cast<uint4*>(sm + L::off_v + (i % kStages) * kStageBytes + token * kD);
@@ -644,7 +669,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int part_ = 0; part_ < kParts; ++part_) tmem_tie8(y[part_]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = fmaf(x.w[k][c + e], fmaf(fmaf(y[2][e], 0x1p-5f, y[1][e]), 0x1p-5f, y[0][e]), o[e]);
+          for (int e = 0; e < 8; ++e) {
+            float v = y[0][e];
+            if constexpr (kParts == 2) v = fmaf(y[1][e], 0x1p-12f, v);
+            else v = fmaf(fmaf(y[kParts - 1][e], 0x1p-5f, y[1][e]), 0x1p-5f, v);
+            o[e] = fmaf(x.w[k][c + e], v, o[e]);
+          }
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {

@@ -75,9 +75,16 @@ def wanted(s, windows, lens, sm_scale=None):
                          sm_scale)
 
 
-def check(got, want, dtype, D):
+def two_parts(s):
+    """Whether a call's probabilities go into the product in two parts (see attention_bounds)."""
+    rows, Hq, D = s["q"].shape
+    mean = -(-rows * (Hq // s["k_cache"].shape[1]) // s["page_table"].shape[0])
+    return s["q"].dtype == torch.bfloat16 and D == 128 and mean > 32
+
+
+def check(got, want, dtype, D, two=False):
     out, lse = want[0], want[1]
-    b, z = ref.attention_bounds(*want, dtype, D)
+    b, z = ref.attention_bounds(*want, dtype, D, two)
     o, l = got["out"].cpu().double(), got["lse"].cpu().double()
     assert torch.equal(torch.isneginf(l), torch.isneginf(lse))
     fine = torch.isfinite(lse)
@@ -110,7 +117,7 @@ def test_attention(case):
     windows, lens, Hq, H, D, size, dtype, mask, layout = case
     s = make(11, windows, lens, Hq, H, D, size, dtype, mask, layout)
     got = tv.window_attention(**s, lse=True)
-    check(got, wanted(s, windows, lens), dtype, D)
+    check(got, wanted(s, windows, lens), dtype, D, two_parts(s))
     again = tv.window_attention(**s, lse=True)
     assert torch.equal(got["out"], again["out"]) and torch.equal(got["lse"], again["lse"])
 

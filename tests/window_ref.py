@@ -88,17 +88,20 @@ def attention(q, k_cache, v_cache, k_scale, v_scale, table, lens, windows, k_new
     return out, lse, absv, big, count, floor
 
 
-def attention_bounds(out, lse, absv, big, count, floor, dtype, D):
+def attention_bounds(out, lse, absv, big, count, floor, dtype, D, two_parts=False):
     """How far the kernel may be off, from its roundings.
     Scores: D + 8 fp32 roundings or truncations of partial sums no larger than sum |q k|
     (2^-23 each), and an error of each q of 2^-17 of the largest of its row block (e4m3 parts: the
     largest lies in [2^7, 2^8), the last part is rounded to a multiple of 2^-9 or better):
     d = (D + 8) 2^-23 sum |q k| + 2^-17 max |q| sum |k|; the exponent's
     argument is rounded in log2 units, at most as large (2^-23 of it) and the hardware 2^x is
-    good to 2^-22. Probabilities: 2^-11 (fp16). Sums over n tokens: n 2^-23. The quotient of two
+    good to 2^-22. Probabilities: 2^-11 (fp16); two_parts (bf16, head_dim 128, more than 32 rows
+    of a KV head a window): an e4m3 part and an e5m2 part of its rest, half a step of either,
+    2^-4 2^-3 = 2^-7. Sums over n tokens: n 2^-23. The quotient of two
     such sums doubles what they share. The output is rounded by eps / 2 of its value."""
     d = (D + 8) * 2.0 ** -23 * big + 2.0 ** -17 * floor + 2.0 ** -21
-    share = 2.0 ** -11 + 2 * d + 2 * count * 2.0 ** -23
+    prob = 2.0 ** -7 if two_parts else 2.0 ** -11
+    share = prob + 2 * d + 2 * count * 2.0 ** -23
     half = torch.finfo(dtype).eps / 2
     tiny = torch.finfo(dtype).tiny
     b = half * out.abs() + (1 + half) * absv * share[..., None] + tiny
