@@ -324,8 +324,9 @@ ts_status ts_verify_chain_greedy_static(const void* target_logits, ts_dtype dt, 
  * (a page of one head): value = code * scale. Page ids outside [0, num_pages) are never
  * accessed: their tokens count as absent (attention), read back as 0 and are not stored.
  * seq_lens[b] is taken as clamped to [0, max_pages * page_size].
- * Base addresses and strides (in bytes) must be multiples of 16, head_dim must be 64 or 128,
- * page_size 16, 32, 64 or 128 (else TS_ERR_INVALID_ARG). */
+ * Base addresses and strides (in bytes) must be multiples of 16, the cache's strides positive and
+ * below 2^40, head_dim must be 64 or 128, page_size 16, 32, 64 or 128 (else
+ * TS_ERR_INVALID_ARG). */
 #define TS_F16 2 /* a dtype of the calls below only */
 #define TS_MAX_WINDOW (TS_MAX_DRAFT + 1)
 

@@ -109,6 +109,11 @@ ts_status check_cache(const ts_kv_cache* c) {
   if (!multiple16(c->k, c->k_page_stride, c->k_head_stride) || c->k_token_stride % 16 ||
       !multiple16(c->v, c->v_page_stride, c->v_head_stride) || c->v_token_stride % 16)
     return fail(TS_ERR_INVALID_ARG, "the cache needs 16-byte aligned addresses and strides");
+  // what a tensor map can hold
+  auto bad = [](int64_t stride, int64_t extent) { return extent > 1 && (stride <= 0 || stride >= (int64_t)1 << 40); };
+  if (bad(c->k_page_stride, c->num_pages) || bad(c->v_page_stride, c->num_pages) || bad(c->k_head_stride, c->heads) ||
+      bad(c->v_head_stride, c->heads) || bad(c->k_token_stride, 2) || bad(c->v_token_stride, 2))
+    return fail(TS_ERR_INVALID_ARG, "the cache's strides must be positive and below 2^40");
   return TS_OK;
 }
 

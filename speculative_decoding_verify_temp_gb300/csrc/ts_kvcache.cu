@@ -24,21 +24,27 @@ constexpr int kAppendThreads = 128;
 constexpr int kReadThreads = 256;
 constexpr int kReadRows = 16;
 
-// Eight elements of a row, widened to fp32 (exact).
+// Eight elements of a row: as they lie in memory, and widened to fp32 (exact).
 template <typename T>
 struct Src;
 template <>
 struct Src<float> {
-  __device__ __forceinline__ static void load8(const void* p, float* x) {
-    const float4 a = __ldg(static_cast<const float4*>(p)), b = __ldg(static_cast<const float4*>(p) + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  struct Raw {
+    float4 a, b;
+  };
+  __device__ __forceinline__ static Raw load(const void* p) {
+    return {__ldg(static_cast<const float4*>(p)), __ldg(static_cast<const float4*>(p) + 1)};
+  }
+  __device__ __forceinline__ static void widen(const Raw& r, float* x) {
+    x[0] = r.a.x, x[1] = r.a.y, x[2] = r.a.z, x[3] = r.a.w;
+    x[4] = r.b.x, x[5] = r.b.y, x[6] = r.b.z, x[7] = r.b.w;
   }
 };
 template <>
 struct Src<__nv_bfloat16> {
-  __device__ __forceinline__ static void load8(const void* p, float* x) {
-    const uint4 r = __ldg(static_cast<const uint4*>(p));
+  typedef uint4 Raw;
+  __device__ __forceinline__ static Raw load(const void* p) { return __ldg(static_cast<const uint4*>(p)); }
+  __device__ __forceinline__ static void widen(const Raw& r, float* x) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -49,8 +55,9 @@ struct Src<__nv_bfloat16> {
 };
 template <>
 struct Src<__half> {
-  __device__ __forceinline__ static void load8(const void* p, float* x) {
-    const uint4 r = __ldg(static_cast<const uint4*>(p));
+  typedef uint4 Raw;
+  __device__ __forceinline__ static Raw load(const void* p) { return __ldg(static_cast<const uint4*>(p)); }
+  __device__ __forceinline__ static void widen(const Raw& r, float* x) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -83,17 +90,18 @@ __device__ __forceinline__ Rows rows_of(const ts_kv_append_args& a, int64_t batc
   return {r0, r1 - r0};
 }
 
-// One CTA: every `step`-th block that request b touches in head h of K or V. The block's
-// rows are read twice, for the maximum and for the codes (the second time from L1/L2).
-// Bound: HBM for prompts; for the few rows after a verify step, the chain of dependent
-// loads seq_len -> page -> rows.
-template <typename T>
+// One CTA: every `step`-th block that request b touches in head h of K or V. N = the eighths of
+// a thousand elements of a block: a thread holds N times eight of them in registers between the
+// maximum and the codes, with all loads in flight at once. Bound: HBM for prompts (24 k rows of
+// 8 heads of 128, 147 MB of traffic); for the few rows after a verify step, the chain of
+// dependent loads seq_len -> page -> rows.
+template <typename T, int D, int N>
 __global__ void __launch_bounds__(kAppendThreads) k_kv_append(ts_kv_cache c, ts_kv_append_args a, int32_t step) {
+  constexpr int per_row = D / 8, n = N * kAppendThreads * 8 / D;  // n: page_size
   const int64_t unit = blockIdx.x / step;
   const int h = (int)(unit % c.heads);
   const bool is_v = (unit / c.heads) & 1;
   const int64_t b = unit / (2 * c.heads);
-  const int n = c.page_size, D = c.head_dim, per_row = D / 8;
   const int64_t cap = (int64_t)c.max_pages * n;
   const int64_t len = min((int64_t)max(c.seq_lens[b], 0), cap);
   const Rows rows = rows_of(a, c.batch, b);
@@ -103,29 +111,34 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(ts_kv_cache c, ts_
   float* scales = is_v ? c.v_scale : c.k_scale;
   __shared__ int32_t s_max[kAppendThreads / 32];
 
-  auto row_at = [&](int64_t j) -> int64_t {
-    const int64_t r = rows.first < 0 ? (int64_t)a.src_index[b * a.ld_src + j] : rows.first + j;
-    return r >= 0 && r < a.total_rows ? r : -1;
-  };
-
   for (int64_t p = len / n + blockIdx.x % step;; p += step) {
     const int64_t lo = max(len, p * n), hi = min(min(len + rows.count, (p + 1) * n), cap);
     if (lo >= hi) return;
     const int64_t page = c.page_table[b * c.ld_table + p];
-    if (page < 0 || page >= c.num_pages) continue;
-    char* block = static_cast<char*>(is_v ? c.v : c.k) + page * (is_v ? c.v_page_stride : c.k_page_stride) +
-                  h * (is_v ? c.v_head_stride : c.k_head_stride);
+    const bool stored = page >= 0 && page < c.num_pages;
     const int held = (int)(lo - p * n);  // earlier tokens of the block
-    const int chunks = (int)(hi - lo) * per_row;
-    const float old = scales[page * c.heads + h];
+    const int chunks = stored ? (int)(hi - lo) * per_row : 0;
+    // eight elements of row i / per_row of the block's new rows
+    typename Src<T>::Raw raw[N];
+    uint32_t there = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = k * kAppendThreads + threadIdx.x;
+      if (i >= chunks) continue;
+      const int64_t j = lo - len + i / per_row;
+      const int64_t r = rows.first < 0 ? (int64_t)a.src_index[b * a.ld_src + j] : rows.first + j;
+      if (r < 0 || r >= a.total_rows) continue;
+      there |= 1u << k;
+      raw[k] = Src<T>::load(src + r * src_ld + (int64_t)(i % per_row) * 8 * sizeof(T));
+    }
+    const float old = stored ? scales[page * c.heads + h] : 0.f;
     // the largest finite magnitude, as bits (-1: no row to store)
-    int32_t top = -1;
-    for (int i = threadIdx.x; i < chunks; i += kAppendThreads) {
-      const int64_t r = row_at(lo - len + i / per_row);
-      if (r < 0) continue;
+    int32_t top = there ? 0 : -1;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      if (!(there >> k & 1)) continue;
       float x[8];
-      Src<T>::load8(src + r * src_ld + (int64_t)(i % per_row) * 8 * sizeof(T), x);
-      top = max(top, 0);
+      Src<T>::widen(raw[k], x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int32_t m = __float_as_int(fabsf(x[e]));
@@ -139,17 +152,25 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(ts_kv_cache c, ts_
 #pragma unroll
     for (int w = 0; w < kAppendThreads / 32; ++w) top = max(top, s_max[w]);
     if (top < 0) continue;
+    char* block = static_cast<char*>(is_v ? c.v : c.k) + page * (is_v ? c.v_page_stride : c.k_page_stride) +
+                  h * (is_v ? c.v_head_stride : c.k_head_stride);
     float scale = block_scale(__int_as_float(top));
     if (held) scale = fmaxf(old, scale);
     const bool pow2 = (__float_as_uint(scale) & 0x7FFFFFu) == 0;  // false: a caller's own scale
     const float inv = 1.f / scale;
-    for (int i = threadIdx.x; i < chunks; i += kAppendThreads) {
-      const int64_t r = row_at(lo - len + i / per_row);
-      if (r < 0) continue;
-      float x[8];
-      Src<T>::load8(src + r * src_ld + (int64_t)(i % per_row) * 8 * sizeof(T), x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = pow2 ? x[e] * inv : __fdiv_rn(x[e], scale);
+    for (int k = 0; k < N; ++k) {
+      if (!(there >> k & 1)) continue;
+      const int i = k * kAppendThreads + threadIdx.x;
+      float x[8];
+      Src<T>::widen(raw[k], x);
+      if (pow2) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= inv;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __fdiv_rn(x[e], scale);
+      }
       uint2 w;
       w.x = e4m3x4(x[0], x[1], x[2], x[3]);
       w.y = e4m3x4(x[4], x[5], x[6], x[7]);
@@ -157,10 +178,16 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(ts_kv_cache c, ts_
     }
     if (held && scale != old) {
       const float ratio = __fdiv_rn(old, scale);
-      for (int i = threadIdx.x; i < held * (D / 4); i += kAppendThreads) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(block + (i / (D / 4)) * tok_ld + (i % (D / 4)) * 4);
-        const float4 f = e4m3x4_to_f32(*w);
-        *w = e4m3x4(f.x * ratio, f.y * ratio, f.z * ratio, f.w * ratio);
+      for (int i = threadIdx.x; i < held * (D / 16); i += kAppendThreads) {
+        uint4* at = reinterpret_cast<uint4*>(block + (i / (D / 16)) * tok_ld + (i % (D / 16)) * 16);
+        const uint4 v = *at;
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 f = e4m3x4_to_f32(w[k]);
+          w[k] = e4m3x4(f.x * ratio, f.y * ratio, f.z * ratio, f.w * ratio);
+        }
+        *at = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
     if (threadIdx.x == 0) scales[page * c.heads + h] = scale;
@@ -229,34 +256,46 @@ __global__ void __launch_bounds__(kReadThreads) k_kv_read(ts_kv_cache c, ts_kv_r
   }
   __syncthreads();
   const int D = c.head_dim, parts = D / 16;
-  const int per_row = c.heads * parts;
-  for (int i = threadIdx.x; i < kReadRows * per_row; i += kReadThreads) {
-    const int t = i / per_row, h = i % per_row / parts, part = i % parts;
-    const int64_t page = s_page[t];
-    if (page == -2) continue;
-    uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;
-    float ks = 0.f, vs = 0.f;
-    if (page >= 0) {
-      kw = ldg_stream(static_cast<const char*>(c.k) + page * c.k_page_stride + h * c.k_head_stride +
-                      s_slot[t] * c.k_token_stride + part * 16);
-      vw = ldg_stream(static_cast<const char*>(c.v) + page * c.v_page_stride + h * c.v_head_stride +
-                      s_slot[t] * c.v_token_stride + part * 16);
-      ks = __ldg(c.k_scale + page * c.heads + h);
-      vs = __ldg(c.v_scale + page * c.heads + h);
+  const int per_row = c.heads * parts, all = kReadRows * per_row;
+  constexpr int kAtOnce = 4;  // steps whose loads are in flight together
+  for (int i0 = threadIdx.x; i0 < all; i0 += kAtOnce * kReadThreads) {
+    uint4 kw[kAtOnce], vw[kAtOnce];
+    float ks[kAtOnce], vs[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = i0 + u * kReadThreads;
+      kw[u] = vw[u] = make_uint4(0, 0, 0, 0);
+      ks[u] = vs[u] = 0.f;
+      if (i >= all) continue;
+      const int t = i / per_row, h = i % per_row / parts, part = i % parts;
+      const int64_t page = s_page[t];
+      if (page < 0) continue;
+      kw[u] = ldg_stream(static_cast<const char*>(c.k) + page * c.k_page_stride + h * c.k_head_stride +
+                         s_slot[t] * c.k_token_stride + part * 16);
+      vw[u] = ldg_stream(static_cast<const char*>(c.v) + page * c.v_page_stride + h * c.v_head_stride +
+                         s_slot[t] * c.v_token_stride + part * 16);
+      ks[u] = __ldg(c.k_scale + page * c.heads + h);
+      vs[u] = __ldg(c.v_scale + page * c.heads + h);
     }
-    const int64_t at = (((r0 + t) * c.heads + h) * D + part * 16) * (int64_t)sizeof(T);
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      const uint4 w = which ? vw : kw;
-      const float s = which ? vs : ks;
-      const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-      float x[16];
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = i0 + u * kReadThreads;
+      if (i >= all || s_page[i / per_row] == -2) continue;
+      const int t = i / per_row, h = i % per_row / parts, part = i % parts;
+      const int64_t at = (((r0 + t) * c.heads + h) * D + part * 16) * (int64_t)sizeof(T);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 f = e4m3x4_to_f32(words[j]);
-        x[4 * j] = f.x * s, x[4 * j + 1] = f.y * s, x[4 * j + 2] = f.z * s, x[4 * j + 3] = f.w * s;
+      for (int which = 0; which < 2; ++which) {
+        const uint4 w = which ? vw[u] : kw[u];
+        const float s = which ? vs[u] : ks[u];
+        const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+        float x[16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 f = e4m3x4_to_f32(words[j]);
+          x[4 * j] = f.x * s, x[4 * j + 1] = f.y * s, x[4 * j + 2] = f.z * s, x[4 * j + 3] = f.w * s;
+        }
+        store16<T>(static_cast<char*>(which ? a.v_out : a.k_out) + at, x);
       }
-      store16<T>(static_cast<char*>(which ? a.v_out : a.k_out) + at, x);
     }
   }
 }
@@ -279,8 +318,21 @@ cudaError_t launch_kv_append(const ts_kv_cache& c, const ts_kv_append_args& a, i
   const int64_t want = (rows + c.page_size - 1) / c.page_size + 1;
   const int64_t fill = ((int64_t)sms * 32 + units - 1) / units;
   const int64_t step = std::max<int64_t>(2, std::min(want, fill));
+  const int n = c.page_size * c.head_dim / (kAppendThreads * 8);
   return by_dtype(a.dtype, [&](auto t) {
-    k_kv_append<decltype(t)><<<(unsigned)(units * step), kAppendThreads, 0, s>>>(c, a, (int32_t)step);
+    auto go = [&](auto kernel) { kernel<<<(unsigned)(units * step), kAppendThreads, 0, s>>>(c, a, (int32_t)step); };
+    using T = decltype(t);
+    if (c.head_dim == 64) {
+      if (n == 1) go(k_kv_append<T, 64, 1>);
+      else if (n == 2) go(k_kv_append<T, 64, 2>);
+      else if (n == 4) go(k_kv_append<T, 64, 4>);
+      else go(k_kv_append<T, 64, 8>);
+    } else {
+      if (n == 2) go(k_kv_append<T, 128, 2>);
+      else if (n == 4) go(k_kv_append<T, 128, 4>);
+      else if (n == 8) go(k_kv_append<T, 128, 8>);
+      else go(k_kv_append<T, 128, 16>);
+    }
   });
 }
 

@@ -375,7 +375,7 @@ constexpr int smem_bytes(int D, int rows) {
 template <int D, int MT, typename T>
 cudaError_t launch(const Params& p, int sms, cudaStream_t s) {
   constexpr int ROWS = 16 * MT, bytes = smem_bytes(D, ROWS);
-  cudaError_t e = cudaFuncSetAttribute(k_window<D, MT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  cudaError_t e = allow_smem<k_window<D, MT, T>>(bytes);
   if (e != cudaSuccess) return e;
   const int grid = sms * kCtasPerSm;
   if (p.a.k_new) {
@@ -385,15 +385,14 @@ cudaError_t launch(const Params& p, int sms, cudaStream_t s) {
     k_window<D, MT, T><<<grid, kThreads, bytes, s>>>(p);
     e = cudaGetLastError();
   }
-  if (e != cudaSuccess) return e;
+  // units of one tile are never split
+  if (e != cudaSuccess || (int64_t)p.c.max_pages * p.c.page_size <= kTile) return e;
   return launch_after(k_join<D, ROWS, kTile, T>, dim3(grid, ROWS / 4), 128, 0, s, p);
 }
 
 template <int MT>
 cudaError_t launch_mt(const Params& p, int sms, cudaStream_t s) {
   const bool bf16 = p.a.dtype == TS_BF16;
-  if (p.c.head_dim == 128)
-    return bf16 ? launch<128, MT, __nv_bfloat16>(p, sms, s) : launch<128, MT, __half>(p, sms, s);
   return bf16 ? launch<64, MT, __nv_bfloat16>(p, sms, s) : launch<64, MT, __half>(p, sms, s);
 }
 
@@ -447,12 +446,7 @@ cudaError_t launch_window(const ts_kv_cache& c, const ts_attn_args& a, void* ws,
   p.scale_log2 = a.sm_scale * kLog2e;
   lay_out(p, ws, sms);
   if (!a.k_new) p.own_ml = nullptr;
-  if (c.head_dim == 128) {
-    bool done = false;
-    const cudaError_t e = launch_window_tc(p, block_rows(p), sms, s, &done);
-    if (done || e != cudaSuccess) return e;
-    return launch_mt<2>(p, sms, s);
-  }
+  if (c.head_dim == 128) return launch_window_tc(p, block_rows(p), sms, s);
   return block_rows(p) == 16 ? launch_mt<1>(p, sms, s) : launch_mt<2>(p, sms, s);
 }
 

@@ -5,6 +5,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/ts_verify.h"
 #include "ts_common.cuh"
 #include "ts_internal.h"
@@ -298,6 +300,20 @@ __global__ void __launch_bounds__(128) k_join(const __grid_constant__ WindowPara
     *reinterpret_cast<uint32_t*>(static_cast<char*>(p.a.out) + (at * D + lane * PER + e) * 2) =
         pack<T>(fmaf(acc[e], by, o.x * own), fmaf(acc[e + 1], by, o.y * own));
   }
+}
+
+// Lets a kernel have this much dynamic shared memory, once on each device.
+template <auto kernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // Launches with programmatic stream serialisation: the kernel may start before the one

@@ -262,6 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t *full = is_k ? x.k_full : x.v_full, *empty = is_k ? x.k_empty : x.v_empty;
       const int per_tile = kTile >> p.page_shift, per_round = 32 / per_tile;  // pages, tiles
       const int page_bytes = p.c.page_size * kD;
+      const int32_t outside = (int32_t)max(p.c.num_pages, (int64_t)1);  // reads as zeros
       // the lane's page of round r of a segment, or -1
       auto page_of = [&](const Segment& g, int r) -> int32_t {
         const int i = g.t0 * per_tile + r * 32 + lane;
@@ -301,9 +302,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!stopped(&x.stop)) {
               if (lane == 0) mbar_arrive_expect_tx(&full[st], kStageBytes);
               __syncwarp();
-              // a page outside the tensor reads as zeros
               if (at >= 0 && at < per_tile)
-                tma_load_4d(ring + st * kStageBytes + at * page_bytes, map, 0, 0, s.kvh, page >= 0 ? page : (int32_t)p.c.num_pages, &full[st]);
+                tma_load_4d(ring + st * kStageBytes + at * page_bytes, map, 0, 0, s.kvh, page >= 0 ? page : outside, &full[st]);
             }
             if (is_k) {
               if (at >= 0 && at < per_tile) {
@@ -735,11 +735,12 @@ EncodeTiled encoder() {
 
 // K or V as [pages][heads][tokens of a page][D] bytes; a box is one page of one head.
 bool page_map(CUtensorMap* map, const ts_kv_cache& c, void* base, int64_t page_stride, int64_t head_stride, int64_t token_stride) {
-  const cuuint64_t dims[4] = {(cuuint64_t)kD, (cuuint64_t)c.page_size, (cuuint64_t)c.heads, (cuuint64_t)c.num_pages};
+  // the stride of an extent of one is never used, but has to be a valid one
+  if (c.heads == 1) head_stride = token_stride;
+  if (c.num_pages <= 1) page_stride = token_stride;
+  const cuuint64_t dims[4] = {(cuuint64_t)kD, (cuuint64_t)c.page_size, (cuuint64_t)c.heads, (cuuint64_t)std::max<int64_t>(c.num_pages, 1)};
   const cuuint64_t strides[3] = {(cuuint64_t)token_stride, (cuuint64_t)head_stride, (cuuint64_t)page_stride};
   const cuuint32_t box[4] = {(cuuint32_t)kD, (cuuint32_t)c.page_size, 1, 1}, step[4] = {1, 1, 1, 1};
-  for (int64_t st : {page_stride, head_stride, token_stride})
-    if (st <= 0 || st >= (int64_t)1 << 40) return false;
   return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -747,10 +748,11 @@ bool page_map(CUtensorMap* map, const ts_kv_cache& c, void* base, int64_t page_s
 template <int ROWS, int QP, typename T>
 cudaError_t launch(const WindowParams& p, const CUtensorMap& k, const CUtensorMap& v, int sms, cudaStream_t s) {
   constexpr int bytes = smem_bytes<ROWS, QP>();
-  cudaError_t e = cudaFuncSetAttribute(k_window_tc<ROWS, QP, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  cudaError_t e = allow_smem<k_window_tc<ROWS, QP, T>>(bytes);
   if (e != cudaSuccess) return e;
   k_window_tc<ROWS, QP, T><<<sms, kThreads, bytes, s>>>(p, k, v);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((int64_t)p.c.max_pages * p.c.page_size <= kTile) return cudaSuccess;  // units of one tile are never split
   return launch_after(k_join<kD, ROWS, kTile, T>, dim3(sms, ROWS / 4), 128, 0, s, p);
 }
 
@@ -765,15 +767,15 @@ cudaError_t window_read_error(uint32_t* word, int clear) {
   return e;
 }
 
-cudaError_t launch_window_tc(const WindowParams& params, int rows, int sms, cudaStream_t s, bool* done) {
+cudaError_t launch_window_tc(const WindowParams& params, int rows, int sms, cudaStream_t s) {
   WindowParams p = params;
   p.own_ml = nullptr;  // the window's own part is in the pieces; own_o: a block a CTA
   CUtensorMap k, v;
   const ts_kv_cache& c = p.c;
-  *done = encoder() != nullptr && c.num_pages > 0 && c.num_pages < INT32_MAX &&
-          page_map(&k, c, c.k, c.k_page_stride, c.k_head_stride, c.k_token_stride) &&
-          page_map(&v, c, c.v, c.v_page_stride, c.v_head_stride, c.v_token_stride);
-  if (!*done) return cudaSuccess;
+  if (!encoder()) return cudaErrorNotSupported;
+  if (!page_map(&k, c, c.k, c.k_page_stride, c.k_head_stride, c.k_token_stride) ||
+      !page_map(&v, c, c.v, c.v_page_stride, c.v_head_stride, c.v_token_stride))
+    return cudaErrorInvalidValue;
   const bool bf16 = p.a.dtype == TS_BF16;
   if (rows == 32)
     return bf16 ? launch<32, 2, __nv_bfloat16>(p, k, v, sms, s) : launch<32, 3, __half>(p, k, v, sms, s);

@@ -479,6 +479,7 @@ def gather_logprobs(x, tokens, is_probs: bool = False, workspace=None, out=None,
 
 # ---- around the verify step: a window's attention over the 8-bit cache, the cache, trees ----
 
+_CODES = (torch.float8_e4m3fn, torch.uint8)
 _KV_DTYPES = {torch.float32: TS_F32, torch.bfloat16: TS_BF16, torch.float16: TS_F16}
 
 
@@ -489,73 +490,94 @@ def _kv_dtype(dtype) -> int:
 
 
 class _On:
-    """The device and stream of a call: its outputs and scratch come from that stream's pool,
-    its kernels go to that stream."""
+    """The device and stream of a call that names a stream or is not on the current device: its
+    outputs and scratch come from that stream's pool, its kernels go to that stream."""
 
     def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError("expected CUDA tensors")
-        same = device.index is None or device.index == torch.cuda.current_device()
-        self.contexts = [] if same else [torch.cuda.device(device)]
+        self.contexts = [torch.cuda.device(device)]
         if stream is not None:
             self.contexts.append(torch.cuda.stream(stream))
 
     def __enter__(self):
         for c in self.contexts:
             c.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return torch.cuda.current_stream().cuda_stream
 
     def __exit__(self, *exc):
         for c in reversed(self.contexts):
             c.__exit__(*exc)
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+class _Here:
+    """The usual case: the current stream of the current device."""
+
+    def __init__(self, stream):
+        self.stream = stream
+
+    def __enter__(self):
+        return self.stream
+
+    def __exit__(self, *exc):
+        pass
 
 
-def _int32(name, t, shape):
-    """A contiguous int32 tensor of this shape (None: not given)."""
+def _on(device: int, stream):
+    if device < 0:
+        raise ValueError("expected CUDA tensors")
+    if stream is None and device == torch.cuda.current_device():
+        return _Here(torch._C._cuda_getCurrentRawStream(device))
+    return _On(device, stream)
+
+
+def _same_device(device: int, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"a tensor is on {t.device}, the first one on device {device}")
+
+
+def _int32(name, t, *shape):
+    """The address of a contiguous int32 tensor of this shape (None: not given)."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)}")
     return t.data_ptr()
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens):
-    """The ts_kv_cache of the tensors (pages, heads, page_size, head_dim)."""
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+    """The ts_kv_cache of the tensors (pages, heads, page_size, head_dim) and their device."""
+    shape = k_cache.shape
+    if len(shape) != 4 or shape != v_cache.shape:
         raise ValueError("k_cache and v_cache must be [pages, heads, page_size, head_dim]")
-    for t in (k_cache, v_cache):
-        if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
-            raise TypeError("the cache holds float8_e4m3fn (or its bytes as uint8)")
-        if t.stride(3) != 1:
-            raise ValueError("the cache needs unit stride in the last dimension")
-    n, H, size, D = k_cache.shape
+    n, H, size, D = shape
+    k0, k1, k2, k3 = k_cache.stride()
+    v0, v1, v2, v3 = v_cache.stride()
+    if k_cache.dtype not in _CODES or v_cache.dtype not in _CODES:
+        raise TypeError("the cache holds float8_e4m3fn (or its bytes as uint8)")
+    if k3 != 1 or v3 != 1:
+        raise ValueError("the cache needs unit stride in the last dimension")
     for t in (k_scale, v_scale):
-        if t.dtype != torch.float32 or tuple(t.shape) != (n, H) or not t.is_contiguous():
+        if t.dtype != torch.float32 or t.shape != (n, H) or not t.is_contiguous():
             raise ValueError(f"scales must be contiguous fp32 tensors of shape ({n}, {H})")
     if page_table.dtype != torch.int32 or page_table.dim() != 2 or \
             (page_table.shape[1] > 1 and page_table.stride(1) != 1):
         raise ValueError("page_table must be a 2-D int32 tensor with unit stride in the last dimension")
     B, P = page_table.shape
-    _same_device(k_cache.device, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
-                 page_table=page_table, seq_lens=seq_lens)
-    ks, vs = k_cache.stride(), v_cache.stride()
-    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
+    device = k_cache.get_device()
+    _same_device(device, v_cache, k_scale, v_scale, page_table, seq_lens)
+    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), k0, k1, k2, v0, v1, v2,
                    k_scale.data_ptr(), v_scale.data_ptr(), n, H, D, size, P, page_table.data_ptr(),
-                   max(page_table.stride(0), P) if B > 1 else P, _int32("seq_lens", seq_lens, (B,)), B)
+                   max(page_table.stride(0), P) if B > 1 else P, _int32("seq_lens", seq_lens, B),
+                   B), device
 
 
 def _heads(name, t, heads, D):
     """(rows, row stride, head stride) in bytes of a [rows, heads, D] tensor."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D or t.stride(2) != 1:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != D or stride[2] != 1:
         raise ValueError(f"{name} must be [rows, {heads}, {D}] with unit stride in the last dimension")
     size = t.element_size()
-    return t.shape[0], t.stride(0) * size, t.stride(1) * size
+    return shape[0], stride[0] * size, stride[1] * size
 
 
 def attention_workspace_size(batch: int, rows: int, heads_q: int, heads: int, head_dim: int) -> int:
@@ -580,37 +602,40 @@ def window_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens
     packed by qo_indptr (int32 [B+1]) or rows / B a request; parents (int32 [rows], window
     row numbers) makes each window a tree. sm_scale: 1/sqrt(D) by default. Returns
     dict(out=[rows, Hq, D], lse=[rows, Hq] fp32 or None)."""
-    c = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)
-    D, dev = c.head_dim, k_cache.device
+    c, device = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)
+    D, H, B = c.head_dim, c.heads, c.batch
     if q.dim() != 3:
         raise ValueError("q must be [rows, heads, head_dim]")
-    rows, qr, qh = _heads("q", q, q.shape[1], D)
-    _same_device(dev, q=q, k_new=k_new, v_new=v_new, qo_indptr=qo_indptr, parents=parents, out=out,
-                 workspace=workspace)
+    Hq = q.shape[1]
+    rows, qr, qh = _heads("q", q, Hq, D)
+    _same_device(device, q, k_new, v_new, qo_indptr, parents, out, workspace)
+    k_ptr = v_ptr = None
     kr = kh = vr = vh = 0
     if k_new is not None and v_new is not None:
-        nk, kr, kh = _heads("k_new", k_new, c.heads, D)
-        nv, vr, vh = _heads("v_new", v_new, c.heads, D)
+        nk, kr, kh = _heads("k_new", k_new, H, D)
+        nv, vr, vh = _heads("v_new", v_new, H, D)
         if nk != rows or nv != rows or k_new.dtype != q.dtype or v_new.dtype != q.dtype:
             raise ValueError("k_new and v_new must have the rows and the dtype of q")
-    with _On(dev, stream) as s:
+    if k_new is not None:
+        k_ptr = k_new.data_ptr()
+    if v_new is not None:
+        v_ptr = v_new.data_ptr()
+    with _on(device, stream) as s:
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
             raise ValueError("out must be contiguous, with the shape and dtype of q")
-        z = torch.empty(q.shape[:2], dtype=torch.float32, device=dev) if lse else None
+        z = torch.empty((rows, Hq), dtype=torch.float32, device=q.device) if lse else None
         if workspace is None:
-            workspace = torch.empty(attention_workspace_size(c.batch, rows, q.shape[1], c.heads, D),
-                                    dtype=torch.uint8, device=dev)
-        a = AttnArgs(ctypes.pointer(c), q.data_ptr(), qr, qh, _kv_dtype(q.dtype), q.shape[1],
-                     None if k_new is None else k_new.data_ptr(),
-                     None if v_new is None else v_new.data_ptr(), kr, kh, vr, vh, rows,
-                     _int32("qo_indptr", qo_indptr, (c.batch + 1,)),
-                     _int32("parents", parents, (rows,)),
-                     D ** -0.5 if sm_scale is None else sm_scale, 0.0, out.data_ptr(),
-                     None if z is None else z.data_ptr())
-        _check("ts_window_attention", load().ts_window_attention(
-            ctypes.byref(a), _p(workspace), workspace.numel() * workspace.element_size(), s))
+            workspace = torch.empty(attention_workspace_size(B, rows, Hq, H, D),
+                                    dtype=torch.uint8, device=q.device)
+        a = AttnArgs(ctypes.pointer(c), q.data_ptr(), qr, qh, _kv_dtype(q.dtype), Hq, k_ptr, v_ptr,
+                     kr, kh, vr, vh, rows, _int32("qo_indptr", qo_indptr, B + 1),
+                     _int32("parents", parents, rows), D ** -0.5 if sm_scale is None else sm_scale,
+                     0.0, out.data_ptr(), None if z is None else z.data_ptr())
+        st = load().ts_window_attention(a, workspace.data_ptr(), workspace.nbytes, s)
+        if st:
+            _check("ts_window_attention", st)
     return dict(out=out, lse=z)
 
 
@@ -620,41 +645,49 @@ def kv_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, *,
     each request's seq_lens tokens (which it does not update): the rows src_index[b, :src_len[b]]
     (a verify call's accept_index and accept_length), or the packed rows of qo_indptr, or
     rows / B a request."""
-    c = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)
-    rows, kr, kh = _heads("k", k, c.heads, c.head_dim)
-    nv, vr, vh = _heads("v", v, c.heads, c.head_dim)
+    c, device = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)
+    H, D, B = c.heads, c.head_dim, c.batch
+    rows, kr, kh = _heads("k", k, H, D)
+    nv, vr, vh = _heads("v", v, H, D)
     if nv != rows or v.dtype != k.dtype:
         raise ValueError("v must have the rows and the dtype of k")
-    _same_device(k_cache.device, k=k, v=v, qo_indptr=qo_indptr, src_index=src_index, src_len=src_len)
+    _same_device(device, k, v, qo_indptr, src_index, src_len)
     n = 0
     if src_index is not None:
         if src_index.dim() != 2:
             raise ValueError("src_index must be [B, n]")
         n = src_index.shape[1]
-    with _On(k_cache.device, stream) as s:
+    with _on(device, stream) as s:
         a = KvAppendArgs(ctypes.pointer(c), k.data_ptr(), v.data_ptr(), kr, kh, vr, vh,
-                         _kv_dtype(k.dtype), 0, rows, _int32("src_index", src_index, (c.batch, n)),
-                         _int32("src_len", src_len, (c.batch,)), n,
-                         _int32("qo_indptr", qo_indptr, (c.batch + 1,)))
-        _check("ts_kv_append", load().ts_kv_append(ctypes.byref(a), s))
+                         _kv_dtype(k.dtype), 0, rows, _int32("src_index", src_index, B, n),
+                         _int32("src_len", src_len, B), n, _int32("qo_indptr", qo_indptr, B + 1))
+        st = load().ts_kv_append(a, s)
+        if st:
+            _check("ts_kv_append", st)
 
 
 def kv_read(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, *, out_indptr, total_rows: int,
             start=None, dtype=torch.bfloat16, out=None, stream=None):
     """Reads tokens back: request b's tokens from start[b] (0) on into rows out_indptr[b] ..
     out_indptr[b+1] - 1 of k and v [total_rows, H, D] (out: a pair of such tensors)."""
-    c = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)
-    dev, shape = k_cache.device, (total_rows, c.heads, c.head_dim)
-    with _On(dev, stream) as s:
-        k, v = out or (torch.empty(shape, dtype=dtype, device=dev) for _ in range(2))
-        for t in (k, v):
-            if t.dtype != k.dtype or tuple(t.shape) != shape or not t.is_contiguous():
-                raise ValueError(f"outputs must be contiguous tensors of shape {shape} and one dtype")
-        _same_device(dev, out_indptr=out_indptr, start=start, k=k, v=v)
-        a = KvReadArgs(ctypes.pointer(c), _int32("out_indptr", out_indptr, (c.batch + 1,)),
-                       _int32("start", start, (c.batch,)), total_rows, _kv_dtype(k.dtype), 0,
-                       k.data_ptr(), v.data_ptr())
-        _check("ts_kv_read", load().ts_kv_read(ctypes.byref(a), s))
+    c, device = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)
+    B, shape = c.batch, (total_rows, c.heads, c.head_dim)
+    with _on(device, stream) as s:
+        if out is None:
+            k = torch.empty(shape, dtype=dtype, device=k_cache.device)
+            v = torch.empty(shape, dtype=dtype, device=k_cache.device)
+        else:
+            k, v = out
+            for t in (k, v):
+                if t.dtype != k.dtype or t.shape != shape or not t.is_contiguous():
+                    raise ValueError(f"outputs must be contiguous tensors of shape {shape} and one dtype")
+        _same_device(device, out_indptr, start, k, v)
+        a = KvReadArgs(ctypes.pointer(c), _int32("out_indptr", out_indptr, B + 1),
+                       _int32("start", start, B), total_rows, _kv_dtype(k.dtype), 0, k.data_ptr(),
+                       v.data_ptr())
+        st = load().ts_kv_read(a, s)
+        if st:
+            _check("ts_kv_read", st)
     return dict(k=k, v=v)
 
 
@@ -673,14 +706,17 @@ def tree_spec_sampling(target_probs, D: int, tokens, parents, uniforms, *, qo_in
         raise ValueError("target_probs must have one row for each token")
     if uniforms.dtype != torch.float32 or uniforms.numel() != rows or not uniforms.is_contiguous():
         raise ValueError("uniforms must be a contiguous fp32 tensor with one coin for each token")
-    dev = target_probs.device
-    _same_device(dev, tokens=tokens, parents=parents, uniforms=uniforms, qo_indptr=qo_indptr)
-    with _On(dev, stream) as s:
-        acc, alen, aidx, lp = outputs or _chain_outputs(B, D + 1, dev, accept_index, logprobs)
-        a = TreeArgs(target_probs.data_ptr(), V, ld, B, rows,
-                     _int32("qo_indptr", qo_indptr, (B + 1,)),
-                     _int32("tokens", tokens, tokens.shape), _int32("parents", parents, tokens.shape),
-                     uniforms.data_ptr(), D, 0, acc.data_ptr(), alen.data_ptr(),
-                     None if aidx is None else aidx.data_ptr(), None if lp is None else lp.data_ptr())
-        _check("ts_tree_spec_sampling", load().ts_tree_spec_sampling(ctypes.byref(a), s))
+    device = target_probs.get_device()
+    _same_device(device, tokens, parents, uniforms, qo_indptr)
+    with _on(device, stream) as s:
+        acc, alen, aidx, lp = outputs or _chain_outputs(B, D + 1, target_probs.device, accept_index,
+                                                        logprobs)
+        a = TreeArgs(target_probs.data_ptr(), V, ld, B, rows, _int32("qo_indptr", qo_indptr, B + 1),
+                     _int32("tokens", tokens, *tokens.shape),
+                     _int32("parents", parents, *tokens.shape), uniforms.data_ptr(), D, 0,
+                     acc.data_ptr(), alen.data_ptr(), None if aidx is None else aidx.data_ptr(),
+                     None if lp is None else lp.data_ptr())
+        st = load().ts_tree_spec_sampling(a, s)
+        if st:
+            _check("ts_tree_spec_sampling", st)
     return dict(accepted_tokens=acc, accept_length=alen, accept_index=aidx, logprobs=lp)

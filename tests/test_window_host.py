@@ -70,6 +70,7 @@ BAD_CACHES = [
     (dict(num_pages=-1), "num_pages"), (dict(max_pages=-1), "max_pages"),
     (dict(max_pages=1 << 27, ld_table=1 << 27), "max_pages"), (dict(ld_table=3), "ld_table"),
     (dict(k=FAKE + 8), "aligned"), (dict(v_token_stride=100), "aligned"), (dict(k_head_stride=24), "aligned"),
+    (dict(k_page_stride=-16384), "positive"), (dict(v_head_stride=0), "positive"), (dict(k_token_stride=1 << 41), "positive"),
     (dict(k=None), "required"), (dict(v_scale=None), "required"), (dict(seq_lens=None), "required"),
     (dict(page_table=None), "required"),
 ]
