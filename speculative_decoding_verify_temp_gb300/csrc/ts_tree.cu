@@ -7,9 +7,11 @@
 // over the CTAs, whose warps sum contiguous runs of it; the sums meet through distributed
 // shared memory and the CTA that owns the crossing reads its run again (from L2).
 //
-// Sums: a lane adds its elements in fp32 with the rounding errors carried along (TwoSum), to
-// about 2^-48 of its sum, and everything above a lane is double. Doubles throughout would be
-// bound by the double-precision units, a sixty-fourth of the fp32 rate.
+// Sums are pairs of fp32 numbers (a value and the rounding errors carried along, Knuth's
+// TwoSum), good to about 2^-46: the double-precision units have about a sixtieth of the fp32
+// rate and several times its latency, and with them the scans and the search took longer than
+// the row's reading (33 us for 64 trees of vocabulary 128256). Only a node's test is formed in
+// double, a few operations a node.
 #include <stdint.h>
 
 #include <cooperative_groups.h>
@@ -27,33 +29,55 @@ constexpr int kTreeWarps = kTreeThreads / 32;
 constexpr int kTreeMaxCluster = 8;
 constexpr int kMarkBits = 2048;  // filter of the vectors that hold a removed token
 
+// A sum: h + l, |l| at most half a step of h.
+struct alignas(8) Sum {
+  float h, l;
+};
+
+__device__ __forceinline__ Sum operator+(Sum a, Sum b) {
+  const float s = __fadd_rn(a.h, b.h), z = __fsub_rn(s, a.h);
+  const float e = __fadd_rn(__fadd_rn(__fsub_rn(a.h, __fsub_rn(s, z)), __fsub_rn(b.h, z)), __fadd_rn(a.l, b.l));
+  const float h = __fadd_rn(s, e);
+  return {h, __fsub_rn(e, __fsub_rn(h, s))};
+}
+__device__ __forceinline__ Sum operator*(float u, Sum a) {
+  const float p = __fmul_rn(u, a.h), e = __fmaf_rn(u, a.h, -p);
+  return Sum{p, 0.f} + Sum{__fmaf_rn(u, a.l, e), 0.f};
+}
+__device__ __forceinline__ bool operator>(Sum a, Sum b) { return a.h > b.h || (a.h == b.h && a.l > b.l); }
+
+__device__ __forceinline__ Sum shuffle(Sum v, int from) {
+  return {__shfl_sync(0xffffffffu, v.h, from), __shfl_sync(0xffffffffu, v.l, from)};
+}
+
+__device__ __forceinline__ Sum warp_sum(Sum v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    v = v + Sum{__shfl_xor_sync(0xffffffffu, v.h, o), __shfl_xor_sync(0xffffffffu, v.l, o)};
+  return v;
+}
+
+// Sum over the lanes up to this one.
+__device__ __forceinline__ Sum warp_scan(Sum v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Sum t = {__shfl_up_sync(0xffffffffu, v.h, o), __shfl_up_sync(0xffffffffu, v.l, o)};
+    if (lane >= o) v = t + v;
+  }
+  return v;
+}
+
 struct TreeShared {
   int32_t parent[TS_MAX_WINDOW], token[TS_MAX_WINDOW], next[TS_MAX_WINDOW], path[TS_MAX_WINDOW + 1];
   double px[TS_MAX_WINDOW];
   int32_t removed[TS_MAX_WINDOW];
   int32_t n_removed, kept, limited;
   uint32_t mark[kMarkBits / 32];
-  double sums[kTreeMaxCluster * kTreeWarps];  // every warp's sum over the cluster
-  double mine[kTreeWarps];
-  double part[kTreeWarps];
+  Sum sums[kTreeMaxCluster * kTreeWarps];  // every warp's sum over the cluster
+  Sum mine[kTreeWarps];
+  Sum part[kTreeWarps];
   int32_t found;
 };
-
-__device__ __forceinline__ double warp_sum_f64(double v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// Inclusive sum over the lanes up to this one.
-__device__ __forceinline__ double warp_scan_f64(double v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double t = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += t;
-  }
-  return v;
-}
 
 // s + e += x, the error of s kept in e (Knuth's TwoSum).
 __device__ __forceinline__ void two_add(float& s, float& e, float x) {
@@ -63,7 +87,7 @@ __device__ __forceinline__ void two_add(float& s, float& e, float x) {
 }
 
 template <bool VEC>
-__global__ void __launch_bounds__(kTreeThreads) k_tree(ts_tree_args a) {
+__global__ void __launch_bounds__(kTreeThreads, 4) k_tree(ts_tree_args a) {
   __shared__ TreeShared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
@@ -104,23 +128,29 @@ __global__ void __launch_bounds__(kTreeThreads) k_tree(ts_tree_args a) {
     sh.px[tid] = real ? (double)a.target_probs[(row0 + p) * a.ld + x] : 0.0;
   }
   if (tid < kMarkBits / 32) sh.mark[tid] = 0;
-  const double u_last = (double)a.uniforms[row0];
+  const float u_last = a.uniforms[row0];
   __syncthreads();
 
   // 2. its test, if its earlier siblings were all rejected; a token that one of them holds
   // has no mass left
   const int my_parent = tid < n ? sh.parent[tid] : -1;
   bool again = false;
-  if (my_parent >= 0)
-    for (int j = 1; j < tid; ++j) again |= sh.parent[j] == my_parent && sh.token[j] == sh.token[tid];
+  uint64_t before = 0;  // its earlier siblings (bit j - 1: node j)
+  if (my_parent >= 0) {
+#pragma unroll 8
+    for (int j = 1; j < tid; ++j) {
+      const bool sibling = sh.parent[j] == my_parent;
+      before |= (uint64_t)sibling << (j - 1);
+      again |= sibling && sh.token[j] == sh.token[tid];
+    }
+  }
   __syncthreads();
   if (again) sh.px[tid] = 0.0;
   __syncthreads();
   bool test = false;
   if (my_parent >= 0) {
     double gone = 0.0;
-    for (int j = 1; j < tid; ++j)
-      if (sh.parent[j] == my_parent) gone += sh.px[j];
+    for (; before; before &= before - 1) gone += sh.px[__ffsll(before)];
     test = __dmul_rn((double)coin, 1.0 - gone) < sh.px[tid];
   }
   // the first sibling that passes: the lowest row wins
@@ -181,7 +211,8 @@ __global__ void __launch_bounds__(kTreeThreads) k_tree(ts_tree_args a) {
       for (int e = 0; e < 4; ++e)
         if ((int64_t)sh.removed[k] == v * 4 + e) x[e] = 0.f;
   };
-  double total = 0.0, w0 = 0.0, w1 = 0.0, upto = 0.0;
+  const Sum none = {0.f, 0.f};
+  Sum total = none, w0 = none, w1 = none, upto = none;
   for (int round = 0; round < 2; ++round) {
     const int64_t lo = min(vecs, (rank * (int64_t)kTreeWarps + warp) * per), hi = min(vecs, lo + per);
     float s[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
@@ -204,30 +235,28 @@ __global__ void __launch_bounds__(kTreeThreads) k_tree(ts_tree_args a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) two_add(s[i], e[i], x[i]);
     }
-    double mass = 0.0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) mass += (double)s[i] + (double)e[i];
-    mass = warp_sum_f64(mass);
+    const Sum mass = warp_sum((Sum{s[0], e[0]} + Sum{s[1], e[1]}) + (Sum{s[2], e[2]} + Sum{s[3], e[3]}));
     if (lane == 0) sh.mine[warp] = mass;
     cluster.sync();
     if (tid < runs) sh.sums[tid] = *cluster.map_shared_rank(&sh.mine[tid % kTreeWarps], tid / kTreeWarps);
     cluster.sync();  // all have read: the sums may be written again, or the CTA may leave
     // lane l of every warp: runs 2l and 2l + 1
-    w0 = 2 * lane < runs ? sh.sums[2 * lane] : 0.0;
-    w1 = 2 * lane + 1 < runs ? sh.sums[2 * lane + 1] : 0.0;
-    upto = warp_scan_f64(w0 + w1, lane);
-    total = __shfl_sync(0xffffffffu, upto, 31);
-    if (total > 0.0 || n_removed == 0) break;
+    w0 = 2 * lane < runs ? sh.sums[2 * lane] : none;
+    w1 = 2 * lane + 1 < runs ? sh.sums[2 * lane + 1] : none;
+    upto = warp_scan(w0 + w1, lane);
+    total = shuffle(upto, 31);
+    if (total.h > 0.f || n_removed == 0) break;
     n_removed = 0;  // nothing is left without the rejected children: draw from p itself
   }
 
   // 5. the run that holds the crossing (without one, by rounding or a coin of 1: the last
   // run that has mass)
-  const double want = __dmul_rn(u_last, total);
-  const double before1 = upto - w1, before0 = before1 - w0;
-  const unsigned cross0 = __ballot_sync(0xffffffffu, w0 > 0.0 && before0 + w0 > want);
-  const unsigned cross1 = __ballot_sync(0xffffffffu, w1 > 0.0 && upto > want);
-  const unsigned mass0 = __ballot_sync(0xffffffffu, w0 > 0.0), mass1 = __ballot_sync(0xffffffffu, w1 > 0.0);
+  const Sum want = u_last * total;
+  const Sum before0 = {__shfl_up_sync(0xffffffffu, upto.h, 1), __shfl_up_sync(0xffffffffu, upto.l, 1)};
+  const Sum below0 = lane ? before0 : none, below1 = below0 + w0;
+  const unsigned cross0 = __ballot_sync(0xffffffffu, w0.h > 0.f && below1 > want);
+  const unsigned cross1 = __ballot_sync(0xffffffffu, w1.h > 0.f && upto > want);
+  const unsigned mass0 = __ballot_sync(0xffffffffu, w0.h > 0.f), mass1 = __ballot_sync(0xffffffffu, w1.h > 0.f);
   int run = 0;
   if (cross0 | cross1) {
     const int l = __ffs(cross0 | cross1) - 1;
@@ -236,39 +265,40 @@ __global__ void __launch_bounds__(kTreeThreads) k_tree(ts_tree_args a) {
     const int l = 31 - __clz(mass0 | mass1);
     run = 2 * l + (mass1 >> l & 1u ? 1 : 0);
   }
-  const double below = __shfl_sync(0xffffffffu, run & 1 ? before1 : before0, run >> 1);
+  const Sum below = shuffle(run & 1 ? below1 : below0, run >> 1);
   if (run / kTreeWarps != rank) return;
 
   // 6. the crossing within the run: a contiguous piece a thread
   const int64_t lo = min(vecs, run * per), hi = min(vecs, lo + per);
   const int64_t piece = (hi - lo + kTreeThreads - 1) / kTreeThreads;
   const int64_t plo = min(hi, lo + tid * piece), phi = min(hi, plo + piece);
-  double mass = 0.0;
+  Sum mass = none;
   for (int64_t v = plo; v < phi; ++v) {
     float x[4];
     load(v, x);
     drop(v, x);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mass += (double)x[i];
+    for (int i = 0; i < 4; ++i) two_add(mass.h, mass.l, x[i]);
   }
-  const double in_warp = warp_scan_f64(mass, lane);
+  mass = none + mass;
+  const Sum in_warp = warp_scan(mass, lane);
   if (lane == 31) sh.part[warp] = in_warp;
   __syncthreads();
-  double base = below;
-#pragma unroll
-  for (int w = 0; w < kTreeWarps; ++w) base += w < warp ? sh.part[w] : 0.0;
-  base += in_warp - mass;
-  const bool cross = mass > 0.0 && base + mass > want;
+  Sum base = below;  // the mass before this thread's piece
+  for (int w = 0; w < warp; ++w) base = base + sh.part[w];
+  const Sum lanes = {__shfl_up_sync(0xffffffffu, in_warp.h, 1), __shfl_up_sync(0xffffffffu, in_warp.l, 1)};
+  if (lane) base = base + lanes;
+  const bool cross = mass.h > 0.f && base + mass > want;
   // the first piece that crosses; else the last one with mass
   const int first = __syncthreads_or(cross);
-  if (first ? cross : mass > 0.0) {
+  if (first ? cross : mass.h > 0.f) {
     if (first) atomicMin(reinterpret_cast<uint32_t*>(&sh.found), (uint32_t)tid);
     else atomicMax(&sh.found, tid);
   }
   __syncthreads();
   if (sh.found < 0 ? tid == 0 : tid == sh.found) {
     int64_t token = a.vocab - 1;
-    double acc = base;
+    Sum acc = base;
     bool done = sh.found < 0;
     for (int64_t v = plo; v < phi && !done; ++v) {
       float x[4];
@@ -276,7 +306,7 @@ __global__ void __launch_bounds__(kTreeThreads) k_tree(ts_tree_args a) {
       drop(v, x);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        acc += (double)x[i];
+        acc = acc + Sum{x[i], 0.f};
         if (!done && x[i] > 0.f) {
           token = v * 4 + i;
           done = acc > want;
