@@ -356,7 +356,8 @@ typedef struct ts_attn_args {
                                 (bytes, multiples of 16): head_dim values of `dtype` */
   int64_t q_row_stride, q_head_stride;
   int32_t dtype;             /* TS_BF16 or TS_F16: q, k_new, v_new and out */
-  int32_t heads_q;           /* a multiple of cache->heads; head h reads KV head
+  int32_t heads_q;           /* a multiple of cache->heads, at most 65536 (total_rows *
+                                heads_q below 2^31); head h reads KV head
                                 h / (heads_q / heads) */
   const void* k_new;         /* the window's own K and V, one row for each row of q, laid out
                                 like q with `heads` heads; both NULL: cached tokens only */
@@ -367,7 +368,8 @@ typedef struct ts_attn_args {
                                 qo_indptr[b+1] - 1, at most TS_MAX_WINDOW; NULL: total_rows /
                                 batch rows each. A window that does not fit is skipped (its
                                 outputs are left as they were), as are rows that no window
-                                owns */
+                                owns. Must not decrease from the second entry on (rows of
+                                windows behind a fall: unspecified values) */
   const int32_t* parents;    /* [total_rows] or NULL. NULL: row t of a window sees its own
                                 rows 0..t. Else the window is a tree: row t sees itself and
                                 its ancestors; parents[r] is the window row of r's parent,
@@ -382,9 +384,12 @@ typedef struct ts_attn_args {
  * out = sum_i softmax(score)_i v_i. A row that sees no token gives 0 and lse -inf. Tokens
  * that a row does not see have no effect on it, whatever they hold.
  * Scores, softmax statistics and sums are fp32; cached K and V enter the products as they
- * are, q relative to its row's largest value and the probabilities in 11 significant bits.
- * Scales of V below 2^-100 count as 2^-100. Workspace: ts_attention_workspace_size bytes
- * of scratch (no zero fill needed). */
+ * are. q is good to 2^-17 of the largest |q| that shares its row block (up to 64 rows of the
+ * query heads of a KV head; exact where it is above 2^-9 of it), probabilities to 2^-11, or
+ * to 2^-7 for bf16 with head_dim 128 and more than 32 rows of a KV head a window on average
+ * (total_rows * heads_q / heads > 32 * batch). Scales of V below 2^-100 count as 2^-100.
+ * Workspace: ts_attention_workspace_size bytes of scratch (no zero fill needed) that no other
+ * call uses meanwhile. */
 ts_status ts_window_attention(const ts_attn_args* args, void* workspace, size_t ws_bytes,
                               cudaStream_t stream);
 size_t ts_attention_workspace_size(int64_t batch, int64_t total_rows, int32_t heads_q,
@@ -415,8 +420,9 @@ typedef struct ts_kv_append_args {
  * earlier tokens' codes are rounded again to the new scale. Codes are code = e4m3(x / scale),
  * to nearest, ties to even, saturating (infinities too; NaN stays NaN). Row numbers outside
  * [0, total_rows) and a qo_indptr pair that does not fit store nothing (their positions are
- * left as they were), nor does a position past the page table. No two requests may store to
- * the same page in one call, and a page that is stored to must not be read meanwhile. */
+ * left as they were), nor does a position past the page table. No two entries of the page
+ * tables that are stored to in one call may name the same page, and a page that is stored to
+ * must not be read meanwhile. */
 ts_status ts_kv_append(const ts_kv_append_args* args, cudaStream_t stream);
 
 typedef struct ts_kv_read_args {

@@ -91,6 +91,8 @@ bool multiple16(const void* p, int64_t a, int64_t b) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && a % 16 == 0 && b % 16 == 0;
 }
 
+constexpr int32_t kMaxHeadsQ = 1 << 16;
+
 // The calls on a KV cache.
 ts_status check_cache(const ts_kv_cache* c) {
   if (!c) return fail(TS_ERR_INVALID_ARG, "cache is NULL");
@@ -662,11 +664,12 @@ ts_status ts_window_attention(const ts_attn_args* p, void* workspace, size_t ws_
   const ts_kv_cache& c = *p->cache;
   if (p->dtype != TS_BF16 && p->dtype != TS_F16)
     return fail(TS_ERR_UNSUPPORTED_DTYPE, "attention takes bf16 or fp16, not dtype %d", p->dtype);
-  if (p->heads_q < 1 || p->heads_q % c.heads)
-    return fail(TS_ERR_INVALID_ARG, "heads_q (%d) must be a multiple of the cache's %d heads", p->heads_q, c.heads);
+  if (p->heads_q < 1 || p->heads_q > kMaxHeadsQ || p->heads_q % c.heads)
+    return fail(TS_ERR_INVALID_ARG, "heads_q (%d) must be a multiple of the cache's %d heads, at most %d", p->heads_q,
+                c.heads, kMaxHeadsQ);
   if ((st = check_window(p->qo_indptr, p->total_rows, c.batch)) != TS_OK) return st;
-  if (p->total_rows * (int64_t)p->heads_q > (int64_t)1 << 31)
-    return fail(TS_ERR_INVALID_ARG, "total_rows * heads_q is above 2^31");
+  if (p->total_rows * (int64_t)p->heads_q >= (int64_t)1 << 31)
+    return fail(TS_ERR_INVALID_ARG, "total_rows * heads_q must be below 2^31");
   if (!p->q || !p->out || (p->k_new == nullptr) != (p->v_new == nullptr))
     return fail(TS_ERR_INVALID_ARG, "q and out are required, k_new and v_new come together");
   if (p->parents && !p->k_new)
@@ -684,7 +687,7 @@ ts_status ts_window_attention(const ts_attn_args* p, void* workspace, size_t ws_
 size_t ts_attention_workspace_size(int64_t batch, int64_t total_rows, int32_t heads_q,
                                    int32_t heads, int32_t head_dim) {
   if (batch < 1 || batch > 1 << 16 || total_rows < 1 || total_rows > batch * TS_MAX_WINDOW || heads < 1 ||
-      heads_q < 1 || heads_q % heads || (head_dim != 64 && head_dim != 128))
+      heads_q < 1 || heads_q > kMaxHeadsQ || heads_q % heads || (head_dim != 64 && head_dim != 128))
     return 0;
   return tsv::window_workspace(batch, total_rows, heads_q, heads, head_dim, sm_count());
 }
@@ -706,7 +709,7 @@ ts_status ts_kv_append(const ts_kv_append_args* p, cudaStream_t stream) {
     return fail(TS_ERR_INVALID_ARG, "total_rows must be a multiple of batch without src_index and qo_indptr");
   if (!multiple16(p->k, p->k_row_stride, p->k_head_stride) || !multiple16(p->v, p->v_row_stride, p->v_head_stride))
     return fail(TS_ERR_INVALID_ARG, "k and v need 16-byte aligned addresses and strides");
-  return launched(tsv::launch_kv_append(c, *p, sm_count(), stream), "cache append launch");
+  return launched(tsv::launch_kv_append(c, *p, stream), "cache append launch");
 }
 
 ts_status ts_kv_read(const ts_kv_read_args* p, cudaStream_t stream) {
@@ -720,7 +723,7 @@ ts_status ts_kv_read(const ts_kv_read_args* p, cudaStream_t stream) {
     return fail(TS_ERR_INVALID_ARG, "total_rows must be in [1, 2^30]");
   if (!multiple16(p->k_out, 0, 0) || !multiple16(p->v_out, 0, 0))
     return fail(TS_ERR_INVALID_ARG, "k_out and v_out must be 16-byte aligned");
-  return launched(tsv::launch_kv_read(*p->cache, *p, stream), "cache read launch");
+  return launched(tsv::launch_kv_read(*p->cache, *p, sm_count(), stream), "cache read launch");
 }
 
 ts_status ts_tree_spec_sampling(const ts_tree_args* p, cudaStream_t stream) {

@@ -266,8 +266,8 @@ size_t window_workspace(int64_t batch, int64_t total_rows, int heads_q, int head
 cudaError_t window_read_error(uint32_t* word, int clear);
 struct WindowParams;
 cudaError_t launch_window_tc(const WindowParams& p, int rows, int sms, cudaStream_t s);  // head_dim 128
-cudaError_t launch_kv_append(const ts_kv_cache& c, const ts_kv_append_args& a, int sms, cudaStream_t s);
-cudaError_t launch_kv_read(const ts_kv_cache& c, const ts_kv_read_args& a, cudaStream_t s);
+cudaError_t launch_kv_append(const ts_kv_cache& c, const ts_kv_append_args& a, cudaStream_t s);
+cudaError_t launch_kv_read(const ts_kv_cache& c, const ts_kv_read_args& a, int sms, cudaStream_t s);
 cudaError_t launch_tree(const ts_tree_args& a, int sms, cudaStream_t s);
 
 }  // namespace tsv

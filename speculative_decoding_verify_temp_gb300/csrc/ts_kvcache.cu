@@ -1,7 +1,7 @@
 // The 8-bit KV cache: quantising rows as they are written and reading them back.
 //
 //   k_kv_append  one CTA a block (a page of one head of K or V) that the call touches
-//   k_kv_read    one CTA for 16 consecutive output rows, all heads
+//   k_kv_read    one CTA for 16 (or 4) consecutive output rows, all heads
 //
 // A block's scale is a power of two, so that dividing by it is exact: the code is the
 // element's own significand rounded to four bits, and rounding the block again to a larger
@@ -22,7 +22,7 @@ namespace {
 
 constexpr int kAppendThreads = 128;
 constexpr int kReadThreads = 256;
-constexpr int kReadRows = 16;
+constexpr int kReadRows = 16;  // most rows of a CTA
 
 // Eight elements of a row: as they lie in memory, and widened to fp32 (exact).
 template <typename T>
@@ -94,7 +94,8 @@ __device__ __forceinline__ Rows rows_of(const ts_kv_append_args& a, int64_t batc
 // a thousand elements of a block: a thread holds N times eight of them in registers between the
 // maximum and the codes, with all loads in flight at once. Bound: HBM for prompts (24 k rows of
 // 8 heads of 128, 147 MB of traffic); for the few rows after a verify step, the chain of
-// dependent loads seq_len -> page -> rows.
+// dependent loads seq_len -> page -> rows (128 windows: 8 us). The prompts' 24 k rows take 34 us, 4.3
+// TB/s (64 when the rows were read twice).
 template <typename T, int D, int N>
 __global__ void __launch_bounds__(kAppendThreads) k_kv_append(ts_kv_cache c, ts_kv_append_args a, int32_t step) {
   constexpr int per_row = D / 8, n = N * kAppendThreads * 8 / D;  // n: page_size
@@ -222,14 +223,15 @@ __device__ __forceinline__ void store16<__half>(void* p, const float* x) {
   store16_half<__half2>(p, x, [](float u, float v) { return __floats2half2_rn(u, v); });
 }
 
-// One CTA: kReadRows output rows, whose request and page one thread each looks up; then 16
-// codes a thread. Bound: HBM (the writes are two to four times the reads).
+// One CTA: n output rows, whose request and page one thread each looks up; then 16
+// codes a thread. Bound: HBM (the writes are two to four times the reads): 67 us for 62 k tokens of 8
+// heads of 128 to bf16, 5.7 TB/s.
 template <typename T>
-__global__ void __launch_bounds__(kReadThreads) k_kv_read(ts_kv_cache c, ts_kv_read_args a) {
+__global__ void __launch_bounds__(kReadThreads) k_kv_read(ts_kv_cache c, ts_kv_read_args a, int n) {
   __shared__ int64_t s_page[kReadRows];  // -1: zeros, -2: no row
   __shared__ int32_t s_slot[kReadRows];
-  const int64_t r0 = (int64_t)blockIdx.x * kReadRows;
-  if (threadIdx.x < kReadRows) {
+  const int64_t r0 = (int64_t)blockIdx.x * n;
+  if (threadIdx.x < n) {
     const int64_t r = r0 + threadIdx.x;
     int64_t page = -2;
     int32_t slot = 0;
@@ -256,7 +258,7 @@ __global__ void __launch_bounds__(kReadThreads) k_kv_read(ts_kv_cache c, ts_kv_r
   }
   __syncthreads();
   const int D = c.head_dim, parts = D / 16;
-  const int per_row = c.heads * parts, all = kReadRows * per_row;
+  const int per_row = c.heads * parts, all = n * per_row;
   constexpr int kAtOnce = 4;  // steps whose loads are in flight together
   for (int i0 = threadIdx.x; i0 < all; i0 += kAtOnce * kReadThreads) {
     uint4 kw[kAtOnce], vw[kAtOnce];
@@ -310,14 +312,13 @@ cudaError_t by_dtype(int32_t dt, F f) {
 
 }  // namespace
 
-cudaError_t launch_kv_append(const ts_kv_cache& c, const ts_kv_append_args& a, int sms, cudaStream_t s) {
+cudaError_t launch_kv_append(const ts_kv_cache& c, const ts_kv_append_args& a, cudaStream_t s) {
   const int64_t units = c.batch * c.heads * 2;
-  // CTAs a unit: the blocks an average request touches (a unit strides over the rest), at
-  // least 2 (a window that crosses a page), no more than fill the GPU twice over
+  // CTAs a unit: the blocks an average request touches (a unit strides over the rest: 24 k rows in
+  // 34 us, 158 with 2 CTAs a unit), at least 2 (a window that crosses a page)
   const int64_t rows = a.src_index ? a.ld_src : (a.total_rows + c.batch - 1) / c.batch;
   const int64_t want = (rows + c.page_size - 1) / c.page_size + 1;
-  const int64_t fill = ((int64_t)sms * 32 + units - 1) / units;
-  const int64_t step = std::max<int64_t>(2, std::min(want, fill));
+  const int64_t step = std::max<int64_t>(2, std::min(want, ((int64_t)1 << 30) / units));
   const int n = c.page_size * c.head_dim / (kAppendThreads * 8);
   return by_dtype(a.dtype, [&](auto t) {
     auto go = [&](auto kernel) { kernel<<<(unsigned)(units * step), kAppendThreads, 0, s>>>(c, a, (int32_t)step); };
@@ -336,9 +337,12 @@ cudaError_t launch_kv_append(const ts_kv_cache& c, const ts_kv_append_args& a, i
   });
 }
 
-cudaError_t launch_kv_read(const ts_kv_cache& c, const ts_kv_read_args& a, cudaStream_t s) {
-  const int64_t grid = (a.total_rows + kReadRows - 1) / kReadRows;
-  return by_dtype(a.dtype, [&](auto t) { k_kv_read<decltype(t)><<<(unsigned)grid, kReadThreads, 0, s>>>(c, a); });
+cudaError_t launch_kv_read(const ts_kv_cache& c, const ts_kv_read_args& a, int sms, cudaStream_t s) {
+  // few rows are spread further: 300 rows of 2 heads of 64 in 3.5 us, 4.2 with 16; more CTAs than run at
+  // once only repeat the lookup (62 k rows of 8 heads of 128: 67 us with 16 rows, 72 with 8)
+  const int n = a.total_rows * c.heads * c.head_dim < (int64_t)sms * kReadThreads * 64 ? 4 : kReadRows;
+  const int64_t grid = (a.total_rows + n - 1) / n;
+  return by_dtype(a.dtype, [&](auto t) { k_kv_read<decltype(t)><<<(unsigned)grid, kReadThreads, 0, s>>>(c, a, n); });
 }
 
 }  // namespace tsv

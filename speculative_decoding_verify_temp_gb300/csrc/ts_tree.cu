@@ -10,8 +10,8 @@
 // Sums are pairs of fp32 numbers (a value and the rounding errors carried along, Knuth's
 // TwoSum), good to about 2^-46: the double-precision units have about a sixtieth of the fp32
 // rate and several times its latency, and with them the scans and the search took longer than
-// the row's reading (33 us for 64 trees of vocabulary 128256). Only a node's test is formed in
-// double, a few operations a node.
+// the row's reading (33 us for 64 trees of vocabulary 128256, 18 now; 256 trees of 151936: 43 us,
+// 3.6 TB/s). Only a node's test is formed in double, a few operations a node.
 #include <stdint.h>
 
 #include <cooperative_groups.h>
@@ -27,6 +27,7 @@ namespace {
 constexpr int kTreeThreads = 256;
 constexpr int kTreeWarps = kTreeThreads / 32;
 constexpr int kTreeMaxCluster = 8;
+constexpr int kTreeCtasPerSm = 4;
 constexpr int kMarkBits = 2048;  // filter of the vectors that hold a removed token
 
 // A sum: h + l, |l| at most half a step of h.
@@ -87,7 +88,7 @@ __device__ __forceinline__ void two_add(float& s, float& e, float x) {
 }
 
 template <bool VEC>
-__global__ void __launch_bounds__(kTreeThreads, 4) k_tree(ts_tree_args a) {
+__global__ void __launch_bounds__(kTreeThreads, kTreeCtasPerSm) k_tree(ts_tree_args a) {
   __shared__ TreeShared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
@@ -330,9 +331,10 @@ __global__ void __launch_bounds__(kTreeThreads, 4) k_tree(ts_tree_args a) {
 }  // namespace
 
 cudaError_t launch_tree(const ts_tree_args& a, int sms, cudaStream_t s) {
-  // CTAs a request: enough to fill the GPU a few times over, runs of 16 vectors a lane or more
+  // CTAs a request: as many as run at once (256 trees of vocabulary 151936: 43 us with 2, 46
+  // with 4 CTAs each; 64 of 128256: 18 us with 8, 27 with 2), runs of 16 vectors a lane or more
   int ranks = 1;
-  while (ranks < kTreeMaxCluster && a.batch * ranks < (int64_t)sms * 4 &&
+  while (ranks < kTreeMaxCluster && a.batch * ranks * 2 <= (int64_t)sms * kTreeCtasPerSm &&
          a.vocab > (int64_t)ranks * kTreeThreads * 4 * 4)
     ranks *= 2;
   cudaLaunchConfig_t cfg = {};

@@ -563,12 +563,14 @@ def _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens):
             (page_table.shape[1] > 1 and page_table.stride(1) != 1):
         raise ValueError("page_table must be a 2-D int32 tensor with unit stride in the last dimension")
     B, P = page_table.shape
+    ld = page_table.stride(0) if B > 1 and P > 0 else P
+    if ld < P:
+        raise ValueError("the rows of page_table must not overlap")
     device = k_cache.get_device()
     _same_device(device, v_cache, k_scale, v_scale, page_table, seq_lens)
     return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), k0, k1, k2, v0, v1, v2,
                    k_scale.data_ptr(), v_scale.data_ptr(), n, H, D, size, P, page_table.data_ptr(),
-                   max(page_table.stride(0), P) if B > 1 else P, _int32("seq_lens", seq_lens, B),
-                   B), device
+                   ld, _int32("seq_lens", seq_lens, B), B), device
 
 
 def _heads(name, t, heads, D):
@@ -629,6 +631,8 @@ def window_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens
         if workspace is None:
             workspace = torch.empty(attention_workspace_size(B, rows, Hq, H, D),
                                     dtype=torch.uint8, device=q.device)
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
         a = AttnArgs(ctypes.pointer(c), q.data_ptr(), qr, qh, _kv_dtype(q.dtype), Hq, k_ptr, v_ptr,
                      kr, kh, vr, vh, rows, _int32("qo_indptr", qo_indptr, B + 1),
                      _int32("parents", parents, rows), D ** -0.5 if sm_scale is None else sm_scale,
@@ -711,11 +715,16 @@ def tree_spec_sampling(target_probs, D: int, tokens, parents, uniforms, *, qo_in
     with _on(device, stream) as s:
         acc, alen, aidx, lp = outputs or _chain_outputs(B, D + 1, target_probs.device, accept_index,
                                                         logprobs)
+        if outputs:
+            _same_device(device, acc, alen, aidx, lp)
+            if lp is not None and (lp.dtype != torch.float32 or lp.shape != (B, D + 1) or
+                                   not lp.is_contiguous()):
+                raise ValueError(f"logprobs must be a contiguous fp32 tensor of shape ({B}, {D + 1})")
         a = TreeArgs(target_probs.data_ptr(), V, ld, B, rows, _int32("qo_indptr", qo_indptr, B + 1),
                      _int32("tokens", tokens, *tokens.shape),
                      _int32("parents", parents, *tokens.shape), uniforms.data_ptr(), D, 0,
-                     acc.data_ptr(), alen.data_ptr(), None if aidx is None else aidx.data_ptr(),
-                     None if lp is None else lp.data_ptr())
+                     _int32("accepted_tokens", acc, B, D + 1), _int32("accept_length", alen, B),
+                     _int32("accept_index", aidx, B, D + 1), None if lp is None else lp.data_ptr())
         st = load().ts_tree_spec_sampling(a, s)
         if st:
             _check("ts_tree_spec_sampling", st)

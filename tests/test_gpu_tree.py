@@ -187,3 +187,14 @@ def test_streams_and_graph():
     torch.cuda.synchronize()
     for n in want:
         assert torch.equal(got[n], want[n]) and torch.equal(captured[n], want[n])
+
+
+def test_outputs_that_do_not_fit_are_refused():
+    s, _ = make(10, [5] * 3, 100)
+    new = lambda *shape: torch.empty(shape, dtype=torch.int32).cuda()  # noqa: E731
+    good = [new(3, 5), new(3), new(3, 5), torch.empty((3, 5)).cuda()]
+    tv.tree_spec_sampling(D=4, **s, outputs=good)
+    for i, bad in ((0, new(3, 4)), (1, new(2)), (2, new(5, 3).t()), (3, torch.empty((3, 4)).cuda()),
+                   (0, new(3, 5).long()), (3, new(3, 5)), (1, torch.empty(3, dtype=torch.int32))):
+        with pytest.raises(ValueError):
+            tv.tree_spec_sampling(D=4, **s, outputs=good[:i] + [bad] + good[i + 1:])

@@ -200,3 +200,18 @@ def test_binding_refuses_bad_rows():
         tv.tree_spec_sampling(p, 1, i, i, torch.zeros((2, 3)))
     with pytest.raises(TypeError):
         tv.tree_spec_sampling(p.half(), 1, i, i, torch.zeros((2, 2)))
+
+
+def test_binding_refuses_overlapping_page_tables():
+    # requests that share a prefix have tables of their own that name the same pages
+    c = replaced(4, torch.zeros((1, 2), dtype=torch.int32).expand(2, 2))
+    x = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
+    for call in (lambda: tv.kv_append(x, x, *c), lambda: tv.window_attention(x, *c),
+                 lambda: tv.kv_read(*c, out_indptr=torch.zeros(3, dtype=torch.int32), total_rows=4)):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+
+
+def test_attention_refuses_heads_past_its_indices(lib):
+    refused(lib, "ts_window_attention", attn(heads_q=1 << 17), "multiple", 1)
+    assert lib.ts_attention_workspace_size(2, 6, 1 << 17, 8, 128) == 0
