@@ -1,8 +1,10 @@
-// Attention of drafted windows over the 8-bit paged KV cache and over themselves.
+// Attention of drafted windows over the 8-bit paged KV cache and over themselves: the workspace,
+// and the kernels for head_dim 64 (128: ts_window_tc.cu).
 //
-//   k_window   the (request, KV head, row block) units cut into tiles of 64 tokens; the tiles
-//              of the whole call lie in one line that the CTAs share equally
-//   k_join     joins the pieces of units that more than one CTA worked on
+//   k_window_own  the window's own tokens, for every row
+//   k_window      the cached tokens: the (request, KV head, row block) units cut into tiles of 64
+//                 tokens; the tiles of the whole call lie in one line that the CTAs share equally
+//   k_join        joins the pieces of units that more than one CTA worked on
 //
 // A unit's rows are the window rows of the query heads that share a KV head. Each of a CTA's
 // four warps takes 16 tokens of a tile (they lie in one block, so K and V have one scale each)
@@ -37,9 +39,9 @@ constexpr int kMinTiles = 4;      // least tiles a CTA takes: pieces of 256 toke
 
 using Params = WindowParams;
 
-template <int D, int MT, typename T>
+template <int MT, typename T>
 __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Params p) {
-  constexpr int ROWS = 16 * MT;
+  constexpr int D = 64, ROWS = 16 * MT;
   constexpr int KS = D / 16;        // k16 steps over the dims
   constexpr int NT = D / 8;         // n8 tiles over the dims
   constexpr int VW = D / 32;        // words of a token's V codes a lane holds
@@ -70,21 +72,13 @@ __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Par
 
     // ---- Q: row i of the unit is window row (block*ROWS + i) / group of head kvh*group +
     // the remainder. Each row's factor, then the fragments.
-    auto q_row = [&](int i) -> const char* {
-      const int j = block * ROWS + i;
-      return static_cast<const char*>(p.a.q) + (r.row0 + j / p.group) * p.a.q_row_stride +
-             (int64_t)(kvh * p.group + j % p.group) * p.a.q_head_stride;
-    };
     __syncthreads();  // the previous unit's reads of shared memory are done
     for (int i = warp; i < ROWS; i += kWarps) {
       float top = 0.f;
       if (i < rows) {
-        const uint32_t* q = reinterpret_cast<const uint32_t*>(q_row(i));
-#pragma unroll
-        for (int k = 0; k < D / 64; ++k) {
-          const float2 f = unpack<T>(q[lane + 32 * k]);
-          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(q_row(p, sg, ROWS, i));
+        const float2 f = unpack<T>(q[lane]);
+        top = fmaxf(fabsf(f.x), fabsf(f.y));
       }
       top = warp_max(top);
       // 2^e <= top < 2^(e+1); the row is divided by 2^e
@@ -94,8 +88,8 @@ __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Par
     __syncthreads();
     for (int i = tid; i < MT * KS * 32; i += kThreads) {
       const int l = i & 31, ks = i / 32 % KS, mt = i / 32 / KS, qc = l & 3, qg = l >> 2;
-      // K's lane qc holds dims 64h + 16qc .. + 15; step 4h + k takes dims 4k .. 4k + 3 of them
-      const int dim = (ks / 4) * 64 + qc * 16 + (ks % 4) * 4;
+      // K's lane qc holds dims 16qc .. + 15; step k takes dims 4k .. 4k + 3 of them
+      const int dim = qc * 16 + ks * 4;
       uint32_t w[4];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -103,7 +97,7 @@ __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Par
         uint2 x = make_uint2(0, 0);
         float inv = 1.f;
         if (row < rows) {
-          x = *reinterpret_cast<const uint2*>(q_row(row) + dim * 2);
+          x = *reinterpret_cast<const uint2*>(q_row(p, sg, ROWS, row) + dim * 2);
           inv = __uint_as_float(0x7F000000u - __float_as_uint(s_fac[row]));  // 1 / 2^e
         }
         const float2 u = unpack<T>(x.x), v = unpack<T>(x.y);
@@ -183,7 +177,7 @@ __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Par
     const char* vc = static_cast<const char*>(p.c.v) + kvh * p.c.v_head_stride;
     const int32_t* table = p.c.page_table + sg.b * p.c.ld_table;
     struct Loaded {
-      uint4 k[2][D / 64];
+      uint4 k[2];
       uint32_t v[4][VW];
       float ks, vs;
     };
@@ -200,21 +194,15 @@ __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Par
       for (int n = 0; n < 2; ++n) {
         const bool ok = page >= 0 && tok + n * 8 + g < r.len;
         const char* at = kc + page * p.c.k_page_stride + (int64_t)(slot + n * 8 + g) * p.c.k_token_stride + c * 16;
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) x.k[n][h] = ok ? ldg_stream(at + h * 64) : make_uint4(0, 0, 0, 0);
+        x.k[n] = ok ? ldg_stream(at) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int tt = 2 * c + (i & 1) + (i >> 1) * 8;
         const bool ok = page >= 0 && tok + tt < r.len;
         const char* at = vc + page * p.c.v_page_stride + (int64_t)(slot + tt) * p.c.v_token_stride + g * (D / 8);
-        if constexpr (VW == 4) {
-          const uint4 w = ok ? ldg_stream(at) : make_uint4(0, 0, 0, 0);
-          x.v[i][0] = w.x, x.v[i][1] = w.y, x.v[i][2] = w.z, x.v[i][3] = w.w;
-        } else {
-          const uint2 w = ok ? __ldg(reinterpret_cast<const uint2*>(at)) : make_uint2(0, 0);
-          x.v[i][0] = w.x, x.v[i][1] = w.y;
-        }
+        const uint2 w = ok ? __ldg(reinterpret_cast<const uint2*>(at)) : make_uint2(0, 0);
+        x.v[i][0] = w.x, x.v[i][1] = w.y;
       }
       x.ks = x.vs = 1.f;
       if (page >= 0) {
@@ -245,8 +233,8 @@ __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Par
         uint32_t kb[2][2];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const uint4 w4 = now.k[n][ks / 4];
-          const uint32_t w = ks % 4 == 0 ? w4.x : ks % 4 == 1 ? w4.y : ks % 4 == 2 ? w4.z : w4.w;
+          const uint4 w4 = now.k[n];
+          const uint32_t w = ks == 0 ? w4.x : ks == 1 ? w4.y : ks == 2 ? w4.z : w4.w;
           kb[n][0] = e4m3x2_to_f16x2((uint16_t)w);
           kb[n][1] = e4m3x2_to_f16x2((uint16_t)(w >> 16));
         }
@@ -372,17 +360,17 @@ constexpr int smem_bytes(int D, int rows) {
   return rows / 16 * (D / 16) * 32 * 16 + rows * 4 + kWarps * rows * (D + 4) * 4 + kWarps * rows * 8;
 }
 
-template <int D, int MT, typename T>
+template <int MT, typename T>
 cudaError_t launch(const Params& p, int sms, cudaStream_t s) {
-  constexpr int ROWS = 16 * MT, bytes = smem_bytes(D, ROWS);
-  cudaError_t e = allow_smem<k_window<D, MT, T>>(bytes);
+  constexpr int D = 64, ROWS = 16 * MT, bytes = smem_bytes(D, ROWS);
+  cudaError_t e = allow_smem<k_window<MT, T>>(bytes);
   if (e != cudaSuccess) return e;
   const int grid = sms * kCtasPerSm;
   if (p.a.k_new) {
     if ((e = launch_own<D, ROWS, T>(p, s)) != cudaSuccess) return e;
-    e = launch_after(k_window<D, MT, T>, dim3(grid), kThreads, bytes, s, p);
+    e = launch_after(k_window<MT, T>, dim3(grid), kThreads, bytes, s, p);
   } else {
-    k_window<D, MT, T><<<grid, kThreads, bytes, s>>>(p);
+    k_window<MT, T><<<grid, kThreads, bytes, s>>>(p);
     e = cudaGetLastError();
   }
   // units of one tile are never split
@@ -393,12 +381,14 @@ cudaError_t launch(const Params& p, int sms, cudaStream_t s) {
 template <int MT>
 cudaError_t launch_mt(const Params& p, int sms, cudaStream_t s) {
   const bool bf16 = p.a.dtype == TS_BF16;
-  return bf16 ? launch<64, MT, __nv_bfloat16>(p, sms, s) : launch<64, MT, __half>(p, sms, s);
+  return bf16 ? launch<MT, __nv_bfloat16>(p, sms, s) : launch<MT, __half>(p, sms, s);
 }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// The rows of a block: by the average window.
+// The rows of a block: by the average window. head_dim 128, ragged chains of 4 to 20 rows: 162 us
+// with 32, 189 with 64; trees of 256 rows: 416 with 32, 330 with 64. head_dim 64, one row of 4
+// heads over 37 tokens: 9.7 us with 16, 11.1 with 32.
 int block_rows(const WindowParams& p) {
   const int64_t rows = (p.a.total_rows * p.group + p.c.batch - 1) / p.c.batch;
   if (p.c.head_dim == 128) return rows <= 32 ? 32 : 64;

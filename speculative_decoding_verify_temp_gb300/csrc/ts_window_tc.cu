@@ -19,8 +19,8 @@
 // 2^-20, where the row's largest p is between 2^4 and 2^8. bf16 calls with blocks of 64 rows take
 // two parts (their output has 8 bits): e4m3, and e5m2 for the rest times 2^12: 7 bits and half a
 // step, down to 2^-24. The columns of TMEM that this leaves are second buffers of S, so that the
-// first products run a whole round of turns ahead: 330 us against 392 for 16 trees of 32 nodes
-// over 8191 tokens. Blocks of 32 rows have four turns, and the three parts of one type go
+// first products run a whole round of turns ahead: 331 us against 392 for 16 trees of 32 nodes
+// over 8191 tokens (317 now). Blocks of 32 rows have four turns, and the three parts of one type go
 // through one instruction (222 clocks a tile against 384 for two types).
 //
 // A softmax thread is a token: it reads its row of S^T from TMEM, the scales of its block and
@@ -334,9 +334,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t i = 0, u = 0;
 #pragma unroll 1
       while (line.next(p, s)) {
+#pragma unroll 1
+        for (int r = lane >> 1; r < s.rows; r += 16)  // on its way while the unit before is worked on
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q_row(p, s, ROWS, r) + (lane & 1) * 128));
         wait(&x.q_empty, (u & 1) ^ 1, &x.stop);
         __syncwarp();
-        const float scale = split_q<ROWS, QP, T>(p, s, s_q);
+        const float scale = split_q<ROWS, QP, T>(p, s, q_exponent<ROWS, T>(p, s), s_q);
         if (lane == 0) x.q_scale = scale;
         fence_async_shared();
         __syncwarp();
