@@ -388,11 +388,15 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // The rows of a block: by the average window. head_dim 128, ragged chains of 4 to 20 rows: 162 us
 // with 32, 189 with 64; trees of 256 rows: 416 with 32, 330 with 64. head_dim 64, one row of 4
-// heads over 37 tokens: 9.7 us with 16, 11.1 with 32.
+// heads over 37 tokens: 9.7 us with 16, 11.1 with 32; 62 windows of 176 rows with 8 heads of 4495
+// tokens: 559 us with 64 (K and V are converted once a block), 685 with 32; but 9 windows of 232
+// rows with 2 heads of 2569 tokens, too few units for 64 rows: 52 and 41. In between by the room
+// in the page tables (426 k tokens of all heads: 129 and 130).
 int block_rows(const WindowParams& p) {
   const int64_t rows = (p.a.total_rows * p.group + p.c.batch - 1) / p.c.batch;
   if (p.c.head_dim == 128) return rows <= 32 ? 32 : 64;
-  return rows <= 16 ? 16 : 32;
+  const int64_t room = p.c.batch * p.c.heads * p.c.max_pages * p.c.page_size;
+  return rows <= 16 ? 16 : rows <= 32 || room < 1 << 19 ? 32 : 64;
 }
 
 // Lays the workspace out; returns its bytes.
@@ -421,6 +425,8 @@ size_t window_workspace(int64_t batch, int64_t total_rows, int heads_q, int head
   p.c.batch = batch;
   p.c.heads = heads;
   p.c.head_dim = head_dim;
+  p.c.max_pages = 1 << 30;  // as large a room as a call can have: its blocks need the most
+  p.c.page_size = 1;
   p.a.total_rows = total_rows;
   p.a.heads_q = heads_q;
   p.group = heads_q / heads;
@@ -437,7 +443,11 @@ cudaError_t launch_window(const ts_kv_cache& c, const ts_attn_args& a, void* ws,
   lay_out(p, ws, sms);
   if (!a.k_new) p.own_ml = nullptr;
   if (c.head_dim == 128) return launch_window_tc(p, block_rows(p), sms, s);
-  return block_rows(p) == 16 ? launch_mt<1>(p, sms, s) : launch_mt<2>(p, sms, s);
+  switch (block_rows(p)) {
+    case 16: return launch_mt<1>(p, sms, s);
+    case 32: return launch_mt<2>(p, sms, s);
+    default: return launch_mt<4>(p, sms, s);
+  }
 }
 
 }  // namespace tsv

@@ -122,6 +122,20 @@ def test_attention(case):
     assert torch.equal(got["out"], again["out"]) and torch.equal(got["lse"], again["lse"])
 
 
+@pytest.mark.parametrize("windows,lens,Hq,H,size,dtype,mask,layout", [
+    ([12, 9, 20], [300, 64, 0], 8, 2, 16, torch.bfloat16, "chain", "pages"),
+    ([65, 20], [200, 5000], 4, 2, 64, torch.float16, "tree", "tokens"),
+    ([17, 33, 40], [63, 65, 129], 2, 1, 128, torch.bfloat16, "none", "pool"),
+])
+def test_blocks_of_64_rows(windows, lens, Hq, H, size, dtype, mask, layout):
+    # many rows a KV head and room in the page tables for more than 2^19 tokens: wider blocks
+    s = make(31, windows, lens, Hq, H, 64, size, dtype, mask, layout)
+    room = 2 ** 19 // (size * H * len(windows)) + 1
+    s["page_table"] = torch.cat([s["page_table"], torch.full((len(windows), room), -1, dtype=torch.int32).cuda()], 1)
+    got = tv.window_attention(**s, lse=True)
+    check(got, wanted(s, windows, lens), dtype, 64)
+
+
 def test_equal_windows_need_no_indptr():
     s = make(3, [4, 4, 4], [50, 0, 333], 8, 2, 128, 16, torch.bfloat16)
     a = tv.window_attention(**s)["out"]
