@@ -216,47 +216,45 @@ struct QWalk {
   }
 };
 
-// The exponent field of the block's largest |q|, by one warp: 2^(e - 127) <= |q| < 2^(e - 126).
-template <int ROWS, typename T>
-__device__ __forceinline__ int q_exponent(const WindowParams& p, const Segment& s) {
-  float top = 0.f;
-  QWalk q(p, s, ROWS);
-#pragma unroll 1
-  for (int r = 0; r < s.rows; r += 2) {
-    const uint4 w = q.next();
-    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack<T>(x[i]);
-      top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-    }
-  }
-  return min(max((int)(__float_as_uint(warp_max(top)) >> 23), 27), 227);
+// Two fp16 or bf16 magnitudes, the larger bit pattern of eight side by side.
+__device__ __forceinline__ uint32_t largest_of_8(const uint4& w) {
+  const uint32_t sign = 0x7FFF7FFFu;
+  const uint32_t m = __vmaxu2(__vmaxu2(w.x & sign, w.y & sign), __vmaxu2(w.z & sign, w.w & sign));
+  return max(m >> 16, m & 0xFFFFu);
 }
 
 // Q in e4m3 parts, by one warp, into shared memory as the product wants it: rows of 128 bytes,
-// the 16-byte pieces of row r at their place XOR r % 8. The block is scaled by a power of two
-// to below 2^8 and each value split into PARTS codes, each the rounded rest of the ones before.
-// Four significant bits a part: two parts hold a bf16 value, three an fp16 value, exactly down
-// to 2^-9 of the block's largest magnitude, below that to within 2^-17 of it. Rows behind the
-// block's last are zeros up to a multiple of 16. e: q_exponent. Returns the scale that the codes
-// stand for.
+// the 16-byte pieces of row r at their place XOR r % 8. Each row is scaled by a power of two of
+// its own, so that its largest magnitude lies in [2^7, 2^8) and no row has to do with another
+// (one scale a block cost the small rows their bits, and an infinity all rows theirs), and each value split
+// into PARTS codes, each the rounded rest of the ones before. Four significant bits a part down to
+// steps of 2^-9: two parts hold a bf16 value exactly down to 2^-9 of the row's largest, three an
+// fp16 value down to 2^-6 of it, smaller ones to within 2^-17 of it. Rows behind the block's last
+// are zeros up to a multiple of 16. fac: what a row's codes stand for, times `by`; NaN, and with it the
+// row's scores, where a value is not finite.
 template <int ROWS, int PARTS, typename T>
-__device__ __forceinline__ float split_q(const WindowParams& p, const Segment& s, int e, unsigned char* out) {
+__device__ __forceinline__ void split_q(const WindowParams& p, const Segment& s, float by, unsigned char* out, float* fac) {
   constexpr int D = 128;
   const int lane = threadIdx.x & 31, piece = lane & 15;
-  const float by = __uint_as_float((uint32_t)(254 + 7 - e) << 23);
   QWalk q(p, s, ROWS);
 #pragma unroll 1
   for (int r = lane >> 4; r < (s.rows + 15 & ~15); r += 2) {
     const uint4 w = q.next();
     const uint32_t y[4] = {w.x, w.y, w.z, w.w};
+    // the two rows' largest magnitudes, as bits: a reduction each, which do not wait for each other
+    const uint32_t mine = largest_of_8(w);
+    const uint32_t even = __reduce_max_sync(0xffffffffu, lane < 16 ? mine : 0u), odd = __reduce_max_sync(0xffffffffu, lane < 16 ? 0u : mine);
+    const uint32_t top = lane < 16 ? even : odd;
+    // the exponent field of the largest as a float; both factors stay normal
+    const int e = min(max((int)(__float_as_uint(unpack<T>(top).x) >> 23), 8), 254);
+    const float scale = __uint_as_float((uint32_t)(254 + 7 - e) << 23);
+    if (piece == 0) fac[r] = not_finite<T>(top) ? NAN : __uint_as_float((uint32_t)(e - 7) << 23) * by;
     float x[8];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float2 f = unpack<T>(y[k]);
-      x[2 * k] = f.x * by;
-      x[2 * k + 1] = f.y * by;
+      x[2 * k] = f.x * scale;
+      x[2 * k + 1] = f.y * scale;
     }
 #pragma unroll
     for (int part = 0; part < PARTS; ++part) {
@@ -270,7 +268,6 @@ __device__ __forceinline__ float split_q(const WindowParams& p, const Segment& s
       *reinterpret_cast<uint2*>(out + part * ROWS * D + r * D + ((piece >> 1) ^ (r & 7)) * 16 + (piece & 1) * 8) = make_uint2(z[0], z[1]);
     }
   }
-  return __uint_as_float((uint32_t)(e - 7) << 23);
 }
 
 // The window's own part of every row into own_o and own_ml: one CTA a row block of a KV head,

@@ -90,9 +90,10 @@ struct Shared {
   uint64_t s_full[2 * kGroups], s_free[2 * kGroups];  // a buffer's
   uint64_t p_full[kGroups], o_done[kGroups];          // a turn's
   uint64_t q_full, q_empty, o_free, trees_full;
-  float q_scale;                            // what Q's codes stand for
+  float q_fac[ROWS];                        // the factors of a unit's rows (split_q)
   float ks[kMeta][8], vs[kMeta][8];         // scales of a tile's pages (vs 0: no such page)
   alignas(16) float neg_m[kGroups][kCols];  // a group's references, negated; read as vectors
+  alignas(16) float fac[kGroups][kCols];    // a group's rows' factors
   alignas(16) float delta[kGroups][kCols];
   float red[kGroups][4][kCols];
   float w[kGroups + 1][ROWS];  // a row's factors: the turns', and the window's own part
@@ -106,6 +107,7 @@ struct Shared {
 };
 
 static_assert(offsetof(Shared<32>, neg_m) % 16 == 0 && offsetof(Shared<64>, neg_m) % 16 == 0 &&
+                  offsetof(Shared<32>, fac) % 16 == 0 && offsetof(Shared<64>, fac) % 16 == 0 &&
                   offsetof(Shared<32>, delta) % 16 == 0 && offsetof(Shared<64>, delta) % 16 == 0 &&
                   Layout<32, 2>::off_x % 16 == 0 && Layout<64, 3>::off_x % 16 == 0,
               "vector loads");
@@ -238,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&x.o_done[i], 1);
     }
     mbar_init(&x.q_full, 1);
-    mbar_init(&x.q_empty, 1 + kGroups);  // the products, and the groups have read the scale
+    mbar_init(&x.q_empty, 1 + kGroups);  // the products, and the groups have read the factors
     mbar_init(&x.o_free, kSoftmaxThreads / 32);
     mbar_init(&x.trees_full, 1);
     x.stop = 0;
@@ -339,8 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           asm volatile("prefetch.global.L2 [%0];" ::"l"(q_row(p, s, ROWS, r) + (lane & 1) * 128));
         wait(&x.q_empty, (u & 1) ^ 1, &x.stop);
         __syncwarp();
-        const float scale = split_q<ROWS, QP, T>(p, s, q_exponent<ROWS, T>(p, s), s_q);
-        if (lane == 0) x.q_scale = scale;
+        split_q<ROWS, QP, T>(p, s, p.scale_log2, s_q, x.q_fac);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(&x.q_full);
@@ -460,10 +461,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       wait(&x.q_full, u & 1, &x.stop);
-      const float q_scale = x.q_scale * p.scale_log2;
 #pragma unroll
       for (int r = 0; r < kCols / 2; ++r) l[r] = 0;
-      if (token < kCols) x.neg_m[group][token] = 0.f;
+      if (token < kCols) {
+        x.neg_m[group][token] = 0.f;
+        x.fac[group][token] = x.q_fac[col0 + token];
+      }
       if (tid < s.rows) x.at[tid] = (int32_t)s.at(p, ROWS, tid);
       bool fresh = true;  // no token of this unit seen yet: the references are not set
       bar_sync(1 + group, kGroupThreads);
@@ -476,14 +479,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&x.meta_full[slot], i / kMeta & 1, &x.stop);
         const float ks = x.ks[slot][token >> p.page_shift], vs = x.vs[slot][token >> p.page_shift];
         const bool valid = vs > 0.f && (s.t0 + j) * kTile + token < s.r.len;
-        const float f = ks * q_scale, lv = __log2f(vs), inv_v = valid ? 1.f / vs : 0.f;
+        const float lv = __log2f(vs), inv_v = valid ? 1.f / vs : 0.f;
         wait(&x.s_full[buf], i / L::s_bufs & 1, &x.stop);
         __syncwarp();
         tc_fence_after();
         // 16 rows a step (registers); rows behind the block's last are skipped. First whether a
         // score is too far above its reference, then, from TMEM again, P.
         const bool all_valid = __all_sync(0xffffffffu, valid);
-        const f32x2 f2 = pair(f, f), lv2 = pair(lv, lv);
+        const f32x2 ks2 = pair(ks, ks), lv2 = pair(lv, lv);
         // scores less references of rows c .. c + 15
         auto scores = [&](int c, float* y) {
           tmem_ld16(my_s + c, y);
@@ -492,8 +495,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int r = 0; r < 16; r += 4) {
             const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(&x.neg_m[group][c + r]);
-            const float2 a = unpair(fma2(pair(y[r], y[r + 1]), f2, add2(lv2, m.x)));
-            const float2 b = unpair(fma2(pair(y[r + 2], y[r + 3]), f2, add2(lv2, m.y)));
+            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&x.fac[group][c + r]);
+            const float2 a = unpair(fma2(pair(y[r], y[r + 1]), mul2(ks2, f.x), add2(lv2, m.x)));
+            const float2 b = unpair(fma2(pair(y[r + 2], y[r + 3]), mul2(ks2, f.y), add2(lv2, m.y)));
             y[r] = a.x, y[r + 1] = a.y, y[r + 2] = b.x, y[r + 3] = b.y;
           }
           if (!all_valid) {

@@ -1,0 +1,20 @@
+"""What window attention's header says of q, by arithmetic on the CPU: values split into e4m3
+parts as the kernel for head_dim 128 splits them."""
+import pytest
+import torch
+
+from tests.window_ref import e4m3
+
+
+@pytest.mark.parametrize("dtype,parts,exact", [(torch.bfloat16, 2, -9), (torch.float16, 3, -6)])
+def test_q_in_parts(dtype, parts, exact):
+    # the row's largest magnitude is scaled into [2^7, 2^8); every value below it, in each binade
+    bits = 8 if dtype == torch.bfloat16 else 11
+    grid = torch.arange(2 ** (bits - 1), 2 ** bits, dtype=torch.float64) * 2.0 ** (1 - bits)
+    for binade in range(-30, 1):
+        x = grid * 2.0 ** (7 + binade)
+        rest = x.clone()
+        for _ in range(parts):
+            rest -= e4m3(rest)
+        assert rest.abs().max() <= 2.0 ** (7 - 17)
+        assert (rest == 0).all() == (binade >= exact)
