@@ -75,15 +75,19 @@ __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Par
     __syncthreads();  // the previous unit's reads of shared memory are done
     for (int i = warp; i < ROWS; i += kWarps) {
       float top = 0.f;
+      uint32_t bad = 0;
       if (i < rows) {
-        const uint32_t* q = reinterpret_cast<const uint32_t*>(q_row(p, sg, ROWS, i));
-        const float2 f = unpack<T>(q[lane]);
+        const uint32_t w = reinterpret_cast<const uint32_t*>(q_row(p, sg, ROWS, i))[lane];
+        const float2 f = unpack<T>(w);
         top = fmaxf(fabsf(f.x), fabsf(f.y));
+        bad = not_finite<T>(w);
       }
       top = warp_max(top);
-      // 2^e <= top < 2^(e+1); the row is divided by 2^e
-      const int e = min(max((int)(__float_as_uint(top) >> 23), 27), 227);
-      if (lane == 0) s_fac[i] = __uint_as_float((uint32_t)e << 23);
+      // 2^e <= top < 2^(e+1); the row is divided by 2^e (both factors stay normal: by 2^126 above
+      // that). A row with a value that is not finite: NaN, and with it its scores
+      const int e = min(max((int)(__float_as_uint(top) >> 23), 1), 253);
+      bad = __any_sync(0xffffffffu, bad);
+      if (lane == 0) s_fac[i] = bad ? NAN : __uint_as_float((uint32_t)e << 23);
     }
     __syncthreads();
     for (int i = tid; i < MT * KS * 32; i += kThreads) {

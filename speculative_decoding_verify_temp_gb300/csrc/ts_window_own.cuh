@@ -61,7 +61,7 @@ __device__ __forceinline__ bool own_part(const WindowParams& p, const Segment& s
     sees[h] = i >= s.rows ? Sees{0, 0} : trees ? trees[t] : chain_sees(t);
   }
   o += (i0 + g) * ld + 2 * c;
-  uint32_t odd = 0;
+  uint32_t odd = 0, bad[2] = {0, 0};  // values of V, of the rows' q that are not finite
   // the last window row of these rows: no row sees a token behind its own
   const int last = (s.block * ROWS + min(i0 + 15, s.rows - 1)) / p.group;
 #pragma unroll 1
@@ -75,7 +75,10 @@ __device__ __forceinline__ bool own_part(const WindowParams& p, const Segment& s
       const int dim = ks * 32 + c * 8;
       uint4 qw[2], kw[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) qw[h] = q[h] ? __ldg(reinterpret_cast<const uint4*>(q[h] + dim * 2)) : make_uint4(0, 0, 0, 0);
+      for (int h = 0; h < 2; ++h) {
+        qw[h] = q[h] ? __ldg(reinterpret_cast<const uint4*>(q[h] + dim * 2)) : make_uint4(0, 0, 0, 0);
+        bad[h] |= not_finite<T>(qw[h].x) | not_finite<T>(qw[h].y) | not_finite<T>(qw[h].z) | not_finite<T>(qw[h].w);
+      }
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         kw[n] = make_uint4(0, 0, 0, 0);
@@ -145,6 +148,7 @@ __device__ __forceinline__ bool own_part(const WindowParams& p, const Segment& s
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
+    if (bad[h]) l[h] = NAN;  // even where its scores are all -inf: a row sees itself at least
     l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
     l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
     if (c == 0) ml[i0 + h * 8 + g] = make_float2(m[h], l[h]);

@@ -69,3 +69,44 @@ def test_rows_of_very_different_sizes(D, Hq, dtype):
     s["q"][:, 1] *= 4096
     s["q"][5] = (s["q"][5].float() * 4096).clamp(-32000, 32000).to(dtype)
     check_rows(tv.window_attention(**s, lse=True), wanted(s, windows, lens), s)
+
+
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("Hq", [4, 8, 32])  # blocks of 16, 32 and 64 rows
+@pytest.mark.parametrize("mask", ["chain", "none"])
+def test_a_value_that_is_not_finite_stays_in_its_row_64(value, Hq, mask):
+    for dtype in (BF16, F16):
+        stays_in_its_row(make(53, [6, 3], [700, 10], Hq, 2, 64, 16, dtype, mask), value)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,mask", [([20], "none"), ([0], "chain"), ([20], "chain"), ([0], "none")])
+def test_an_infinity_whose_scores_are_all_minus_infinity(D, lens, mask):
+    # K is negative everywhere, one query +inf: each of its scores is -inf, and it is NaN all the
+    # same (without a token to see: 0)
+    for dtype in (BF16, F16):
+        s = make(54, [3], lens, 4, 2, D, 16, dtype, mask, garbage=False)
+        s["q"] = s["q"].contiguous()
+        s["k_cache"] = (-s["k_cache"].float().abs() - 1).to(ref.F8)
+        if mask != "none":
+            s["k_new"] = -s["k_new"].abs() - 1
+        s["q"][1, 2, 3] = math.inf
+        got = tv.window_attention(**s, lse=True)
+        rest = torch.ones((3, 4), dtype=torch.bool)
+        rest[1, 2] = False
+        if lens == [0] and mask == "none":
+            assert (got["out"] == 0).all() and torch.isneginf(got["lse"]).all()
+            continue
+        assert torch.isnan(got["out"][1, 2]).all() and torch.isnan(got["lse"][1, 2])
+        assert torch.isfinite(got["out"].cpu()[rest].float()).all() and torch.isfinite(got["lse"].cpu()[rest]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq", [4, 32])
+@pytest.mark.parametrize("by", [2.0 ** 104, 2.0 ** -104])
+def test_queries_near_the_ends_of_bf16(D, Hq, by):
+    windows, lens = [4, 3], [200, 33]
+    s = make(55, windows, lens, Hq, 2, D, 16, BF16)
+    s["q"] = (s["q"].float() * by).to(BF16)
+    scale = 0.1 / by
+    check_rows(tv.window_attention(**s, sm_scale=scale, lse=True), wanted(s, windows, lens, scale), s)
