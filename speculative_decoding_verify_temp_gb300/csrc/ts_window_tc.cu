@@ -10,18 +10,24 @@
 // is the M = 128 of the instruction and the window's rows, few as they are, its N:
 //
 //   S^T [128 tokens x ROWS] = K [128 x D] (Q_hi + Q_lo (+ Q_lo2))^T      one accumulator
-//   O^T [D x 2, 3 ROWS]    += V^T [D x 128 tokens] [P_hi | P_lo (| P_lo2)] one accumulator a part
+//   O^T [D x 2 or 3 ROWS]   += V^T [D x 128 tokens] P^T, P in three parts, accumulators as below
 //
 // P = 2^(x - m) with a reference m a row (x in log2 units, V's scale in the exponent as in
 // ts_window.cu); a reference follows only when a score exceeds it by 2^8 (one vote a tile), and
-// then O is scaled in TMEM. Parts of P: the fp16 rounding of p in three codes, the second and
-// third scaled by 2^5 and 2^10, so that all 11 bits are kept down to 2^-9, and values down to
-// 2^-20, where the row's largest p is between 2^4 and 2^8. bf16 calls with blocks of 64 rows take
-// two parts (their output has 8 bits): e4m3, and e5m2 for the rest times 2^12: 7 bits and half a
-// step, down to 2^-24. The columns of TMEM that this leaves are second buffers of S, so that the
-// first products run a whole round of turns ahead: 331 us against 392 for 16 trees of 32 nodes
-// over 8191 tokens (317 now). Blocks of 32 rows have four turns, and the three parts of one type go
-// through one instruction (222 clocks a tile against 384 for two types).
+// then O is scaled in TMEM. Parts of P: the fp16 rounding of p in three codes, the row's largest p
+// between 2^4 and 2^8.
+//
+//   32 rows  e4m3, each rest scaled by 2^5: an accumulator a part, one instruction (222 clocks a
+//            tile against 384 for two types). All 11 bits of p down to 2^-9, values down to 2^-20.
+//   64 rows  e4m3; its rest in e5m2 as it is, so that both share an accumulator; and what is left times
+//            2^9 in e4m3. All 11 bits down to 2^-8, values down to 2^-19. The columns of TMEM that
+//            this saves are second buffers of S, so that the first products run a whole round
+//            of turns ahead (with the parts of 32 rows: 390 us for 16 trees of 32 nodes
+//            over 8191 tokens, 351 with these).
+//
+// (Two parts, e4m3 and 2^12 times the rest in e5m2, were faster by a little. Below 2^-10 the second
+// alone holds p then, in three bits: behind a large probability many small ones, all alike, err by
+// up to 12 % to the same side.)
 //
 // A softmax thread is a token: it reads its row of S^T from TMEM, the scales of its block and
 // its validity are its own, and it writes its row of P. Its work on a tile is a chain of waits
@@ -58,6 +64,7 @@ constexpr int kSoftmaxThreads = kGroups * kGroupThreads;
 constexpr int kThreads = kSoftmaxThreads + 128;
 constexpr int kCols = 32;          // rows of a block that a softmax thread has scores of
 constexpr int kMinTiles = 2;       // least tiles a CTA takes: pieces of 256 tokens or more
+constexpr int kParts = 3;          // of a probability
 constexpr float kHead = 4.f;       // a reference is set this far below the largest score
 constexpr int kBarAll = kGroups + 1;  // named barrier of all softmax threads; 1 .. kGroups: a group's
 
@@ -66,7 +73,6 @@ __device__ uint32_t g_window_error;
 template <int ROWS, int QP>
 struct Layout {
   static constexpr int q_bytes = QP * ROWS * kD;
-  static constexpr int kParts = ROWS == 64 && QP == 2 ? 2 : 3;  // of a probability
   static constexpr int p_part = ROWS * kTile;
   static constexpr bool split = ROWS == 2 * kCols;        // two groups share a tile's rows
   static constexpr int turns = split ? kGroups / 2 : kGroups;  // tiles in work at a time
@@ -75,8 +81,9 @@ struct Layout {
   static constexpr int off_p = off_q + q_bytes;
   static constexpr int off_x = off_p + turns * kParts * p_part;
   // TMEM columns: the buffers of S, then the turns' O, a part after the other
-  static constexpr int s_bufs = kParts == 2 ? 2 * turns : turns;
-  static constexpr int col_o = s_bufs * ROWS, o_cols = kParts * ROWS;
+  static constexpr int s_bufs = split ? 2 * turns : turns;
+  static constexpr int accs = split ? 2 : 3;  // accumulators
+  static constexpr int col_o = s_bufs * ROWS, o_cols = accs * ROWS;
   static constexpr int tmem_cols = 512;
   // a tile's scales are overwritten kMeta tiles later, when the first product of the tile kStages
   // before that one is done, and with it the groups' reading of the scores s_bufs before that
@@ -174,25 +181,31 @@ __device__ __forceinline__ float reduce_columns(float* x, int lane, F f) {
   return f(x[0], __shfl_xor_sync(0xffffffffu, x[0], 16));
 }
 
-// Four probabilities (two fp16 pairs) in parts: codes[0 .. N-1].
-template <int N>
+// Four probabilities (two fp16 pairs) in parts, for three accumulators; or for two: then codes[1] is
+// the third part, so that the two of e4m3 lie side by side, and codes[2] the second.
+template <int ACCS>
 __device__ __forceinline__ void split_p(__half2 a, __half2 b, uint32_t* codes) {
 #pragma unroll
-  for (int part = 0; part < N; ++part) {
-    if (N == 2 && part == 1) {
-      asm("{\n .reg .b16 u, v;\n cvt.rn.satfinite.e5m2x2.f16x2 u, %1;\n cvt.rn.satfinite.e5m2x2.f16x2 v, %2;\n mov.b32 %0, {u, v};\n}\n"
-          : "=r"(codes[part])
-          : "r"(*reinterpret_cast<const uint32_t*>(&a)), "r"(*reinterpret_cast<const uint32_t*>(&b)));
-      return;
-    }
+  for (int part = 0; part < ACCS; ++part) {
     uint32_t back_a, back_b;
     asm("{\n .reg .b16 u, v;\n cvt.rn.satfinite.e4m3x2.f16x2 u, %3;\n cvt.rn.satfinite.e4m3x2.f16x2 v, %4;\n"
         " mov.b32 %0, {u, v};\n cvt.rn.f16x2.e4m3x2 %1, u;\n cvt.rn.f16x2.e4m3x2 %2, v;\n}\n"
         : "=r"(codes[part]), "=r"(back_a), "=r"(back_b)
         : "r"(*reinterpret_cast<const uint32_t*>(&a)), "r"(*reinterpret_cast<const uint32_t*>(&b)));
-    const __half2 by = __float2half2_rn(N == 2 ? 4096.f : 32.f);
-    a = __hmul2(__hsub2(a, *reinterpret_cast<const __half2*>(&back_a)), by);
-    b = __hmul2(__hsub2(b, *reinterpret_cast<const __half2*>(&back_b)), by);
+    a = __hsub2(a, *reinterpret_cast<const __half2*>(&back_a));
+    b = __hsub2(b, *reinterpret_cast<const __half2*>(&back_b));
+    if (ACCS == 2 && part == 0) {  // e5m2: the upper byte of an fp16
+      asm("{\n .reg .b16 u, v;\n cvt.rn.satfinite.e5m2x2.f16x2 u, %1;\n cvt.rn.satfinite.e5m2x2.f16x2 v, %2;\n mov.b32 %0, {u, v};\n}\n"
+          : "=r"(codes[2])
+          : "r"(*reinterpret_cast<const uint32_t*>(&a)), "r"(*reinterpret_cast<const uint32_t*>(&b)));
+      back_a = __byte_perm(codes[2], 0, 0x1404);
+      back_b = __byte_perm(codes[2], 0, 0x3424);
+      a = __hsub2(a, *reinterpret_cast<const __half2*>(&back_a));
+      b = __hsub2(b, *reinterpret_cast<const __half2*>(&back_b));
+    }
+    const __half2 by = __float2half2_rn(ACCS == 2 ? 512.f : 32.f);
+    a = __hmul2(a, by);
+    b = __hmul2(b, by);
   }
 }
 
@@ -214,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* s_p = sm + L::off_p;
   Shared<ROWS>& x = *reinterpret_cast<Shared<ROWS>*>(sm + L::off_x);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kParts = L::kParts, kFirst = kSoftmaxThreads / 32;  // the warps behind the softmax groups
+  constexpr int kFirst = kSoftmaxThreads / 32;  // the warps behind the softmax groups
   int4 desc = make_int4(-1, 0, 0, 0);
   grid_launch();
   Line<ROWS, kTile> line;
@@ -406,15 +419,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (stopped(&x.stop)) continue;
             tc_fence_after();
             const uint32_t d = tmem + L::col_o + w * L::o_cols, a = v_lo + st * (kStageBytes / 16), b = p_lo + w * (kParts * L::p_part / 16);
-            // three parts of one type: columns side by side in one instruction; two of different
-            // types: one after the other
-            constexpr int kAtOnce = kParts == 3 ? 3 : 1;
+            // the parts of one type: columns side by side in one instruction
 #pragma unroll
-            for (int part = 0; part < kParts; part += kAtOnce)
+            for (int k = 0; k < kTile / 32; ++k)
+              mma_f8(d, a + k * (32 * kD / 16), v_hi, b + k * (32 * ROWS / 16), p_hi, f8_idesc(kD, L::accs * ROWS, true, true), j >= L::turns || k > 0);
+            if constexpr (L::accs == 2)
 #pragma unroll
               for (int k = 0; k < kTile / 32; ++k)
-                mma_f8(d + part * ROWS, a + k * (32 * kD / 16), v_hi, b + part * (L::p_part / 16) + k * (32 * ROWS / 16), p_hi,
-                       f8_idesc(kD, kAtOnce * ROWS, true, true, kParts == 2 && part == 1), j >= L::turns || k > 0);
+                mma_f8(d, a + k * (32 * kD / 16), v_hi, b + 2 * (L::p_part / 16) + k * (32 * ROWS / 16), p_hi, f8_idesc(kD, ROWS, true, true, true), true);
             mma_commit(&x.o_done[w]);
             mma_commit(&x.v_empty[st]);
           }
@@ -554,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;  // the same for every thread
               const float by[8] = {ex2(a.x), ex2(a.y), ex2(a.z), ex2(a.w), ex2(b.x), ex2(b.y), ex2(b.z), ex2(b.w)};
 #pragma unroll 1
-              for (int part = 0; part < kParts; ++part) {
+              for (int part = 0; part < L::accs; ++part) {
                 float o[8];
                 tmem_ld8(my_o + part * ROWS + c, o);
                 tmem_wait_ld();
@@ -584,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float e0 = ex2(y[4 * k]), e1 = ex2(y[4 * k + 1]), e2 = ex2(y[4 * k + 2]), e3 = ex2(y[4 * k + 3]);
             l[r] = fma2(pair(e0, e1), inv2, l[r]);
             l[r + 1] = fma2(pair(e2, e3), inv2, l[r + 1]);
-            split_p<kParts>(__floats2half2_rn(e0, e1), __floats2half2_rn(e2, e3), codes[k]);
+            split_p<L::accs>(__floats2half2_rn(e0, e1), __floats2half2_rn(e2, e3), codes[k]);
           }
 #pragma unroll
           for (int part = 0; part < kParts; ++part)
@@ -669,17 +681,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int k = 0; k < L::turns; ++k) {
           if (!x.live[L::split ? 2 * k : k]) continue;  // both groups of a turn see the same tokens
-          float y[kParts][8];
+          float y[L::accs][8];
 #pragma unroll
-          for (int part_ = 0; part_ < kParts; ++part_) tmem_ld8(quarter + L::col_o + k * L::o_cols + part_ * ROWS + c, y[part_]);
+          for (int part_ = 0; part_ < L::accs; ++part_) tmem_ld8(quarter + L::col_o + k * L::o_cols + part_ * ROWS + c, y[part_]);
           tmem_wait_ld();
 #pragma unroll
-          for (int part_ = 0; part_ < kParts; ++part_) tmem_tie8(y[part_]);
+          for (int part_ = 0; part_ < L::accs; ++part_) tmem_tie8(y[part_]);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             float v = y[0][e];
-            if constexpr (kParts == 2) v = fmaf(y[1][e], 0x1p-12f, v);
-            else v = fmaf(fmaf(y[kParts - 1][e], 0x1p-5f, y[1][e]), 0x1p-5f, v);
+            if constexpr (L::accs == 2) v = fmaf(y[1][e], 0x1p-9f, v);
+            else v = fmaf(fmaf(y[L::accs - 1][e], 0x1p-5f, y[1][e]), 0x1p-5f, v);
             o[e] = fmaf(x.w[k][c + e], v, o[e]);
           }
         }
