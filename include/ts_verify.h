@@ -386,7 +386,8 @@ typedef struct ts_attn_args {
  * Scores, softmax statistics and sums are fp32; cached K and V enter the products as they
  * are. q is good to 2^-17 of the largest |q| of its row and head (bf16: exact where it is above 2^-9
  * of it, fp16: above 2^-6). Rows and heads do not affect each other: one whose q holds a value
- * that is not finite gives NaN (if it sees a token), it alone. Probabilities are good to 2^-11.
+ * that is not finite gives NaN (if it sees a token), it alone. Probabilities
+ * are good to 2^-11 each; what the smallest lose beyond that is together below 2^-11 of their row's sum.
  * Scales of V below 2^-100 count as 2^-100.
  * Workspace: ts_attention_workspace_size bytes of scratch (no zero fill needed) that no other
  * call uses meanwhile. */

@@ -25,6 +25,11 @@
 //            of turns ahead (with the parts of 32 rows: 390 us for 16 trees of 32 nodes
 //            over 8191 tokens, 351 with these).
 //
+// What the smallest lose, 2^-19 each at most, comes to 2^-7 in the kLook tiles of a turn; after as many
+// a row whose largest p is below 2^4 has its reference lowered. So the loss stays below 2^-11 of the
+// row's sum however many small ones follow a large one. References are whole numbers: scaling by
+// them is exact.
+//
 // (Two parts, e4m3 and 2^12 times the rest in e5m2, were faster by a little. Below 2^-10 the second
 // alone holds p then, in three bits: behind a large probability many small ones, all alike, err by
 // up to 12 % to the same side.)
@@ -65,7 +70,9 @@ constexpr int kThreads = kSoftmaxThreads + 128;
 constexpr int kCols = 32;          // rows of a block that a softmax thread has scores of
 constexpr int kMinTiles = 2;       // least tiles a CTA takes: pieces of 256 tokens or more
 constexpr int kParts = 3;          // of a probability
-constexpr float kHead = 4.f;       // a reference is set this far below the largest score
+constexpr float kHead = 4.f;       // a reference is set this far (up to 1 more) below the largest score
+constexpr int kLook = 32;          // tiles of a turn after which references may be lowered
+constexpr float kDeep = 12.f;      // the most that a reference lies below an earlier one of its row (sums must not overflow)
 constexpr int kBarAll = kGroups + 1;  // named barrier of all softmax threads; 1 .. kGroups: a group's
 
 __device__ uint32_t g_window_error;
@@ -101,7 +108,8 @@ struct Shared {
   float ks[kMeta][8], vs[kMeta][8];         // scales of a tile's pages (vs 0: no such page)
   alignas(16) float neg_m[kGroups][kCols];  // a group's references, negated; read as vectors
   alignas(16) float fac[kGroups][kCols];    // a group's rows' factors
-  alignas(16) float delta[kGroups][kCols];
+  alignas(16) float delta[kGroups][kCols];  // factors of outputs and sums whose references move
+  float peak[kGroups][kCols];               // the rows' largest references so far
   float red[kGroups][4][kCols];
   float w[kGroups + 1][ROWS];  // a row's factors: the turns', and the window's own part
   float2 own[ROWS];            // the own part's references and sums
@@ -207,6 +215,12 @@ __device__ __forceinline__ void split_p(__half2 a, __half2 b, uint32_t* codes) {
     a = __hmul2(a, by);
     b = __hmul2(b, by);
   }
+}
+
+// 2^x for a whole number x, exactly (0 below 2^-126).
+__device__ __forceinline__ float power_of_2(float x) {
+  const int e = (int)fminf(x, 127.f);
+  return e < -126 ? 0.f : __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
 // A value that the compiler knows nothing about: branches on it are not merged into copies of
@@ -476,11 +490,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int r = 0; r < kCols / 2; ++r) l[r] = 0;
       if (token < kCols) {
-        x.neg_m[group][token] = 0.f;
+        x.neg_m[group][token] = token < rows ? 0.f : kNone;  // no row: its scores ask for nothing
         x.fac[group][token] = x.q_fac[col0 + token];
       }
       if (tid < s.rows) x.at[tid] = (int32_t)s.at(p, ROWS, tid);
       bool fresh = true;  // no token of this unit seen yet: the references are not set
+      int look = j0 + kLook * L::turns;  // the tile from which on references may be lowered
       bar_sync(1 + group, kGroupThreads);
       if (token == 0) mbar_arrive(&x.q_empty);
       int j = j0;
@@ -518,7 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         float top = -INFINITY;
-        if (!fresh) {
+        const bool looks = j >= look;
+        if (!fresh && !looks) {
 #pragma unroll 1
           for (int c = 0; c < rows; c += 16) {
             float y[16];
@@ -527,8 +543,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int r = 0; r < 16; ++r) top = fmaxf(top, y[r]);
           }
         }
-        if (bar_or(1 + group, kGroupThreads, fresh || top > kSlack)) {
-          // rows whose largest score is that far up get a new reference
+        if (bar_or(1 + group, kGroupThreads, fresh || looks || top > kSlack)) {
+          // rows whose largest score is that far up get a new reference (and at a look those where
+          // it is below 2^kHead): each by its own scores, whatever its neighbours do
 #pragma unroll 1
           for (int c = 0; c < rows; c += 16) {
             float y[16];
@@ -537,24 +554,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane < 16) x.red[group][warp & 3][c + lane] = v;
           }
           const bool any_valid = bar_or(1 + group, kGroupThreads, valid);
+          bool moves = false;
           if (token < kCols) {
             float d = -INFINITY;
             if (token < rows) {
 #pragma unroll
               for (int k = 0; k < 4; ++k) d = fmaxf(d, x.red[group][k][token]);
             }
-            d = (fresh ? d > -INFINITY : d > kSlack) ? d - kHead : 0.f;
-            x.delta[group][token] = -d;
-            x.neg_m[group][token] -= d;
+            const float old = -x.neg_m[group][token], low = x.peak[group][token] - kDeep;
+            float m = old;
+            if (d > -INFINITY) {
+              if (fresh || d > kSlack) m = old + floorf(d - kHead);
+              else if (looks && d < kHead) m = fmaxf(old + floorf(d - kHead), low);
+            }
+            moves = m != old;
+            x.delta[group][token] = power_of_2(old - m);
+            x.neg_m[group][token] = -m;
+            x.peak[group][token] = fresh ? (d > -INFINITY ? m : kNone) : fmaxf(low + kDeep, m);
           }
-          bar_sync(1 + group, kGroupThreads);
-          if (!fresh) {
+          if (bar_or(1 + group, kGroupThreads, moves) && !fresh) {
 #pragma unroll
             for (int r = 0; r < kCols / 2; r += 2) {
               const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(&x.delta[group][2 * r]);
-              const float2 a = unpair(d.x), b = unpair(d.y);
-              l[r] = mul2(l[r], pair(ex2(a.x), ex2(a.y)));
-              l[r + 1] = mul2(l[r + 1], pair(ex2(b.x), ex2(b.y)));
+              l[r] = mul2(l[r], d.x);
+              l[r + 1] = mul2(l[r + 1], d.y);
             }
             wait(&x.o_done[turn], phase ^ 1, &x.stop);
             __syncwarp();
@@ -562,9 +585,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int c = 0; c < rows; c += 8) {
               const float4 a = *reinterpret_cast<const float4*>(&x.delta[group][c]), b = *reinterpret_cast<const float4*>(&x.delta[group][c + 4]);
-              if (a.x == 0.f && a.y == 0.f && a.z == 0.f && a.w == 0.f && b.x == 0.f && b.y == 0.f && b.z == 0.f && b.w == 0.f)
-                continue;  // the same for every thread
-              const float by[8] = {ex2(a.x), ex2(a.y), ex2(a.z), ex2(a.w), ex2(b.x), ex2(b.y), ex2(b.z), ex2(b.w)};
+              const float by[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+              bool moved = false;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) moved |= by[e] != 1.f;
+              if (!moved) continue;  // the same for every thread
 #pragma unroll 1
               for (int part = 0; part < L::accs; ++part) {
                 float o[8];
@@ -578,7 +603,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_wait_st();
           }
-          if (any_valid) fresh = false;
+          if (any_valid) {
+            fresh = false;
+            if (looks) look = j + kLook * L::turns;
+          }
         }
         // P's place: the product that read it is done (one of an earlier unit was awaited there)
         if (j >= L::turns) wait(&x.o_done[turn], phase ^ 1, &x.stop);

@@ -70,3 +70,43 @@ def check(n, at, rows, D, dtype):
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_small_probabilities_behind_a_large_one_128(dtype, rows, n, at):
     check(n, {"first": 0, "middle": n // 2, "last": n - 1}[at], rows, 128, dtype)
+
+
+@pytest.mark.parametrize("at", ["first", "middle", "last"])
+@pytest.mark.parametrize("n", [32768, 131072])
+@pytest.mark.parametrize("rows", [(1, 8), (8, 8)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_many_small_probabilities_behind_a_large_one_128(dtype, rows, n, at):
+    check(n, {"first": 0, "middle": n // 2, "last": n - 1}[at], rows, 128, dtype)
+
+
+def test_references_that_rise_and_fall_again():
+    # large tokens at the beginning, in the middle and at the end of a long context of small ones, which
+    # are larger in its second half: against the softmax in 64 bits
+    n, page, D, T, Hq = 70001, 128, 128, 2, 4
+    for dtype in (BF16, F16):
+        B = torch.cuda.get_device_properties(0).multi_processor_count
+        score = torch.zeros(n, dtype=torch.float64)
+        score[n // 2:] = 0.5
+        score[[3, 20011, 35000, 35001, 69999]] = torch.tensor([1.0, 0.875, 1.125, 0.75, 1.0], dtype=torch.float64)
+        v = torch.randn(n, generator=torch.Generator().manual_seed(1)).to(F8).double()
+        pages = -(-n // page)
+        k_cache, v_cache = torch.zeros((2, pages * page, D))
+        k_cache[:n, 0] = score.float()
+        v_cache[:n] = v.float()[:, None]
+        a = torch.arange(8, 24, 2, dtype=torch.float64)  # a row's scores: a times those
+        q = torch.zeros((T, Hq, D), dtype=torch.float64)
+        q[:, :, 0] = a.view(T, Hq)
+        ones = torch.ones((pages, 1)).cuda()
+        got = tv.window_attention(
+            q.to(dtype).repeat(B, 1, 1).cuda(), k_cache.view(pages, 1, page, D).to(F8).cuda(),
+            v_cache.view(pages, 1, page, D).to(F8).cuda(), ones, ones.clone(),
+            torch.arange(pages, dtype=torch.int32).repeat(B, 1).cuda(),
+            torch.full((B,), n, dtype=torch.int32).cuda(), sm_scale=1.0, lse=True)
+        w = torch.softmax(a[:, None] * score, -1)
+        out, absv = w @ v, w @ v.abs()
+        o = got["out"].cpu().double().view(B, T * Hq, D)
+        # as in check, with |v| below 5
+        half, share = torch.finfo(dtype).eps / 2, 2.0 ** -11 + 2.0 ** -16 + 2 * (n / 32 + 64) * 2.0 ** -23
+        far = (o - out[:, None]).abs() - (half * out.abs() + (1 + half) * (absv * share + 5 * 2.0 ** -11))[:, None]
+        assert far.max() <= 0, far.max()
