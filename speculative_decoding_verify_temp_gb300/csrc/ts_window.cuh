@@ -15,8 +15,6 @@
 
 namespace tsv {
 
-constexpr float kSlack = 8.f;       // how far, in log2, a score may exceed its row's reference
-
 struct WindowParams {
   ts_kv_cache c;
   ts_attn_args a;

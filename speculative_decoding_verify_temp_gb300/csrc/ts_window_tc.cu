@@ -70,6 +70,7 @@ constexpr int kThreads = kSoftmaxThreads + 128;
 constexpr int kCols = 32;          // rows of a block that a softmax thread has scores of
 constexpr int kMinTiles = 2;       // least tiles a CTA takes: pieces of 256 tokens or more
 constexpr int kParts = 3;          // of a probability
+constexpr float kSlack = 8.f;      // how far, in log2, a score may exceed its row's reference
 constexpr float kHead = 4.f;       // a reference is set this far (up to 1 more) below the largest score
 constexpr int kLook = 32;          // tiles of a turn after which references may be lowered
 constexpr float kDeep = 12.f;      // the most that a reference lies below an earlier one of its row (sums must not overflow)

@@ -110,3 +110,11 @@ def test_references_that_rise_and_fall_again():
         half, share = torch.finfo(dtype).eps / 2, 2.0 ** -11 + 2.0 ** -16 + 2 * (n / 32 + 64) * 2.0 ** -23
         far = (o - out[:, None]).abs() - (half * out.abs() + (1 + half) * (absv * share + 5 * 2.0 ** -11))[:, None]
         assert far.max() <= 0, far.max()
+
+
+@pytest.mark.parametrize("at", ["first", "middle", "last"])
+@pytest.mark.parametrize("n", [1000, 131072, 524288])
+@pytest.mark.parametrize("rows", [(1, 8), (4, 8), (8, 8)])  # blocks of 16, 32 and 64 rows
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_many_small_probabilities_behind_a_large_one_64(dtype, rows, n, at):
+    check(n, {"first": 0, "middle": n // 2, "last": n - 1}[at], rows, 64, dtype)
