@@ -136,23 +136,25 @@ __device__ __forceinline__ bool stopped(const int32_t* stop) { return *reinterpr
 
 // Waits for a phase; gives up after two to three turns of the clock's upper word (4 to 7 s) and
 // sets *stop, or when that is set. Written out for size: it stands in every loop, and the loops
-// of the six roles have to stay in the instruction caches.
+// of the six roles have to stay in the instruction caches. The lanes of a warp need not see the phase at
+// the same try: they part here, and callers bring them together (__syncwarp) before anything that takes a
+// whole warp.
 __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, int32_t* stop) {
   asm volatile(
       "{\n .reg .pred p;\n .reg .u32 t0, t1, f;\n"
       " mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n"
-      " @p bra.uni DONE_%=;\n"
+      " @p bra DONE_%=;\n"
       " mov.u32 t0, %%clock_hi;\n"
       "AGAIN_%=:\n"
       " mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n"
-      " @p bra.uni DONE_%=;\n"
+      " @p bra DONE_%=;\n"
       " ld.volatile.shared.u32 f, [%2];\n"
       " setp.ne.u32 p, f, 0;\n"
-      " @p bra.uni DONE_%=;\n"
+      " @p bra DONE_%=;\n"
       " mov.u32 t1, %%clock_hi;\n"
       " sub.u32 t1, t1, t0;\n"
       " setp.lt.u32 p, t1, 3;\n"
-      " @p bra.uni AGAIN_%=;\n"
+      " @p bra AGAIN_%=;\n"
       " st.volatile.shared.u32 [%2], 1;\n"
       "DONE_%=:\n}\n" ::"r"(smem_u32(bar)),
       "r"(parity), "r"(smem_u32(stop))
@@ -488,6 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       wait(&x.q_full, u & 1, &x.stop);
+      __syncwarp();
 #pragma unroll
       for (int r = 0; r < kCols / 2; ++r) l[r] = 0;
       if (token < kCols) {
