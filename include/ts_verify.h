@@ -88,12 +88,13 @@ const char* ts_last_error_message(void);
 ts_status ts_device_error(uint32_t* word_host, int clear);
 
 /* Sets how many SM clock cycles a stage wait of the chain kernel (ts_chain_spec_sampling
- * from logits) may take before it gives up; 0 restores the default of 2^32 (about 2 s).
+ * from logits), or a wait of ts_window_attention with head_dim 128, may take before it gives
+ * up; 0 restores the default of 2^32 (about 2 s).
  * Process-wide; takes effect for calls enqueued afterwards. A CTA whose wait gives up
  * issues no more copies, waits (on the long budget) for the copies it has in flight,
  * and leaves the requests it had not finished with accept_length = 0; their other
- * outputs are unspecified. ts_device_error then reports TS_ERR_TIMEOUT. A diagnostic:
- * it exists so that this path can be tested. */
+ * outputs are unspecified, as are all outputs of an attention call. ts_device_error then
+ * reports TS_ERR_TIMEOUT. A diagnostic: it exists so that this path can be tested. */
 ts_status ts_set_wait_cycles(uint64_t cycles);
 
 /* Temperature softmax [TS-FI verify(): softmax(logits, temperature)].

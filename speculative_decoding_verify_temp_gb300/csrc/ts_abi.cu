@@ -16,7 +16,8 @@ namespace {
 
 thread_local char g_msg[512] = "";
 
-// SM clock cycles a stage wait of the chain kernel may take before it gives up.
+// SM clock cycles a stage wait of the chain kernel, or a wait of window attention, may take
+// before it gives up.
 constexpr uint64_t kDefaultWaitCycles = (uint64_t)1 << 32;
 std::atomic<uint64_t> g_wait_cycles{kDefaultWaitCycles};
 
@@ -681,7 +682,8 @@ ts_status ts_window_attention(const ts_attn_args* p, void* workspace, size_t ws_
   const size_t need = tsv::window_workspace(c.batch, p->total_rows, p->heads_q, c.heads, c.head_dim, sm_count());
   if (!workspace || ws_bytes < need || !multiple16(workspace, 0, 0))
     return fail(TS_ERR_INVALID_ARG, "workspace must have %zu 16-byte aligned bytes (got %zu)", need, ws_bytes);
-  return launched(tsv::launch_window(c, *p, workspace, sm_count(), stream), "window attention launch");
+  const uint64_t wait_cycles = g_wait_cycles.load(std::memory_order_relaxed);
+  return launched(tsv::launch_window(c, *p, workspace, sm_count(), wait_cycles, stream), "window attention launch");
 }
 
 size_t ts_attention_workspace_size(int64_t batch, int64_t total_rows, int32_t heads_q,

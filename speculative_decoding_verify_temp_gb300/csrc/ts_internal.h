@@ -261,7 +261,8 @@ int staged_max_vocab(int bf16);
 // ---------------------------------------------------------------------------------
 // Around the verify step (ts_window.cu, ts_kvcache.cu, ts_tree.cu): arguments checked by
 // the ABI.
-cudaError_t launch_window(const ts_kv_cache& c, const ts_attn_args& a, void* ws, int sms, cudaStream_t s);
+cudaError_t launch_window(const ts_kv_cache& c, const ts_attn_args& a, void* ws, int sms, uint64_t wait_cycles,
+                          cudaStream_t s);
 size_t window_workspace(int64_t batch, int64_t total_rows, int heads_q, int heads, int head_dim, int sms);
 cudaError_t window_read_error(uint32_t* word, int clear);
 struct WindowParams;

@@ -441,13 +441,15 @@ size_t window_workspace(int64_t batch, int64_t total_rows, int heads_q, int head
   return lay_out(p, nullptr, sms);
 }
 
-cudaError_t launch_window(const ts_kv_cache& c, const ts_attn_args& a, void* ws, int sms, cudaStream_t s) {
+cudaError_t launch_window(const ts_kv_cache& c, const ts_attn_args& a, void* ws, int sms, uint64_t wait_cycles,
+                          cudaStream_t s) {
   Params p{};
   p.c = c;
   p.a = a;
   p.page_shift = __builtin_ctz((unsigned)c.page_size);
   p.group = a.heads_q / c.heads;
   p.scale_log2 = a.sm_scale * kLog2e;
+  p.wait_cycles = wait_cycles;
   lay_out(p, ws, sms);
   if (!a.k_new) p.own_ml = nullptr;
   if (c.head_dim == 128) return launch_window_tc(p, block_rows(p), sms, s);

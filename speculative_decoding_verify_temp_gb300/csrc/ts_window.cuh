@@ -26,6 +26,7 @@ struct WindowParams {
                     // CTA's first piece ends its unit}
   float* own_o;      // [total_rows * heads_q][D] the window's own part: outputs,
   float2* own_ml;    // [total_rows * heads_q] references and sums
+  uint64_t wait_cycles;  // SM clock cycles that a wait may take (ts_window_tc.cu)
 };
 
 constexpr float kNone = -1e30f;     // the reference before any token

@@ -119,8 +119,12 @@ struct Shared {
   Sees trees[TS_MAX_WINDOW];
   int32_t live[kGroups];
   uint32_t tmem;
-  int32_t stop;
+  alignas(16) int32_t stop;
+  uint64_t wait_cycles;  // 8 bytes behind stop: wait reads it
 };
+static_assert(offsetof(Shared<32>, wait_cycles) == offsetof(Shared<32>, stop) + 8 &&
+                  offsetof(Shared<64>, wait_cycles) == offsetof(Shared<64>, stop) + 8,
+              "wait");
 
 static_assert(offsetof(Shared<32>, neg_m) % 16 == 0 && offsetof(Shared<64>, neg_m) % 16 == 0 &&
                   offsetof(Shared<32>, fac) % 16 == 0 && offsetof(Shared<64>, fac) % 16 == 0 &&
@@ -134,26 +138,27 @@ static_assert(smem_bytes<64, 3>() <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ bool stopped(const int32_t* stop) { return *reinterpret_cast<const volatile int32_t*>(stop) != 0; }
 
-// Waits for a phase; gives up after two to three turns of the clock's upper word (4 to 7 s) and
+// Waits for a phase; gives up after the call's budget of SM clock cycles (8 bytes behind stop) and
 // sets *stop, or when that is set. Written out for size: it stands in every loop, and the loops
 // of the six roles have to stay in the instruction caches. The lanes of a warp need not see the phase at
 // the same try: they part here, and callers bring them together (__syncwarp) before anything that takes a
 // whole warp.
 __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, int32_t* stop) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .u32 t0, t1, f;\n"
+      "{\n .reg .pred p;\n .reg .u32 f;\n .reg .u64 t0, t1, b;\n"
       " mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n"
       " @p bra DONE_%=;\n"
-      " mov.u32 t0, %%clock_hi;\n"
+      " mov.u64 t0, %%clock64;\n"
       "AGAIN_%=:\n"
       " mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n"
       " @p bra DONE_%=;\n"
       " ld.volatile.shared.u32 f, [%2];\n"
       " setp.ne.u32 p, f, 0;\n"
       " @p bra DONE_%=;\n"
-      " mov.u32 t1, %%clock_hi;\n"
-      " sub.u32 t1, t1, t0;\n"
-      " setp.lt.u32 p, t1, 3;\n"
+      " mov.u64 t1, %%clock64;\n"
+      " sub.u64 t1, t1, t0;\n"
+      " ld.shared.u64 b, [%2 + 8];\n"
+      " setp.le.u64 p, t1, b;\n"
       " @p bra AGAIN_%=;\n"
       " st.volatile.shared.u32 [%2], 1;\n"
       "DONE_%=:\n}\n" ::"r"(smem_u32(bar)),
@@ -274,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&x.o_free, kSoftmaxThreads / 32);
     mbar_init(&x.trees_full, 1);
     x.stop = 0;
+    x.wait_cycles = p.wait_cycles;
     fence_mbar_init();
   }
   tc_fence_before();
@@ -330,8 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < end; ++j, ++i) {
             const int at = lane - j * per_tile, st = i % kStages;
             wait(&empty[st], (i / kStages & 1) ^ 1, &x.stop);
-            __syncwarp();
-            if (!stopped(&x.stop)) {
+            if (!__any_sync(0xffffffffu, stopped(&x.stop))) {  // one answer a warp: its lanes meet inside
               if (lane == 0) mbar_arrive_expect_tx(&full[st], kStageBytes);
               __syncwarp();
               if (at >= 0 && at < per_tile)
@@ -753,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) p.desc[blockIdx.x] = desc;
   }
   if (stopped(&x.stop)) {
-    if (tid == 0) atomicOr(&g_window_error, 1u);
+    atomicOr(&g_window_error, 1u);  // by any thread: one may have left its loops before another gave up
     // copies in flight land before the CTA leaves its shared memory
     const long long t0 = clock64();
     while (clock64() - t0 < (1ll << 26)) {

@@ -298,7 +298,8 @@ def device_error(clear: bool = True) -> int:
 
 
 def set_wait_cycles(cycles: int) -> None:
-    """Sets the chain kernel's stage-wait budget in SM clock cycles (0: the default)."""
+    """Sets the budget in SM clock cycles of the chain kernel's stage waits and of window
+    attention's waits (0: the default)."""
     _check("ts_set_wait_cycles", load().ts_set_wait_cycles(int(cycles)))
 
 
