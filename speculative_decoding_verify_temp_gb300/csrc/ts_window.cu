@@ -44,7 +44,7 @@ constexpr int kMinTiles = 4;      // least tiles a CTA takes: pieces of 256 toke
 using Params = WindowParams;
 
 template <int MT, typename T>
-__global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Params p) {
+__device__ __forceinline__ void attend(const Params& p) {
   constexpr int D = 64, ROWS = 16 * MT;
   constexpr int KS = D / 16;        // k16 steps over the dims
   constexpr int NT = D / 8;         // n8 tiles over the dims
@@ -61,7 +61,6 @@ __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Par
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int64_t cta = blockIdx.x;
   int4 desc = make_int4(-1, 0, 0, 0);
-  grid_launch();
   Line<ROWS, kTile> line;
   if (!line_begin<ROWS, kTile, kThreads>(p, kMinTiles, line)) {
     if (tid == 0) p.desc[cta] = desc;
@@ -364,47 +363,75 @@ __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Par
   if (tid == 0) p.desc[cta] = desc;
 }
 
+template <int MT, typename T>
+__global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Params p) {
+  grid_launch();
+  attend<MT, T>(p);
+}
+
+// More than 32 rows a window: blocks of 64 rows, for which K and V are converted half as often, where the
+// cached tokens are many; blocks of 32 where the ends of units weigh more. Tiles a CTA in blocks of
+// 64, us with 64 and with 32 rows: 5: 83 and 56; 8: 69 and 59; 16: 136 and 136; 26: 66 and 58; 41: 97 and
+// 100; 66: 143 and 150; 111: 174 and 203; 344: 559 and 686. The lengths are on the device, so the choice is made here.
+constexpr int kWideTiles = 36;
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_window_rows(const __grid_constant__ Params p) {
+  grid_launch();
+  const bool wide = line_length<64, kTile, kThreads>(p) >= (int64_t)kWideTiles * gridDim.x;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.wide = wide;
+  if (wide) attend<4, T>(p);
+  else attend<2, T>(p);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(128) k_join_rows(const __grid_constant__ Params p) {
+  grid_wait();
+  if (*p.wide) join_row<64, 64, kTile, T>(p);
+  else join_row<64, 32, kTile, T>(p);
+}
+
 constexpr int smem_bytes(int D, int rows) {
   return rows / 16 * (D / 16) * 32 * 16 + rows * 4 + kWarps * rows * (D + 4) * 4 + kWarps * rows * 8;
 }
 
-template <int MT, typename T>
+// kernel, join: k_window and k_join, or k_window_rows and k_join_rows, for blocks of at most ROWS rows.
+template <auto kernel, auto join, int ROWS, typename T>
 cudaError_t launch(const Params& p, int sms, cudaStream_t s) {
-  constexpr int D = 64, ROWS = 16 * MT, bytes = smem_bytes(D, ROWS);
-  cudaError_t e = allow_smem<k_window<MT, T>>(bytes);
+  constexpr int D = 64, bytes = smem_bytes(D, ROWS);
+  cudaError_t e = allow_smem<kernel>(bytes);
   if (e != cudaSuccess) return e;
   const int grid = sms * kCtasPerSm;
   if (p.a.k_new) {
     if ((e = launch_own<D, ROWS, T>(p, s)) != cudaSuccess) return e;
-    e = launch_after(k_window<MT, T>, dim3(grid), kThreads, bytes, s, p);
+    e = launch_after(kernel, dim3(grid), kThreads, bytes, s, p);
   } else {
-    k_window<MT, T><<<grid, kThreads, bytes, s>>>(p);
+    kernel<<<grid, kThreads, bytes, s>>>(p);
     e = cudaGetLastError();
   }
   // units of one tile are never split
   if (e != cudaSuccess || (int64_t)p.c.max_pages * p.c.page_size <= kTile) return e;
-  return launch_after(k_join<D, ROWS, kTile, T>, dim3(grid, ROWS / 4), 128, 0, s, p);
+  return launch_after(join, dim3(grid, ROWS / 4), 128, 0, s, p);
 }
 
-template <int MT>
-cudaError_t launch_mt(const Params& p, int sms, cudaStream_t s) {
-  const bool bf16 = p.a.dtype == TS_BF16;
-  return bf16 ? launch<MT, __nv_bfloat16>(p, sms, s) : launch<MT, __half>(p, sms, s);
+template <typename T>
+cudaError_t launch_64(const Params& p, int rows, int sms, cudaStream_t s) {
+  switch (rows) {
+    case 16: return launch<k_window<1, T>, k_join<64, 16, kTile, T>, 16, T>(p, sms, s);
+    case 32: return launch<k_window<2, T>, k_join<64, 32, kTile, T>, 32, T>(p, sms, s);
+    default: return launch<k_window_rows<T>, k_join_rows<T>, 64, T>(p, sms, s);
+  }
 }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // The rows of a block: by the average window. head_dim 128, ragged chains of 4 to 20 rows: 162 us
 // with 32, 189 with 64; trees of 256 rows: 416 with 32, 330 with 64. head_dim 64, one row of 4
-// heads over 37 tokens: 9.7 us with 16, 11.1 with 32; 62 windows of 176 rows with 8 heads of 4495
-// tokens: 559 us with 64 (K and V are converted once a block), 685 with 32; but 9 windows of 232
-// rows with 2 heads of 2569 tokens, too few units for 64 rows: 52 and 41. In between by the room
-// in the page tables (426 k tokens of all heads: 129 and 130).
+// heads over 37 tokens: 9.7 us with 16, 11.1 with 32; 64 there means at most 64 (k_window_rows).
 int block_rows(const WindowParams& p) {
   const int64_t rows = (p.a.total_rows * p.group + p.c.batch - 1) / p.c.batch;
   if (p.c.head_dim == 128) return rows <= 32 ? 32 : 64;
-  const int64_t room = p.c.batch * p.c.heads * p.c.max_pages * p.c.page_size;
-  return rows <= 16 ? 16 : rows <= 32 || room < 1 << 19 ? 32 : 64;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
 // Lays the workspace out; returns its bytes.
@@ -418,6 +445,7 @@ size_t lay_out(WindowParams& p, void* ws, int sms) {
     return at;
   };
   p.desc = reinterpret_cast<int4*>(take(ctas * sizeof(int4)));
+  p.wide = reinterpret_cast<int32_t*>(take(sizeof(int32_t)));
   p.part = reinterpret_cast<float*>(take(2 * ctas * slot_floats(rows, D) * sizeof(float)));
   const size_t n = (size_t)p.a.total_rows * p.a.heads_q;
   // the window's own part: of every row, or (ts_window_tc.cu) of a block a CTA
@@ -433,8 +461,6 @@ size_t window_workspace(int64_t batch, int64_t total_rows, int heads_q, int head
   p.c.batch = batch;
   p.c.heads = heads;
   p.c.head_dim = head_dim;
-  p.c.max_pages = 1 << 30;  // as large a room as a call can have: its blocks need the most
-  p.c.page_size = 1;
   p.a.total_rows = total_rows;
   p.a.heads_q = heads_q;
   p.group = heads_q / heads;
@@ -453,11 +479,8 @@ cudaError_t launch_window(const ts_kv_cache& c, const ts_attn_args& a, void* ws,
   lay_out(p, ws, sms);
   if (!a.k_new) p.own_ml = nullptr;
   if (c.head_dim == 128) return launch_window_tc(p, block_rows(p), sms, s);
-  switch (block_rows(p)) {
-    case 16: return launch_mt<1>(p, sms, s);
-    case 32: return launch_mt<2>(p, sms, s);
-    default: return launch_mt<4>(p, sms, s);
-  }
+  const int rows = block_rows(p);
+  return a.dtype == TS_BF16 ? launch_64<__nv_bfloat16>(p, rows, sms, s) : launch_64<__half>(p, rows, sms, s);
 }
 
 }  // namespace tsv

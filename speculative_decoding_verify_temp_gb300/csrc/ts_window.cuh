@@ -24,6 +24,7 @@ struct WindowParams {
   float* part;      // [2 * CTAs][rows * (D + 2)] pieces: outputs, references, sums
   int4* desc;       // [CTAs] {tail unit's request, its head and row block, rows, 0 | 1: the
                     // CTA's first piece ends its unit}
+  int32_t* wide;    // blocks of 64 rows (head_dim 64, where the kernel chooses)
   float* own_o;      // [total_rows * heads_q][D] the window's own part: outputs,
   float2* own_ml;    // [total_rows * heads_q] references and sums
   uint64_t wait_cycles;  // SM clock cycles that a wait may take (ts_window_tc.cu)
@@ -165,11 +166,11 @@ struct Line {
 
 // Where the share of CTA blockIdx.x begins, found by the whole CTA: thread i adds up its own
 // run of requests, the sums are scanned, and the thread whose run holds the beginning looks
-// it up. Returns false for a CTA without work. most: a CTA takes this many tiles at least, or as
+// it up. Returns false for a CTA without work. least_tiles: a CTA takes this many tiles at least, or as
 // many as an average unit has where that is less (14 windows of 8 rows over 4 tokens, head_dim 64:
 // 16 us, 39 with four such units a CTA).
 template <int ROWS, int TILE, int THREADS>
-__device__ __forceinline__ bool line_begin(const WindowParams& p, int most, Line<ROWS, TILE>& line) {
+__device__ __forceinline__ bool line_begin(const WindowParams& p, int least_tiles, Line<ROWS, TILE>& line) {
   static_assert(THREADS % 32 == 0, "whole warps");
   __shared__ int64_t s_scan[THREADS / 32], s_start;
   __shared__ uint32_t s_units[THREADS / 32];  // below 2^28: total_rows * heads_q is below 2^31
@@ -205,7 +206,7 @@ __device__ __forceinline__ bool line_begin(const WindowParams& p, int most, Line
     all += s_scan[w];
     units += s_units[w];
   }
-  const int64_t least = all < (int64_t)most * units ? max(all / max(units, 1u), (int64_t)1) : most;
+  const int64_t least = all < (int64_t)least_tiles * units ? max(all / max(units, 1u), (int64_t)1) : least_tiles;
   const int64_t share = max((all + gridDim.x - 1) / gridDim.x, least);
   const int64_t begin = min(all, blockIdx.x * share), end = min(all, begin + share);
   if (begin < end && upto - mine <= begin && begin < upto) {  // one thread
@@ -232,6 +233,23 @@ __device__ __forceinline__ bool line_begin(const WindowParams& p, int most, Line
   line.block = unit % line.r.blocks;
   line.left = end - begin;
   return true;
+}
+
+// The tiles of the whole line, by the whole CTA.
+template <int ROWS, int TILE, int THREADS>
+__device__ __forceinline__ int64_t line_length(const WindowParams& p) {
+  __shared__ int64_t s_sum[THREADS / 32];
+  int64_t mine = 0;
+#pragma unroll 1
+  for (int64_t b = threadIdx.x; b < p.c.batch; b += THREADS) mine += request<ROWS, TILE>(p, raw_request(p, b)).weight(p.c.heads);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = mine;
+  __syncthreads();
+  int64_t all = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) all += s_sum[w];
+  return all;
 }
 
 // A piece's slot: [rows][D] outputs, then [rows] references, then [rows] sums.
@@ -266,8 +284,7 @@ __device__ __forceinline__ float finish_row(const WindowParams& p, int64_t at, f
 // One warp a row of a unit that spans CTAs: the piece of the CTA where it begins (slot
 // 2i + 1), then the first pieces (slots 2j) of the CTAs after it up to the one that ends it.
 template <int D, int ROWS, int TILE, typename T>
-__global__ void __launch_bounds__(128) k_join(const __grid_constant__ WindowParams p) {
-  grid_wait();
+__device__ __forceinline__ void join_row(const WindowParams& p) {
   const int first = blockIdx.x, lane = threadIdx.x & 31;
   const int row = blockIdx.y * 4 + (threadIdx.x >> 5);
   const int4 d = p.desc[first];
@@ -313,6 +330,12 @@ __global__ void __launch_bounds__(128) k_join(const __grid_constant__ WindowPara
     *reinterpret_cast<uint32_t*>(static_cast<char*>(p.a.out) + (at * D + lane * PER + e) * 2) =
         pack<T>(fmaf(acc[e], by, o.x * own), fmaf(acc[e + 1], by, o.y * own));
   }
+}
+
+template <int D, int ROWS, int TILE, typename T>
+__global__ void __launch_bounds__(128) k_join(const __grid_constant__ WindowParams p) {
+  grid_wait();
+  join_row<D, ROWS, TILE, T>(p);
 }
 
 // Lets a kernel have this much dynamic shared memory, once on each device.
