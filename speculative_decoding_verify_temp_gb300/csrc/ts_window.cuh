@@ -30,7 +30,7 @@ struct WindowParams {
   uint64_t wait_cycles;  // SM clock cycles that a wait may take (ts_window_tc.cu)
 };
 
-constexpr float kNone = -1e30f;     // the reference before any token
+constexpr float kNone = -3.4028234664e38f;  // the reference before any token: no score is below it
 
 template <typename T>
 __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1);

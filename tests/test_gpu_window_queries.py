@@ -110,3 +110,25 @@ def test_queries_near_the_ends_of_bf16(D, Hq, by):
     s["q"] = (s["q"].float() * by).to(BF16)
     scale = 0.1 / by
     check_rows(tv.window_attention(**s, sm_scale=scale, lse=True), wanted(s, windows, lens, scale), s)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq", [2, 64])
+@pytest.mark.parametrize("n,own", [(1, False), (40, False), (0, True), (40, True)])
+def test_scores_far_below_zero(D, Hq, n, own):
+    # every score is -D 1e30, which fp32 holds: the softmax is the mean of V all the same
+    q = torch.ones((1, Hq, D), dtype=BF16, device="cuda")
+    pages = 3
+    k = torch.full((pages, 1, 16, D), -1.0).to(ref.F8).cuda()
+    v = torch.randn((pages, 1, 16, D), generator=torch.Generator().manual_seed(56)).to(ref.F8).cuda()
+    ones = torch.ones((pages, 1), device="cuda")
+    new = dict(k_new=-q[:, :1], v_new=torch.full((1, 1, D), 0.5, dtype=BF16, device="cuda")) if own else {}
+    got = tv.window_attention(q, k, v, ones, ones.clone(), torch.arange(pages, dtype=torch.int32)[None].cuda(),
+                              torch.tensor([n], dtype=torch.int32).cuda(), sm_scale=1e30, lse=True, **new)
+    x = v.float().double().view(-1, D)[:n]
+    if own:
+        x = torch.cat([x, torch.full((1, D), 0.5, dtype=torch.float64, device="cuda")])
+    # equal scores: each is one product, the same for all, so that every probability is exact; sums and
+    # the output are rounded
+    assert ((got["out"].double() - x.mean(0)).abs() <= 2.0 ** -8 * x.mean(0).abs() + 2.0 ** -14 * x.abs().max()).all()
+    assert ((got["lse"].double() / (-D * 1e30) - 1).abs() <= 2.0 ** -18).all()
