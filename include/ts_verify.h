@@ -389,7 +389,7 @@ typedef struct ts_attn_args {
  * of it, fp16: above 2^-6). Rows and heads do not affect each other: one whose q holds a value
  * that is not finite gives NaN (if it sees a token), it alone. Probabilities
  * are good to 2^-11 each; what the smallest lose beyond that is together below 2^-11 of their row's sum.
- * Scales of V below 2^-100 count as 2^-100.
+ * Scales of V below 2^-80 count as 2^-80.
  * Workspace: ts_attention_workspace_size bytes of scratch (no zero fill needed) that no other
  * call uses meanwhile. */
 ts_status ts_window_attention(const ts_attn_args* args, void* workspace, size_t ws_bytes,

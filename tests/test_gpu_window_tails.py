@@ -118,3 +118,33 @@ def test_references_that_rise_and_fall_again():
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_many_small_probabilities_behind_a_large_one_64(dtype, rows, n, at):
     check(n, {"first": 0, "middle": n // 2, "last": n - 1}[at], rows, 64, dtype)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows", [(1, 8), (8, 8)])
+@pytest.mark.parametrize("large_first", [True, False])
+@pytest.mark.parametrize("vscale", [2.0 ** -100, 2.0 ** -80, 1.0, 2.0 ** 80])
+def test_sums_stay_in_range(vscale, large_first, rows, D):
+    # half of the tokens have score a, half 0, V is vscale everywhere. Sums hold probabilities over V's
+    # scale (2^-80 at least): references that rise late or fall must not take them out of fp32's range
+    n, page, (T, Hq) = 131072, 128, rows
+    B = torch.cuda.get_device_properties(0).multi_processor_count * (1 if D == 128 else 2)
+    pages = n // page
+    k = torch.zeros((pages, 1, page, D))
+    k[:pages // 2 if large_first else pages, 0, :, 0] = 1.0
+    if not large_first:
+        k[:pages // 2] = 0.0
+    a = 4 + torch.arange(T * Hq, dtype=torch.float64) * (128 // (T * Hq)) / 8
+    q = torch.zeros((T, Hq, D), dtype=torch.float64)
+    q[:, :, 0] = a.view(T, Hq)
+    ones = torch.ones((pages, 1)).cuda()
+    got = tv.window_attention(
+        q.to(BF16).repeat(B, 1, 1).cuda(), k.to(F8).cuda(), torch.ones_like(k).to(F8).cuda(), ones, ones * vscale,
+        torch.arange(pages, dtype=torch.int32).repeat(B, 1).cuda(),
+        torch.full((B,), n, dtype=torch.int32).cuda(), sm_scale=1.0, lse=True)
+    sums = (n / 32 + 64) * 2.0 ** -23  # as in check
+    o = got["out"].cpu().double() / max(vscale, 2.0 ** -80)
+    assert ((o - 1).abs() <= 2.0 ** -8 + (1 + 2.0 ** -8) * (2.0 ** -10 + 2.0 ** -16 + 2 * sums)).all(), (o - 1).abs().max()
+    lse = a + math.log(n // 2) + torch.log1p(torch.exp(-a))
+    z = (got["lse"].cpu().double().view(B, T * Hq) - lse).abs()
+    assert (z <= 2.0 ** -17 + sums + 2.0 ** -22 * (lse + 1)).all(), z.max()
