@@ -148,3 +148,32 @@ def test_sums_stay_in_range(vscale, large_first, rows, D):
     lse = a + math.log(n // 2) + torch.log1p(torch.exp(-a))
     z = (got["lse"].cpu().double().view(B, T * Hq) - lse).abs()
     assert (z <= 2.0 ** -17 + sums + 2.0 ** -22 * (lse + 1)).all(), z.max()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows", [(1, 8), (8, 8)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_a_token_that_outweighs_the_rest_comes_out_as_it_is(dtype, rows, D):
+    # two tokens, scores a and 0, V with a scale of any value: the large one's probability must not be rounded in
+    # the products alone. Its exponent and 2^x to 2^-18, the small one's rounding 2^-11 e^-6
+    T, Hq = rows
+    B = 64
+    g = torch.Generator().manual_seed(81)
+    k = torch.zeros((B, 1, 16, D))
+    k[:, 0, 0, 0] = 1.0
+    v = (torch.randn((B, 1, 16, D), generator=g) * 50).to(F8)
+    vs = torch.rand((B, 1), generator=g) + 0.5
+    a = 6 + torch.arange(T * Hq, dtype=torch.float64) / 16
+    q = torch.zeros((T, Hq, D), dtype=torch.float64)
+    q[:, :, 0] = a.view(T, Hq)
+    assert torch.equal(q.to(dtype).double(), q)
+    got = tv.window_attention(q.to(dtype).repeat(B, 1, 1).cuda(), k.to(F8).cuda(), v.cuda(), torch.ones((B, 1)).cuda(),
+                              vs.cuda(), torch.arange(B, dtype=torch.int32)[:, None].cuda(),
+                              torch.full((B,), 2, dtype=torch.int32).cuda(), sm_scale=1.0)["out"]
+    x = v.float().double()[:, 0, :2] * vs.double()[:, :, None]         # [B, 2, D]
+    w = torch.sigmoid(a)[None, :, None]
+    out = w * x[:, None, 0] + (1 - w) * x[:, None, 1]
+    off = (got.cpu().double().view(B, T * Hq, D) - out).abs()
+    top = x.abs().amax(1)[:, None]
+    far = off - (torch.finfo(dtype).eps / 2 * out.abs() + 1.01 * (2.0 ** -16 + 2.0 ** -11 * math.exp(-6)) * top)
+    assert far.max() <= 0, far.max()
