@@ -214,7 +214,7 @@ __device__ __forceinline__ void attend(const Params& p) {
       x.ks = x.vs = 1.f;
       if (page >= 0) {
         x.ks = __ldg(p.c.k_scale + (int64_t)page * p.c.heads + kvh);
-        x.vs = fmaxf(__ldg(p.c.v_scale + (int64_t)page * p.c.heads + kvh), kLeastScale);
+        x.vs = scale_of_v(__ldg(p.c.v_scale + (int64_t)page * p.c.heads + kvh), x.ks);
       }
     };
     Loaded next;

@@ -35,6 +35,11 @@ constexpr float kNone = -3.4028234664e38f;  // the reference before any token: n
 // V's scales are taken as this at least. Sums hold p / scale, p at most 2^15 (head_dim 64) or, where a
 // reference was lowered, 2^20 (128): 2^100 times the tokens stays in fp32's range.
 constexpr float kLeastScale = 0x1p-80f;
+// A NaN, which that would hide, reaches the rows through the scores.
+__device__ __forceinline__ float scale_of_v(float vs, float& ks) {
+  if (vs != vs) ks = vs;
+  return fmaxf(vs, kLeastScale);
+}
 
 template <typename T>
 __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1);

@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (page < 0 || !is_k) return;
         const int64_t at = (int64_t)page * p.c.heads + g.kvh;
         ks = __ldg(p.c.k_scale + at);
-        vs = fmaxf(__ldg(p.c.v_scale + at), kLeastScale);
+        vs = scale_of_v(__ldg(p.c.v_scale + at), ks);
       };
       Segment ahead;
       bool more = line.next(p, s);
