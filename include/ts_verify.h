@@ -444,6 +444,95 @@ typedef struct ts_kv_read_args {
  * [0, total_rows] is skipped. Rows that no request owns are left as they were. */
 ts_status ts_kv_read(const ts_kv_read_args* args, cudaStream_t stream);
 
+/* ---- The pages of the cache among requests -------------------------------------------------
+ *
+ * A pool's pages have counted holders: refcount[p] (int32 [num_pages]) is the number of table
+ * entries that hold page p, and of whatever else the caller counts for it (a prefix kept for
+ * later). A page with a count of 0 or less is free. The entries of request b are the first
+ * ceil(seq_len[b] / page_size) of its row; those that name no page of the pool are carried along
+ * and count for nothing. The calls below run on the device alone, in stream order, so that a
+ * captured step can fork, grow and end requests:
+ *
+ *   ts_kv_fork      continuations of requests: tables that name the same pages
+ *   ts_kv_reserve   room for the tokens a step will append, with a copy of a page that others
+ *                   hold too: ts_kv_append may write to what it returns
+ *   ts_kv_free      requests end
+ *   ts_kv_compact   the live pages move to the lowest ids, so that the pool can shrink
+ *
+ * Results do not depend on timing: pages are given out by number, lowest first. refcount_out may
+ * be refcount (in place) or an array apart from it; table_out may be the cache's page_table, with
+ * its ld (in place; not for ts_kv_fork), or apart from it. Arrays that overlap otherwise give
+ * TS_ERR_INVALID_ARG. Nothing else may use the pool's tables, counts or pages meanwhile. */
+typedef struct ts_kv_fork_args {
+  const ts_kv_cache* cache;  /* host struct: the sources */
+  const int32_t* sources;    /* [n]: request i of the result continues request sources[i];
+                                outside [0, batch): an empty one (length 0) */
+  int64_t n;                 /* in [1, 65536] */
+  const int32_t* refcount;   /* [num_pages] */
+  int32_t* refcount_out;     /* [num_pages]: one more for each entry of the result */
+  int32_t* table_out;        /* [n, ld_out]: max_pages entries a row, -1 behind the last */
+  int64_t ld_out;            /* >= max_pages */
+  int32_t* lens_out;         /* [n] */
+} ts_kv_fork_args;
+
+/* All pages are shared, a last page that is partly filled too: ts_kv_reserve parts it before
+ * anything is appended. The sources go on to hold theirs. */
+ts_status ts_kv_fork(const ts_kv_fork_args* args, cudaStream_t stream);
+
+typedef struct ts_kv_free_args {
+  const ts_kv_cache* cache;  /* host struct */
+  const int32_t* release;    /* [batch]: requests with a value other than 0 end; NULL: all */
+  const int32_t* refcount;   /* [num_pages] */
+  int32_t* refcount_out;     /* [num_pages]: one less for each entry of an ended request */
+} ts_kv_free_args;
+
+/* Tables and lengths are left as they are: an ended request's row names pages that are no longer
+ * its own, and must not be released twice. */
+ts_status ts_kv_free(const ts_kv_free_args* args, cudaStream_t stream);
+
+typedef struct ts_kv_reserve_args {
+  const ts_kv_cache* cache;  /* host struct; seq_lens: tokens now (not updated) */
+  const int32_t* new_lens;   /* [batch] tokens to have room for, taken as clamped to
+                                [seq_len, max_pages * page_size] */
+  const int32_t* refcount;   /* [num_pages] */
+  int32_t* refcount_out;     /* [num_pages] */
+  int32_t* table_out;        /* [batch, ld_out]: max_pages entries a row, -1 behind the last */
+  int64_t ld_out;
+  int32_t* reserved;         /* [batch] out: tokens the request has room for: new_lens[b], or
+                                seq_len[b] where the pool had too few pages */
+} ts_kv_reserve_args;
+
+/* Request b asks for the pages that new_lens[b] tokens need beyond the ones it has, and, if it grows
+ * and its last page is partly filled and has more than one holder, for a page to copy that one to
+ * (codes of its seq_len % page_size tokens, scales), whose count falls by one. Where the requests
+ * of this call that would copy a page are as many as its holders, the last of them keeps it
+ * instead. Pages are given out in request order, the copy first, the lowest free page (of those
+ * free before the call) first, each with a count of 1. A request is served if the pages asked for
+ * by it and those before it are there, or if it asks for none and keeps none in that way; one that is not
+ * served keeps its row, its pages and its length. Its own requests aside, a copied page is not
+ * written. Workspace: ts_kv_pages_workspace_size bytes of scratch (no zero fill needed) that no
+ * other call uses meanwhile. */
+ts_status ts_kv_reserve(const ts_kv_reserve_args* args, void* workspace, size_t ws_bytes,
+                        cudaStream_t stream);
+
+typedef struct ts_kv_compact_args {
+  const ts_kv_cache* cache;  /* host struct */
+  const int32_t* refcount;   /* [num_pages] */
+  int32_t* refcount_out;     /* [num_pages] */
+  int32_t* table_out;        /* [batch, ld_out]: max_pages entries a row; -1 behind the last and
+                                where an entry names no live page */
+  int64_t ld_out;
+  int32_t* live;             /* [1] out: n, the pages with a count above 0 */
+} ts_kv_compact_args;
+
+/* The k-th lowest live page with an id of n or more moves (codes of K and V, scales, count) to the
+ * k-th lowest free page below n; the tables follow. Afterwards pages 0 .. n - 1 are the live
+ * ones; the others are as they were. Tables that are not in the batch do not follow. Workspace as
+ * for ts_kv_reserve. */
+ts_status ts_kv_compact(const ts_kv_compact_args* args, void* workspace, size_t ws_bytes,
+                        cudaStream_t stream);
+size_t ts_kv_pages_workspace_size(int64_t batch, int64_t num_pages);
+
 typedef struct ts_tree_args {
   const float* target_probs; /* [total_rows, ld] fp32: p of each node */
   int64_t vocab, ld;

@@ -10,8 +10,13 @@ from .tsverify import (  # noqa: F401
     gather_logprobs,
     gumbel_max_sample,
     kv_append,
+    kv_compact,
+    kv_fork,
+    kv_free,
     kv_read,
+    kv_reserve,
     make_attention_workspace,
+    make_pages_workspace,
     make_workspace,
     softmax_temp,
     topk_topp_renorm,

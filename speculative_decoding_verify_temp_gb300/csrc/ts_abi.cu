@@ -135,6 +135,38 @@ ts_status check_window(const int32_t* qo_indptr, int64_t total_rows, int64_t bat
   return TS_OK;
 }
 
+// Arrays that are the same (same: allowed) or apart. Bytes; an empty one overlaps nothing.
+bool overlap(const void* a, int64_t bytes_a, const void* b, int64_t bytes_b, bool same) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  if (bytes_a <= 0 || bytes_b <= 0 || (same && x == y)) return false;
+  return x < y + (uintptr_t)bytes_b && y < x + (uintptr_t)bytes_a;
+}
+
+// refcount and refcount_out of a call on a pool.
+ts_status check_counts(const ts_kv_cache& c, const int32_t* in, int32_t* out) {
+  if (c.num_pages > 0 && (!in || !out)) return fail(TS_ERR_INVALID_ARG, "refcount and refcount_out are required");
+  if (overlap(in, c.num_pages * 4, out, c.num_pages * 4, true))
+    return fail(TS_ERR_INVALID_ARG, "refcount_out must be refcount or apart from it");
+  return TS_OK;
+}
+
+// A table of `rows` rows that a call writes.
+ts_status check_table(const ts_kv_cache& c, const int32_t* out, int64_t ld, int64_t rows, bool in_place) {
+  if (c.max_pages > 0 && !out) return fail(TS_ERR_INVALID_ARG, "table_out is required");
+  if (ld < c.max_pages || ld > (int64_t)1 << 40) return fail(TS_ERR_INVALID_ARG, "ld_out must be >= max_pages");
+  auto bytes = [&](int64_t r, int64_t l) { return c.max_pages ? ((r - 1) * l + c.max_pages) * 4 : 0; };
+  if (overlap(out, bytes(rows, ld), c.page_table, bytes(c.batch, c.ld_table), in_place && (ld == c.ld_table || c.batch == 1)))
+    return fail(TS_ERR_INVALID_ARG, "table_out must be %sapart from page_table", in_place ? "page_table, with its ld, or " : "");
+  return TS_OK;
+}
+
+ts_status check_pages_workspace(const ts_kv_cache& c, const void* ws, size_t bytes) {
+  const size_t need = tsv::pages_workspace(c.batch, c.num_pages);
+  if (!ws || bytes < need || !multiple16(ws, 0, 0))
+    return fail(TS_ERR_INVALID_ARG, "workspace must have %zu 16-byte aligned bytes (got %zu)", need, bytes);
+  return TS_OK;
+}
+
 ts_status launched(cudaError_t e, const char* what) {
   if (e != cudaSuccess) return cuda_fail(e, what);
   g_msg[0] = 0;
@@ -726,6 +758,60 @@ ts_status ts_kv_read(const ts_kv_read_args* p, cudaStream_t stream) {
   if (!multiple16(p->k_out, 0, 0) || !multiple16(p->v_out, 0, 0))
     return fail(TS_ERR_INVALID_ARG, "k_out and v_out must be 16-byte aligned");
   return launched(tsv::launch_kv_read(*p->cache, *p, sm_count(), stream), "cache read launch");
+}
+
+ts_status ts_kv_fork(const ts_kv_fork_args* p, cudaStream_t stream) {
+  if (!p) return fail(TS_ERR_INVALID_ARG, "args is NULL");
+  ts_status st;
+  if ((st = check_cache(p->cache)) != TS_OK) return st;
+  const ts_kv_cache& c = *p->cache;
+  if (p->n < 1 || p->n > 1 << 16) return fail(TS_ERR_INVALID_ARG, "n must be in [1, 65536]");
+  if (!p->sources || !p->lens_out) return fail(TS_ERR_INVALID_ARG, "sources and lens_out are required");
+  if ((st = check_counts(c, p->refcount, p->refcount_out)) != TS_OK) return st;
+  if ((st = check_table(c, p->table_out, p->ld_out, p->n, false)) != TS_OK) return st;
+  if (overlap(p->lens_out, p->n * 4, c.seq_lens, c.batch * 4, false) || overlap(p->lens_out, p->n * 4, p->sources, p->n * 4, false))
+    return fail(TS_ERR_INVALID_ARG, "lens_out must be apart from seq_lens and sources");
+  return launched(tsv::launch_kv_fork(c, *p, sm_count(), stream), "fork launch");
+}
+
+ts_status ts_kv_free(const ts_kv_free_args* p, cudaStream_t stream) {
+  if (!p) return fail(TS_ERR_INVALID_ARG, "args is NULL");
+  ts_status st;
+  if ((st = check_cache(p->cache)) != TS_OK) return st;
+  if ((st = check_counts(*p->cache, p->refcount, p->refcount_out)) != TS_OK) return st;
+  return launched(tsv::launch_kv_free(*p->cache, *p, sm_count(), stream), "free launch");
+}
+
+ts_status ts_kv_reserve(const ts_kv_reserve_args* p, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  if (!p) return fail(TS_ERR_INVALID_ARG, "args is NULL");
+  ts_status st;
+  if ((st = check_cache(p->cache)) != TS_OK) return st;
+  const ts_kv_cache& c = *p->cache;
+  if (!p->new_lens || !p->reserved) return fail(TS_ERR_INVALID_ARG, "new_lens and reserved are required");
+  if ((st = check_counts(c, p->refcount, p->refcount_out)) != TS_OK) return st;
+  if ((st = check_table(c, p->table_out, p->ld_out, c.batch, true)) != TS_OK) return st;
+  if (overlap(p->reserved, c.batch * 4, c.seq_lens, c.batch * 4, false) ||
+      overlap(p->reserved, c.batch * 4, p->new_lens, c.batch * 4, false))
+    return fail(TS_ERR_INVALID_ARG, "reserved must be apart from seq_lens and new_lens");
+  if ((st = check_pages_workspace(c, workspace, ws_bytes)) != TS_OK) return st;
+  return launched(tsv::launch_kv_reserve(c, *p, workspace, stream), "reserve launch");
+}
+
+ts_status ts_kv_compact(const ts_kv_compact_args* p, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  if (!p) return fail(TS_ERR_INVALID_ARG, "args is NULL");
+  ts_status st;
+  if ((st = check_cache(p->cache)) != TS_OK) return st;
+  const ts_kv_cache& c = *p->cache;
+  if (!p->live) return fail(TS_ERR_INVALID_ARG, "live is required");
+  if ((st = check_counts(c, p->refcount, p->refcount_out)) != TS_OK) return st;
+  if ((st = check_table(c, p->table_out, p->ld_out, c.batch, true)) != TS_OK) return st;
+  if ((st = check_pages_workspace(c, workspace, ws_bytes)) != TS_OK) return st;
+  return launched(tsv::launch_kv_compact(c, *p, workspace, sm_count(), stream), "compact launch");
+}
+
+size_t ts_kv_pages_workspace_size(int64_t batch, int64_t num_pages) {
+  if (batch < 1 || batch > 1 << 16 || num_pages < 0 || num_pages > INT32_MAX) return 0;
+  return tsv::pages_workspace(batch, num_pages);
 }
 
 ts_status ts_tree_spec_sampling(const ts_tree_args* p, cudaStream_t stream) {

@@ -259,8 +259,8 @@ cudaError_t staged_read_error(uint32_t* word, int clear);
 int staged_max_vocab(int bf16);
 
 // ---------------------------------------------------------------------------------
-// Around the verify step (ts_window.cu, ts_kvcache.cu, ts_tree.cu): arguments checked by
-// the ABI.
+// Around the verify step (ts_window.cu, ts_kvcache.cu, ts_kvpages.cu, ts_tree.cu): arguments
+// checked by the ABI.
 cudaError_t launch_window(const ts_kv_cache& c, const ts_attn_args& a, void* ws, int sms, uint64_t wait_cycles,
                           cudaStream_t s);
 size_t window_workspace(int64_t batch, int64_t total_rows, int heads_q, int heads, int head_dim, int sms);
@@ -269,6 +269,11 @@ struct WindowParams;
 cudaError_t launch_window_tc(const WindowParams& p, int rows, int sms, cudaStream_t s);  // head_dim 128
 cudaError_t launch_kv_append(const ts_kv_cache& c, const ts_kv_append_args& a, cudaStream_t s);
 cudaError_t launch_kv_read(const ts_kv_cache& c, const ts_kv_read_args& a, int sms, cudaStream_t s);
+size_t pages_workspace(int64_t batch, int64_t num_pages);
+cudaError_t launch_kv_fork(const ts_kv_cache& c, const ts_kv_fork_args& a, int sms, cudaStream_t s);
+cudaError_t launch_kv_free(const ts_kv_cache& c, const ts_kv_free_args& a, int sms, cudaStream_t s);
+cudaError_t launch_kv_reserve(const ts_kv_cache& c, const ts_kv_reserve_args& a, void* ws, cudaStream_t s);
+cudaError_t launch_kv_compact(const ts_kv_cache& c, const ts_kv_compact_args& a, void* ws, int sms, cudaStream_t s);
 cudaError_t launch_tree(const ts_tree_args& a, int sms, cudaStream_t s);
 
 }  // namespace tsv

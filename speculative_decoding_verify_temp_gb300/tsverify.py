@@ -173,6 +173,55 @@ class KvReadArgs(ctypes.Structure):
     ]
 
 
+class KvForkArgs(ctypes.Structure):
+    """ts_kv_fork_args of include/ts_verify.h."""
+    _fields_ = [
+        ("cache", ctypes.POINTER(KvCache)),
+        ("sources", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("refcount", ctypes.c_void_p),
+        ("refcount_out", ctypes.c_void_p),
+        ("table_out", ctypes.c_void_p),
+        ("ld_out", ctypes.c_int64),
+        ("lens_out", ctypes.c_void_p),
+    ]
+
+
+class KvFreeArgs(ctypes.Structure):
+    """ts_kv_free_args of include/ts_verify.h."""
+    _fields_ = [
+        ("cache", ctypes.POINTER(KvCache)),
+        ("release", ctypes.c_void_p),
+        ("refcount", ctypes.c_void_p),
+        ("refcount_out", ctypes.c_void_p),
+    ]
+
+
+class KvReserveArgs(ctypes.Structure):
+    """ts_kv_reserve_args of include/ts_verify.h."""
+    _fields_ = [
+        ("cache", ctypes.POINTER(KvCache)),
+        ("new_lens", ctypes.c_void_p),
+        ("refcount", ctypes.c_void_p),
+        ("refcount_out", ctypes.c_void_p),
+        ("table_out", ctypes.c_void_p),
+        ("ld_out", ctypes.c_int64),
+        ("reserved", ctypes.c_void_p),
+    ]
+
+
+class KvCompactArgs(ctypes.Structure):
+    """ts_kv_compact_args of include/ts_verify.h."""
+    _fields_ = [
+        ("cache", ctypes.POINTER(KvCache)),
+        ("refcount", ctypes.c_void_p),
+        ("refcount_out", ctypes.c_void_p),
+        ("table_out", ctypes.c_void_p),
+        ("ld_out", ctypes.c_int64),
+        ("live", ctypes.c_void_p),
+    ]
+
+
 class TreeArgs(ctypes.Structure):
     """ts_tree_args of include/ts_verify.h."""
     _fields_ = [
@@ -239,9 +288,15 @@ def load():
     L.ts_window_attention.argtypes = [ctypes.POINTER(AttnArgs), P, ctypes.c_size_t, P]
     L.ts_window_attention.restype = st
     for name, args in (("ts_kv_append", KvAppendArgs), ("ts_kv_read", KvReadArgs),
+                       ("ts_kv_fork", KvForkArgs), ("ts_kv_free", KvFreeArgs),
                        ("ts_tree_spec_sampling", TreeArgs)):
         getattr(L, name).argtypes = [ctypes.POINTER(args), P]
         getattr(L, name).restype = st
+    for name, args in (("ts_kv_reserve", KvReserveArgs), ("ts_kv_compact", KvCompactArgs)):
+        getattr(L, name).argtypes = [ctypes.POINTER(args), P, ctypes.c_size_t, P]
+        getattr(L, name).restype = st
+    L.ts_kv_pages_workspace_size.argtypes = [i64, i64]
+    L.ts_kv_pages_workspace_size.restype = ctypes.c_size_t
     _lib = L
     return L
 
@@ -694,6 +749,125 @@ def kv_read(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, *, out_ind
         if st:
             _check("ts_kv_read", st)
     return dict(k=k, v=v)
+
+
+def _counts(c, refcount, refcount_out):
+    """The addresses of the counts, and the tensor that the call's go to (in place by default)."""
+    if refcount_out is None:
+        refcount_out = refcount
+    return (_int32("refcount", refcount, c.num_pages), _int32("refcount_out", refcount_out, c.num_pages),
+            refcount_out)
+
+
+def _table_out(name, t, rows, P):
+    """The ld of a table that a call writes."""
+    if t.dtype != torch.int32 or t.shape != (rows, P) or (P > 1 and t.stride(1) != 1) or \
+            (rows > 1 and t.stride(0) < P):
+        raise ValueError(f"{name} must be an int32 tensor of shape ({rows}, {P}) with unit stride in the last "
+                         "dimension and rows that do not overlap")
+    return t.stride(0) if rows > 1 and P > 0 else P
+
+
+def pages_workspace_size(batch: int, num_pages: int) -> int:
+    return int(load().ts_kv_pages_workspace_size(batch, num_pages))
+
+
+def make_pages_workspace(batch: int, num_pages: int, device=None):
+    """Scratch for kv_reserve and kv_compact calls of this size that do not overlap."""
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        return torch.empty(pages_workspace_size(batch, num_pages), dtype=torch.uint8, device="cuda")
+
+
+def _pages_workspace(workspace, c, device):
+    if workspace is None:
+        return torch.empty(pages_workspace_size(c.batch, c.num_pages), dtype=torch.uint8, device=device)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace
+
+
+def kv_fork(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, *, sources, refcount,
+            refcount_out=None, out=None, stream=None):
+    """Continuations of requests that share their pages: request i of the result continues
+    request sources[i] (int32 [n]; outside the batch: an empty one). refcount (int32 [pages],
+    holders of each page) counts each entry of the result, in place or into refcount_out.
+    Returns dict(page_table [n, max_pages], seq_lens [n], refcount); out: a pair of tensors for the
+    first two."""
+    c, device = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)
+    count, count_out, refcount_out = _counts(c, refcount, refcount_out)
+    n = sources.shape[0] if sources.dim() == 1 else 0
+    src = _int32("sources", sources, n)
+    _same_device(device, sources, refcount, refcount_out, *(out or ()))
+    with _on(device, stream) as s:
+        if out is None:
+            table = torch.empty((n, c.max_pages), dtype=torch.int32, device=k_cache.device)
+            lens = torch.empty((n,), dtype=torch.int32, device=k_cache.device)
+        else:
+            table, lens = out
+        a = KvForkArgs(ctypes.pointer(c), src, n, count, count_out, table.data_ptr(),
+                       _table_out("page_table of out", table, n, c.max_pages), _int32("seq_lens of out", lens, n))
+        st = load().ts_kv_fork(a, s)
+        if st:
+            _check("ts_kv_fork", st)
+    return dict(page_table=table, seq_lens=lens, refcount=refcount_out)
+
+
+def kv_free(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, *, refcount, release=None,
+            refcount_out=None, stream=None):
+    """Releases the pages of the requests with release[b] != 0 (int32 [B]; without it: of all):
+    each of their entries counts one holder less in refcount (int32 [pages]), in place or into
+    refcount_out, which is returned. Tables and lengths stay as they are."""
+    c, device = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)
+    count, count_out, refcount_out = _counts(c, refcount, refcount_out)
+    _same_device(device, refcount, refcount_out, release)
+    with _on(device, stream) as s:
+        a = KvFreeArgs(ctypes.pointer(c), _int32("release", release, c.batch), count, count_out)
+        st = load().ts_kv_free(a, s)
+        if st:
+            _check("ts_kv_free", st)
+    return refcount_out
+
+
+def kv_reserve(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, *, new_lens, refcount,
+               refcount_out=None, page_table_out=None, workspace=None, stream=None):
+    """Room for new_lens (int32 [B]) tokens, ready for kv_append: fresh pages, and a copy of a
+    last page that others hold too. refcount and page_table are updated in place, or into
+    refcount_out and page_table_out. Returns dict(page_table, refcount, reserved): reserved[b]
+    is new_lens[b], or seq_lens[b] where the pool had too few pages left."""
+    c, device = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)
+    count, count_out, refcount_out = _counts(c, refcount, refcount_out)
+    table = page_table if page_table_out is None else page_table_out
+    ld = _table_out("page_table_out", table, c.batch, c.max_pages)
+    new = _int32("new_lens", new_lens, c.batch)
+    _same_device(device, new_lens, refcount, refcount_out, table, workspace)
+    with _on(device, stream) as s:
+        reserved = torch.empty((c.batch,), dtype=torch.int32, device=k_cache.device)
+        workspace = _pages_workspace(workspace, c, k_cache.device)
+        a = KvReserveArgs(ctypes.pointer(c), new, count, count_out, table.data_ptr(), ld, reserved.data_ptr())
+        st = load().ts_kv_reserve(a, workspace.data_ptr(), workspace.nbytes, s)
+        if st:
+            _check("ts_kv_reserve", st)
+    return dict(page_table=table, refcount=refcount_out, reserved=reserved)
+
+
+def kv_compact(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, *, refcount,
+               refcount_out=None, page_table_out=None, workspace=None, stream=None):
+    """Moves the live pages (refcount above 0) to the lowest ids, and the tables with them, in
+    place or into refcount_out and page_table_out. Returns dict(page_table, refcount, live):
+    live int32 [1], the number of live pages."""
+    c, device = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)
+    count, count_out, refcount_out = _counts(c, refcount, refcount_out)
+    table = page_table if page_table_out is None else page_table_out
+    ld = _table_out("page_table_out", table, c.batch, c.max_pages)
+    _same_device(device, refcount, refcount_out, table, workspace)
+    with _on(device, stream) as s:
+        live = torch.empty((1,), dtype=torch.int32, device=k_cache.device)
+        workspace = _pages_workspace(workspace, c, k_cache.device)
+        a = KvCompactArgs(ctypes.pointer(c), count, count_out, table.data_ptr(), ld, live.data_ptr())
+        st = load().ts_kv_compact(a, workspace.data_ptr(), workspace.nbytes, s)
+        if st:
+            _check("ts_kv_compact", st)
+    return dict(page_table=table, refcount=refcount_out, live=live)
 
 
 def tree_spec_sampling(target_probs, D: int, tokens, parents, uniforms, *, qo_indptr=None,
