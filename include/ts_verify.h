@@ -397,6 +397,31 @@ ts_status ts_window_attention(const ts_attn_args* args, void* workspace, size_t 
 size_t ts_attention_workspace_size(int64_t batch, int64_t total_rows, int32_t heads_q,
                                    int32_t heads, int32_t head_dim);
 
+typedef struct ts_shared_args {
+  const ts_attn_args* attn;     /* host struct: the windows, as for ts_window_attention */
+  const int32_t* group_indptr;  /* [groups + 1]: group g is the requests group_indptr[g] ..
+                                   group_indptr[g+1] - 1. Must not decrease; a pair that does not
+                                   fit is no group, and a request in none shares nothing */
+  const int32_t* shared_lens;   /* [groups] tokens that the requests of a group have in common */
+  int64_t groups;               /* in [1, 65536] */
+} ts_shared_args;
+
+/* ts_window_attention for requests that continue common prefixes: the first tokens of a group's
+ * requests are read and multiplied once, for the rows of all of its windows together. How many
+ * tokens: shared_lens[g], at most the least seq_len of the group's requests that have a window, in
+ * whole pages; the rest of a request is read for that request. The pages of the shared tokens
+ * must be the same in the tables of all of the group's requests (as ts_kv_fork leaves them): they
+ * are taken from the first one with a window. With such tables the result is that of
+ * ts_window_attention, to the same accuracy and with the same treatment of rows that see nothing, of values
+ * that are not finite and of pages outside the pool; q is good to 2^-31 of the largest |q| of its row
+ * and head in its products with shared tokens. Workspace:
+ * ts_shared_attention_workspace_size bytes of scratch (no zero fill needed) that no other call uses
+ * meanwhile. */
+ts_status ts_shared_attention(const ts_shared_args* args, void* workspace, size_t ws_bytes,
+                              cudaStream_t stream);
+size_t ts_shared_attention_workspace_size(int64_t batch, int64_t groups, int64_t total_rows,
+                                          int32_t heads_q, int32_t heads, int32_t head_dim);
+
 typedef struct ts_kv_append_args {
   const ts_kv_cache* cache;  /* host struct; seq_lens: tokens before the call (not updated) */
   const void* k;             /* row r, head h at k + r*k_row_stride + h*k_head_stride (bytes,

@@ -17,7 +17,9 @@ from .tsverify import (  # noqa: F401
     kv_reserve,
     make_attention_workspace,
     make_pages_workspace,
+    make_shared_attention_workspace,
     make_workspace,
+    shared_attention,
     softmax_temp,
     topk_topp_renorm,
     tree_spec_sampling,

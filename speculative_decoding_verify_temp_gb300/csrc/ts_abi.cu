@@ -16,8 +16,8 @@ namespace {
 
 thread_local char g_msg[512] = "";
 
-// SM clock cycles a stage wait of the chain kernel, or a wait of window attention, may take
-// before it gives up.
+// SM clock cycles a stage wait of the chain kernel, or a wait of window or shared attention, may
+// take before it gives up.
 constexpr uint64_t kDefaultWaitCycles = (uint64_t)1 << 32;
 std::atomic<uint64_t> g_wait_cycles{kDefaultWaitCycles};
 
@@ -167,6 +167,30 @@ ts_status check_pages_workspace(const ts_kv_cache& c, const void* ws, size_t byt
   return TS_OK;
 }
 
+ts_status check_attention(const ts_attn_args* p) {
+  if (!p) return fail(TS_ERR_INVALID_ARG, "args is NULL");
+  ts_status st;
+  if ((st = check_cache(p->cache)) != TS_OK) return st;
+  const ts_kv_cache& c = *p->cache;
+  if (p->dtype != TS_BF16 && p->dtype != TS_F16)
+    return fail(TS_ERR_UNSUPPORTED_DTYPE, "attention takes bf16 or fp16, not dtype %d", p->dtype);
+  if (p->heads_q < 1 || p->heads_q > kMaxHeadsQ || p->heads_q % c.heads)
+    return fail(TS_ERR_INVALID_ARG, "heads_q (%d) must be a multiple of the cache's %d heads, at most %d", p->heads_q,
+                c.heads, kMaxHeadsQ);
+  if ((st = check_window(p->qo_indptr, p->total_rows, c.batch)) != TS_OK) return st;
+  if (p->total_rows * (int64_t)p->heads_q >= (int64_t)1 << 31)
+    return fail(TS_ERR_INVALID_ARG, "total_rows * heads_q must be below 2^31");
+  if (!p->q || !p->out || (p->k_new == nullptr) != (p->v_new == nullptr))
+    return fail(TS_ERR_INVALID_ARG, "q and out are required, k_new and v_new come together");
+  if (p->parents && !p->k_new)
+    return fail(TS_ERR_INVALID_ARG, "parents describe the window's own rows: k_new and v_new are required");
+  if (!multiple16(p->q, p->q_row_stride, p->q_head_stride) ||
+      !multiple16(p->k_new, p->k_row_stride, p->k_head_stride) ||
+      !multiple16(p->v_new, p->v_row_stride, p->v_head_stride) || !multiple16(p->out, 0, 0))
+    return fail(TS_ERR_INVALID_ARG, "q, k_new, v_new and out need 16-byte aligned addresses and strides");
+  return TS_OK;
+}
+
 ts_status launched(cudaError_t e, const char* what) {
   if (e != cudaSuccess) return cuda_fail(e, what);
   g_msg[0] = 0;
@@ -240,13 +264,14 @@ ts_status ts_device_error(uint32_t* word_host, int clear) {
   if (!word_host) return fail(TS_ERR_INVALID_ARG, "word_host is NULL");
   uint32_t w = 0;
   cudaError_t e = tsv::staged_read_error(&w, clear);
-  uint32_t w2 = 0, w3 = 0, w4 = 0, w5 = 0;
+  uint32_t w2 = 0, w3 = 0, w4 = 0, w5 = 0, w6 = 0;
   if (e == cudaSuccess) e = tsv::row_read_error(&w2, clear);
   if (e == cudaSuccess) e = tsv::softmax_read_error(&w3, clear);
   if (e == cudaSuccess) e = tsv::chain_read_error(&w4, clear);
   if (e == cudaSuccess) e = tsv::window_read_error(&w5, clear);
+  if (e == cudaSuccess) e = tsv::shared_read_error(&w6, clear);
   if (e != cudaSuccess) return cuda_fail(e, "reading the device error word");
-  w |= (w2 << 8) | (w3 << 16) | (w4 << 24) | (w5 << 27);
+  w |= (w2 << 8) | (w3 << 16) | (w4 << 24) | (w5 << 27) | (w6 << 28);
   *word_host = w;
   if (w) return fail(TS_ERR_TIMEOUT, "a bounded device wait gave up (word 0x%x)", w);
   g_msg[0] = 0;
@@ -691,26 +716,9 @@ ts_status ts_gather_logprobs(const void* x, ts_dtype dt, int32_t is_probs, int64
 
 ts_status ts_window_attention(const ts_attn_args* p, void* workspace, size_t ws_bytes,
                               cudaStream_t stream) {
-  if (!p) return fail(TS_ERR_INVALID_ARG, "args is NULL");
   ts_status st;
-  if ((st = check_cache(p->cache)) != TS_OK) return st;
+  if ((st = check_attention(p)) != TS_OK) return st;
   const ts_kv_cache& c = *p->cache;
-  if (p->dtype != TS_BF16 && p->dtype != TS_F16)
-    return fail(TS_ERR_UNSUPPORTED_DTYPE, "attention takes bf16 or fp16, not dtype %d", p->dtype);
-  if (p->heads_q < 1 || p->heads_q > kMaxHeadsQ || p->heads_q % c.heads)
-    return fail(TS_ERR_INVALID_ARG, "heads_q (%d) must be a multiple of the cache's %d heads, at most %d", p->heads_q,
-                c.heads, kMaxHeadsQ);
-  if ((st = check_window(p->qo_indptr, p->total_rows, c.batch)) != TS_OK) return st;
-  if (p->total_rows * (int64_t)p->heads_q >= (int64_t)1 << 31)
-    return fail(TS_ERR_INVALID_ARG, "total_rows * heads_q must be below 2^31");
-  if (!p->q || !p->out || (p->k_new == nullptr) != (p->v_new == nullptr))
-    return fail(TS_ERR_INVALID_ARG, "q and out are required, k_new and v_new come together");
-  if (p->parents && !p->k_new)
-    return fail(TS_ERR_INVALID_ARG, "parents describe the window's own rows: k_new and v_new are required");
-  if (!multiple16(p->q, p->q_row_stride, p->q_head_stride) ||
-      !multiple16(p->k_new, p->k_row_stride, p->k_head_stride) ||
-      !multiple16(p->v_new, p->v_row_stride, p->v_head_stride) || !multiple16(p->out, 0, 0))
-    return fail(TS_ERR_INVALID_ARG, "q, k_new, v_new and out need 16-byte aligned addresses and strides");
   const size_t need = tsv::window_workspace(c.batch, p->total_rows, p->heads_q, c.heads, c.head_dim, sm_count());
   if (!workspace || ws_bytes < need || !multiple16(workspace, 0, 0))
     return fail(TS_ERR_INVALID_ARG, "workspace must have %zu 16-byte aligned bytes (got %zu)", need, ws_bytes);
@@ -724,6 +732,27 @@ size_t ts_attention_workspace_size(int64_t batch, int64_t total_rows, int32_t he
       heads_q < 1 || heads_q > kMaxHeadsQ || heads_q % heads || (head_dim != 64 && head_dim != 128))
     return 0;
   return tsv::window_workspace(batch, total_rows, heads_q, heads, head_dim, sm_count());
+}
+
+ts_status ts_shared_attention(const ts_shared_args* p, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  if (!p) return fail(TS_ERR_INVALID_ARG, "args is NULL");
+  ts_status st;
+  if ((st = check_attention(p->attn)) != TS_OK) return st;
+  const ts_attn_args& a = *p->attn;
+  const ts_kv_cache& c = *a.cache;
+  if (p->groups < 1 || p->groups > 1 << 16) return fail(TS_ERR_INVALID_ARG, "groups must be in [1, 65536]");
+  if (!p->group_indptr || !p->shared_lens) return fail(TS_ERR_INVALID_ARG, "group_indptr and shared_lens are required");
+  const size_t need = tsv::shared_workspace(c.batch, p->groups, a.total_rows, a.heads_q, c.heads, c.head_dim, sm_count());
+  if (!workspace || ws_bytes < need || !multiple16(workspace, 0, 0))
+    return fail(TS_ERR_INVALID_ARG, "workspace must have %zu 16-byte aligned bytes (got %zu)", need, ws_bytes);
+  const uint64_t wait_cycles = g_wait_cycles.load(std::memory_order_relaxed);
+  return launched(tsv::launch_shared(*p, workspace, sm_count(), wait_cycles, stream), "shared attention launch");
+}
+
+size_t ts_shared_attention_workspace_size(int64_t batch, int64_t groups, int64_t total_rows, int32_t heads_q, int32_t heads,
+                                          int32_t head_dim) {
+  if (groups < 1 || groups > 1 << 16 || ts_attention_workspace_size(batch, total_rows, heads_q, heads, head_dim) == 0) return 0;
+  return tsv::shared_workspace(batch, groups, total_rows, heads_q, heads, head_dim, sm_count());
 }
 
 ts_status ts_kv_append(const ts_kv_append_args* p, cudaStream_t stream) {

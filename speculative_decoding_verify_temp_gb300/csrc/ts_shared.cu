@@ -1,0 +1,725 @@
+// Attention of windows whose requests share a prefix: the prefix is read and multiplied once for all
+// rows of a group, the rest of each request by window attention (ts_window.cu, ts_window_tc.cu),
+// which takes the prefix's part of a row in.
+//
+//   k_plan         the groups: rows, shared tokens (whole pages); what each request has left
+//   k_prefix       one persistent CTA an SM: the shared tokens of the groups
+//   k_prefix_join  joins the pieces of units that more than one CTA worked on
+//
+// The rows of a group's windows, all query heads of a KV head, are one matrix, so the products are
+// proper matrix products: 128 rows of Q are the M = 128 of tcgen05.mma (kind f16),
+//
+//   S [128 x 128 tokens] = Q [128 x D] K^T        O [128 x D] += P [128 x 128 tokens] V
+//
+// with S, P and O in TMEM. K and V codes become fp16 (exact) on their way into shared memory,
+// once for the two blocks of 128 rows that a CTA works on; Q is fp16 with a factor a row: a power
+// of two that puts the row's largest magnitude into [2^14, 2^15), so that bf16 values are exact down to
+// 2^-31 of it. P = 2^(x - m) is rounded to fp16 (2^-11), m a reference of the row that is set 2^7 below the
+// largest score so far and follows when that is 2^15 above it, as in ts_window.cu: the small ones
+// lose at most 2^-25 each, 2^-11 of the row's sum in 2^21 tokens. V's scale is in the exponent.
+//
+// Two slots, each 128 rows and 128 threads, a thread a row (no reduction crosses threads): while one
+// slot's scores are made into P, the tensor cores work on the other's products. More than 128 rows
+// of a block: a slot takes 128 of them, both work on every tile. At most 128: both slots have the
+// same rows and take turns at the tiles, and meet at the end. Eight warps bring K and V through
+// registers (a tile ahead); a lane of the last warp issues the products.
+//
+// Every wait is bounded, as in ts_window_tc.cu.
+#include <stddef.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "ts_window.cuh"
+
+namespace tsv {
+
+struct PrefixParams {
+  ts_kv_cache c;  // batch: the groups; page_table: the requests'
+  ts_attn_args a;
+  int32_t page_shift;
+  int32_t group;
+  float scale_log2;
+  const int4* groups;  // {first row, rows, shared tokens, first request with a window}
+  float* part;         // [2 * CTAs] pieces of kBlock rows: outputs, references, sums
+  int4* desc;          // as WindowParams'
+  float* pre_o;
+  float2* pre_ml;
+  uint64_t wait_cycles;
+};
+
+__device__ __forceinline__ RawReq raw_request(const PrefixParams& p, int64_t g) {
+  if (g >= p.c.batch) return {0, 0, 0, 0};
+  const int4 x = p.groups[g];
+  return {x.x, x.x + x.y, x.z, 0};
+}
+template <int ROWS, int TILE>
+__device__ __forceinline__ Req request(const PrefixParams& p, const RawReq& raw) {
+  Req r;
+  r.row0 = raw.row0;
+  r.rows = raw.len > 0 ? raw.row1 - raw.row0 : 0;
+  r.skip = 0;
+  r.len = raw.len;
+  r.blocks = (int)(((unsigned)r.rows * p.group + ROWS - 1) / ROWS);
+  r.tiles = max((int)((unsigned)(r.len + TILE - 1) / TILE), 1);
+  return r;
+}
+
+namespace {
+
+constexpr int kTile = 128;
+constexpr int kRows = 128;   // of a slot
+constexpr int kBlock = 2 * kRows;
+constexpr int kConvert = 8;  // warps that bring K and V
+constexpr int kThreads = 256 + kConvert * 32 + 32;
+constexpr int kMeta = 8;     // tiles whose scales are in shared memory
+constexpr float kSlack = 15.f, kHead = 7.f;
+constexpr int kMinTiles = 1;
+constexpr int kPlanThreads = 1024;
+
+__device__ uint32_t g_prefix_error;
+
+template <int D>
+struct Layout {
+  static constexpr int stages = D == 128 ? 2 : 4;  // of K, and of V
+  static constexpr int atoms = D / 64;             // of 64 values (128 bytes) a row
+  static constexpr int atom_bytes = kTile * 128;
+  static constexpr int tile_bytes = atoms * atom_bytes;
+  static constexpr int off_k = 2 * tile_bytes;     // Q of both slots before
+  static constexpr int off_v = off_k + stages * tile_bytes;
+  static constexpr int off_x = off_v + stages * tile_bytes;
+  static constexpr int col_o = 2 * kTile;          // TMEM: S (and P) of both slots, then O
+};
+
+// A slot's outputs on their way to the other's: 32 columns, padded
+constexpr int kMeetLd = 36;
+
+struct Shared {
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], meta_full[kMeta];
+  uint64_t s_full[2], p_full[2], o_done[2], q_full, q_empty;
+  alignas(16) float4 meta[kMeta][8];  // of 16 tokens: K's scale, log2 of V's, 1 / V's, 1 (0: not there)
+  alignas(16) float meet[kRows * kMeetLd];
+  float2 ml[2][kRows];
+  uint32_t tmem;
+  alignas(16) int32_t stop;
+  uint64_t wait_cycles;  // 8 bytes behind stop: wait reads it
+};
+static_assert(offsetof(Shared, wait_cycles) == offsetof(Shared, stop) + 8, "wait");
+
+template <int D>
+constexpr int smem_bytes() { return Layout<D>::off_x + (int)sizeof(Shared) + 1024; }
+static_assert(smem_bytes<128>() <= 227 * 1024, "shared memory");
+
+// ---- the groups
+
+__global__ void __launch_bounds__(kPlanThreads) k_plan(ts_kv_cache c, ts_attn_args a, ts_shared_args sh, int page_shift,
+                                                       int4* groups, int32_t* first) {
+  grid_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int64_t b = threadIdx.x; b < c.batch; b += kPlanThreads) first[b] = 0;
+  __syncthreads();
+  WindowParams w{};  // windows as window attention reads them
+  w.c = c;
+  w.a = a;
+  w.page_shift = page_shift;
+  w.group = 1;
+  for (int64_t g = warp; g < sh.groups; g += kPlanThreads / 32) {
+    int64_t b0 = sh.group_indptr[g], b1 = sh.group_indptr[g + 1];
+    if (b0 < 0 || b1 > c.batch || b1 < b0) b0 = b1 = 0;
+    int least = INT32_MAX, lo = INT32_MAX, hi = 0, head = INT32_MAX;
+    for (int64_t b = b0 + lane; b < b1; b += 32) {
+      const Req r = request<1, 1>(w, raw_request(w, b));
+      if (r.rows == 0) continue;
+      least = min(least, r.len);
+      lo = min(lo, (int)r.row0);
+      hi = max(hi, (int)r.row0 + r.rows);
+      head = min(head, (int)b);
+    }
+    least = __reduce_min_sync(0xffffffffu, least);
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    head = __reduce_min_sync(0xffffffffu, head);
+    const bool some = lo < hi;
+    const int s = some ? max(min(least, sh.shared_lens[g]), 0) >> page_shift << page_shift : 0;
+    if (lane == 0) groups[g] = some ? make_int4(lo, hi - lo, s, head) : make_int4(0, 0, 0, 0);
+    for (int64_t b = b0 + lane; b < b1; b += 32) {
+      const Req r = request<1, 1>(w, raw_request(w, b));
+      if (r.rows) first[b] = s;
+    }
+  }
+}
+
+// ---- the shared tokens
+
+// 16 codes to fp16.
+__device__ __forceinline__ void widen(const uint4& w, uint4& lo, uint4& hi) {
+  lo.x = e4m3x2_to_f16x2((uint16_t)w.x), lo.y = e4m3x2_to_f16x2((uint16_t)(w.x >> 16));
+  lo.z = e4m3x2_to_f16x2((uint16_t)w.y), lo.w = e4m3x2_to_f16x2((uint16_t)(w.y >> 16));
+  hi.x = e4m3x2_to_f16x2((uint16_t)w.z), hi.y = e4m3x2_to_f16x2((uint16_t)(w.z >> 16));
+  hi.z = e4m3x2_to_f16x2((uint16_t)w.w), hi.w = e4m3x2_to_f16x2((uint16_t)(w.w >> 16));
+}
+
+// A thread's row of Q as fp16 into its place (rows of 128 bytes in atoms of 64 values, the 16-byte
+// pieces of row r at their place XOR r % 8). Returns what a unit of its products stands for.
+template <int D, typename T>
+__device__ __forceinline__ float load_q(const char* q, unsigned char* to, int r) {
+  uint4 w[D / 8];
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) w[i] = q ? __ldg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0, 0, 0, 0);
+  uint32_t top = 0, bad = 0;
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    const uint32_t sign = 0x7FFF7FFFu;
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[i].x & sign, w[i].y & sign), __vmaxu2(w[i].z & sign, w[i].w & sign)));
+    bad |= not_finite<T>(w[i].x) | not_finite<T>(w[i].y) | not_finite<T>(w[i].z) | not_finite<T>(w[i].w);
+  }
+  // the exponent field of the largest as a float; both factors stay normal
+  const int e = min(max((int)(__float_as_uint(unpack<T>(max(top >> 16, top & 0xFFFFu)).x) >> 23), 15), 254);
+  const float by = __uint_as_float((uint32_t)(268 - e) << 23);
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = unpack<T>(x[k]);
+      x[k] = f16x2(f.x * by, f.y * by);
+    }
+    *reinterpret_cast<uint4*>(to + (i >> 3) * Layout<D>::atom_bytes + r * 128 + ((i & 7) ^ (r & 7)) * 16) = make_uint4(x[0], x[1], x[2], x[3]);
+  }
+  return bad ? NAN : __uint_as_float((uint32_t)(e - 14) << 23);
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ PrefixParams p) {
+  using L = Layout<D>;
+  constexpr int ST = L::stages;
+  extern __shared__ unsigned char raw_smem[];
+  unsigned char* sm = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
+  Shared& x = *reinterpret_cast<Shared*>(sm + L::off_x);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kIssue = 8 + kConvert;  // the warp that issues the products
+  int4 desc = make_int4(-1, 0, 0, 0);
+  grid_launch();
+  grid_wait();
+  Line<kBlock, kTile, PrefixParams> line;
+  if (!line_begin<kBlock, kTile, kThreads>(p, kMinTiles, line)) {
+    if (tid == 0) p.desc[blockIdx.x] = desc;
+    return;
+  }
+  if (warp == kIssue) tmem_alloc(&x.tmem, 512);
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&x.k_full[i], kConvert);
+      mbar_init(&x.k_empty[i], 1);
+      mbar_init(&x.v_full[i], kConvert);
+      mbar_init(&x.v_empty[i], 1);
+    }
+    for (int i = 0; i < kMeta; ++i) mbar_init(&x.meta_full[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&x.s_full[i], 1);
+      mbar_init(&x.p_full[i], 4);
+      mbar_init(&x.o_done[i], 1);
+    }
+    mbar_init(&x.q_full, 8);
+    mbar_init(&x.q_empty, 1);
+    x.stop = 0;
+    x.wait_cycles = p.wait_cycles;
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = x.tmem;
+  Segment s{};
+
+  if (warp == kIssue) {
+    // ---- the products, by a lane. Tiles are counted through the CTA's units; tile i is in stage i % ST.
+    const uint32_t q_lo = desc_lo(smem_u32(sm), 16), k_lo = desc_lo(smem_u32(sm) + L::off_k, 16);
+    const uint32_t v_lo = desc_lo(smem_u32(sm) + L::off_v, L::atom_bytes), hi = desc_hi(1024, kSwizzle128);
+    uint32_t i = 0, u = 0, jobs[2] = {0, 0};
+#pragma unroll 1
+    while (line.next(p, s)) {
+      const int n = s.t1 - s.t0;
+      const bool wide = s.rows > kRows;
+      wait(&x.q_full, u & 1, &x.stop);
+      __syncwarp();
+      if (lane == 0) {
+        auto scores = [&](int slot, int j, bool last) {  // last: of those that read the tile
+          const int st = (i + j) % ST;
+          wait(&x.k_full[st], (i + j) / ST & 1, &x.stop);
+          if (stopped(&x.stop)) return;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t at = (k >> 2) * (L::atom_bytes / 16) + (k & 3) * 2;
+            mma_f16(tmem + slot * kTile, q_lo + slot * (L::tile_bytes / 16) + at, hi, k_lo + st * (L::tile_bytes / 16) + at, hi,
+                    f16_idesc(kRows, kTile, false), k > 0);
+          }
+          mma_commit(&x.s_full[slot]);
+          if (last) mma_commit(&x.k_empty[st]);
+        };
+        auto outputs = [&](int slot, int j, bool fresh, bool last) {
+          const int st = (i + j) % ST;
+          wait(&x.v_full[st], (i + j) / ST & 1, &x.stop);
+          wait(&x.p_full[slot], jobs[slot] & 1, &x.stop);
+          ++jobs[slot];
+          if (stopped(&x.stop)) return;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            mma_f16_ts(tmem + L::col_o + slot * D, tmem + slot * kTile + k * 8, v_lo + st * (L::tile_bytes / 16) + k * (16 * 128 / 16), hi,
+                       f16_idesc(kRows, D, true), !fresh || k > 0);
+          mma_commit(&x.o_done[slot]);
+          if (last) mma_commit(&x.v_empty[st]);
+        };
+        if (wide) {
+          scores(0, 0, false);
+          scores(1, 0, true);
+#pragma unroll 1
+          for (int j = 0; j < n; ++j) {
+#pragma unroll 1
+            for (int slot = 0; slot < 2; ++slot) {
+              outputs(slot, j, j == 0, slot == 1);
+              if (j + 1 < n) scores(slot, j + 1, slot == 1);
+            }
+          }
+        } else {
+          scores(0, 0, true);
+          if (n > 1) scores(1, 1, true);
+#pragma unroll 1
+          for (int j = 0; j < n; ++j) {
+            outputs(j & 1, j, j < 2, true);
+            if (j + 2 < n) scores(j & 1, j + 2, true);
+          }
+        }
+        mma_commit(&x.q_empty);
+      }
+      __syncwarp();
+      i += n;
+      ++u;
+    }
+  } else if (warp >= 8) {
+    // ---- K and V: the threads share a tile's pieces of 16 codes; loads are a tile ahead, page numbers two
+    constexpr int kPer = D / 16, kStep = kConvert * 32 / kPer, N = kTile / kStep;  // pieces of a token, tokens a step
+    const int ct = tid - 256, piece = ct % kPer, tok = ct / kPer;
+    const int atom = piece >> 2, chunk = (piece & 3) * 2;
+    struct Tile {
+      int32_t page = -1;  // of the lane's 16 tokens (lanes 0 .. 7)
+      int kvh = 0;
+      bool is = false;
+    };
+    int j = 0;
+    const int32_t* table = nullptr;
+    bool more = line.next(p, s);
+    if (more) table = p.c.page_table + (int64_t)p.groups[s.b].w * p.c.ld_table;
+    auto next_tile = [&]() {
+      Tile t;
+      if (!more) return t;
+      t.is = true;
+      t.kvh = s.kvh;
+      const int at = (s.t0 + j) * kTile + lane * 16;
+      if (lane < 8 && at < s.r.len) {
+        const int32_t id = table[at >> p.page_shift];
+        if (id >= 0 && id < p.c.num_pages) t.page = id;
+      }
+      if (++j == s.t1 - s.t0) {
+        j = 0;
+        more = line.next(p, s);
+        if (more) table = p.c.page_table + (int64_t)p.groups[s.b].w * p.c.ld_table;
+      }
+      return t;
+    };
+    uint4 k[N], v[N];
+    float ks = 0.f, vs = 0.f;
+    auto fetch = [&](const Tile& t, const void* base, int64_t page_ld, int64_t head_ld, int64_t token_ld, uint4* to) {
+      const char* at = static_cast<const char*>(base) + t.kvh * head_ld + piece * 16;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const int token = tok + e * kStep;
+        const int32_t page = __shfl_sync(0xffffffffu, t.page, token >> 4);  // one for the warp's tokens
+        to[e] = page >= 0 ? ldg_stream(at + page * page_ld + (token & (p.c.page_size - 1)) * token_ld) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto fetch_k = [&](const Tile& t) { fetch(t, p.c.k, p.c.k_page_stride, p.c.k_head_stride, p.c.k_token_stride, k); };
+    auto fetch_v = [&](const Tile& t) { fetch(t, p.c.v, p.c.v_page_stride, p.c.v_head_stride, p.c.v_token_stride, v); };
+    auto fetch_scales = [&](const Tile& t) {
+      ks = vs = 0.f;
+      if (warp != 8 || t.page < 0) return;
+      const int64_t at = (int64_t)t.page * p.c.heads + t.kvh;
+      ks = __ldg(p.c.k_scale + at);
+      vs = scale_of_v(__ldg(p.c.v_scale + at), ks);
+    };
+    auto put = [&](unsigned char* stage, const uint4* from) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const int token = tok + e * kStep;
+        uint4 lo, hi;
+        widen(from[e], lo, hi);
+        unsigned char* row = stage + atom * L::atom_bytes + token * 128;
+        // the second atom's lanes store their halves the other way round: no two at one bank
+        const int first = chunk + (atom & 1);
+        *reinterpret_cast<uint4*>(row + ((first ^ (token & 7)) * 16)) = atom & 1 ? hi : lo;
+        *reinterpret_cast<uint4*>(row + (((first ^ 1) ^ (token & 7)) * 16)) = atom & 1 ? lo : hi;
+      }
+      fence_async_shared();
+      __syncwarp();
+    };
+    Tile now = next_tile();
+    fetch_scales(now);
+    fetch_k(now);
+    fetch_v(now);
+    Tile then = next_tile();
+    uint32_t i = 0;
+#pragma unroll 1
+    while (now.is) {
+      const int st = i % ST;
+      const uint32_t phase = i / ST & 1;
+      if (warp == 8) {
+        // its place was last read kMeta tiles ago: the products of later tiles have been issued since
+        if (lane < 8) x.meta[i % kMeta][lane] = make_float4(ks, __log2f(vs), 1.f / vs, now.page >= 0 ? 1.f : 0.f);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x.meta_full[i % kMeta]);
+        if (then.is) fetch_scales(then);
+      }
+      wait(&x.k_empty[st], phase ^ 1, &x.stop);
+      __syncwarp();
+      put(sm + L::off_k + st * L::tile_bytes, k);
+      if (lane == 0) mbar_arrive(&x.k_full[st]);
+      if (then.is) fetch_k(then);
+      wait(&x.v_empty[st], phase ^ 1, &x.stop);
+      __syncwarp();
+      put(sm + L::off_v + st * L::tile_bytes, v);
+      if (lane == 0) mbar_arrive(&x.v_full[st]);
+      if (then.is) fetch_v(then);
+      now = then;
+      if (now.is) then = next_tile();
+      ++i;
+    }
+  } else {
+    // ---- softmax: a thread is a row of its slot
+    const int slot = warp >> 2, r = tid & (kRows - 1);
+    const uint32_t quarter = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's lanes
+    const uint32_t my_s = quarter + slot * kTile, my_o = quarter + L::col_o + slot * D;
+    uint32_t i0 = 0, u = 0, jobs = 0;
+#pragma unroll 1
+    while (line.next(p, s)) {
+      const int n = s.t1 - s.t0;
+      const bool wide = s.rows > kRows;
+      const int row = wide ? slot * kRows + r : r;  // of the block
+      const int step = wide ? 1 : 2, j0 = wide ? 0 : slot;
+      const bool mine = row < s.rows;
+      const bool active = (wide ? slot * kRows : 0) + (warp & 3) * 32 < s.rows;  // any row of the warp
+      const int64_t at = mine ? s.at(p, kBlock, row) : 0;
+      wait(&x.q_empty, (u & 1) ^ 1, &x.stop);
+      __syncwarp();
+      const char* q = nullptr;
+      if (mine) {
+        const int64_t w = at / p.a.heads_q;
+        q = static_cast<const char*>(p.a.q) + w * p.a.q_row_stride + (at - w * p.a.heads_q) * p.a.q_head_stride;
+      }
+      const float fac = load_q<D, T>(q, sm + slot * L::tile_bytes, r) * p.scale_log2;
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&x.q_full);
+      float m = kNone, l = 0.f;
+      const uint32_t before = jobs;
+#pragma unroll 1
+      for (int j = j0; j < n; j += step, ++jobs) {
+        const uint32_t i = i0 + j;
+        wait(&x.meta_full[i % kMeta], i / kMeta & 1, &x.stop);
+        wait(&x.s_full[slot], jobs & 1, &x.stop);
+        __syncwarp();
+        tc_fence_after();
+        const float4* meta = x.meta[i % kMeta];
+        if (active) {
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < kTile; c += 32) {
+            float y[32];
+            tmem_ld32(my_s + c, y);
+            tmem_wait_ld();
+            tmem_tie32(y);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float4 g = meta[c / 16 + h];
+              if (g.w == 0.f) continue;  // the same for every thread
+              const f32x2 a = pair(fac * g.x, fac * g.x), b = pair(g.y, g.y);
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                const float2 z = unpair(fma2(pair(y[16 * h + e], y[16 * h + e + 1]), a, b));
+                top = fmaxf(top, fmaxf(z.x, z.y));
+              }
+            }
+          }
+          const bool moves = top > m + kSlack;
+          if (__any_sync(0xffffffffu, moves)) {
+            // only where needed: a row's result must not depend on its neighbours'
+            const float to = moves ? top - kHead : m, by = ex2(m - to);
+            m = to;
+            l *= by;
+            if (jobs != before) {
+              wait(&x.o_done[slot], (jobs - 1) & 1, &x.stop);
+              __syncwarp();
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D; c += 8) {
+                float o[8];
+                tmem_ld8(my_o + c, o);
+                tmem_wait_ld();
+                tmem_tie8(o);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] *= by;
+                tmem_st8(my_o + c, o);
+              }
+            }
+          }
+#pragma unroll 1
+          for (int c = 0; c < kTile; c += 32) {
+            float y[32];
+            uint32_t w[16];
+            tmem_ld32(my_s + c, y);
+            tmem_wait_ld();
+            tmem_tie32(y);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float4 g = meta[c / 16 + h];
+              if (g.w == 0.f) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[8 * h + e] = 0;
+                continue;
+              }
+              // the score as above, then less the reference: at most kSlack, however large both are
+              const f32x2 a = pair(fac * g.x, fac * g.x), b = pair(g.y, g.y), less = pair(-m, -m);
+              f32x2 sum = 0;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float2 z = unpair(add2(fma2(pair(y[16 * h + 2 * e], y[16 * h + 2 * e + 1]), a, b), less));
+                const float e0 = ex2(z.x), e1 = ex2(z.y);
+                sum = add2(sum, pair(e0, e1));
+                w[8 * h + e] = f16x2(e0, e1);
+              }
+              const float2 both = unpair(sum);
+              l = fmaf(both.x + both.y, g.z, l);
+            }
+            tmem_st16(my_s + c / 2, w);  // P lies over the scores that have been read
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x.p_full[slot]);
+      }
+      // ---- the end of the unit
+      const bool live = jobs != before;
+      if (live) wait(&x.o_done[slot], (jobs - 1) & 1, &x.stop);
+      __syncwarp();
+      tc_fence_after();
+      const bool whole = s.whole();
+      float* part = p.part + (2 * (int64_t)blockIdx.x + (s.t0 == 0 ? 1 : 0)) * slot_floats(kBlock, D);
+      float* to = whole ? p.pre_o + at * D : part + (int64_t)row * D;
+      float by = 1.f;
+      if (!wide) {  // the slots meet
+        x.ml[slot][r] = make_float2(m, l);
+        bar_sync(1, 256);
+        const float2 other = x.ml[slot ^ 1][r];
+        const float top = fmaxf(m, other.x);
+        by = live ? ex2(m - top) : 0.f;
+        l = fmaf(l, by, other.y * ex2(other.x - top));
+        m = top;
+      }
+      if (mine && (wide || slot == 0)) {
+        if (whole) p.pre_ml[at] = make_float2(m, l);
+        else part[kBlock * D + row] = m, part[kBlock * D + kBlock + row] = l;
+      }
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        if (live) {
+          tmem_ld32(my_o + c, o);
+          tmem_wait_ld();
+          tmem_tie32(o);
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = live ? o[e] * by : 0.f;
+        if (!wide) {
+          float4* meet = reinterpret_cast<float4*>(x.meet + r * kMeetLd);
+          if (slot == 1) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) meet[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+          bar_sync(1, 256);
+          if (slot == 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 y = meet[e];
+              o[4 * e] += y.x, o[4 * e + 1] += y.y, o[4 * e + 2] += y.z, o[4 * e + 3] += y.w;
+            }
+          }
+        }
+        if (mine && (wide || slot == 0)) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(to + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+        if (!wide) bar_sync(1, 256);
+      }
+      tc_fence_before();
+      if (!whole) {
+        if (s.t0 == 0) {
+          desc.x = s.b;
+          desc.y = s.kvh * s.r.blocks + s.block;
+          desc.z = s.rows;
+        } else {
+          desc.w = s.t1 == s.r.tiles ? 1 : 0;
+        }
+      }
+      i0 += n;
+      ++u;
+    }
+    if (tid == 0) p.desc[blockIdx.x] = desc;
+  }
+  if (stopped(&x.stop)) {
+    atomicOr(&g_prefix_error, 1u);
+    // products in flight are done before the CTA leaves its memory
+    const long long t0 = clock64();
+    while (clock64() - t0 < (1ll << 26)) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kIssue) {
+    tc_fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+// One warp a row of a unit that spans CTAs, as join_row, into the rows' prefix part.
+template <int D>
+__global__ void __launch_bounds__(128) k_prefix_join(const __grid_constant__ PrefixParams p) {
+  grid_launch();
+  grid_wait();
+  const int first = blockIdx.x, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * 4 + (threadIdx.x >> 5);
+  const int4 d = p.desc[first];
+  if (d.x < 0 || row >= d.z) return;
+  int pieces = 1;
+  for (;; pieces += 32) {
+    const int i = first + pieces + lane;
+    const unsigned ends = __ballot_sync(0xffffffffu, i >= (int)gridDim.x || p.desc[i].w != 0);
+    if (ends) {
+      pieces += __ffs(ends);
+      break;
+    }
+  }
+  auto piece = [&](int i) { return p.part + (int64_t)(i ? 2 * (first + i) : 2 * first + 1) * slot_floats(kBlock, D); };
+  float top = kNone;
+  for (int i = lane; i < pieces; i += 32) top = fmaxf(top, piece(i)[kBlock * D + row]);
+  top = warp_max(top);
+  constexpr int PER = D / 32;
+  float2 acc[PER / 2];
+#pragma unroll
+  for (int e = 0; e < PER / 2; ++e) acc[e] = make_float2(0.f, 0.f);
+  float sum = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < pieces; ++i) {
+    const float* y = piece(i);
+    const float by = ex2(y[kBlock * D + row] - top);
+    sum = fmaf(by, y[kBlock * D + kBlock + row], sum);
+#pragma unroll
+    for (int e = 0; e < PER / 2; ++e) add_scaled(acc[e], by, *reinterpret_cast<const float2*>(y + row * D + lane * PER + 2 * e));
+  }
+  Segment s;
+  s.r = request<kBlock, kTile>(p, raw_request(p, d.x));
+  s.kvh = d.y / s.r.blocks;
+  s.block = d.y % s.r.blocks;
+  const int64_t at = s.at(p, kBlock, row);
+  if (lane == 0) p.pre_ml[at] = make_float2(top, sum);
+#pragma unroll
+  for (int e = 0; e < PER / 2; ++e) *reinterpret_cast<float2*>(p.pre_o + at * D + lane * PER + 2 * e) = acc[e];
+}
+
+template <int D, typename T>
+cudaError_t launch(const PrefixParams& p, int sms, cudaStream_t s) {
+  constexpr int bytes = smem_bytes<D>();
+  cudaError_t e = allow_smem<k_prefix<D, T>>(bytes);
+  if (e != cudaSuccess) return e;
+  if ((e = launch_after(k_prefix<D, T>, dim3(sms), kThreads, bytes, s, p)) != cudaSuccess) return e;
+  return launch_after(k_prefix_join<D>, dim3(sms, kBlock / 4), 128, 0, s, p);
+}
+
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+struct Scratch {
+  int4* groups;
+  int32_t* first;
+  float* pre_o;
+  float2* pre_ml;
+  int4* desc;
+  float* part;
+  char* window;  // window attention's workspace
+};
+
+size_t lay_out(Scratch& x, int64_t batch, int64_t groups, int64_t total_rows, int heads_q, int heads, int D, int sms, void* ws) {
+  size_t off = 0;
+  auto take = [&](auto*& at, size_t n) {
+    at = reinterpret_cast<std::remove_reference_t<decltype(at)>>(static_cast<char*>(ws) + off);
+    off += up256(n * sizeof(*at));
+  };
+  const size_t rows = (size_t)total_rows * heads_q;
+  take(x.groups, (size_t)groups);
+  take(x.first, (size_t)batch);
+  take(x.pre_o, rows * D);
+  take(x.pre_ml, rows);
+  take(x.desc, (size_t)sms);
+  take(x.part, (size_t)2 * sms * slot_floats(kBlock, D));
+  take(x.window, window_workspace(batch, total_rows, heads_q, heads, D, sms));
+  return off;
+}
+
+}  // namespace
+
+size_t shared_workspace(int64_t batch, int64_t groups, int64_t total_rows, int heads_q, int heads, int head_dim, int sms) {
+  Scratch x;
+  return lay_out(x, batch, groups, total_rows, heads_q, heads, head_dim, sms, nullptr);
+}
+
+cudaError_t shared_read_error(uint32_t* word, int clear) {
+  cudaError_t e = cudaMemcpyFromSymbol(word, g_prefix_error, sizeof(uint32_t));
+  if (e == cudaSuccess && clear && *word) {
+    const uint32_t zero = 0;
+    e = cudaMemcpyToSymbol(g_prefix_error, &zero, sizeof(zero));
+  }
+  return e;
+}
+
+cudaError_t launch_shared(const ts_shared_args& sh, void* ws, int sms, uint64_t wait_cycles, cudaStream_t s) {
+  const ts_attn_args& a = *sh.attn;
+  const ts_kv_cache& c = *a.cache;
+  Scratch x;
+  lay_out(x, c.batch, sh.groups, a.total_rows, a.heads_q, c.heads, c.head_dim, sms, ws);
+  PrefixParams p{};
+  p.c = c;
+  p.c.batch = sh.groups;
+  p.a = a;
+  p.page_shift = __builtin_ctz((unsigned)c.page_size);
+  p.group = a.heads_q / c.heads;
+  p.scale_log2 = a.sm_scale * kLog2e;
+  p.groups = x.groups;
+  p.part = x.part;
+  p.desc = x.desc;
+  p.pre_o = x.pre_o;
+  p.pre_ml = x.pre_ml;
+  p.wait_cycles = wait_cycles;
+  k_plan<<<1, kPlanThreads, 0, s>>>(c, a, sh, p.page_shift, x.groups, x.first);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  if (a.dtype == TS_BF16)
+    e = c.head_dim == 128 ? launch<128, __nv_bfloat16>(p, sms, s) : launch<64, __nv_bfloat16>(p, sms, s);
+  else
+    e = c.head_dim == 128 ? launch<128, __half>(p, sms, s) : launch<64, __half>(p, sms, s);
+  if (e != cudaSuccess) return e;
+  const SharedPrefix front = {x.first, x.pre_o, x.pre_ml};
+  return launch_window(c, a, x.window, sms, wait_cycles, s, &front);
+}
+
+}  // namespace tsv

@@ -37,6 +37,27 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a_lo, uint32_t a_hi,
       : "memory");
 }
 
+// Instruction descriptor of kind::f16: fp16 operands, fp32 accumulators. b_mn as above.
+__host__ __device__ constexpr uint32_t f16_idesc(int m, int n, bool b_mn) {
+  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+// One thread: D (TMEM) = A B (+ D), k = 16; A in shared memory, or (_ts) in TMEM.
+__device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                        uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.u32 p, %6, 0;\n mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.u32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+
 // One thread: arrives on `bar` when the thread's MMAs so far are complete.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
@@ -78,14 +99,81 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, float* x) {
         "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
       : "r"(addr));
 }
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float* x) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(x[8]),
+        "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15]), "=f"(x[16]), "=f"(x[17]),
+        "=f"(x[18]), "=f"(x[19]), "=f"(x[20]), "=f"(x[21]), "=f"(x[22]), "=f"(x[23]), "=f"(x[24]), "=f"(x[25]), "=f"(x[26]),
+        "=f"(x[27]), "=f"(x[28]), "=f"(x[29]), "=f"(x[30]), "=f"(x[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(x[0]),
+      "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]), "r"(x[8]), "r"(x[9]), "r"(x[10]), "r"(x[11]),
+      "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15]), "r"(addr)
+      : "memory");
+}
 // After tmem_wait_ld: no use of the loaded values moves ahead of the wait.
 __device__ __forceinline__ void tmem_tie16(float* x) {
   asm volatile("" : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7]),
                     "+f"(x[8]), "+f"(x[9]), "+f"(x[10]), "+f"(x[11]), "+f"(x[12]), "+f"(x[13]), "+f"(x[14]), "+f"(x[15]));
 }
+__device__ __forceinline__ void tmem_tie32(float* x) {
+  tmem_tie16(x);
+  tmem_tie16(x + 16);
+}
 __device__ __forceinline__ void tmem_tie8(float* x) {
   asm volatile("" : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7]));
 }
+
+// ---- bounded waits and named barriers
+__device__ __forceinline__ bool stopped(const int32_t* stop) { return *reinterpret_cast<const volatile int32_t*>(stop) != 0; }
+
+// Waits for a phase; gives up after the call's budget of SM clock cycles (8 bytes behind stop) and
+// sets *stop, or when that is set. Written out for size: it stands in every loop, and the loops
+// of a kernel's roles have to stay in the instruction caches. The lanes of a warp need not see the phase at
+// the same try: they part here, and callers bring them together (__syncwarp) before anything that takes a
+// whole warp.
+__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, int32_t* stop) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .u32 f;\n .reg .u64 t0, t1, b;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n"
+      " @p bra DONE_%=;\n"
+      " mov.u64 t0, %%clock64;\n"
+      "AGAIN_%=:\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n"
+      " @p bra DONE_%=;\n"
+      " ld.volatile.shared.u32 f, [%2];\n"
+      " setp.ne.u32 p, f, 0;\n"
+      " @p bra DONE_%=;\n"
+      " mov.u64 t1, %%clock64;\n"
+      " sub.u64 t1, t1, t0;\n"
+      " ld.shared.u64 b, [%2 + 8];\n"
+      " setp.le.u64 p, t1, b;\n"
+      " @p bra AGAIN_%=;\n"
+      " st.volatile.shared.u32 [%2], 1;\n"
+      "DONE_%=:\n}\n" ::"r"(smem_u32(bar)),
+      "r"(parity), "r"(smem_u32(stop))
+      : "memory");
+}
+
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool bar_or(int id, int threads, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred.aligned q, %2, %3, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+
 
 // ---- two fp32 operations an instruction
 typedef unsigned long long f32x2;

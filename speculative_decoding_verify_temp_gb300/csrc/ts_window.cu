@@ -182,7 +182,7 @@ __device__ __forceinline__ void attend(const Params& p) {
     // ---- cached tokens
     const char* kc = static_cast<const char*>(p.c.k) + kvh * p.c.k_head_stride;
     const char* vc = static_cast<const char*>(p.c.v) + kvh * p.c.v_head_stride;
-    const int32_t* table = p.c.page_table + sg.b * p.c.ld_table;
+    const int32_t* table = p.c.page_table + sg.b * p.c.ld_table + r.skip;
     struct Loaded {
       uint4 k[2];
       uint32_t v[4][VW];
@@ -335,12 +335,18 @@ __device__ __forceinline__ void attend(const Params& p) {
       }
       if (whole) {
         const int64_t at = sg.at(p, ROWS, row);
-        float own;
-        const float by = finish_row(p, at, top, sum, own);  // the row's threads write the same lse
+        float own, pre;
+        const float by = finish_row(p, r, at, top, sum, own, pre);  // the row's threads write the same lse
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (p.own_ml) v = *reinterpret_cast<const float4*>(p.own_o + at * D + d);
-        const uint2 w = make_uint2(pack<T>(fmaf(acc.x, by, v.x * own), fmaf(acc.y, by, v.y * own)),
-                                   pack<T>(fmaf(acc.z, by, v.z * own), fmaf(acc.w, by, v.w * own)));
+        float2 lo = make_float2(v.x * own, v.y * own), hi = make_float2(v.z * own, v.w * own);
+        if (pre != 0.f) {
+          v = *reinterpret_cast<const float4*>(p.pre_o + at * D + d);
+          add_scaled(lo, pre, make_float2(v.x, v.y));
+          add_scaled(hi, pre, make_float2(v.z, v.w));
+        }
+        const uint2 w = make_uint2(pack<T>(fmaf(acc.x, by, lo.x), fmaf(acc.y, by, lo.y)),
+                                   pack<T>(fmaf(acc.z, by, hi.x), fmaf(acc.w, by, hi.y)));
         *reinterpret_cast<uint2*>(static_cast<char*>(p.a.out) + (at * D + d) * 2) = w;
       } else {
         *reinterpret_cast<float4*>(part + row * D + d) = acc;
@@ -468,7 +474,7 @@ size_t window_workspace(int64_t batch, int64_t total_rows, int heads_q, int head
 }
 
 cudaError_t launch_window(const ts_kv_cache& c, const ts_attn_args& a, void* ws, int sms, uint64_t wait_cycles,
-                          cudaStream_t s) {
+                          cudaStream_t s, const SharedPrefix* front) {
   Params p{};
   p.c = c;
   p.a = a;
@@ -478,6 +484,11 @@ cudaError_t launch_window(const ts_kv_cache& c, const ts_attn_args& a, void* ws,
   p.wait_cycles = wait_cycles;
   lay_out(p, ws, sms);
   if (!a.k_new) p.own_ml = nullptr;
+  if (front) {
+    p.first = front->first;
+    p.pre_o = front->pre_o;
+    p.pre_ml = front->pre_ml;
+  }
   if (c.head_dim == 128) return launch_window_tc(p, block_rows(p), sms, s);
   const int rows = block_rows(p);
   return a.dtype == TS_BF16 ? launch_64<__nv_bfloat16>(p, rows, sms, s) : launch_64<__half>(p, rows, sms, s);

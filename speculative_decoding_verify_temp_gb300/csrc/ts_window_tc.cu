@@ -114,7 +114,7 @@ struct Shared {
   alignas(16) float delta[kGroups][kCols];  // factors of outputs and sums whose references move
   float peak[kGroups][kCols];               // the rows' largest references so far
   float red[kGroups][4][kCols];
-  float w[kGroups + 1][ROWS];  // a row's factors: the turns', and the window's own part
+  float w[kGroups + 2][ROWS];  // a row's factors: the turns', the window's own part, and that of the tokens in front
   float2 own[ROWS];            // the own part's references and sums
   int32_t at[ROWS];            // a row's index in [total_rows][heads_q]
   int32_t parents[TS_MAX_WINDOW];
@@ -137,50 +137,6 @@ static_assert(offsetof(Shared<32>, neg_m) % 16 == 0 && offsetof(Shared<64>, neg_
 template <int ROWS, int QP>
 constexpr int smem_bytes() { return Layout<ROWS, QP>::off_x + (int)sizeof(Shared<ROWS>) + 1024; }
 static_assert(smem_bytes<64, 3>() <= 227 * 1024, "shared memory");
-
-__device__ __forceinline__ bool stopped(const int32_t* stop) { return *reinterpret_cast<const volatile int32_t*>(stop) != 0; }
-
-// Waits for a phase; gives up after the call's budget of SM clock cycles (8 bytes behind stop) and
-// sets *stop, or when that is set. Written out for size: it stands in every loop, and the loops
-// of the six roles have to stay in the instruction caches. The lanes of a warp need not see the phase at
-// the same try: they part here, and callers bring them together (__syncwarp) before anything that takes a
-// whole warp.
-__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, int32_t* stop) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .u32 f;\n .reg .u64 t0, t1, b;\n"
-      " mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n"
-      " @p bra DONE_%=;\n"
-      " mov.u64 t0, %%clock64;\n"
-      "AGAIN_%=:\n"
-      " mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n"
-      " @p bra DONE_%=;\n"
-      " ld.volatile.shared.u32 f, [%2];\n"
-      " setp.ne.u32 p, f, 0;\n"
-      " @p bra DONE_%=;\n"
-      " mov.u64 t1, %%clock64;\n"
-      " sub.u64 t1, t1, t0;\n"
-      " ld.shared.u64 b, [%2 + 8];\n"
-      " setp.le.u64 p, t1, b;\n"
-      " @p bra AGAIN_%=;\n"
-      " st.volatile.shared.u32 [%2], 1;\n"
-      "DONE_%=:\n}\n" ::"r"(smem_u32(bar)),
-      "r"(parity), "r"(smem_u32(stop))
-      : "memory");
-}
-
-__device__ __forceinline__ void bar_sync(int id, int threads) {
-  asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-__device__ __forceinline__ bool bar_or(int id, int threads, bool x) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred.aligned q, %2, %3, p;\n"
-      " selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"((uint32_t)x), "r"(id), "r"(threads)
-      : "memory");
-  return r != 0;
-}
 
 // Of the lanes' 16 columns x: lane l gets the reduction of column l % 16 over the lanes. 16 shuffles.
 template <int O, typename F>
@@ -301,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto page_of = [&](const Segment& g, int r) -> int32_t {
         const int i = g.t0 * per_tile + r * 32 + lane;
         if (i >= g.t1 * per_tile || (int64_t)i << p.page_shift >= g.r.len) return -1;
-        const int32_t id = p.c.page_table[g.b * p.c.ld_table + i];
+        const int32_t id = p.c.page_table[g.b * p.c.ld_table + g.r.skip + i];
         return id >= 0 && id < p.c.num_pages ? id : -1;
       };
       auto scales_of = [&](const Segment& g, int32_t page, float& ks, float& vs) {
@@ -670,12 +626,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_sync(kBarAll, kSoftmaxThreads);
       tc_fence_after();
       const bool whole = s.whole();
+      const bool in_front = p.pre_ml && s.t0 == 0 && s.r.skip > 0;  // the first piece takes that part too
       float* part = p.part + (2 * (int64_t)blockIdx.x + (s.t0 == 0 ? 1 : 0)) * slot_floats(ROWS, kD);
       if (tid < s.rows) {
         const int r = tid, c = r % kCols;
         float m[L::turns], sum[L::turns];
         const float2 ml = own ? x.own[r] : make_float2(kNone, 0.f);
-        float to = ml.x;
+        const float2 front = in_front ? p.pre_ml[x.at[r]] : make_float2(kNone, 0.f);
+        float to = fmaxf(ml.x, front.x);
 #pragma unroll
         for (int k = 0; k < L::turns; ++k) {
           const int g = L::split ? 2 * k + r / kCols : k;
@@ -687,6 +645,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float by = ex2(ml.x - to), all = by * ml.y;
         x.w[L::turns][r] = by;
+        const float pre = ex2(front.x - to);
+        all = fmaf(pre, front.y, all);
 #pragma unroll
         for (int k = 0; k < L::turns; ++k) {
           m[k] = ex2(m[k] - to);
@@ -700,6 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           part[ROWS * kD + ROWS + r] = all;
         }
         x.w[L::turns][r] *= by;
+        x.w[L::turns + 1][r] = pre * by;
 #pragma unroll
         for (int k = 0; k < L::turns; ++k) x.w[k][r] = m[k] * by;
       }
@@ -711,6 +672,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         float o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = own && c + e < s.rows ? x.w[L::turns][c + e] * own_o[(c + e) * kD + d] : 0.f;
+        if (in_front) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (c + e < s.rows && x.w[L::turns + 1][c + e] != 0.f)
+              o[e] = fmaf(x.w[L::turns + 1][c + e], p.pre_o[(int64_t)x.at[c + e] * kD + d], o[e]);
+        }
 #pragma unroll 1
         for (int k = 0; k < L::turns; ++k) {
           if (!x.live[L::split ? 2 * k : k]) continue;  // both groups of a turn see the same tokens
@@ -805,7 +772,9 @@ cudaError_t launch(const WindowParams& p, const CUtensorMap& k, const CUtensorMa
   k_window_tc<ROWS, QP, T><<<sms, kThreads, bytes, s>>>(p, k, v);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if ((int64_t)p.c.max_pages * p.c.page_size <= kTile) return cudaSuccess;  // units of one tile are never split
-  return launch_after(k_join<kD, ROWS, kTile, T>, dim3(sms, ROWS / 4), 128, 0, s, p);
+  WindowParams joined = p;
+  joined.pre_ml = nullptr;  // in the pieces
+  return launch_after(k_join<kD, ROWS, kTile, T>, dim3(sms, ROWS / 4), 128, 0, s, joined);
 }
 
 }  // namespace

@@ -139,6 +139,16 @@ class AttnArgs(ctypes.Structure):
     ]
 
 
+class SharedArgs(ctypes.Structure):
+    """ts_shared_args of include/ts_verify.h."""
+    _fields_ = [
+        ("attn", ctypes.POINTER(AttnArgs)),
+        ("group_indptr", ctypes.c_void_p),
+        ("shared_lens", ctypes.c_void_p),
+        ("groups", ctypes.c_int64),
+    ]
+
+
 class KvAppendArgs(ctypes.Structure):
     """ts_kv_append_args of include/ts_verify.h."""
     _fields_ = [
@@ -287,6 +297,10 @@ def load():
     L.ts_attention_workspace_size.restype = ctypes.c_size_t
     L.ts_window_attention.argtypes = [ctypes.POINTER(AttnArgs), P, ctypes.c_size_t, P]
     L.ts_window_attention.restype = st
+    L.ts_shared_attention_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32]
+    L.ts_shared_attention_workspace_size.restype = ctypes.c_size_t
+    L.ts_shared_attention.argtypes = [ctypes.POINTER(SharedArgs), P, ctypes.c_size_t, P]
+    L.ts_shared_attention.restype = st
     for name, args in (("ts_kv_append", KvAppendArgs), ("ts_kv_read", KvReadArgs),
                        ("ts_kv_fork", KvForkArgs), ("ts_kv_free", KvFreeArgs),
                        ("ts_tree_spec_sampling", TreeArgs)):
@@ -660,13 +674,22 @@ def window_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens
     packed by qo_indptr (int32 [B+1]) or rows / B a request; parents (int32 [rows], window
     row numbers) makes each window a tree. sm_scale: 1/sqrt(D) by default. Returns
     dict(out=[rows, Hq, D], lse=[rows, Hq] fp32 or None)."""
-    c, device = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)
+    cache = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)
+    return _attend(cache, None, q, k_new, v_new, qo_indptr, parents, sm_scale, lse, out, workspace, stream)
+
+
+def _attend(cache, shared, q, k_new, v_new, qo_indptr, parents, sm_scale, lse, out, workspace, stream):
+    """Window attention, or, with shared = (group_indptr, shared_lens), shared attention."""
+    c, device = cache
     D, H, B = c.head_dim, c.heads, c.batch
     if q.dim() != 3:
         raise ValueError("q must be [rows, heads, head_dim]")
     Hq = q.shape[1]
     rows, qr, qh = _heads("q", q, Hq, D)
-    _same_device(device, q, k_new, v_new, qo_indptr, parents, out, workspace)
+    _same_device(device, q, k_new, v_new, qo_indptr, parents, out, workspace, *(shared or ()))
+    if shared:
+        groups = shared[1].shape[0] if shared[1].dim() == 1 else 0
+        shared = _int32("group_indptr", shared[0], groups + 1), _int32("shared_lens", shared[1], groups), groups
     k_ptr = v_ptr = None
     kr = kh = vr = vh = 0
     if k_new is not None and v_new is not None:
@@ -685,18 +708,48 @@ def window_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens
             raise ValueError("out must be contiguous, with the shape and dtype of q")
         z = torch.empty((rows, Hq), dtype=torch.float32, device=q.device) if lse else None
         if workspace is None:
-            workspace = torch.empty(attention_workspace_size(B, rows, Hq, H, D),
-                                    dtype=torch.uint8, device=q.device)
+            size = shared_attention_workspace_size(B, groups, rows, Hq, H, D) if shared else \
+                attention_workspace_size(B, rows, Hq, H, D)
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
         elif not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         a = AttnArgs(ctypes.pointer(c), q.data_ptr(), qr, qh, _kv_dtype(q.dtype), Hq, k_ptr, v_ptr,
                      kr, kh, vr, vh, rows, _int32("qo_indptr", qo_indptr, B + 1),
                      _int32("parents", parents, rows), D ** -0.5 if sm_scale is None else sm_scale,
                      0.0, out.data_ptr(), None if z is None else z.data_ptr())
-        st = load().ts_window_attention(a, workspace.data_ptr(), workspace.nbytes, s)
+        if shared:
+            st = load().ts_shared_attention(SharedArgs(ctypes.pointer(a), *shared), workspace.data_ptr(),
+                                            workspace.nbytes, s)
+        else:
+            st = load().ts_window_attention(a, workspace.data_ptr(), workspace.nbytes, s)
         if st:
-            _check("ts_window_attention", st)
+            _check("ts_shared_attention" if shared else "ts_window_attention", st)
     return dict(out=out, lse=z)
+
+
+def shared_attention_workspace_size(batch: int, groups: int, rows: int, heads_q: int, heads: int,
+                                    head_dim: int) -> int:
+    return int(load().ts_shared_attention_workspace_size(batch, groups, rows, heads_q, heads, head_dim))
+
+
+def make_shared_attention_workspace(batch: int, groups: int, rows: int, heads_q: int, heads: int, head_dim: int,
+                                    device=None):
+    """Scratch for shared_attention calls of this size that do not overlap."""
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        return torch.empty(shared_attention_workspace_size(batch, groups, rows, heads_q, heads, head_dim),
+                           dtype=torch.uint8, device="cuda")
+
+
+def shared_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, *, group_indptr, shared_lens,
+                     k_new=None, v_new=None, qo_indptr=None, parents=None, sm_scale=None, lse: bool = False,
+                     out=None, workspace=None, stream=None):
+    """window_attention of requests that continue common prefixes: group g is the requests
+    group_indptr[g] .. group_indptr[g+1] - 1 (int32 [groups+1]); the whole pages among the first
+    shared_lens[g] tokens (int32 [groups]) must be the same in all of its tables (kv_fork leaves
+    them so) and are read once for the group. Everything else as for window_attention."""
+    cache = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)
+    return _attend(cache, (group_indptr, shared_lens), q, k_new, v_new, qo_indptr, parents, sm_scale, lse, out,
+                   workspace, stream)
 
 
 def kv_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, *, qo_indptr=None,
