@@ -2,7 +2,8 @@
 // rows of a group, the rest of each request by window attention (ts_window.cu, ts_window_tc.cu),
 // which takes the prefix's part of a row in.
 //
-//   k_plan         the groups: rows, shared tokens (whole pages); what each request has left
+//   k_plan         the groups: rows, shared tokens (whole pages); what each request has left; how
+//                  many CTAs go through the tokens side by side
 //   k_prefix       one persistent CTA an SM: the shared tokens of the groups
 //   k_prefix_join  joins the pieces of units that more than one CTA worked on
 //
@@ -21,8 +22,11 @@
 // Two slots, each 128 rows and 128 threads, a thread a row (no reduction crosses threads): while one
 // slot's scores are made into P, the tensor cores work on the other's products. More than 128 rows
 // of a block: a slot takes 128 of them, both work on every tile. At most 128: both slots have the
-// same rows and take turns at the tiles, and meet at the end. Eight warps bring K and V through
-// registers (a tile ahead); a lane of the last warp issues the products.
+// same rows and take turns at the tiles, and meet at the end. TMA brings the pages, up to three tiles of
+// K or V ahead; four warps make their codes fp16 and a lane of another issues the products.
+//
+// Groups with many rows: CTAs in gangs of up to 8 take the same share of the tokens at the same time, a
+// block of rows each, so that a tile comes from DRAM once for a gang.
 //
 // Every wait is bounded, as in ts_window_tc.cu.
 #include <stddef.h>
@@ -42,8 +46,9 @@ struct PrefixParams {
   int32_t group;
   float scale_log2;
   const int4* groups;  // {first row, rows, shared tokens, first request with a window}
+  const int32_t* gang; // CTAs that share tokens
   float* part;         // [2 * CTAs] pieces of kBlock rows: outputs, references, sums
-  int4* desc;          // as WindowParams'
+  int4* desc;          // [CTAs] {tail unit's group, its head, rows, 2 * its block | the CTA's first piece ends its unit}
   float* pre_o;
   float2* pre_ml;
   uint64_t wait_cycles;
@@ -61,7 +66,8 @@ __device__ __forceinline__ Req request(const PrefixParams& p, const RawReq& raw)
   r.rows = raw.len > 0 ? raw.row1 - raw.row0 : 0;
   r.skip = 0;
   r.len = raw.len;
-  r.blocks = (int)(((unsigned)r.rows * p.group + ROWS - 1) / ROWS);
+  r.blocks = (int)(((unsigned)r.rows * p.group + ROWS - 1) / ROWS);  // here: sets of as many as a gang takes
+  r.blocks = (r.blocks + *p.gang - 1) / *p.gang;
   r.tiles = max((int)((unsigned)(r.len + TILE - 1) / TILE), 1);
   return r;
 }
@@ -71,10 +77,17 @@ namespace {
 constexpr int kTile = 128;
 constexpr int kRows = 128;   // of a slot
 constexpr int kBlock = 2 * kRows;
-constexpr int kConvert = 8;  // warps that bring K and V
-constexpr int kThreads = 256 + kConvert * 32 + 32;
+constexpr int kConvert = 4;  // warps that make codes fp16
+constexpr int kThreads = 256 + kConvert * 32 + 128;
+// Registers of a thread: 128 at launch (512 threads), then by role
+constexpr int kSoftmaxRegs = 184, kConvertRegs = 80, kIssueRegs = 64;
+static_assert(256 * kSoftmaxRegs + kConvert * 32 * kConvertRegs + 128 * kIssueRegs <= kThreads * 128, "registers");
+constexpr int kMaxGang = 8;
 constexpr int kMeta = 8;     // tiles whose scales are in shared memory
-constexpr float kSlack = 15.f, kHead = 7.f;
+constexpr float kHead = 7.f;         // a reference is set this far, in log2, below the largest score
+constexpr float kMostSum = 32768.f;  // of a tile's probabilities, where the reference stays
+constexpr float kSlack = 8.f;        // how far a score may be above it where it is looked at: 128 * 2^8 = kMostSum
+constexpr float kMostRef = 65536.f;  // references of at most this size: scores and reference in one operation
 constexpr int kMinTiles = 1;
 constexpr int kPlanThreads = 1024;
 
@@ -82,25 +95,28 @@ __device__ uint32_t g_prefix_error;
 
 template <int D>
 struct Layout {
-  static constexpr int stages = D == 128 ? 2 : 4;  // of K, and of V
-  static constexpr int atoms = D / 64;             // of 64 values (128 bytes) a row
-  static constexpr int atom_bytes = kTile * 128;
+  static constexpr int k_stages = D == 128 ? 2 : 4;  // tiles of K in fp16
+  static constexpr int v_halves = D == 128 ? 3 : 8;  // halves of tiles of V
+  static constexpr int units = D == 128 ? 3 : 6;     // tiles of K or V as they come: K, V, K, ...
+  static constexpr int atoms = D / 64;               // of 64 values (128 bytes) a row
+  static constexpr int atom_bytes = kTile * 128;     // of Q and K; of a half of V half as many
   static constexpr int tile_bytes = atoms * atom_bytes;
-  static constexpr int off_k = 2 * tile_bytes;     // Q of both slots before
-  static constexpr int off_v = off_k + stages * tile_bytes;
-  static constexpr int off_x = off_v + stages * tile_bytes;
-  static constexpr int col_o = 2 * kTile;          // TMEM: S (and P) of both slots, then O
+  static constexpr int unit_bytes = kTile * D;
+  static constexpr int off_k = 2 * tile_bytes;       // Q of both slots before
+  static constexpr int off_v = off_k + k_stages * tile_bytes;
+  static constexpr int off_raw = off_v + v_halves * tile_bytes / 2;
+  static constexpr int off_x = off_raw + units * unit_bytes;
+  static constexpr int col_o = 2 * kTile;            // TMEM: S (and P) of both slots, then O
 };
 
-// A slot's outputs on their way to the other's: 32 columns, padded
-constexpr int kMeetLd = 36;
+// Where the slots meet, in the place of Q: 32 columns of outputs, padded, then references and sums.
+constexpr int kMeetLd = 36, kMeetMl = kRows * kMeetLd * 4;
+static_assert(kMeetMl + 2 * kRows * 8 <= 2 * Layout<64>::tile_bytes, "Q's place");
 
 struct Shared {
-  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], meta_full[kMeta];
+  uint64_t k_full[4], k_empty[4], v_full[8], v_empty[8], raw_full[6], raw_empty[6], meta_full[kMeta];
   uint64_t s_full[2], p_full[2], o_done[2], q_full, q_empty;
-  alignas(16) float4 meta[kMeta][8];  // of 16 tokens: K's scale, log2 of V's, 1 / V's, 1 (0: not there)
-  alignas(16) float meet[kRows * kMeetLd];
-  float2 ml[2][kRows];
+  alignas(16) float4 meta[kMeta][8];  // of 16 tokens: K's scale, log2 of V's, 1 / V's, 2 (0: not there; 1: others of the tile are not)
   uint32_t tmem;
   alignas(16) int32_t stop;
   uint64_t wait_cycles;  // 8 bytes behind stop: wait reads it
@@ -111,12 +127,40 @@ template <int D>
 constexpr int smem_bytes() { return Layout<D>::off_x + (int)sizeof(Shared) + 1024; }
 static_assert(smem_bytes<128>() <= 227 * 1024, "shared memory");
 
+// All threads of four neighbouring warps.
+template <int N, bool MORE>
+__device__ __forceinline__ void set_regs() {
+  if constexpr (MORE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// A CTA's share: its gang's, of which it takes one block of each set.
+struct Share {
+  Line<kBlock, kTile, PrefixParams> line;
+  int gang, rank;
+  __device__ __forceinline__ bool begin(const PrefixParams& p) {
+    gang = *p.gang;
+    rank = blockIdx.x % gang;
+    return line_begin<kBlock, kTile, kThreads>(p, kMinTiles, line, blockIdx.x / gang, gridDim.x / gang);
+  }
+  __device__ __forceinline__ bool next(const PrefixParams& p, Segment& s) {
+    while (line.next(p, s)) {
+      s.block = s.block * gang + rank;
+      s.rows = min(kBlock, s.r.rows * p.group - s.block * kBlock);
+      if (s.rows > 0) return true;
+    }
+    return false;
+  }
+};
+
 // ---- the groups
 
 __global__ void __launch_bounds__(kPlanThreads) k_plan(ts_kv_cache c, ts_attn_args a, ts_shared_args sh, int page_shift,
-                                                       int4* groups, int32_t* first) {
+                                                       int4* groups, int32_t* first, int32_t* gang, int most) {
   grid_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ unsigned long long s_cost[4];  // tiles, as gangs of 1, 2, 4 and 8 go through them
+  if (threadIdx.x < 4) s_cost[threadIdx.x] = 0;
   for (int64_t b = threadIdx.x; b < c.batch; b += kPlanThreads) first[b] = 0;
   __syncthreads();
   WindowParams w{};  // windows as window attention reads them
@@ -143,10 +187,20 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(ts_kv_cache c, ts_attn_ar
     const bool some = lo < hi;
     const int s = some ? max(min(least, sh.shared_lens[g]), 0) >> page_shift << page_shift : 0;
     if (lane == 0) groups[g] = some ? make_int4(lo, hi - lo, s, head) : make_int4(0, 0, 0, 0);
+    if (lane < 4 && s > 0) {
+      const int64_t blocks = ((int64_t)(hi - lo) * (a.heads_q / c.heads) + kBlock - 1) / kBlock;
+      atomicAdd(&s_cost[lane], (unsigned long long)((s + kTile - 1) / kTile * ((blocks + (1 << lane) - 1) >> lane << lane)));
+    }
     for (int64_t b = b0 + lane; b < b1; b += 32) {
       const Req r = request<1, 1>(w, raw_request(w, b));
       if (r.rows) first[b] = s;
     }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {  // the largest that leaves at most a 32nd of the work to no one
+    int k = 3;
+    while (k > 0 && (1 << k > most || s_cost[k] > s_cost[0] + s_cost[0] / 32)) --k;
+    *gang = 1 << k;
   }
 }
 
@@ -164,22 +218,23 @@ __device__ __forceinline__ void widen(const uint4& w, uint4& lo, uint4& hi) {
 // pieces of row r at their place XOR r % 8). Returns what a unit of its products stands for.
 template <int D, typename T>
 __device__ __forceinline__ float load_q(const char* q, unsigned char* to, int r) {
-  uint4 w[D / 8];
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i) w[i] = q ? __ldg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0, 0, 0, 0);
+  // twice, the second time from L1: held in registers a row would take half of them
+  auto load = [&](int i) { return q ? __ldg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0, 0, 0, 0); };
   uint32_t top = 0, bad = 0;
-#pragma unroll
+#pragma unroll 4
   for (int i = 0; i < D / 8; ++i) {
+    const uint4 w = load(i);
     const uint32_t sign = 0x7FFF7FFFu;
-    top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[i].x & sign, w[i].y & sign), __vmaxu2(w[i].z & sign, w[i].w & sign)));
-    bad |= not_finite<T>(w[i].x) | not_finite<T>(w[i].y) | not_finite<T>(w[i].z) | not_finite<T>(w[i].w);
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & sign, w.y & sign), __vmaxu2(w.z & sign, w.w & sign)));
+    bad |= not_finite<T>(w.x) | not_finite<T>(w.y) | not_finite<T>(w.z) | not_finite<T>(w.w);
   }
   // the exponent field of the largest as a float; both factors stay normal
   const int e = min(max((int)(__float_as_uint(unpack<T>(max(top >> 16, top & 0xFFFFu)).x) >> 23), 15), 254);
   const float by = __uint_as_float((uint32_t)(268 - e) << 23);
-#pragma unroll
+#pragma unroll 4
   for (int i = 0; i < D / 8; ++i) {
-    uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    const uint4 w = load(i);
+    uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float2 f = unpack<T>(x[k]);
@@ -191,9 +246,9 @@ __device__ __forceinline__ float load_q(const char* q, unsigned char* to, int r)
 }
 
 template <int D, typename T>
-__global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ PrefixParams p) {
+__global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ PrefixParams p, const __grid_constant__ CUtensorMap k_map,
+                                                        const __grid_constant__ CUtensorMap v_map) {
   using L = Layout<D>;
-  constexpr int ST = L::stages;
   extern __shared__ unsigned char raw_smem[];
   unsigned char* sm = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
   Shared& x = *reinterpret_cast<Shared*>(sm + L::off_x);
@@ -202,18 +257,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
   int4 desc = make_int4(-1, 0, 0, 0);
   grid_launch();
   grid_wait();
-  Line<kBlock, kTile, PrefixParams> line;
-  if (!line_begin<kBlock, kTile, kThreads>(p, kMinTiles, line)) {
+  Share line;
+  if (!line.begin(p)) {
     if (tid == 0) p.desc[blockIdx.x] = desc;
     return;
   }
   if (warp == kIssue) tmem_alloc(&x.tmem, 512);
   if (tid == 0) {
-    for (int i = 0; i < ST; ++i) {
+    for (int i = 0; i < L::k_stages; ++i) {
       mbar_init(&x.k_full[i], kConvert);
       mbar_init(&x.k_empty[i], 1);
+    }
+    for (int i = 0; i < L::v_halves; ++i) {
       mbar_init(&x.v_full[i], kConvert);
       mbar_init(&x.v_empty[i], 1);
+    }
+    for (int i = 0; i < L::units; ++i) {
+      mbar_init(&x.raw_full[i], 1);
+      mbar_init(&x.raw_empty[i], kConvert);
     }
     for (int i = 0; i < kMeta; ++i) mbar_init(&x.meta_full[i], 1);
     for (int i = 0; i < 2; ++i) {
@@ -233,170 +294,207 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
   const uint32_t tmem = x.tmem;
   Segment s{};
 
-  if (warp == kIssue) {
-    // ---- the products, by a lane. Tiles are counted through the CTA's units; tile i is in stage i % ST.
-    const uint32_t q_lo = desc_lo(smem_u32(sm), 16), k_lo = desc_lo(smem_u32(sm) + L::off_k, 16);
-    const uint32_t v_lo = desc_lo(smem_u32(sm) + L::off_v, L::atom_bytes), hi = desc_hi(1024, kSwizzle128);
-    uint32_t i = 0, u = 0, jobs[2] = {0, 0};
+  if (warp >= kIssue) {
+    set_regs<kIssueRegs, false>();
+    if (warp == kIssue) {
+      // ---- the products. Tiles are counted through the CTA's units; tile i is in stage i % k_stages, its
+      // halves of V in those of 2 i and 2 i + 1 % v_halves.
+      const uint32_t leader = elect_one(), tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t q_lo = desc_lo(smem_u32(sm), 16), k_lo = desc_lo(smem_u32(sm) + L::off_k, 16);
+      const uint32_t v_lo = desc_lo(smem_u32(sm) + L::off_v, L::atom_bytes / 2), hi = desc_hi(1024, kSwizzle128);
+      uint32_t i = 0, u = 0, jobs0 = 0, jobs1 = 0;
+      auto scores = [&](int slot, uint32_t t, bool last) {  // of tile t; last: of those that read it
+        const int st = t % L::k_stages;
+        wait(&x.k_full[st], t / L::k_stages & 1, &x.stop);
+        __syncwarp();
+        tc_fence_after();
+        const uint32_t d = tm + slot * kTile, a = q_lo + slot * (L::tile_bytes / 16), b = k_lo + st * (L::tile_bytes / 16);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t at = (k >> 2) * (L::atom_bytes / 16) + (k & 3) * 2;
+          mma_f16(leader, d, a + at, hi, b + at, hi, f16_idesc(kRows, kTile, false), k > 0);
+        }
+        mma_commit(leader, &x.s_full[slot]);
+        if (last) mma_commit(leader, &x.k_empty[st]);
+      };
+      auto outputs = [&](int slot, uint32_t t, bool fresh, bool last) {
+        const uint32_t jobs = slot ? jobs1++ : jobs0++;
+        const uint32_t d = tm + L::col_o + slot * D, a = tm + slot * kTile;
+        wait(&x.p_full[slot], jobs & 1, &x.stop);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t h = 2 * t + half, st = h % L::v_halves;
+          wait(&x.v_full[st], h / L::v_halves & 1, &x.stop);
+          __syncwarp();
+          tc_fence_after();
+          const uint32_t b = v_lo + st * (L::tile_bytes / 32);
+#pragma unroll
+          for (int k = 0; k < kTile / 32; ++k)
+            mma_f16_ts(leader, d, a + half * (kTile / 4) + k * 8, b + k * (16 * 128 / 16), hi, f16_idesc(kRows, D, true), !fresh || half > 0 || k > 0);
+          if (last) mma_commit(leader, &x.v_empty[st]);
+        }
+        mma_commit(leader, &x.o_done[slot]);
+      };
 #pragma unroll 1
-    while (line.next(p, s)) {
-      const int n = s.t1 - s.t0;
-      const bool wide = s.rows > kRows;
-      wait(&x.q_full, u & 1, &x.stop);
-      __syncwarp();
-      if (lane == 0) {
-        auto scores = [&](int slot, int j, bool last) {  // last: of those that read the tile
-          const int st = (i + j) % ST;
-          wait(&x.k_full[st], (i + j) / ST & 1, &x.stop);
-          if (stopped(&x.stop)) return;
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t at = (k >> 2) * (L::atom_bytes / 16) + (k & 3) * 2;
-            mma_f16(tmem + slot * kTile, q_lo + slot * (L::tile_bytes / 16) + at, hi, k_lo + st * (L::tile_bytes / 16) + at, hi,
-                    f16_idesc(kRows, kTile, false), k > 0);
-          }
-          mma_commit(&x.s_full[slot]);
-          if (last) mma_commit(&x.k_empty[st]);
-        };
-        auto outputs = [&](int slot, int j, bool fresh, bool last) {
-          const int st = (i + j) % ST;
-          wait(&x.v_full[st], (i + j) / ST & 1, &x.stop);
-          wait(&x.p_full[slot], jobs[slot] & 1, &x.stop);
-          ++jobs[slot];
-          if (stopped(&x.stop)) return;
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_f16_ts(tmem + L::col_o + slot * D, tmem + slot * kTile + k * 8, v_lo + st * (L::tile_bytes / 16) + k * (16 * 128 / 16), hi,
-                       f16_idesc(kRows, D, true), !fresh || k > 0);
-          mma_commit(&x.o_done[slot]);
-          if (last) mma_commit(&x.v_empty[st]);
-        };
+      while (line.next(p, s)) {
+        // the same for every lane, as the compiler is to see
+        const int n = __shfl_sync(0xffffffffu, s.t1 - s.t0, 0);
+        const bool wide = __shfl_sync(0xffffffffu, s.rows, 0) > kRows;
+        wait(&x.q_full, u & 1, &x.stop);
+        __syncwarp();
         if (wide) {
-          scores(0, 0, false);
-          scores(1, 0, true);
+          scores(0, i, false);
+          scores(1, i, true);
 #pragma unroll 1
-          for (int j = 0; j < n; ++j) {
-#pragma unroll 1
-            for (int slot = 0; slot < 2; ++slot) {
-              outputs(slot, j, j == 0, slot == 1);
-              if (j + 1 < n) scores(slot, j + 1, slot == 1);
-            }
+          for (int j = 0; j < n; ++j, ++i) {
+            outputs(0, i, j == 0, false);
+            if (j + 1 < n) scores(0, i + 1, false);
+            outputs(1, i, j == 0, true);
+            if (j + 1 < n) scores(1, i + 1, true);
           }
-        } else {
-          scores(0, 0, true);
-          if (n > 1) scores(1, 1, true);
+        } else {  // tiles in turn
+          scores(0, i, true);
+          if (n > 1) scores(1, i + 1, true);
 #pragma unroll 1
-          for (int j = 0; j < n; ++j) {
-            outputs(j & 1, j, j < 2, true);
-            if (j + 2 < n) scores(j & 1, j + 2, true);
+          for (int j = 0; j < n; j += 2) {
+            outputs(0, i + j, j == 0, true);
+            if (j + 2 < n) scores(0, i + j + 2, true);
+            if (j + 1 < n) outputs(1, i + j + 1, j == 0, true);
+            if (j + 3 < n) scores(1, i + j + 3, true);
+          }
+          i += n;
+        }
+        mma_commit(leader, &x.q_empty);
+        ++u;
+      }
+    } else if (warp == kIssue + 1) {
+      // ---- loads: lanes hold a tile's pages and bring them, K and V in turn; page numbers come two
+      // tiles ahead, scales one.
+      struct Tile {
+        int32_t page = -1;
+        int kvh = 0;
+        bool is = false;
+      };
+      const int per_tile = kTile >> p.page_shift, page_bytes = D << p.page_shift;
+      const int32_t outside = (int32_t)max(p.c.num_pages, (int64_t)1);  // reads as zeros
+      int j = 0;
+      const int32_t* table = nullptr;
+      bool more = line.next(p, s);
+      if (more) table = p.c.page_table + (int64_t)p.groups[s.b].w * p.c.ld_table;
+      auto next_tile = [&]() {
+        Tile t;
+        if (!more) return t;
+        t.is = true;
+        t.kvh = s.kvh;
+        const int at = (s.t0 + j) * per_tile + lane;
+        if (lane < per_tile && at << p.page_shift < s.r.len) {
+          const int32_t id = table[at];
+          if (id >= 0 && id < p.c.num_pages) t.page = id;
+        }
+        if (++j == s.t1 - s.t0) {
+          j = 0;
+          more = line.next(p, s);
+          if (more) table = p.c.page_table + (int64_t)p.groups[s.b].w * p.c.ld_table;
+        }
+        return t;
+      };
+      float ks, vs;
+      auto fetch_scales = [&](const Tile& t) {
+        ks = vs = 0.f;
+        if (t.page < 0) return;
+        const int64_t at = (int64_t)t.page * p.c.heads + t.kvh;
+        ks = __ldg(p.c.k_scale + at);
+        vs = __ldg(p.c.v_scale + at);
+      };
+      Tile now = next_tile();
+      fetch_scales(now);
+      Tile then = next_tile();
+      uint32_t i = 0;
+#pragma unroll 1
+      while (now.is) {
+#pragma unroll 1
+        for (int v = 0; v < 2; ++v) {
+          const uint32_t n = 2 * i + v, st = n % L::units;
+          wait(&x.raw_empty[st], (n / L::units & 1) ^ 1, &x.stop);
+          if (!__any_sync(0xffffffffu, stopped(&x.stop))) {  // one answer a warp: its lanes meet inside
+            if (lane == 0) mbar_arrive_expect_tx(&x.raw_full[st], L::unit_bytes);
+            __syncwarp();
+            if (lane < per_tile)
+              tma_load_4d(sm + L::off_raw + st * L::unit_bytes + lane * page_bytes, v ? &v_map : &k_map, 0, 0, now.kvh,
+                          now.page >= 0 ? now.page : outside, &x.raw_full[st]);
           }
         }
-        mma_commit(&x.q_empty);
+        // the scales' place was last read kMeta tiles ago: the products of later tiles have been issued since
+        const bool all = __all_sync(0xffffffffu, lane >= per_tile || now.page >= 0);
+        float4 g = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (now.page >= 0) {
+          g.x = ks;
+          vs = scale_of_v(vs, g.x);
+          g.y = __log2f(vs), g.z = 1.f / vs, g.w = all ? 2.f : 1.f;
+        }
+        if (lane < per_tile)
+          for (int k = 0; k < 8 / per_tile; ++k) x.meta[i % kMeta][lane * (8 / per_tile) + k] = g;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x.meta_full[i % kMeta]);
+        now = then;
+        fetch_scales(now);
+        if (now.is) then = next_tile();
+        ++i;
       }
-      __syncwarp();
-      i += n;
-      ++u;
     }
   } else if (warp >= 8) {
-    // ---- K and V: the threads share a tile's pieces of 16 codes; loads are a tile ahead, page numbers two
-    constexpr int kPer = D / 16, kStep = kConvert * 32 / kPer, N = kTile / kStep;  // pieces of a token, tokens a step
-    const int ct = tid - 256, piece = ct % kPer, tok = ct / kPer;
-    const int atom = piece >> 2, chunk = (piece & 3) * 2;
-    struct Tile {
-      int32_t page = -1;  // of the lane's 16 tokens (lanes 0 .. 7)
-      int kvh = 0;
-      bool is = false;
-    };
-    int j = 0;
-    const int32_t* table = nullptr;
-    bool more = line.next(p, s);
-    if (more) table = p.c.page_table + (int64_t)p.groups[s.b].w * p.c.ld_table;
-    auto next_tile = [&]() {
-      Tile t;
-      if (!more) return t;
-      t.is = true;
-      t.kvh = s.kvh;
-      const int at = (s.t0 + j) * kTile + lane * 16;
-      if (lane < 8 && at < s.r.len) {
-        const int32_t id = table[at >> p.page_shift];
-        if (id >= 0 && id < p.c.num_pages) t.page = id;
-      }
-      if (++j == s.t1 - s.t0) {
-        j = 0;
-        more = line.next(p, s);
-        if (more) table = p.c.page_table + (int64_t)p.groups[s.b].w * p.c.ld_table;
-      }
-      return t;
-    };
-    uint4 k[N], v[N];
-    float ks = 0.f, vs = 0.f;
-    auto fetch = [&](const Tile& t, const void* base, int64_t page_ld, int64_t head_ld, int64_t token_ld, uint4* to) {
-      const char* at = static_cast<const char*>(base) + t.kvh * head_ld + piece * 16;
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const int token = tok + e * kStep;
-        const int32_t page = __shfl_sync(0xffffffffu, t.page, token >> 4);  // one for the warp's tokens
-        to[e] = page >= 0 ? ldg_stream(at + page * page_ld + (token & (p.c.page_size - 1)) * token_ld) : make_uint4(0, 0, 0, 0);
-      }
-    };
-    auto fetch_k = [&](const Tile& t) { fetch(t, p.c.k, p.c.k_page_stride, p.c.k_head_stride, p.c.k_token_stride, k); };
-    auto fetch_v = [&](const Tile& t) { fetch(t, p.c.v, p.c.v_page_stride, p.c.v_head_stride, p.c.v_token_stride, v); };
-    auto fetch_scales = [&](const Tile& t) {
-      ks = vs = 0.f;
-      if (warp != 8 || t.page < 0) return;
-      const int64_t at = (int64_t)t.page * p.c.heads + t.kvh;
-      ks = __ldg(p.c.k_scale + at);
-      vs = scale_of_v(__ldg(p.c.v_scale + at), ks);
-    };
-    auto put = [&](unsigned char* stage, const uint4* from) {
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const int token = tok + e * kStep;
+    set_regs<kConvertRegs, false>();
+    // ---- codes to fp16, 16 a step of a thread
+    constexpr int kPer = D / 16, kStep = kConvert * 32 / kPer;  // pieces of a token, tokens a step
+    const int ct = tid - 256, piece = ct % kPer, tok = ct / kPer, atom = piece >> 2;
+    // the second atom's lanes store their halves the other way round: no two at one bank
+    const int chunk = (piece & 3) * 2 + (atom & 1);
+    const int swizzled = (chunk ^ (tok & 7)) * 16;  // steps are multiples of 8 tokens
+    // n tokens of a unit into an array of rows of 128 bytes
+    auto widen_all = [&](const unsigned char* from, unsigned char* to, int atom_bytes, int n) {
+      const unsigned char* a = from + tok * D + piece * 16;
+      unsigned char* b = to + atom * atom_bytes + tok * 128;
+#pragma unroll 4
+      for (int e = 0; e < n; e += kStep) {
         uint4 lo, hi;
-        widen(from[e], lo, hi);
-        unsigned char* row = stage + atom * L::atom_bytes + token * 128;
-        // the second atom's lanes store their halves the other way round: no two at one bank
-        const int first = chunk + (atom & 1);
-        *reinterpret_cast<uint4*>(row + ((first ^ (token & 7)) * 16)) = atom & 1 ? hi : lo;
-        *reinterpret_cast<uint4*>(row + (((first ^ 1) ^ (token & 7)) * 16)) = atom & 1 ? lo : hi;
+        widen(*reinterpret_cast<const uint4*>(a + e * D), lo, hi);
+        *reinterpret_cast<uint4*>(b + e * 128 + swizzled) = atom & 1 ? hi : lo;
+        *reinterpret_cast<uint4*>(b + e * 128 + (swizzled ^ 16)) = atom & 1 ? lo : hi;
       }
       fence_async_shared();
       __syncwarp();
     };
-    Tile now = next_tile();
-    fetch_scales(now);
-    fetch_k(now);
-    fetch_v(now);
-    Tile then = next_tile();
     uint32_t i = 0;
 #pragma unroll 1
-    while (now.is) {
-      const int st = i % ST;
-      const uint32_t phase = i / ST & 1;
-      if (warp == 8) {
-        // its place was last read kMeta tiles ago: the products of later tiles have been issued since
-        if (lane < 8) x.meta[i % kMeta][lane] = make_float4(ks, __log2f(vs), 1.f / vs, now.page >= 0 ? 1.f : 0.f);
+    while (line.next(p, s)) {
+#pragma unroll 1
+      for (int j = s.t0; j < s.t1; ++j, ++i) {
+        uint32_t n = 2 * i, st = n % L::units;
+        wait(&x.raw_full[st], n / L::units & 1, &x.stop);
+        const uint32_t k = i % L::k_stages;
+        wait(&x.k_empty[k], (i / L::k_stages & 1) ^ 1, &x.stop);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&x.meta_full[i % kMeta]);
-        if (then.is) fetch_scales(then);
+        widen_all(sm + L::off_raw + st * L::unit_bytes, sm + L::off_k + k * L::tile_bytes, L::atom_bytes, kTile);
+        if (lane == 0) {
+          mbar_arrive(&x.k_full[k]);
+          mbar_arrive(&x.raw_empty[st]);
+        }
+        ++n, st = n % L::units;
+        wait(&x.raw_full[st], n / L::units & 1, &x.stop);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t h = 2 * i + half, v = h % L::v_halves;
+          wait(&x.v_empty[v], (h / L::v_halves & 1) ^ 1, &x.stop);
+          __syncwarp();
+          widen_all(sm + L::off_raw + st * L::unit_bytes + half * (L::unit_bytes / 2), sm + L::off_v + v * (L::tile_bytes / 2),
+                    L::atom_bytes / 2, kTile / 2);
+          if (lane == 0) mbar_arrive(&x.v_full[v]);
+        }
+        if (lane == 0) mbar_arrive(&x.raw_empty[st]);
       }
-      wait(&x.k_empty[st], phase ^ 1, &x.stop);
-      __syncwarp();
-      put(sm + L::off_k + st * L::tile_bytes, k);
-      if (lane == 0) mbar_arrive(&x.k_full[st]);
-      if (then.is) fetch_k(then);
-      wait(&x.v_empty[st], phase ^ 1, &x.stop);
-      __syncwarp();
-      put(sm + L::off_v + st * L::tile_bytes, v);
-      if (lane == 0) mbar_arrive(&x.v_full[st]);
-      if (then.is) fetch_v(then);
-      now = then;
-      if (now.is) then = next_tile();
-      ++i;
     }
   } else {
+    set_regs<kSoftmaxRegs, true>();
     // ---- softmax: a thread is a row of its slot
     const int slot = warp >> 2, r = tid & (kRows - 1);
     const uint32_t quarter = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's lanes
@@ -433,32 +531,60 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
         tc_fence_after();
         const float4* meta = x.meta[i % kMeta];
         if (active) {
-          float top = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < kTile; c += 32) {
-            float y[32];
-            tmem_ld32(my_s + c, y);
-            tmem_wait_ld();
-            tmem_tie32(y);
+          // Without a look at the largest score: the tile's probabilities with the reference as it is, kept
+          // in registers; their sum tells whether one was too far above it.
+          uint32_t w[kTile / 2];
+          float all = 0.f, part = 0.f;  // of the tile: probabilities, and each over its scale of V
+          bool again = meta[0].w != 2.f || !(fabsf(m) <= kMostRef);
+          if (!__any_sync(0xffffffffu, again)) {
+            float y[2][32];
+            tmem_ld32(my_s, y[0]);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float4 g = meta[c / 16 + h];
-              if (g.w == 0.f) continue;  // the same for every thread
-              const f32x2 a = pair(fac * g.x, fac * g.x), b = pair(g.y, g.y);
+            for (int c = 0; c < kTile / 32; ++c) {
+              tmem_wait_ld();
+              tmem_tie32(y[c & 1]);
+              if (c + 1 < kTile / 32) tmem_ld32(my_s + (c + 1) * 32, y[(c + 1) & 1]);
 #pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                const float2 z = unpair(fma2(pair(y[16 * h + e], y[16 * h + e + 1]), a, b));
-                top = fmaxf(top, fmaxf(z.x, z.y));
+              for (int h = 0; h < 2; ++h) {
+                const float4 g = meta[2 * c + h];
+                const float* v = y[c & 1] + 16 * h;
+                const f32x2 a = pair(fac * g.x, fac * g.x), b = pair(g.y - m, g.y - m);
+                f32x2 sum[2] = {0, 0};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float2 z = unpair(fma2(pair(v[2 * e], v[2 * e + 1]), a, b));
+                  const float e0 = ex2(z.x), e1 = ex2(z.y);
+                  sum[e & 1] = add2(sum[e & 1], pair(e0, e1));
+                  w[16 * c + 8 * h + e] = f16x2(e0, e1);
+                }
+                const float2 both = unpair(add2(sum[0], sum[1]));
+                all += both.x + both.y;
+                part = fmaf(both.x + both.y, g.z, part);
               }
             }
+            again = all > kMostSum;
           }
-          const bool moves = top > m + kSlack;
-          if (__any_sync(0xffffffffu, moves)) {
-            // only where needed: a row's result must not depend on its neighbours'
-            const float to = moves ? top - kHead : m, by = ex2(m - to);
+          if (__any_sync(0xffffffffu, again)) {
+            // Rows whose largest score is too far up get a new reference, each by its own scores, whatever
+            // its neighbours do; then all rows' probabilities once more. Scores are rounded before the
+            // reference is subtracted: the difference is at most kSlack, however large both are.
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < kTile; c += 16) {
+              const float4 g = meta[c / 16];
+              if (g.w == 0.f) continue;  // the same for every thread
+              float y[16];
+              tmem_ld16(my_s + c, y);
+              tmem_wait_ld();
+              tmem_tie16(y);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) top = fmaxf(top, fmaf(y[e], fac * g.x, g.y));
+            }
+            const float to = top > m + kSlack ? top - kHead : m, by = ex2(m - to);
+            const bool moves = to != m;
             m = to;
             l *= by;
-            if (jobs != before) {
+            if (__any_sync(0xffffffffu, moves) && jobs != before) {
               wait(&x.o_done[slot], (jobs - 1) & 1, &x.stop);
               __syncwarp();
               tc_fence_after();
@@ -473,37 +599,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
                 tmem_st8(my_o + c, o);
               }
             }
-          }
-#pragma unroll 1
-          for (int c = 0; c < kTile; c += 32) {
-            float y[32];
-            uint32_t w[16];
-            tmem_ld32(my_s + c, y);
-            tmem_wait_ld();
-            tmem_tie32(y);
+            part = 0.f;
+            const bool plain = !(fabsf(m) <= kMostRef);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float4 g = meta[c / 16 + h];
-              if (g.w == 0.f) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[8 * h + e] = 0;
-                continue;
-              }
-              // the score as above, then less the reference: at most kSlack, however large both are
-              const f32x2 a = pair(fac * g.x, fac * g.x), b = pair(g.y, g.y), less = pair(-m, -m);
-              f32x2 sum = 0;
+            for (int c = 0; c < kTile / 16; ++c) {
+              const float4 g = meta[c];
+              float y[16], sum = 0.f;
+              tmem_ld16(my_s + 16 * c, y);
+              tmem_wait_ld();
+              tmem_tie16(y);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const float2 z = unpair(add2(fma2(pair(y[16 * h + 2 * e], y[16 * h + 2 * e + 1]), a, b), less));
-                const float e0 = ex2(z.x), e1 = ex2(z.y);
-                sum = add2(sum, pair(e0, e1));
-                w[8 * h + e] = f16x2(e0, e1);
+                float z0 = fmaf(y[2 * e], fac * g.x, plain ? g.y : g.y - m), z1 = fmaf(y[2 * e + 1], fac * g.x, plain ? g.y : g.y - m);
+                if (plain) z0 -= m, z1 -= m;
+                const float e0 = g.w == 0.f ? 0.f : ex2(z0), e1 = g.w == 0.f ? 0.f : ex2(z1);
+                sum += e0 + e1;
+                w[8 * c + e] = f16x2(e0, e1);
               }
-              const float2 both = unpair(sum);
-              l = fmaf(both.x + both.y, g.z, l);
+              part = fmaf(sum, g.w == 0.f ? 0.f : g.z, part);
             }
-            tmem_st16(my_s + c / 2, w);  // P lies over the scores that have been read
           }
+          l += part;
+          // P lies over the scores, which have been read
+#pragma unroll
+          for (int c = 0; c < kTile / 2; c += 16) tmem_st16(my_s + c, w + c);
           tmem_wait_st();
         }
         tc_fence_before();
@@ -519,10 +638,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
       float* part = p.part + (2 * (int64_t)blockIdx.x + (s.t0 == 0 ? 1 : 0)) * slot_floats(kBlock, D);
       float* to = whole ? p.pre_o + at * D : part + (int64_t)row * D;
       float by = 1.f;
-      if (!wide) {  // the slots meet
-        x.ml[slot][r] = make_float2(m, l);
+      if (!wide) {  // the slots meet, when the last scores of both are formed and Q has been read
         bar_sync(1, 256);
-        const float2 other = x.ml[slot ^ 1][r];
+        float2* ml = reinterpret_cast<float2*>(sm + kMeetMl);
+        ml[slot * kRows + r] = make_float2(m, l);
+        bar_sync(1, 256);
+        const float2 other = ml[(slot ^ 1) * kRows + r];
         const float top = fmaxf(m, other.x);
         by = live ? ex2(m - top) : 0.f;
         l = fmaf(l, by, other.y * ex2(other.x - top));
@@ -536,14 +657,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
       for (int c = 0; c < D; c += 32) {
         float o[32];
         if (live) {
-          tmem_ld32(my_o + c, o);
+          tmem_ld16(my_o + c, o);
+          tmem_ld16(my_o + c + 16, o + 16);
           tmem_wait_ld();
           tmem_tie32(o);
         }
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = live ? o[e] * by : 0.f;
         if (!wide) {
-          float4* meet = reinterpret_cast<float4*>(x.meet + r * kMeetLd);
+          float4* meet = reinterpret_cast<float4*>(sm) + r * (kMeetLd / 4);
           if (slot == 1) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) meet[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
@@ -567,10 +689,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
       if (!whole) {
         if (s.t0 == 0) {
           desc.x = s.b;
-          desc.y = s.kvh * s.r.blocks + s.block;
+          desc.y = s.kvh;
           desc.z = s.rows;
+          desc.w |= s.block << 1;
         } else {
-          desc.w = s.t1 == s.r.tiles ? 1 : 0;
+          desc.w |= s.t1 == s.r.tiles ? 1 : 0;
         }
       }
       i0 += n;
@@ -602,16 +725,17 @@ __global__ void __launch_bounds__(128) k_prefix_join(const __grid_constant__ Pre
   const int row = blockIdx.y * 4 + (threadIdx.x >> 5);
   const int4 d = p.desc[first];
   if (d.x < 0 || row >= d.z) return;
+  const int gang = *p.gang;  // the pieces' CTAs are this far apart
   int pieces = 1;
   for (;; pieces += 32) {
-    const int i = first + pieces + lane;
-    const unsigned ends = __ballot_sync(0xffffffffu, i >= (int)gridDim.x || p.desc[i].w != 0);
+    const int i = first + (pieces + lane) * gang;
+    const unsigned ends = __ballot_sync(0xffffffffu, i >= (int)gridDim.x || (p.desc[i].w & 1));
     if (ends) {
       pieces += __ffs(ends);
       break;
     }
   }
-  auto piece = [&](int i) { return p.part + (int64_t)(i ? 2 * (first + i) : 2 * first + 1) * slot_floats(kBlock, D); };
+  auto piece = [&](int i) { return p.part + (int64_t)(i ? 2 * (first + i * gang) : 2 * first + 1) * slot_floats(kBlock, D); };
   float top = kNone;
   for (int i = lane; i < pieces; i += 32) top = fmaxf(top, piece(i)[kBlock * D + row]);
   top = warp_max(top);
@@ -630,8 +754,8 @@ __global__ void __launch_bounds__(128) k_prefix_join(const __grid_constant__ Pre
   }
   Segment s;
   s.r = request<kBlock, kTile>(p, raw_request(p, d.x));
-  s.kvh = d.y / s.r.blocks;
-  s.block = d.y % s.r.blocks;
+  s.kvh = d.y;
+  s.block = d.w >> 1;
   const int64_t at = s.at(p, kBlock, row);
   if (lane == 0) p.pre_ml[at] = make_float2(top, sum);
 #pragma unroll
@@ -641,9 +765,14 @@ __global__ void __launch_bounds__(128) k_prefix_join(const __grid_constant__ Pre
 template <int D, typename T>
 cudaError_t launch(const PrefixParams& p, int sms, cudaStream_t s) {
   constexpr int bytes = smem_bytes<D>();
+  CUtensorMap k, v;
+  const ts_kv_cache& c = p.c;
+  if (!page_map(&k, c, c.k, c.k_page_stride, c.k_head_stride, c.k_token_stride, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !page_map(&v, c, c.v, c.v_page_stride, c.v_head_stride, c.v_token_stride, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cudaErrorInvalidValue;
   cudaError_t e = allow_smem<k_prefix<D, T>>(bytes);
   if (e != cudaSuccess) return e;
-  if ((e = launch_after(k_prefix<D, T>, dim3(sms), kThreads, bytes, s, p)) != cudaSuccess) return e;
+  if ((e = launch_after(k_prefix<D, T>, dim3(sms), kThreads, bytes, s, p, k, v)) != cudaSuccess) return e;
   return launch_after(k_prefix_join<D>, dim3(sms, kBlock / 4), 128, 0, s, p);
 }
 
@@ -651,6 +780,7 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 struct Scratch {
   int4* groups;
+  int32_t* gang;
   int32_t* first;
   float* pre_o;
   float2* pre_ml;
@@ -667,6 +797,7 @@ size_t lay_out(Scratch& x, int64_t batch, int64_t groups, int64_t total_rows, in
   };
   const size_t rows = (size_t)total_rows * heads_q;
   take(x.groups, (size_t)groups);
+  take(x.gang, 1);
   take(x.first, (size_t)batch);
   take(x.pre_o, rows * D);
   take(x.pre_ml, rows);
@@ -705,12 +836,13 @@ cudaError_t launch_shared(const ts_shared_args& sh, void* ws, int sms, uint64_t 
   p.group = a.heads_q / c.heads;
   p.scale_log2 = a.sm_scale * kLog2e;
   p.groups = x.groups;
+  p.gang = x.gang;
   p.part = x.part;
   p.desc = x.desc;
   p.pre_o = x.pre_o;
   p.pre_ml = x.pre_ml;
   p.wait_cycles = wait_cycles;
-  k_plan<<<1, kPlanThreads, 0, s>>>(c, a, sh, p.page_shift, x.groups, x.first);
+  k_plan<<<1, kPlanThreads, 0, s>>>(c, a, sh, p.page_shift, x.groups, x.first, x.gang, std::min(sms, kMaxGang));
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (a.dtype == TS_BF16)

@@ -41,20 +41,36 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a_lo, uint32_t a_hi,
 __host__ __device__ constexpr uint32_t f16_idesc(int m, int n, bool b_mn) {
   return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
-// One thread: D (TMEM) = A B (+ D), k = 16; A in shared memory, or (_ts) in TMEM.
-__device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+// One lane of a warp whose lanes are all here. Products and commits that follow take it as their
+// predicate, so that the warp's flow stays one and descriptors live in uniform registers: the tensor cores'
+// queue is short, and what stands between two products is time that they wait.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r;
+}
+// D (TMEM) = A B (+ D), k = 16; A in shared memory, or (_ts) in TMEM.
+__device__ __forceinline__ void mma_f16(uint32_t elected, uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
                                         uint32_t idesc, bool add) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.u32 p, %6, 0;\n mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n}\n" ::"r"(d),
-      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)add)
+      "{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.u32 p, %6, 0;\n setp.ne.u32 q, %7, 0;\n mov.b64 a, {%1, %2};\n"
+      " mov.b64 b, {%3, %4};\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)add), "r"(elected)
       : "memory");
 }
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_f16_ts(uint32_t elected, uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                           bool add) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.u32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)add)
+      "{\n .reg .pred p, q;\n .reg .b64 b;\n setp.ne.u32 p, %5, 0;\n setp.ne.u32 q, %6, 0;\n mov.b64 b, {%2, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)add), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t elected, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.u32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+      "r"(elected)
       : "memory");
 }
 

@@ -185,8 +185,10 @@ struct Line {
 // it up. Returns false for a CTA without work. least_tiles: a CTA takes this many tiles at least, or as
 // many as an average unit has where that is less (14 windows of 8 rows over 4 tokens, head_dim 64:
 // 16 us, 39 with four such units a CTA).
+// cta of ctas: whose share.
 template <int ROWS, int TILE, int THREADS, typename P>
-__device__ __forceinline__ bool line_begin(const P& p, int least_tiles, Line<ROWS, TILE, P>& line) {
+__device__ __forceinline__ bool line_begin(const P& p, int least_tiles, Line<ROWS, TILE, P>& line, unsigned cta = blockIdx.x,
+                                           unsigned ctas = gridDim.x) {
   static_assert(THREADS % 32 == 0, "whole warps");
   __shared__ int64_t s_scan[THREADS / 32], s_start;
   __shared__ uint32_t s_units[THREADS / 32];  // below 2^28: total_rows * heads_q is below 2^31
@@ -223,8 +225,8 @@ __device__ __forceinline__ bool line_begin(const P& p, int least_tiles, Line<ROW
     units += s_units[w];
   }
   const int64_t least = all < (int64_t)least_tiles * units ? max(all / max(units, 1u), (int64_t)1) : least_tiles;
-  const int64_t share = max((all + gridDim.x - 1) / gridDim.x, least);
-  const int64_t begin = min(all, blockIdx.x * share), end = min(all, begin + share);
+  const int64_t share = max((all + ctas - 1) / ctas, least);
+  const int64_t begin = min(all, cta * share), end = min(all, begin + share);
   if (begin < end && upto - mine <= begin && begin < upto) {  // one thread
     int64_t at = upto - mine;
 #pragma unroll 1
@@ -366,6 +368,11 @@ __global__ void __launch_bounds__(128) k_join(const __grid_constant__ WindowPara
   join_row<D, ROWS, TILE, T>(p);
 }
 
+// The tensor map of K or V, a box a page of one head (ts_window_tc.cu); false: not possible.
+bool page_map(CUtensorMap* map, const ts_kv_cache& c, void* base, int64_t page_stride, int64_t head_stride, int64_t token_stride,
+              CUtensorMapSwizzle swizzle);
+bool encoder_found();  // the driver's encoder of tensor maps
+
 // Lets a kernel have this much dynamic shared memory, once on each device.
 template <auto kernel>
 cudaError_t allow_smem(int bytes) {
@@ -382,8 +389,8 @@ cudaError_t allow_smem(int bytes) {
 
 // Launches with programmatic stream serialisation: the kernel may start before the one
 // before it ends, and waits for it (grid_wait) where it needs its results.
-template <typename K, typename P>
-cudaError_t launch_after(K kernel, dim3 grid, int threads, int smem, cudaStream_t s, const P& p) {
+template <typename K, typename... P>
+cudaError_t launch_after(K kernel, dim3 grid, int threads, int smem, cudaStream_t s, const P&... p) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -394,7 +401,7 @@ cudaError_t launch_after(K kernel, dim3 grid, int threads, int smem, cudaStream_
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p...);
 }
 
 }  // namespace tsv

@@ -735,6 +735,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+template <int ROWS, int QP, typename T>
+cudaError_t launch(const WindowParams& p, const CUtensorMap& k, const CUtensorMap& v, int sms, cudaStream_t s) {
+  constexpr int bytes = smem_bytes<ROWS, QP>();
+  cudaError_t e = allow_smem<k_window_tc<ROWS, QP, T>>(bytes);
+  if (e != cudaSuccess) return e;
+  k_window_tc<ROWS, QP, T><<<sms, kThreads, bytes, s>>>(p, k, v);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((int64_t)p.c.max_pages * p.c.page_size <= kTile) return cudaSuccess;  // units of one tile are never split
+  WindowParams joined = p;
+  joined.pre_ml = nullptr;  // in the pieces
+  return launch_after(k_join<kD, ROWS, kTile, T>, dim3(sms, ROWS / 4), 128, 0, s, joined);
+}
+
+}  // namespace
+
+namespace {
+
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -752,32 +769,23 @@ EncodeTiled encoder() {
   return f;
 }
 
+}  // namespace
+
+bool encoder_found() { return encoder() != nullptr; }
+
 // K or V as [pages][heads][tokens of a page][D] bytes; a box is one page of one head.
-bool page_map(CUtensorMap* map, const ts_kv_cache& c, void* base, int64_t page_stride, int64_t head_stride, int64_t token_stride) {
+bool page_map(CUtensorMap* map, const ts_kv_cache& c, void* base, int64_t page_stride, int64_t head_stride, int64_t token_stride,
+              CUtensorMapSwizzle swizzle) {
+  if (!encoder()) return false;
   // the stride of an extent of one is never used, but has to be a valid one
   if (c.heads == 1) head_stride = token_stride;
   if (c.num_pages <= 1) page_stride = token_stride;
-  const cuuint64_t dims[4] = {(cuuint64_t)kD, (cuuint64_t)c.page_size, (cuuint64_t)c.heads, (cuuint64_t)std::max<int64_t>(c.num_pages, 1)};
+  const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.heads, (cuuint64_t)std::max<int64_t>(c.num_pages, 1)};
   const cuuint64_t strides[3] = {(cuuint64_t)token_stride, (cuuint64_t)head_stride, (cuuint64_t)page_stride};
-  const cuuint32_t box[4] = {(cuuint32_t)kD, (cuuint32_t)c.page_size, 1, 1}, step[4] = {1, 1, 1, 1};
+  const cuuint32_t box[4] = {(cuuint32_t)c.head_dim, (cuuint32_t)c.page_size, 1, 1}, step[4] = {1, 1, 1, 1};
   return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                   swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-template <int ROWS, int QP, typename T>
-cudaError_t launch(const WindowParams& p, const CUtensorMap& k, const CUtensorMap& v, int sms, cudaStream_t s) {
-  constexpr int bytes = smem_bytes<ROWS, QP>();
-  cudaError_t e = allow_smem<k_window_tc<ROWS, QP, T>>(bytes);
-  if (e != cudaSuccess) return e;
-  k_window_tc<ROWS, QP, T><<<sms, kThreads, bytes, s>>>(p, k, v);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if ((int64_t)p.c.max_pages * p.c.page_size <= kTile) return cudaSuccess;  // units of one tile are never split
-  WindowParams joined = p;
-  joined.pre_ml = nullptr;  // in the pieces
-  return launch_after(k_join<kD, ROWS, kTile, T>, dim3(sms, ROWS / 4), 128, 0, s, joined);
-}
-
-}  // namespace
 
 cudaError_t window_read_error(uint32_t* word, int clear) {
   cudaError_t e = cudaMemcpyFromSymbol(word, g_window_error, sizeof(uint32_t));
@@ -793,10 +801,9 @@ cudaError_t launch_window_tc(const WindowParams& params, int rows, int sms, cuda
   p.own_ml = nullptr;  // the window's own part is in the pieces; own_o: a block a CTA
   CUtensorMap k, v;
   const ts_kv_cache& c = p.c;
-  if (!encoder()) return cudaErrorNotSupported;
-  if (!page_map(&k, c, c.k, c.k_page_stride, c.k_head_stride, c.k_token_stride) ||
-      !page_map(&v, c, c.v, c.v_page_stride, c.v_head_stride, c.v_token_stride))
-    return cudaErrorInvalidValue;
+  if (!page_map(&k, c, c.k, c.k_page_stride, c.k_head_stride, c.k_token_stride, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !page_map(&v, c, c.v, c.v_page_stride, c.v_head_stride, c.v_token_stride, CU_TENSOR_MAP_SWIZZLE_128B))
+    return encoder_found() ? cudaErrorInvalidValue : cudaErrorNotSupported;
   const bool bf16 = p.a.dtype == TS_BF16;
   if (rows == 32)
     return bf16 ? launch<32, 2, __nv_bfloat16>(p, k, v, sms, s) : launch<32, 3, __half>(p, k, v, sms, s);
