@@ -255,8 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kIssue = 8 + kConvert;  // the warp that issues the products
   int4 desc = make_int4(-1, 0, 0, 0);
-  grid_launch();
   grid_wait();
+  grid_launch();  // behind the wait: the kernel after the next reads the plan, which it does not wait for by itself
   Share line;
   if (!line.begin(p)) {
     if (tid == 0) p.desc[blockIdx.x] = desc;
@@ -716,15 +716,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
   }
 }
 
-// One warp a row of a unit that spans CTAs, as join_row, into the rows' prefix part.
+// The rows of a unit that spans CTAs, as join_row, into their prefix part: a warp takes every
+// gridDim.y * kJoinWarps-th.
+constexpr int kJoinWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(128) k_prefix_join(const __grid_constant__ PrefixParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_constant__ PrefixParams p) {
   grid_launch();
   grid_wait();
   const int first = blockIdx.x, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * 4 + (threadIdx.x >> 5);
   const int4 d = p.desc[first];
-  if (d.x < 0 || row >= d.z) return;
+  if (d.x < 0) return;
   const int gang = *p.gang;  // the pieces' CTAs are this far apart
   int pieces = 1;
   for (;; pieces += 32) {
@@ -735,31 +736,33 @@ __global__ void __launch_bounds__(128) k_prefix_join(const __grid_constant__ Pre
       break;
     }
   }
-  auto piece = [&](int i) { return p.part + (int64_t)(i ? 2 * (first + i * gang) : 2 * first + 1) * slot_floats(kBlock, D); };
-  float top = kNone;
-  for (int i = lane; i < pieces; i += 32) top = fmaxf(top, piece(i)[kBlock * D + row]);
-  top = warp_max(top);
-  constexpr int PER = D / 32;
-  float2 acc[PER / 2];
-#pragma unroll
-  for (int e = 0; e < PER / 2; ++e) acc[e] = make_float2(0.f, 0.f);
-  float sum = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < pieces; ++i) {
-    const float* y = piece(i);
-    const float by = ex2(y[kBlock * D + row] - top);
-    sum = fmaf(by, y[kBlock * D + kBlock + row], sum);
-#pragma unroll
-    for (int e = 0; e < PER / 2; ++e) add_scaled(acc[e], by, *reinterpret_cast<const float2*>(y + row * D + lane * PER + 2 * e));
-  }
   Segment s;
   s.r = request<kBlock, kTile>(p, raw_request(p, d.x));
   s.kvh = d.y;
   s.block = d.w >> 1;
-  const int64_t at = s.at(p, kBlock, row);
-  if (lane == 0) p.pre_ml[at] = make_float2(top, sum);
+  auto piece = [&](int i) { return p.part + (int64_t)(i ? 2 * (first + i * gang) : 2 * first + 1) * slot_floats(kBlock, D); };
+  for (int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); row < d.z; row += gridDim.y * kJoinWarps) {
+    float top = kNone;
+    for (int i = lane; i < pieces; i += 32) top = fmaxf(top, piece(i)[kBlock * D + row]);
+    top = warp_max(top);
+    constexpr int PER = D / 32;
+    float2 acc[PER / 2];
 #pragma unroll
-  for (int e = 0; e < PER / 2; ++e) *reinterpret_cast<float2*>(p.pre_o + at * D + lane * PER + 2 * e) = acc[e];
+    for (int e = 0; e < PER / 2; ++e) acc[e] = make_float2(0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < pieces; ++i) {
+      const float* y = piece(i);
+      const float by = ex2(y[kBlock * D + row] - top);
+      sum = fmaf(by, y[kBlock * D + kBlock + row], sum);
+#pragma unroll
+      for (int e = 0; e < PER / 2; ++e) add_scaled(acc[e], by, *reinterpret_cast<const float2*>(y + row * D + lane * PER + 2 * e));
+    }
+    const int64_t at = s.at(p, kBlock, row);
+    if (lane == 0) p.pre_ml[at] = make_float2(top, sum);
+#pragma unroll
+    for (int e = 0; e < PER / 2; ++e) *reinterpret_cast<float2*>(p.pre_o + at * D + lane * PER + 2 * e) = acc[e];
+  }
 }
 
 template <int D, typename T>
@@ -773,7 +776,7 @@ cudaError_t launch(const PrefixParams& p, int sms, cudaStream_t s) {
   cudaError_t e = allow_smem<k_prefix<D, T>>(bytes);
   if (e != cudaSuccess) return e;
   if ((e = launch_after(k_prefix<D, T>, dim3(sms), kThreads, bytes, s, p, k, v)) != cudaSuccess) return e;
-  return launch_after(k_prefix_join<D>, dim3(sms, kBlock / 4), 128, 0, s, p);
+  return launch_after(k_prefix_join<D>, dim3(sms, 8), kJoinWarps * 32, 0, s, p);
 }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }

@@ -43,20 +43,28 @@ constexpr int kMinTiles = 4;      // least tiles a CTA takes: pieces of 256 toke
 
 using Params = WindowParams;
 
-template <int MT, typename T>
+// TAIL: in shared attention. The window's own tokens are worked on here, at a unit's beginning, as one
+// more part beside the warps' (a kernel of their own took 8 us).
+template <int D, int MT, typename T, bool TAIL>
 __device__ __forceinline__ void attend(const Params& p) {
-  constexpr int D = 64, ROWS = 16 * MT;
+  constexpr int ROWS = 16 * MT, PARTS = kWarps + (TAIL ? 1 : 0);
   constexpr int KS = D / 16;        // k16 steps over the dims
   constexpr int NT = D / 8;         // n8 tiles over the dims
   constexpr int VW = D / 32;        // words of a token's V codes a lane holds
   extern __shared__ __align__(16) unsigned char smem[];
   // Q fragments [MT][KS][32 lanes] and the factors of their rows; then, for the join of the
-  // warps, [kWarps][ROWS][D + 4] outputs with their references and sums
+  // warps, [PARTS][ROWS][D + 4] outputs with their references and sums
   uint4* s_q = reinterpret_cast<uint4*>(smem);
   float* s_fac = reinterpret_cast<float*>(s_q + MT * KS * 32);
   float* s_o = s_fac + ROWS;
-  float* s_m = s_o + kWarps * ROWS * (D + 4);
-  float* s_l = s_m + kWarps * ROWS;
+  float* s_m = s_o + PARTS * ROWS * (D + 4);
+  float* s_l = s_m + PARTS * ROWS;
+  // TAIL: the window's own references and sums, what a tree's rows see, and its parents (of an odd number
+  // of rows: last)
+  float2* s_ml = reinterpret_cast<float2*>(s_l + PARTS * ROWS);
+  Sees* s_trees = reinterpret_cast<Sees*>(s_ml + ROWS);
+  int32_t* s_parents = reinterpret_cast<int32_t*>(s_trees + TS_MAX_WINDOW);
+  static_assert((MT * KS * 32 * 16 + ROWS * 4 + PARTS * ROWS * (D + 6) * 4) % 8 == 0, "s_ml and s_trees");
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int64_t cta = blockIdx.x;
@@ -80,10 +88,13 @@ __device__ __forceinline__ void attend(const Params& p) {
       float top = 0.f;
       uint32_t bad = 0;
       if (i < rows) {
-        const uint32_t w = reinterpret_cast<const uint32_t*>(q_row(p, sg, ROWS, i))[lane];
-        const float2 f = unpack<T>(w);
-        top = fmaxf(fabsf(f.x), fabsf(f.y));
-        bad = not_finite<T>(w);
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) {
+          const uint32_t w = reinterpret_cast<const uint32_t*>(q_row(p, sg, ROWS, i))[k * 32 + lane];
+          const float2 f = unpack<T>(w);
+          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+          bad |= not_finite<T>(w);
+        }
       }
       top = warp_max(top);
       // 2^e <= top < 2^(e+1); the row is divided by 2^e (both factors stay normal: by 2^126 above
@@ -95,8 +106,8 @@ __device__ __forceinline__ void attend(const Params& p) {
     __syncthreads();
     for (int i = tid; i < MT * KS * 32; i += kThreads) {
       const int l = i & 31, ks = i / 32 % KS, mt = i / 32 / KS, qc = l & 3, qg = l >> 2;
-      // K's lane qc holds dims 16qc .. + 15; step k takes dims 4k .. 4k + 3 of them
-      const int dim = qc * 16 + ks * 4;
+      // K's lane qc holds dims 16qc .. + 15 of each 64; step k takes dims 4k .. 4k + 3 of them
+      const int dim = ks / 4 * 64 + qc * 16 + ks % 4 * 4;
       uint32_t w[4];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -184,7 +195,7 @@ __device__ __forceinline__ void attend(const Params& p) {
     const char* vc = static_cast<const char*>(p.c.v) + kvh * p.c.v_head_stride;
     const int32_t* table = p.c.page_table + sg.b * p.c.ld_table + r.skip;
     struct Loaded {
-      uint4 k[2];
+      uint4 k[2][D / 64];
       uint32_t v[4][VW];
       float ks, vs;
     };
@@ -201,15 +212,21 @@ __device__ __forceinline__ void attend(const Params& p) {
       for (int n = 0; n < 2; ++n) {
         const bool ok = page >= 0 && tok + n * 8 + g < r.len;
         const char* at = kc + page * p.c.k_page_stride + (int64_t)(slot + n * 8 + g) * p.c.k_token_stride + c * 16;
-        x.k[n] = ok ? ldg_stream(at) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) x.k[n][h] = ok ? ldg_stream(at + h * 64) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int tt = 2 * c + (i & 1) + (i >> 1) * 8;
         const bool ok = page >= 0 && tok + tt < r.len;
         const char* at = vc + page * p.c.v_page_stride + (int64_t)(slot + tt) * p.c.v_token_stride + g * (D / 8);
-        const uint2 w = ok ? __ldg(reinterpret_cast<const uint2*>(at)) : make_uint2(0, 0);
-        x.v[i][0] = w.x, x.v[i][1] = w.y;
+        if constexpr (D == 64) {
+          const uint2 w = ok ? __ldg(reinterpret_cast<const uint2*>(at)) : make_uint2(0, 0);
+          x.v[i][0] = w.x, x.v[i][1] = w.y;
+        } else {
+          const uint4 w = ok ? __ldg(reinterpret_cast<const uint4*>(at)) : make_uint4(0, 0, 0, 0);
+          x.v[i][0] = w.x, x.v[i][1] = w.y, x.v[i][2] = w.z, x.v[i][3] = w.w;
+        }
       }
       x.ks = x.vs = 1.f;
       if (page >= 0) {
@@ -220,6 +237,31 @@ __device__ __forceinline__ void attend(const Params& p) {
     Loaded next;
     int32_t page = page_of(t0), page2 = page_of(t0 + 1);
     if (t0 < t1) fetch(t0, page, next);
+    const bool own_here = TAIL && p.a.k_new && t0 == 0;
+    if constexpr (TAIL) {
+      if (own_here) {  // each warp a share of the dims, or of the rows
+        const Sees* trees = nullptr;
+        if (p.a.parents) {
+          for (int i = tid; i < r.rows; i += kThreads) s_parents[i] = p.a.parents[r.row0 + i];
+          __syncthreads();
+          for (int i = tid; i < r.rows; i += kThreads) s_trees[i] = tree_sees(s_parents, i);
+          __syncthreads();
+          trees = s_trees;
+        }
+        float* o_own = s_o + kWarps * ROWS * (D + 4);
+        constexpr int kSlices = kWarps / MT;  // of the dims
+        const int i16 = warp / kSlices * 16, j0 = warp % kSlices * (D / 8 / kSlices), j1 = j0 + D / 8 / kSlices;
+        if (i16 < rows) {
+          const bool odd = own_part<D, ROWS, T>(p, sg, i16, j0, j1, trees, o_own, D + 4, s_ml);
+          if (odd) {
+            __syncwarp();
+#pragma unroll 1
+            for (int i = i16; i < min(rows, i16 + 16); ++i)
+              own_odd<D, ROWS, T>(p, sg, i, j0 * 8, j1 * 8, trees, s_ml[i].x, o_own + i * (D + 4));
+          }
+        }
+      }
+    }
     for (int t = t0; t < t1; ++t) {
       Loaded now = next;
       const int32_t page_now = page;
@@ -240,8 +282,8 @@ __device__ __forceinline__ void attend(const Params& p) {
         uint32_t kb[2][2];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const uint4 w4 = now.k[n];
-          const uint32_t w = ks == 0 ? w4.x : ks == 1 ? w4.y : ks == 2 ? w4.z : w4.w;
+          const uint4 w4 = now.k[n][ks / 4];
+          const uint32_t w = ks % 4 == 0 ? w4.x : ks % 4 == 1 ? w4.y : ks % 4 == 2 ? w4.z : w4.w;
           kb[n][0] = e4m3x2_to_f16x2((uint16_t)w);
           kb[n][1] = e4m3x2_to_f16x2((uint16_t)(w >> 16));
         }
@@ -315,6 +357,14 @@ __device__ __forceinline__ void attend(const Params& p) {
       waited = true;
     }
     __syncthreads();
+    if constexpr (TAIL) {
+      for (int i = tid; i < rows; i += kThreads) {
+        const float2 ml = own_here ? s_ml[i] : make_float2(kNone, 0.f);
+        s_m[kWarps * ROWS + i] = ml.x;
+        s_l[kWarps * ROWS + i] = ml.y;
+      }
+      __syncthreads();
+    }
     const bool whole = sg.whole();
     const int slot = (int)(2 * cta) + (t0 == 0 ? 1 : 0);
     float* part = p.part + (int64_t)slot * slot_floats(ROWS, D);
@@ -322,11 +372,12 @@ __device__ __forceinline__ void attend(const Params& p) {
       const int row = i / (D / 4), d = i % (D / 4) * 4;
       float top = kNone;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w * ROWS + row]);
+      for (int w = 0; w < PARTS; ++w) top = fmaxf(top, s_m[w * ROWS + row]);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       float sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < PARTS; ++w) {
+        if (TAIL && w == kWarps && !own_here) continue;
         const float by = ex2(s_m[w * ROWS + row] - top);
         const float4 v = *reinterpret_cast<const float4*>(s_o + (w * ROWS + row) * (D + 4) + d);
         sum = fmaf(by, s_l[w * ROWS + row], sum);
@@ -372,7 +423,14 @@ __device__ __forceinline__ void attend(const Params& p) {
 template <int MT, typename T>
 __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Params p) {
   grid_launch();
-  attend<MT, T>(p);
+  attend<64, MT, T, false>(p);
+}
+
+// What is left of each request behind a shared prefix, and its window's own tokens.
+template <int D, int MT, typename T>
+__global__ void __launch_bounds__(kThreads) k_tail(const __grid_constant__ Params p) {
+  grid_launch();
+  attend<D, MT, T, true>(p);
 }
 
 // More than 32 rows a window: blocks of 64 rows, for which K and V are converted half as often, where the
@@ -386,8 +444,8 @@ __global__ void __launch_bounds__(kThreads) k_window_rows(const __grid_constant_
   grid_launch();
   const bool wide = line_length<64, kTile, kThreads>(p) >= (int64_t)kWideTiles * gridDim.x;
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.wide = wide;
-  if (wide) attend<4, T>(p);
-  else attend<2, T>(p);
+  if (wide) attend<64, 4, T, false>(p);
+  else attend<64, 2, T, false>(p);
 }
 
 template <typename T>
@@ -397,8 +455,10 @@ __global__ void __launch_bounds__(128) k_join_rows(const __grid_constant__ Param
   else join_row<64, 32, kTile, T>(p);
 }
 
-constexpr int smem_bytes(int D, int rows) {
-  return rows / 16 * (D / 16) * 32 * 16 + rows * 4 + kWarps * rows * (D + 4) * 4 + kWarps * rows * 8;
+constexpr int smem_bytes(int D, int rows, bool tail = false) {
+  const int parts = kWarps + (tail ? 1 : 0);
+  return rows / 16 * (D / 16) * 32 * 16 + rows * 4 + parts * rows * (D + 4) * 4 + parts * rows * 8 +
+         (tail ? TS_MAX_WINDOW * ((int)sizeof(Sees) + 4) + rows * 8 : 0);
 }
 
 // kernel, join: k_window and k_join, or k_window_rows and k_join_rows, for blocks of at most ROWS rows.
@@ -429,6 +489,17 @@ cudaError_t launch_64(const Params& p, int rows, int sms, cudaStream_t s) {
   }
 }
 
+template <int D, int MT, typename T>
+cudaError_t launch_tail(const Params& p, int sms, cudaStream_t s) {
+  constexpr int bytes = smem_bytes(D, 16 * MT, true);
+  cudaError_t e = allow_smem<k_tail<D, MT, T>>(bytes);
+  if (e != cudaSuccess) return e;
+  const int grid = sms * kCtasPerSm;
+  if ((e = launch_after(k_tail<D, MT, T>, dim3(grid), kThreads, bytes, s, p)) != cudaSuccess) return e;
+  if ((int64_t)p.c.max_pages * p.c.page_size <= kTile) return cudaSuccess;  // units of one tile are never split
+  return launch_after(k_join<D, 16 * MT, kTile, T>, dim3(grid, 4 * MT), 128, 0, s, p);
+}
+
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // The rows of a block: by the average window. head_dim 128, ragged chains of 4 to 20 rows: 162 us
@@ -439,6 +510,8 @@ int block_rows(const WindowParams& p) {
   if (p.c.head_dim == 128) return rows <= 32 ? 32 : 64;
   return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
+
+int tail_rows(const WindowParams& p) { return (p.a.total_rows * p.group + p.c.batch - 1) / p.c.batch <= 16 ? 16 : 32; }
 
 // Lays the workspace out; returns its bytes.
 size_t lay_out(WindowParams& p, void* ws, int sms) {
@@ -488,6 +561,14 @@ cudaError_t launch_window(const ts_kv_cache& c, const ts_attn_args& a, void* ws,
     p.first = front->first;
     p.pre_o = front->pre_o;
     p.pre_ml = front->pre_ml;
+    p.own_ml = nullptr;  // in the unit's first piece
+    const bool bf16 = a.dtype == TS_BF16;
+    if (c.head_dim == 64) {
+      if (tail_rows(p) == 16) return bf16 ? launch_tail<64, 1, __nv_bfloat16>(p, sms, s) : launch_tail<64, 1, __half>(p, sms, s);
+      return bf16 ? launch_tail<64, 2, __nv_bfloat16>(p, sms, s) : launch_tail<64, 2, __half>(p, sms, s);
+    }
+    if (tail_rows(p) == 16) return bf16 ? launch_tail<128, 1, __nv_bfloat16>(p, sms, s) : launch_tail<128, 1, __half>(p, sms, s);
+    return bf16 ? launch_tail<128, 2, __nv_bfloat16>(p, sms, s) : launch_tail<128, 2, __half>(p, sms, s);
   }
   if (c.head_dim == 128) return launch_window_tc(p, block_rows(p), sms, s);
   const int rows = block_rows(p);

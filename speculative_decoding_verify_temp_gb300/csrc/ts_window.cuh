@@ -108,7 +108,7 @@ struct RawReq {
 __device__ __forceinline__ RawReq raw_request(const WindowParams& p, int64_t b) {
   RawReq r = {0, 0, 0, 0};
   if (b >= p.c.batch) return r;
-  if (p.first) r.first = p.first[b];
+  if (p.first) r.first = __ldcg(p.first + b);  // from L2: written by a kernel that this one does not wait for by itself
   if (p.a.qo_indptr) {
     r.row0 = p.a.qo_indptr[b];
     r.row1 = p.a.qo_indptr[b + 1];
