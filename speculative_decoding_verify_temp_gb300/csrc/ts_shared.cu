@@ -15,9 +15,9 @@
 // with S, P and O in TMEM. K and V codes become fp16 (exact) on their way into shared memory,
 // once for the two blocks of 128 rows that a CTA works on; Q is fp16 with a factor a row: a power
 // of two that puts the row's largest magnitude into [2^14, 2^15), so that bf16 values are exact down to
-// 2^-31 of it. P = 2^(x - m) is rounded to fp16 (2^-11), m a reference of the row that is set 2^7 below the
-// largest score so far and follows when that is 2^15 above it, as in ts_window.cu: the small ones
-// lose at most 2^-25 each, 2^-11 of the row's sum in 2^21 tokens. V's scale is in the exponent.
+// 2^-31 of it. P = 2^(x - m) is rounded to fp16 (2^-11), m a reference of the row that is set 2^4 below a
+// score and follows when a tile's sum is past fp16's range: the small ones lose at most 2^-25 each, 2^-11
+// of the row's sum in 2^18 tokens of a CTA. V's scale is in the exponent.
 //
 // Two slots, each 128 rows and 128 threads, a thread a row (no reduction crosses threads): while one
 // slot's scores are made into P, the tensor cores work on the other's products. More than 128 rows
@@ -47,6 +47,7 @@ struct PrefixParams {
   float scale_log2;
   const int4* groups;  // {first row, rows, shared tokens, first request with a window}
   const int32_t* gang; // CTAs that share tokens
+  const Start* starts; // [gangs]
   float* part;         // [2 * CTAs] pieces of kBlock rows: outputs, references, sums
   int4* desc;          // [CTAs] {tail unit's group, its head, rows, 2 * its block | the CTA's first piece ends its unit}
   float* pre_o;
@@ -84,9 +85,8 @@ constexpr int kSoftmaxRegs = 184, kConvertRegs = 80, kIssueRegs = 64;
 static_assert(256 * kSoftmaxRegs + kConvert * 32 * kConvertRegs + 128 * kIssueRegs <= kThreads * 128, "registers");
 constexpr int kMaxGang = 8;
 constexpr int kMeta = 8;     // tiles whose scales are in shared memory
-constexpr float kHead = 7.f;         // a reference is set this far, in log2, below the largest score
-constexpr float kMostSum = 32768.f;  // of a tile's probabilities, where the reference stays
-constexpr float kSlack = 8.f;        // how far a score may be above it where it is looked at: 128 * 2^8 = kMostSum
+constexpr float kHead = 4.f;         // a reference is set this far, in log2, below the largest score
+constexpr float kMostSum = 65504.f;  // of a tile's probabilities, where the reference stays: none is past fp16
 constexpr float kMostRef = 65536.f;  // references of at most this size: scores and reference in one operation
 constexpr int kMinTiles = 1;
 constexpr int kPlanThreads = 1024;
@@ -109,9 +109,10 @@ struct Layout {
   static constexpr int col_o = 2 * kTile;            // TMEM: S (and P) of both slots, then O
 };
 
-// Where the slots meet, in the place of Q: 32 columns of outputs, padded, then references and sums.
-constexpr int kMeetLd = 36, kMeetMl = kRows * kMeetLd * 4;
-static_assert(kMeetMl + 2 * kRows * 8 <= 2 * Layout<64>::tile_bytes, "Q's place");
+// Where outputs pass through and the slots meet, in the place of Q: 16 columns, padded, of a slot's rows (each
+// slot's in its own Q; where they meet, in the first's), then references and sums.
+constexpr int kMeetLd = 20, kMeetMl = kRows * kMeetLd * 4;
+static_assert(kMeetMl + 2 * kRows * 8 <= Layout<64>::tile_bytes, "Q's place");
 
 struct Shared {
   uint64_t k_full[4], k_empty[4], v_full[8], v_empty[8], raw_full[6], raw_empty[6], meta_full[kMeta];
@@ -141,7 +142,7 @@ struct Share {
   __device__ __forceinline__ bool begin(const PrefixParams& p) {
     gang = *p.gang;
     rank = blockIdx.x % gang;
-    return line_begin<kBlock, kTile, kThreads>(p, kMinTiles, line, blockIdx.x / gang, gridDim.x / gang);
+    return blockIdx.x / gang < gridDim.x / gang && line_at<kBlock, kTile>(p, p.starts[blockIdx.x / gang], line);
   }
   __device__ __forceinline__ bool next(const PrefixParams& p, Segment& s) {
     while (line.next(p, s)) {
@@ -155,9 +156,11 @@ struct Share {
 
 // ---- the groups
 
-__global__ void __launch_bounds__(kPlanThreads) k_plan(ts_kv_cache c, ts_attn_args a, ts_shared_args sh, int page_shift,
-                                                       int4* groups, int32_t* first, int32_t* gang, int most) {
+__global__ void __launch_bounds__(kPlanThreads) k_plan(const __grid_constant__ PrefixParams p, ts_kv_cache c, ts_shared_args sh,
+                                                       int4* groups, int32_t* first, int32_t* gang, Start* starts, int ctas) {
   grid_launch();
+  const ts_attn_args& a = p.a;
+  const int page_shift = p.page_shift;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __shared__ unsigned long long s_cost[4];  // tiles, as gangs of 1, 2, 4 and 8 go through them
   if (threadIdx.x < 4) s_cost[threadIdx.x] = 0;
@@ -199,9 +202,11 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(ts_kv_cache c, ts_attn_ar
   __syncthreads();
   if (threadIdx.x == 0) {  // the largest that leaves at most a 32nd of the work to no one
     int k = 3;
-    while (k > 0 && (1 << k > most || s_cost[k] > s_cost[0] + s_cost[0] / 32)) --k;
+    while (k > 0 && (1 << k > ctas || s_cost[k] > s_cost[0] + s_cost[0] / 32)) --k;
     *gang = 1 << k;
   }
+  __syncthreads();
+  line_starts<kBlock, kTile, kPlanThreads>(p, kMinTiles, ctas / *gang, starts);
 }
 
 // ---- the shared tokens
@@ -214,35 +219,55 @@ __device__ __forceinline__ void widen(const uint4& w, uint4& lo, uint4& hi) {
   hi.z = e4m3x2_to_f16x2((uint16_t)w.w), hi.w = e4m3x2_to_f16x2((uint16_t)(w.w >> 16));
 }
 
-// A thread's row of Q as fp16 into its place (rows of 128 bytes in atoms of 64 values, the 16-byte
-// pieces of row r at their place XOR r % 8). Returns what a unit of its products stands for.
+// A warp's 32 rows of Q (rows r0 .. r0 + 31 of `left`; the others zeros) as fp16 into their place: rows of 128
+// bytes in atoms of 64 values, the 16-byte pieces of row r at their place XOR r % 8. Returns what a
+// unit of the products of the lane's row stands for. Four steps of loads are in flight, and the code is kept
+// small: it runs once a unit, from cold instruction caches (unrolled sixteen times it took 14 us).
 template <int D, typename T>
-__device__ __forceinline__ float load_q(const char* q, unsigned char* to, int r) {
-  // twice, the second time from L1: held in registers a row would take half of them
-  auto load = [&](int i) { return q ? __ldg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0, 0, 0, 0); };
-  uint32_t top = 0, bad = 0;
-#pragma unroll 4
-  for (int i = 0; i < D / 8; ++i) {
-    const uint4 w = load(i);
-    const uint32_t sign = 0x7FFF7FFFu;
-    top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & sign, w.y & sign), __vmaxu2(w.z & sign, w.w & sign)));
-    bad |= not_finite<T>(w.x) | not_finite<T>(w.y) | not_finite<T>(w.z) | not_finite<T>(w.w);
-  }
-  // the exponent field of the largest as a float; both factors stay normal
-  const int e = min(max((int)(__float_as_uint(unpack<T>(max(top >> 16, top & 0xFFFFu)).x) >> 23), 15), 254);
-  const float by = __uint_as_float((uint32_t)(268 - e) << 23);
-#pragma unroll 4
-  for (int i = 0; i < D / 8; ++i) {
-    const uint4 w = load(i);
-    uint32_t x[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ float load_q(const PrefixParams& p, const Segment& s, int r0, int left, unsigned char* to) {
+  constexpr int kLanes = D / 8, kEach = 32 / kLanes, N = 32 / kEach, kAhead = 4;  // lanes of a row, rows a step, steps
+  const int lane = threadIdx.x & 31, piece = lane % kLanes, sub = lane / kLanes;
+  const int j = s.block * kBlock + r0 + sub;
+  int h = j % p.group;
+  const char* at = static_cast<const char*>(p.a.q) + (s.r.row0 + j / p.group) * p.a.q_row_stride + (int64_t)(s.kvh * p.group + h) * p.a.q_head_stride + piece * 16;
+  const int64_t head = p.a.q_head_stride, row = p.a.q_row_stride - p.group * p.a.q_head_stride;
+  left -= sub;
+  int r = (r0 & (kRows - 1)) + sub;
+  float mine = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < N; i += kAhead) {
+    uint4 w[kAhead];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = unpack<T>(x[k]);
-      x[k] = f16x2(f.x * by, f.y * by);
+    for (int k = 0; k < kAhead; ++k) {
+      w[k] = left > 0 ? __ldg(reinterpret_cast<const uint4*>(at)) : make_uint4(0, 0, 0, 0);
+      left -= kEach;
+      h += kEach;
+      at += kEach * head;
+#pragma unroll 1
+      for (; h >= p.group; h -= p.group) at += row;
     }
-    *reinterpret_cast<uint4*>(to + (i >> 3) * Layout<D>::atom_bytes + r * 128 + ((i & 7) ^ (r & 7)) * 16) = make_uint4(x[0], x[1], x[2], x[3]);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k, r += kEach) {
+      const uint32_t sign = 0x7FFF7FFFu;
+      const uint32_t m = __vmaxu2(__vmaxu2(w[k].x & sign, w[k].y & sign), __vmaxu2(w[k].z & sign, w[k].w & sign));
+      uint32_t top = max(m >> 16, m & 0xFFFFu);  // the largest magnitude of the row, as bits
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // its exponent field as a float; both factors stay normal
+      const int e = min(max((int)(__float_as_uint(unpack<T>(top).x) >> 23), 15), 254);
+      const float by = __uint_as_float((uint32_t)(268 - e) << 23), back = not_finite<T>(top) ? NAN : __uint_as_float((uint32_t)(e - 14) << 23);
+      const float f = __shfl_sync(0xffffffffu, back, lane % kEach * kLanes);  // to the lane whose row it is
+      if (lane / kEach == i + k) mine = f;
+      uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float2 v = unpack<T>(x[c]);
+        x[c] = f16x2(v.x * by, v.y * by);
+      }
+      *reinterpret_cast<uint4*>(to + (piece >> 3) * Layout<D>::atom_bytes + r * 128 + ((piece & 7) ^ (r & 7)) * 16) = make_uint4(x[0], x[1], x[2], x[3]);
+    }
   }
-  return bad ? NAN : __uint_as_float((uint32_t)(e - 14) << 23);
+  return mine;
 }
 
 template <int D, typename T>
@@ -256,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
   constexpr int kIssue = 8 + kConvert;  // the warp that issues the products
   int4 desc = make_int4(-1, 0, 0, 0);
   grid_wait();
-  grid_launch();  // behind the wait: the kernel after the next reads the plan, which it does not wait for by itself
+  grid_launch();  // behind the wait: a CTA of the next kernel reads the plan without one
   Share line;
   if (!line.begin(p)) {
     if (tid == 0) p.desc[blockIdx.x] = desc;
@@ -511,16 +536,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
       const int64_t at = mine ? s.at(p, kBlock, row) : 0;
       wait(&x.q_empty, (u & 1) ^ 1, &x.stop);
       __syncwarp();
-      const char* q = nullptr;
-      if (mine) {
-        const int64_t w = at / p.a.heads_q;
-        q = static_cast<const char*>(p.a.q) + w * p.a.q_row_stride + (at - w * p.a.heads_q) * p.a.q_head_stride;
-      }
-      const float fac = load_q<D, T>(q, sm + slot * L::tile_bytes, r) * p.scale_log2;
+      const int r0 = row - lane;  // the warp's first row
+      const float fac = load_q<D, T>(p, s, r0, s.rows - r0, sm + slot * L::tile_bytes) * p.scale_log2;
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(&x.q_full);
-      float m = kNone, l = 0.f;
+      float m = fac == fac ? kNone : 0.f, l = 0.f;  // a row whose q is not finite asks for nothing
       const uint32_t before = jobs;
 #pragma unroll 1
       for (int j = j0; j < n; j += step, ++jobs) {
@@ -531,13 +552,83 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
         tc_fence_after();
         const float4* meta = x.meta[i % kMeta];
         if (active) {
-          // Without a look at the largest score: the tile's probabilities with the reference as it is, kept
-          // in registers; their sum tells whether one was too far above it.
+          // The tile's probabilities with the reference as it is, kept in registers; their sum tells whether one
+          // was too far above it. Before the unit's first tile, its second, fifth, 17th and so on a row looks at its
+          // largest score and moves its reference up to it, so that rows hardly ever have to in between, where each
+          // holds up its neighbours (document of 131071 tokens: 1121 us without, 876 if none ever moved). What a row
+          // does is its own affair: its result does not depend on its neighbours.
           uint32_t w[kTile / 2];
-          float all = 0.f, part = 0.f;  // of the tile: probabilities, and each over its scale of V
-          bool again = meta[0].w != 2.f || !(fabsf(m) <= kMostRef);
-          if (!__any_sync(0xffffffffu, again)) {
-            float y[2][32];
+          float part = 0.f;  // the tile's probabilities, each over its scale of V
+          const uint32_t nth = jobs - before;
+          const bool partial = !__all_sync(0xffffffffu, meta[0].w == 2.f);  // pages that are not there
+          bool look = partial || ((nth & (nth - 1)) == 0 && (nth & 0x55555555u) == nth), may = look, stored = false;
+#pragma unroll 1
+          for (int pass = 0; pass < 2; ++pass) {
+            if (look) {
+              float top = -INFINITY;
+#pragma unroll 1
+              for (int c = 0; c < kTile; c += 16) {
+                const float4 g = meta[c / 16];
+                if (g.w == 0.f) continue;  // the same for every thread
+                float y[16], z[4];
+                tmem_ld16(my_s + c, y);
+                tmem_wait_ld();
+                tmem_tie16(y);
+                const float a = fac * g.x;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) z[e & 3] = e < 4 ? fmaf(y[e], a, g.y) : fmaxf(z[e & 3], fmaf(y[e], a, g.y));
+                top = fmaxf(top, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])));
+              }
+              const float to = may && top > m + (kHead + 1.f) ? top - kHead : m, by = ex2(m - to);
+              const bool moves = to != m;
+              m = to;
+              if (__any_sync(0xffffffffu, moves) && nth > 0) {
+                l *= by;
+                wait(&x.o_done[slot], (jobs - 1) & 1, &x.stop);
+                __syncwarp();
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                  float o[16];
+                  tmem_ld16(my_o + c, o);
+                  tmem_wait_ld();
+                  tmem_tie16(o);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) o[e] *= by;
+                  tmem_st16(my_o + c, reinterpret_cast<const uint32_t*>(o));
+                }
+              }
+            }
+            const bool far = !(fabsf(m) <= kMostRef);
+            part = 0.f;
+            if (partial || __any_sync(0xffffffffu, far && pass > 0)) {
+              // Scores are rounded before a far reference is subtracted: the difference stays small, however large
+              // both are. The sums' order is that of the other way.
+#pragma unroll 1
+              for (int c = 0; c < kTile; c += 16) {
+                const float4 g = meta[c / 16];
+                float y[16];
+                tmem_ld16(my_s + c, y);
+                tmem_wait_ld();
+                tmem_tie16(y);
+                const bool there = g.w != 0.f;
+                const float a = fac * g.x, b = far ? g.y : g.y - m, less = far ? m : 0.f;
+                f32x2 sum[2] = {0, 0};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float e0 = there ? ex2(fmaf(y[2 * e], a, b) - less) : 0.f;
+                  const float e1 = there ? ex2(fmaf(y[2 * e + 1], a, b) - less) : 0.f;
+                  sum[e & 1] = add2(sum[e & 1], pair(e0, e1));
+                  w[e] = f16x2(e0, e1);
+                }
+                tmem_st8(my_s + c / 2, reinterpret_cast<const float*>(w));  // P over the scores that have been read
+                const float2 both = unpair(add2(sum[0], sum[1]));
+                if (there) part = fmaf(both.x + both.y, g.z, part);
+              }
+              stored = true;
+              break;
+            }
+            float all = 0.f, y[2][32];
             tmem_ld32(my_s, y[0]);
 #pragma unroll
             for (int c = 0; c < kTile / 32; ++c) {
@@ -562,67 +653,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
                 part = fmaf(both.x + both.y, g.z, part);
               }
             }
-            again = all > kMostSum;
+            may = all > kMostSum || far;
+            look = true;
+            if (!__any_sync(0xffffffffu, may)) break;
           }
-          if (__any_sync(0xffffffffu, again)) {
-            // Rows whose largest score is too far up get a new reference, each by its own scores, whatever
-            // its neighbours do; then all rows' probabilities once more. Scores are rounded before the
-            // reference is subtracted: the difference is at most kSlack, however large both are.
-            float top = -INFINITY;
-#pragma unroll 1
-            for (int c = 0; c < kTile; c += 16) {
-              const float4 g = meta[c / 16];
-              if (g.w == 0.f) continue;  // the same for every thread
-              float y[16];
-              tmem_ld16(my_s + c, y);
-              tmem_wait_ld();
-              tmem_tie16(y);
+          if (!stored) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) top = fmaxf(top, fmaf(y[e], fac * g.x, g.y));
-            }
-            const float to = top > m + kSlack ? top - kHead : m, by = ex2(m - to);
-            const bool moves = to != m;
-            m = to;
-            l *= by;
-            if (__any_sync(0xffffffffu, moves) && jobs != before) {
-              wait(&x.o_done[slot], (jobs - 1) & 1, &x.stop);
-              __syncwarp();
-              tc_fence_after();
-#pragma unroll 1
-              for (int c = 0; c < D; c += 8) {
-                float o[8];
-                tmem_ld8(my_o + c, o);
-                tmem_wait_ld();
-                tmem_tie8(o);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] *= by;
-                tmem_st8(my_o + c, o);
-              }
-            }
-            part = 0.f;
-            const bool plain = !(fabsf(m) <= kMostRef);
-#pragma unroll
-            for (int c = 0; c < kTile / 16; ++c) {
-              const float4 g = meta[c];
-              float y[16], sum = 0.f;
-              tmem_ld16(my_s + 16 * c, y);
-              tmem_wait_ld();
-              tmem_tie16(y);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                float z0 = fmaf(y[2 * e], fac * g.x, plain ? g.y : g.y - m), z1 = fmaf(y[2 * e + 1], fac * g.x, plain ? g.y : g.y - m);
-                if (plain) z0 -= m, z1 -= m;
-                const float e0 = g.w == 0.f ? 0.f : ex2(z0), e1 = g.w == 0.f ? 0.f : ex2(z1);
-                sum += e0 + e1;
-                w[8 * c + e] = f16x2(e0, e1);
-              }
-              part = fmaf(sum, g.w == 0.f ? 0.f : g.z, part);
-            }
+            for (int c = 0; c < kTile / 2; c += 16) tmem_st16(my_s + c, w + c);
           }
           l += part;
-          // P lies over the scores, which have been read
-#pragma unroll
-          for (int c = 0; c < kTile / 2; c += 16) tmem_st16(my_s + c, w + c);
           tmem_wait_st();
         }
         tc_fence_before();
@@ -653,35 +692,45 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
         if (whole) p.pre_ml[at] = make_float2(m, l);
         else part[kBlock * D + row] = m, part[kBlock * D + kBlock + row] = l;
       }
+      // 16 columns a step, through the place of Q (each warp its own rows), so that rows are written in runs
+      float4* meet = reinterpret_cast<float4*>(sm) + (wide ? slot * (L::tile_bytes / 16) : 0) + (wide ? warp & 3 : r >> 5) * (32 * kMeetLd / 4);
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        float o[32];
+      for (int c = 0; c < D; c += 16) {
+        float o[16];
         if (live) {
           tmem_ld16(my_o + c, o);
-          tmem_ld16(my_o + c + 16, o + 16);
           tmem_wait_ld();
-          tmem_tie32(o);
+          tmem_tie16(o);
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = live ? o[e] * by : 0.f;
+        for (int e = 0; e < 16; ++e) o[e] = live ? o[e] * by : 0.f;
+        float4* mine_at = meet + lane * (kMeetLd / 4);
         if (!wide) {
-          float4* meet = reinterpret_cast<float4*>(sm) + r * (kMeetLd / 4);
           if (slot == 1) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) meet[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 4; ++e) mine_at[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
           bar_sync(1, 256);
           if (slot == 0) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 y = meet[e];
+            for (int e = 0; e < 4; ++e) {
+              const float4 y = mine_at[e];
               o[4 * e] += y.x, o[4 * e + 1] += y.y, o[4 * e + 2] += y.z, o[4 * e + 3] += y.w;
             }
           }
         }
-        if (mine && (wide || slot == 0)) {
+        if (wide || slot == 0) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(to + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          for (int e = 0; e < 4; ++e) mine_at[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          __syncwarp();
+          // four lanes a row, eight rows a step
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int rr = k * 8 + (lane >> 2);
+            float* dst = reinterpret_cast<float*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine ? to : nullptr), rr));
+            if (dst) *reinterpret_cast<float4*>(dst + c + (lane & 3) * 4) = meet[rr * (kMeetLd / 4) + (lane & 3)];
+          }
+          __syncwarp();
         }
         if (!wide) bar_sync(1, 256);
       }
@@ -717,11 +766,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
 }
 
 // The rows of a unit that spans CTAs, as join_row, into their prefix part: a warp takes every
-// gridDim.y * kJoinWarps-th.
-constexpr int kJoinWarps = 8;
+// kJoinY * kJoinWarps-th.
+constexpr int kJoinWarps = 8, kJoinY = 16;
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_constant__ PrefixParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_constant__ PrefixParams p, const __grid_constant__ WindowParams tail,
+                                                                 int tail_ctas, int rows, Start* starts) {
   grid_launch();
+  if (blockIdx.y == kJoinY) {  // one CTA, while the prefix is worked on: the shares of the kernel behind this one
+    if (blockIdx.x == 0) {
+      if (rows == 16) line_starts<16, kTailTile, kJoinWarps * 32>(tail, kTailLeast, tail_ctas, starts);
+      else line_starts<32, kTailTile, kJoinWarps * 32>(tail, kTailLeast, tail_ctas, starts);
+    }
+    grid_wait();
+    return;
+  }
   grid_wait();
   const int first = blockIdx.x, lane = threadIdx.x & 31;
   const int4 d = p.desc[first];
@@ -741,7 +799,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_co
   s.kvh = d.y;
   s.block = d.w >> 1;
   auto piece = [&](int i) { return p.part + (int64_t)(i ? 2 * (first + i * gang) : 2 * first + 1) * slot_floats(kBlock, D); };
-  for (int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); row < d.z; row += gridDim.y * kJoinWarps) {
+  for (int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); row < d.z; row += kJoinY * kJoinWarps) {
     float top = kNone;
     for (int i = lane; i < pieces; i += 32) top = fmaxf(top, piece(i)[kBlock * D + row]);
     top = warp_max(top);
@@ -766,7 +824,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_co
 }
 
 template <int D, typename T>
-cudaError_t launch(const PrefixParams& p, int sms, cudaStream_t s) {
+cudaError_t launch(const PrefixParams& p, const WindowParams& tail, Start* starts, int sms, cudaStream_t s) {
   constexpr int bytes = smem_bytes<D>();
   CUtensorMap k, v;
   const ts_kv_cache& c = p.c;
@@ -776,7 +834,7 @@ cudaError_t launch(const PrefixParams& p, int sms, cudaStream_t s) {
   cudaError_t e = allow_smem<k_prefix<D, T>>(bytes);
   if (e != cudaSuccess) return e;
   if ((e = launch_after(k_prefix<D, T>, dim3(sms), kThreads, bytes, s, p, k, v)) != cudaSuccess) return e;
-  return launch_after(k_prefix_join<D>, dim3(sms, 8), kJoinWarps * 32, 0, s, p);
+  return launch_after(k_prefix_join<D>, dim3(sms, kJoinY + 1), kJoinWarps * 32, 0, s, p, tail, sms * kTailCtas, tail_rows(tail), starts);
 }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -785,11 +843,12 @@ struct Scratch {
   int4* groups;
   int32_t* gang;
   int32_t* first;
+  Start *starts, *tails;
   float* pre_o;
   float2* pre_ml;
   int4* desc;
   float* part;
-  char* window;  // window attention's workspace
+  char* tail;  // the workspace of what is left
 };
 
 size_t lay_out(Scratch& x, int64_t batch, int64_t groups, int64_t total_rows, int heads_q, int heads, int D, int sms, void* ws) {
@@ -802,11 +861,13 @@ size_t lay_out(Scratch& x, int64_t batch, int64_t groups, int64_t total_rows, in
   take(x.groups, (size_t)groups);
   take(x.gang, 1);
   take(x.first, (size_t)batch);
+  take(x.starts, (size_t)sms);
+  take(x.tails, (size_t)sms * kTailCtas);
   take(x.pre_o, rows * D);
   take(x.pre_ml, rows);
   take(x.desc, (size_t)sms);
   take(x.part, (size_t)2 * sms * slot_floats(kBlock, D));
-  take(x.window, window_workspace(batch, total_rows, heads_q, heads, D, sms));
+  take(x.tail, tail_workspace(batch, total_rows, heads_q, heads, D, sms));
   return off;
 }
 
@@ -845,16 +906,20 @@ cudaError_t launch_shared(const ts_shared_args& sh, void* ws, int sms, uint64_t 
   p.pre_o = x.pre_o;
   p.pre_ml = x.pre_ml;
   p.wait_cycles = wait_cycles;
-  k_plan<<<1, kPlanThreads, 0, s>>>(c, a, sh, p.page_shift, x.groups, x.first, x.gang, std::min(sms, kMaxGang));
+  p.starts = x.starts;
+  WindowParams tail = tail_params(c, a, x.tail, sms);
+  tail.first = x.first;
+  tail.pre_o = x.pre_o;
+  tail.pre_ml = x.pre_ml;
+  tail.starts = x.tails;
+  k_plan<<<1, kPlanThreads, 0, s>>>(p, c, sh, x.groups, x.first, x.gang, x.starts, sms);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (a.dtype == TS_BF16)
-    e = c.head_dim == 128 ? launch<128, __nv_bfloat16>(p, sms, s) : launch<64, __nv_bfloat16>(p, sms, s);
+    e = c.head_dim == 128 ? launch<128, __nv_bfloat16>(p, tail, x.tails, sms, s) : launch<64, __nv_bfloat16>(p, tail, x.tails, sms, s);
   else
-    e = c.head_dim == 128 ? launch<128, __half>(p, sms, s) : launch<64, __half>(p, sms, s);
-  if (e != cudaSuccess) return e;
-  const SharedPrefix front = {x.first, x.pre_o, x.pre_ml};
-  return launch_window(c, a, x.window, sms, wait_cycles, s, &front);
+    e = c.head_dim == 128 ? launch<128, __half>(p, tail, x.tails, sms, s) : launch<64, __half>(p, tail, x.tails, sms, s);
+  return e != cudaSuccess ? e : launch_tails(tail, sms, s);
 }
 
 }  // namespace tsv

@@ -33,9 +33,8 @@ namespace tsv {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 16 * kWarps;
+constexpr int kThreads = 4 * 32;
+constexpr int kTile = 16 * 4;
 constexpr int kCtasPerSm = 2;
 constexpr float kSlack = 15.f;    // how far, in log2, a score may exceed its row's reference
 constexpr float kHead = 7.f;      // a reference is set this far below the largest score
@@ -43,11 +42,12 @@ constexpr int kMinTiles = 4;      // least tiles a CTA takes: pieces of 256 toke
 
 using Params = WindowParams;
 
-// TAIL: in shared attention. The window's own tokens are worked on here, at a unit's beginning, as one
-// more part beside the warps' (a kernel of their own took 8 us).
-template <int D, int MT, typename T, bool TAIL>
+// TAIL: in shared attention. The window's own tokens are worked on here, at a unit's beginning (a kernel of
+// their own took 8 us), in the place of the first warp's outputs, which joins its own with them.
+template <int D, int MT, typename T, bool TAIL = false, int W = 4>
 __device__ __forceinline__ void attend(const Params& p) {
-  constexpr int ROWS = 16 * MT, PARTS = kWarps + (TAIL ? 1 : 0);
+  constexpr int kWarps = W, kThreads = 32 * W, kTile = 16 * W;
+  constexpr int ROWS = 16 * MT, PARTS = W;
   constexpr int KS = D / 16;        // k16 steps over the dims
   constexpr int NT = D / 8;         // n8 tiles over the dims
   constexpr int VW = D / 32;        // words of a token's V codes a lane holds
@@ -70,12 +70,19 @@ __device__ __forceinline__ void attend(const Params& p) {
   const int64_t cta = blockIdx.x;
   int4 desc = make_int4(-1, 0, 0, 0);
   Line<ROWS, kTile> line;
-  if (!line_begin<ROWS, kTile, kThreads>(p, kMinTiles, line)) {
+  bool waited = false;
+  if constexpr (TAIL) {
+    grid_wait();
+    waited = true;
+    if (!line_at<ROWS, kTile>(p, p.starts[cta], line)) {
+      if (tid == 0) p.desc[cta] = desc;
+      return;
+    }
+  } else if (!line_begin<ROWS, kTile, kThreads>(p, kMinTiles, line)) {
     if (tid == 0) p.desc[cta] = desc;
     grid_wait();  // so that this kernel's end is the end of the one before too
     return;
   }
-  bool waited = false;
   Segment sg;
   while (line.next(p, sg)) {
     const Req& r = sg.r;
@@ -84,13 +91,14 @@ __device__ __forceinline__ void attend(const Params& p) {
     // ---- Q: row i of the unit is window row (block*ROWS + i) / group of head kvh*group +
     // the remainder. Each row's factor, then the fragments.
     __syncthreads();  // the previous unit's reads of shared memory are done
+#pragma unroll (TAIL ? 4 : 1)
     for (int i = warp; i < ROWS; i += kWarps) {
       float top = 0.f;
       uint32_t bad = 0;
       if (i < rows) {
 #pragma unroll
         for (int k = 0; k < D / 64; ++k) {
-          const uint32_t w = reinterpret_cast<const uint32_t*>(q_row(p, sg, ROWS, i))[k * 32 + lane];
+          const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(q_row(p, sg, ROWS, i)) + k * 32 + lane);
           const float2 f = unpack<T>(w);
           top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
           bad |= not_finite<T>(w);
@@ -104,6 +112,7 @@ __device__ __forceinline__ void attend(const Params& p) {
       if (lane == 0) s_fac[i] = bad ? NAN : __uint_as_float((uint32_t)e << 23);
     }
     __syncthreads();
+#pragma unroll (TAIL ? 4 : 1)
     for (int i = tid; i < MT * KS * 32; i += kThreads) {
       const int l = i & 31, ks = i / 32 % KS, mt = i / 32 / KS, qc = l & 3, qg = l >> 2;
       // K's lane qc holds dims 16qc .. + 15 of each 64; step k takes dims 4k .. 4k + 3 of them
@@ -115,7 +124,7 @@ __device__ __forceinline__ void attend(const Params& p) {
         uint2 x = make_uint2(0, 0);
         float inv = 1.f;
         if (row < rows) {
-          x = *reinterpret_cast<const uint2*>(q_row(p, sg, ROWS, row) + dim * 2);
+          x = __ldg(reinterpret_cast<const uint2*>(q_row(p, sg, ROWS, row) + dim * 2));
           inv = __uint_as_float(0x7F000000u - __float_as_uint(s_fac[row]));  // 1 / 2^e
         }
         const float2 u = unpack<T>(x.x), v = unpack<T>(x.y);
@@ -231,7 +240,7 @@ __device__ __forceinline__ void attend(const Params& p) {
       x.ks = x.vs = 1.f;
       if (page >= 0) {
         x.ks = __ldg(p.c.k_scale + (int64_t)page * p.c.heads + kvh);
-        x.vs = scale_of_v(__ldg(p.c.v_scale + (int64_t)page * p.c.heads + kvh), x.ks);
+        x.vs = __ldg(p.c.v_scale + (int64_t)page * p.c.heads + kvh);  // not looked at before it is needed
       }
     };
     Loaded next;
@@ -239,7 +248,7 @@ __device__ __forceinline__ void attend(const Params& p) {
     if (t0 < t1) fetch(t0, page, next);
     const bool own_here = TAIL && p.a.k_new && t0 == 0;
     if constexpr (TAIL) {
-      if (own_here) {  // each warp a share of the dims, or of the rows
+      if (own_here) {  // each warp a share of the dims, or of the rows; s_o was read before the sync above
         const Sees* trees = nullptr;
         if (p.a.parents) {
           for (int i = tid; i < r.rows; i += kThreads) s_parents[i] = p.a.parents[r.row0 + i];
@@ -248,20 +257,19 @@ __device__ __forceinline__ void attend(const Params& p) {
           __syncthreads();
           trees = s_trees;
         }
-        float* o_own = s_o + kWarps * ROWS * (D + 4);
-        constexpr int kSlices = kWarps / MT;  // of the dims
-        const int i16 = warp / kSlices * 16, j0 = warp % kSlices * (D / 8 / kSlices), j1 = j0 + D / 8 / kSlices;
-        if (i16 < rows) {
-          const bool odd = own_part<D, ROWS, T>(p, sg, i16, j0, j1, trees, o_own, D + 4, s_ml);
-          if (odd) {
+        constexpr int kSlices = W > MT ? W / MT : 1;  // of the dims
+        const int j0 = warp % kSlices * (D / 8 / kSlices), j1 = j0 + D / 8 / kSlices;
+        for (int i16 = warp / kSlices * 16; i16 < rows; i16 += W / kSlices * 16) {
+          if (own_part<D, ROWS, T>(p, sg, i16, j0, j1, trees, s_o, D + 4, s_ml)) {
             __syncwarp();
 #pragma unroll 1
             for (int i = i16; i < min(rows, i16 + 16); ++i)
-              own_odd<D, ROWS, T>(p, sg, i, j0 * 8, j1 * 8, trees, s_ml[i].x, o_own + i * (D + 4));
+              own_odd<D, ROWS, T>(p, sg, i, j0 * 8, j1 * 8, trees, s_ml[i].x, s_o + i * (D + 4));
           }
         }
       }
     }
+    if (own_here) __syncthreads();
     for (int t = t0; t < t1; ++t) {
       Loaded now = next;
       const int32_t page_now = page;
@@ -295,7 +303,7 @@ __device__ __forceinline__ void attend(const Params& p) {
           mma16816<__half>(x[mt][1], qa, kb[1][0], kb[1][1]);
         }
       }
-      const float lv = __log2f(now.vs), inv_v = 1.f / now.vs;
+      const float vs = scale_of_v(now.vs, now.ks), lv = __log2f(vs), inv_v = 1.f / vs;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -340,31 +348,39 @@ __device__ __forceinline__ void attend(const Params& p) {
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         const int row = mt * 16 + h * 8 + g;
+        float top = m[mt][h];
+        float* at = s_o + (warp * ROWS + row) * (D + 4);
+        float by = 1.f, own = 0.f;
+        const bool joins = TAIL && own_here && warp == 0;
+        if (joins) {
+          const float2 ml = s_ml[row];
+          top = fmaxf(top, ml.x);
+          by = ex2(m[mt][h] - top);
+          own = ex2(ml.x - top);
+          sum = fmaf(sum, by, ml.y * own);
+        }
         if (c == 0) {
-          s_m[warp * ROWS + row] = m[mt][h];
+          s_m[warp * ROWS + row] = top;
           s_l[warp * ROWS + row] = sum;
         }
-        float* at = s_o + (warp * ROWS + row) * (D + 4);
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int j = 0; j < NT; j += 4)
-            *reinterpret_cast<float4*>(at + (2 * c + e) * (D / 8) + j) =
-                make_float4(o[mt][j][2 * h + e], o[mt][j + 1][2 * h + e], o[mt][j + 2][2 * h + e], o[mt][j + 3][2 * h + e]);
+          for (int j = 0; j < NT; j += 4) {
+            float4 v = make_float4(o[mt][j][2 * h + e], o[mt][j + 1][2 * h + e], o[mt][j + 2][2 * h + e], o[mt][j + 3][2 * h + e]);
+            float4* to = reinterpret_cast<float4*>(at + (2 * c + e) * (D / 8) + j);
+            if (joins) {
+              const float4 u = *to;
+              v = make_float4(fmaf(v.x, by, u.x * own), fmaf(v.y, by, u.y * own), fmaf(v.z, by, u.z * own), fmaf(v.w, by, u.w * own));
+            }
+            *to = v;
+          }
       }
     if (!waited) {  // for the window's own part
       grid_wait();
       waited = true;
     }
     __syncthreads();
-    if constexpr (TAIL) {
-      for (int i = tid; i < rows; i += kThreads) {
-        const float2 ml = own_here ? s_ml[i] : make_float2(kNone, 0.f);
-        s_m[kWarps * ROWS + i] = ml.x;
-        s_l[kWarps * ROWS + i] = ml.y;
-      }
-      __syncthreads();
-    }
     const bool whole = sg.whole();
     const int slot = (int)(2 * cta) + (t0 == 0 ? 1 : 0);
     float* part = p.part + (int64_t)slot * slot_floats(ROWS, D);
@@ -377,7 +393,6 @@ __device__ __forceinline__ void attend(const Params& p) {
       float sum = 0.f;
 #pragma unroll
       for (int w = 0; w < PARTS; ++w) {
-        if (TAIL && w == kWarps && !own_here) continue;
         const float by = ex2(s_m[w * ROWS + row] - top);
         const float4 v = *reinterpret_cast<const float4*>(s_o + (w * ROWS + row) * (D + 4) + d);
         sum = fmaf(by, s_l[w * ROWS + row], sum);
@@ -426,11 +441,11 @@ __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Par
   attend<64, MT, T, false>(p);
 }
 
-// What is left of each request behind a shared prefix, and its window's own tokens.
-template <int D, int MT, typename T>
-__global__ void __launch_bounds__(kThreads) k_tail(const __grid_constant__ Params p) {
+// What is left of each request behind a shared prefix, and its window's own tokens: W warps a CTA.
+template <int D, int MT, typename T, int W>
+__global__ void __launch_bounds__(32 * W) k_tail(const __grid_constant__ Params p) {
   grid_launch();
-  attend<D, MT, T, true>(p);
+  attend<D, MT, T, true, W>(p);
 }
 
 // More than 32 rows a window: blocks of 64 rows, for which K and V are converted half as often, where the
@@ -455,9 +470,8 @@ __global__ void __launch_bounds__(128) k_join_rows(const __grid_constant__ Param
   else join_row<64, 32, kTile, T>(p);
 }
 
-constexpr int smem_bytes(int D, int rows, bool tail = false) {
-  const int parts = kWarps + (tail ? 1 : 0);
-  return rows / 16 * (D / 16) * 32 * 16 + rows * 4 + parts * rows * (D + 4) * 4 + parts * rows * 8 +
+constexpr int smem_bytes(int D, int rows, bool tail = false, int warps = 4) {
+  return rows / 16 * (D / 16) * 32 * 16 + rows * 4 + warps * rows * (D + 4) * 4 + warps * rows * 8 +
          (tail ? TS_MAX_WINDOW * ((int)sizeof(Sees) + 4) + rows * 8 : 0);
 }
 
@@ -491,16 +505,22 @@ cudaError_t launch_64(const Params& p, int rows, int sms, cudaStream_t s) {
 
 template <int D, int MT, typename T>
 cudaError_t launch_tail(const Params& p, int sms, cudaStream_t s) {
-  constexpr int bytes = smem_bytes(D, 16 * MT, true);
-  cudaError_t e = allow_smem<k_tail<D, MT, T>>(bytes);
+  constexpr int W = kTailWarps, bytes = smem_bytes(D, 16 * MT, true, W);
+  cudaError_t e = allow_smem<k_tail<D, MT, T, W>>(bytes);
   if (e != cudaSuccess) return e;
-  const int grid = sms * kCtasPerSm;
-  if ((e = launch_after(k_tail<D, MT, T>, dim3(grid), kThreads, bytes, s, p)) != cudaSuccess) return e;
-  if ((int64_t)p.c.max_pages * p.c.page_size <= kTile) return cudaSuccess;  // units of one tile are never split
-  return launch_after(k_join<D, 16 * MT, kTile, T>, dim3(grid, 4 * MT), 128, 0, s, p);
+  const int grid = sms * kTailCtas;
+  if ((e = launch_after(k_tail<D, MT, T, W>, dim3(grid), 32 * W, bytes, s, p)) != cudaSuccess) return e;
+  if ((int64_t)p.c.max_pages * p.c.page_size <= 16 * W) return cudaSuccess;  // units of one tile are never split
+  return launch_after(k_join<D, 16 * MT, 16 * W, T>, dim3(grid, 4 * MT), 128, 0, s, p);
 }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+}  // namespace
+
+int tail_rows(const WindowParams& p) { return (p.a.total_rows * p.group + p.c.batch - 1) / p.c.batch <= 16 ? 16 : 32; }
+
+namespace {
 
 // The rows of a block: by the average window. head_dim 128, ragged chains of 4 to 20 rows: 162 us
 // with 32, 189 with 64; trees of 256 rows: 416 with 32, 330 with 64. head_dim 64, one row of 4
@@ -511,12 +531,10 @@ int block_rows(const WindowParams& p) {
   return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
-int tail_rows(const WindowParams& p) { return (p.a.total_rows * p.group + p.c.batch - 1) / p.c.batch <= 16 ? 16 : 32; }
-
 // Lays the workspace out; returns its bytes.
-size_t lay_out(WindowParams& p, void* ws, int sms) {
-  const int rows = block_rows(p), D = p.c.head_dim;
-  const size_t ctas = (size_t)sms * kCtasPerSm;
+size_t lay_out(WindowParams& p, void* ws, int sms, bool tail = false) {
+  const int rows = tail ? tail_rows(p) : block_rows(p), D = p.c.head_dim;
+  const size_t ctas = (size_t)sms * (tail ? kTailCtas : kCtasPerSm);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     char* at = static_cast<char*>(ws) + off;
@@ -526,6 +544,7 @@ size_t lay_out(WindowParams& p, void* ws, int sms) {
   p.desc = reinterpret_cast<int4*>(take(ctas * sizeof(int4)));
   p.wide = reinterpret_cast<int32_t*>(take(sizeof(int32_t)));
   p.part = reinterpret_cast<float*>(take(2 * ctas * slot_floats(rows, D) * sizeof(float)));
+  if (tail) return off;
   const size_t n = (size_t)p.a.total_rows * p.a.heads_q;
   // the window's own part: of every row, or (ts_window_tc.cu) of a block a CTA
   p.own_o = reinterpret_cast<float*>(take(std::max(n, (size_t)sms * rows) * D * sizeof(float)));
@@ -534,6 +553,38 @@ size_t lay_out(WindowParams& p, void* ws, int sms) {
 }
 
 }  // namespace
+
+size_t tail_workspace(int64_t batch, int64_t total_rows, int heads_q, int heads, int head_dim, int sms) {
+  WindowParams p{};
+  p.c.batch = batch;
+  p.c.heads = heads;
+  p.c.head_dim = head_dim;
+  p.a.total_rows = total_rows;
+  p.a.heads_q = heads_q;
+  p.group = heads_q / heads;
+  return lay_out(p, nullptr, sms, true);
+}
+
+WindowParams tail_params(const ts_kv_cache& c, const ts_attn_args& a, void* ws, int sms) {
+  WindowParams p{};
+  p.c = c;
+  p.a = a;
+  p.page_shift = __builtin_ctz((unsigned)c.page_size);
+  p.group = a.heads_q / c.heads;
+  p.scale_log2 = a.sm_scale * kLog2e;
+  lay_out(p, ws, sms, true);
+  return p;
+}
+
+cudaError_t launch_tails(const WindowParams& p, int sms, cudaStream_t s) {
+  const bool bf16 = p.a.dtype == TS_BF16, small = tail_rows(p) == 16;
+  if (p.c.head_dim == 64) {
+    if (small) return bf16 ? launch_tail<64, 1, __nv_bfloat16>(p, sms, s) : launch_tail<64, 1, __half>(p, sms, s);
+    return bf16 ? launch_tail<64, 2, __nv_bfloat16>(p, sms, s) : launch_tail<64, 2, __half>(p, sms, s);
+  }
+  if (small) return bf16 ? launch_tail<128, 1, __nv_bfloat16>(p, sms, s) : launch_tail<128, 1, __half>(p, sms, s);
+  return bf16 ? launch_tail<128, 2, __nv_bfloat16>(p, sms, s) : launch_tail<128, 2, __half>(p, sms, s);
+}
 
 size_t window_workspace(int64_t batch, int64_t total_rows, int heads_q, int heads, int head_dim, int sms) {
   WindowParams p{};
@@ -547,7 +598,7 @@ size_t window_workspace(int64_t batch, int64_t total_rows, int heads_q, int head
 }
 
 cudaError_t launch_window(const ts_kv_cache& c, const ts_attn_args& a, void* ws, int sms, uint64_t wait_cycles,
-                          cudaStream_t s, const SharedPrefix* front) {
+                          cudaStream_t s) {
   Params p{};
   p.c = c;
   p.a = a;
@@ -557,19 +608,6 @@ cudaError_t launch_window(const ts_kv_cache& c, const ts_attn_args& a, void* ws,
   p.wait_cycles = wait_cycles;
   lay_out(p, ws, sms);
   if (!a.k_new) p.own_ml = nullptr;
-  if (front) {
-    p.first = front->first;
-    p.pre_o = front->pre_o;
-    p.pre_ml = front->pre_ml;
-    p.own_ml = nullptr;  // in the unit's first piece
-    const bool bf16 = a.dtype == TS_BF16;
-    if (c.head_dim == 64) {
-      if (tail_rows(p) == 16) return bf16 ? launch_tail<64, 1, __nv_bfloat16>(p, sms, s) : launch_tail<64, 1, __half>(p, sms, s);
-      return bf16 ? launch_tail<64, 2, __nv_bfloat16>(p, sms, s) : launch_tail<64, 2, __half>(p, sms, s);
-    }
-    if (tail_rows(p) == 16) return bf16 ? launch_tail<128, 1, __nv_bfloat16>(p, sms, s) : launch_tail<128, 1, __half>(p, sms, s);
-    return bf16 ? launch_tail<128, 2, __nv_bfloat16>(p, sms, s) : launch_tail<128, 2, __half>(p, sms, s);
-  }
   if (c.head_dim == 128) return launch_window_tc(p, block_rows(p), sms, s);
   const int rows = block_rows(p);
   return a.dtype == TS_BF16 ? launch_64<__nv_bfloat16>(p, rows, sms, s) : launch_64<__half>(p, rows, sms, s);

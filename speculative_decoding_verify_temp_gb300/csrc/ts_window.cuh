@@ -15,6 +15,12 @@
 
 namespace tsv {
 
+// A share of a line of tiles: `tiles` of them from tile `in` of request b's on (b < 0: none).
+struct alignas(16) Start {
+  int64_t in, tiles;
+  int32_t b, unused[3];
+};
+
 struct WindowParams {
   ts_kv_cache c;
   ts_attn_args a;
@@ -30,6 +36,7 @@ struct WindowParams {
   const int32_t* first;   // [batch] tokens in front that another kernel attended to (whole pages), or NULL
   const float* pre_o;     // [total_rows * heads_q][D] their part: outputs,
   const float2* pre_ml;   // references and sums (of the rows of requests with first > 0)
+  const Start* starts;    // [CTAs] their shares (line_starts), or NULL: each finds its own
   uint64_t wait_cycles;  // SM clock cycles that a wait may take (ts_window_tc.cu)
 };
 
@@ -108,7 +115,7 @@ struct RawReq {
 __device__ __forceinline__ RawReq raw_request(const WindowParams& p, int64_t b) {
   RawReq r = {0, 0, 0, 0};
   if (b >= p.c.batch) return r;
-  if (p.first) r.first = __ldcg(p.first + b);  // from L2: written by a kernel that this one does not wait for by itself
+  if (p.first) r.first = __ldcg(p.first + b);  // the kernel that plans ahead may run while the one that wrote it ends
   if (p.a.qo_indptr) {
     r.row0 = p.a.qo_indptr[b];
     r.row1 = p.a.qo_indptr[b + 1];
@@ -185,10 +192,8 @@ struct Line {
 // it up. Returns false for a CTA without work. least_tiles: a CTA takes this many tiles at least, or as
 // many as an average unit has where that is less (14 windows of 8 rows over 4 tokens, head_dim 64:
 // 16 us, 39 with four such units a CTA).
-// cta of ctas: whose share.
 template <int ROWS, int TILE, int THREADS, typename P>
-__device__ __forceinline__ bool line_begin(const P& p, int least_tiles, Line<ROWS, TILE, P>& line, unsigned cta = blockIdx.x,
-                                           unsigned ctas = gridDim.x) {
+__device__ __forceinline__ bool line_begin(const P& p, int least_tiles, Line<ROWS, TILE, P>& line) {
   static_assert(THREADS % 32 == 0, "whole warps");
   __shared__ int64_t s_scan[THREADS / 32], s_start;
   __shared__ uint32_t s_units[THREADS / 32];  // below 2^28: total_rows * heads_q is below 2^31
@@ -225,8 +230,8 @@ __device__ __forceinline__ bool line_begin(const P& p, int least_tiles, Line<ROW
     units += s_units[w];
   }
   const int64_t least = all < (int64_t)least_tiles * units ? max(all / max(units, 1u), (int64_t)1) : least_tiles;
-  const int64_t share = max((all + ctas - 1) / ctas, least);
-  const int64_t begin = min(all, cta * share), end = min(all, begin + share);
+  const int64_t share = max((all + gridDim.x - 1) / gridDim.x, least);
+  const int64_t begin = min(all, blockIdx.x * share), end = min(all, begin + share);
   if (begin < end && upto - mine <= begin && begin < upto) {  // one thread
     int64_t at = upto - mine;
 #pragma unroll 1
@@ -250,6 +255,83 @@ __device__ __forceinline__ bool line_begin(const P& p, int least_tiles, Line<ROW
   line.kvh = unit / line.r.blocks;
   line.block = unit % line.r.blocks;
   line.left = end - begin;
+  return true;
+}
+
+// n / d for positive numbers: in 32 bits where they fit (a 64-bit division is a hundred instructions).
+__device__ __forceinline__ int64_t divide(int64_t n, int64_t d) {
+  return ((uint64_t)n | (uint64_t)d) >> 32 ? n / d : (int64_t)((uint32_t)n / (uint32_t)d);
+}
+
+// The same for all shares at once, by one CTA, ahead of the kernel whose CTAs begin at them.
+template <int ROWS, int TILE, int THREADS, typename P>
+__device__ __forceinline__ void line_starts(const P& p, int least_tiles, int ctas, Start* starts) {
+  __shared__ int64_t s_upto[THREADS];  // tiles up to the end of each thread's run of requests
+  __shared__ uint32_t s_units;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) s_units = 0;
+  int64_t mine = 0;
+  uint32_t units = 0;
+  const int64_t each = (p.c.batch + THREADS - 1) / THREADS;
+  const int64_t b_lo = min(p.c.batch, tid * each), b_hi = min(p.c.batch, b_lo + each);
+#pragma unroll 1
+  for (int64_t b = b_lo; b < b_hi; ++b) {
+    const Req r = request<ROWS, TILE>(p, raw_request(p, b));
+    mine += r.weight(p.c.heads);
+    units += r.units(p.c.heads);
+  }
+  units = __reduce_add_sync(0xffffffffu, units);
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t t = __shfl_up_sync(0xffffffffu, mine, o);
+    if (lane >= o) mine += t;
+  }
+  s_upto[tid] = mine;
+  __syncthreads();
+  if (lane == 0 && units) atomicAdd(&s_units, units);
+  int64_t before = 0;  // of the warps in front: theirs added up by the lanes
+  for (int w = lane; w < warp; w += 32) before += s_upto[w * 32 + 31];
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  __syncthreads();
+  s_upto[tid] = mine + before;
+  __syncthreads();
+  const int64_t all = s_upto[THREADS - 1];
+  const int64_t least = all < (int64_t)least_tiles * s_units ? max(divide(all, max(s_units, 1u)), (int64_t)1) : least_tiles;
+  const int64_t share = max(divide(all + ctas - 1, ctas), least);
+#pragma unroll 1
+  for (int i = tid; i < ctas; i += THREADS) {
+    Start s = {0, 0, -1, {}};
+    const int64_t begin = i * share;
+    if (begin < all) {
+      int t = 0;  // the first thread whose run ends behind the beginning
+#pragma unroll 1
+      for (int step = THREADS / 2; step > 0; step >>= 1)
+        if (s_upto[t + step - 1] <= begin) t += step;
+      int64_t at = t ? s_upto[t - 1] : 0, b = t * each;
+#pragma unroll 1
+      for (; each > 1; ++b) {
+        const int64_t w = request<ROWS, TILE>(p, raw_request(p, b)).weight(p.c.heads);
+        if (begin < at + w) break;
+        at += w;
+      }
+      s = {begin - at, min(share, all - begin), (int32_t)b, {}};
+    }
+    starts[i] = s;
+  }
+}
+
+template <int ROWS, int TILE, typename P>
+__device__ __forceinline__ bool line_at(const P& p, const Start& at, Line<ROWS, TILE, P>& line) {
+  if (at.b < 0) return false;
+  line.b = at.b;
+  line.r = request<ROWS, TILE>(p, raw_request(p, line.b));
+  line.after = raw_request(p, line.b + 1);
+  const int64_t unit = divide(at.in, line.r.tiles);
+  line.tile = (int32_t)(at.in - unit * line.r.tiles);
+  line.kvh = (int32_t)divide(unit, line.r.blocks);
+  line.block = (int32_t)(unit - (int64_t)line.kvh * line.r.blocks);
+  line.left = at.tiles;
   return true;
 }
 
@@ -367,6 +449,14 @@ __global__ void __launch_bounds__(128) k_join(const __grid_constant__ WindowPara
   grid_wait();
   join_row<D, ROWS, TILE, T>(p);
 }
+
+// What is left of the requests behind a shared prefix (ts_window.cu): CTAs of kTailWarps warps, blocks of
+// tail_rows rows; first, pre_o, pre_ml and starts are the caller's.
+constexpr int kTailWarps = 4, kTailCtas = 2, kTailTile = 16 * kTailWarps, kTailLeast = 4;
+int tail_rows(const WindowParams& p);
+size_t tail_workspace(int64_t batch, int64_t total_rows, int heads_q, int heads, int head_dim, int sms);
+WindowParams tail_params(const ts_kv_cache& c, const ts_attn_args& a, void* ws, int sms);
+cudaError_t launch_tails(const WindowParams& p, int sms, cudaStream_t s);
 
 // The tensor map of K or V, a box a page of one head (ts_window_tc.cu); false: not possible.
 bool page_map(CUtensorMap* map, const ts_kv_cache& c, void* base, int64_t page_stride, int64_t head_stride, int64_t token_stride,
