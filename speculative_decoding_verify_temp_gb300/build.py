@@ -17,9 +17,9 @@ OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtsverify.so")
 SOURCES = ["ts_abi.cu", "ts_stream.cu", "ts_sample.cu", "ts_staged.cu", "ts_chain.cu",
            "ts_gumbel.cu", "ts_window.cu", "ts_window_tc.cu", "ts_shared.cu",
-           "ts_kvcache.cu", "ts_kvpages.cu", "ts_tree.cu"]
+           "ts_tail.cu", "ts_kvcache.cu", "ts_kvpages.cu", "ts_tree.cu"]
 HEADERS = ["ts_common.cuh", "ts_internal.h", "ts_select.cuh", "ts_rowutil.cuh", "ts_kv.cuh",
-           "ts_tc.cuh", "ts_window.cuh", "ts_window_own.cuh"]
+           "ts_tc.cuh", "ts_window.cuh", "ts_window_own.cuh", "ts_tail.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2"]
 

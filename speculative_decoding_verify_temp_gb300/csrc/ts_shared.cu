@@ -1,6 +1,6 @@
 // Attention of windows whose requests share a prefix: the prefix is read and multiplied once for all
-// rows of a group, the rest of each request by window attention (ts_window.cu, ts_window_tc.cu),
-// which takes the prefix's part of a row in.
+// rows of a group, the rest of each request by ts_tail.cu, which takes the prefix's part of a
+// row in.
 //
 //   k_plan         the groups: rows, shared tokens (whole pages); what each request has left; how
 //                  many CTAs go through the tokens side by side
@@ -35,7 +35,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "ts_window.cuh"
+#include "ts_tail.h"
 
 namespace tsv {
 
@@ -56,16 +56,15 @@ struct PrefixParams {
 };
 
 __device__ __forceinline__ RawReq raw_request(const PrefixParams& p, int64_t g) {
-  if (g >= p.c.batch) return {0, 0, 0, 0};
+  if (g >= p.c.batch) return {0, 0, 0};
   const int4 x = p.groups[g];
-  return {x.x, x.x + x.y, x.z, 0};
+  return {x.x, x.x + x.y, x.z};
 }
 template <int ROWS, int TILE>
 __device__ __forceinline__ Req request(const PrefixParams& p, const RawReq& raw) {
   Req r;
   r.row0 = raw.row0;
   r.rows = raw.len > 0 ? raw.row1 - raw.row0 : 0;
-  r.skip = 0;
   r.len = raw.len;
   r.blocks = (int)(((unsigned)r.rows * p.group + ROWS - 1) / ROWS);  // here: sets of as many as a gang takes
   r.blocks = (r.blocks + *p.gang - 1) / *p.gang;
@@ -769,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
 // kJoinY * kJoinWarps-th.
 constexpr int kJoinWarps = 8, kJoinY = 16;
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_constant__ PrefixParams p, const __grid_constant__ WindowParams tail,
+__global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_constant__ PrefixParams p, const __grid_constant__ TailParams tail,
                                                                  int tail_ctas, int rows, Start* starts) {
   grid_launch();
   if (blockIdx.y == kJoinY) {  // one CTA, while the prefix is worked on: the shares of the kernel behind this one
@@ -824,7 +823,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_co
 }
 
 template <int D, typename T>
-cudaError_t launch(const PrefixParams& p, const WindowParams& tail, Start* starts, int sms, cudaStream_t s) {
+cudaError_t launch(const PrefixParams& p, const TailParams& tail, Start* starts, int sms, cudaStream_t s) {
   constexpr int bytes = smem_bytes<D>();
   CUtensorMap k, v;
   const ts_kv_cache& c = p.c;
@@ -907,7 +906,7 @@ cudaError_t launch_shared(const ts_shared_args& sh, void* ws, int sms, uint64_t 
   p.pre_ml = x.pre_ml;
   p.wait_cycles = wait_cycles;
   p.starts = x.starts;
-  WindowParams tail = tail_params(c, a, x.tail, sms);
+  TailParams tail = tail_params(c, a, x.tail, sms);
   tail.first = x.first;
   tail.pre_o = x.pre_o;
   tail.pre_ml = x.pre_ml;
@@ -919,7 +918,7 @@ cudaError_t launch_shared(const ts_shared_args& sh, void* ws, int sms, uint64_t 
     e = c.head_dim == 128 ? launch<128, __nv_bfloat16>(p, tail, x.tails, sms, s) : launch<64, __nv_bfloat16>(p, tail, x.tails, sms, s);
   else
     e = c.head_dim == 128 ? launch<128, __half>(p, tail, x.tails, sms, s) : launch<64, __half>(p, tail, x.tails, sms, s);
-  return e != cudaSuccess ? e : launch_tails(tail, sms, s);
+  return e != cudaSuccess ? e : launch_tail(tail, sms, s);
 }
 
 }  // namespace tsv

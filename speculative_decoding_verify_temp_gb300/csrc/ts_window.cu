@@ -33,8 +33,9 @@ namespace tsv {
 
 namespace {
 
-constexpr int kThreads = 4 * 32;
-constexpr int kTile = 16 * 4;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTile = 16 * kWarps;
 constexpr int kCtasPerSm = 2;
 constexpr float kSlack = 15.f;    // how far, in log2, a score may exceed its row's reference
 constexpr float kHead = 7.f;      // a reference is set this far below the largest score
@@ -42,47 +43,31 @@ constexpr int kMinTiles = 4;      // least tiles a CTA takes: pieces of 256 toke
 
 using Params = WindowParams;
 
-// TAIL: in shared attention. The window's own tokens are worked on here, at a unit's beginning (a kernel of
-// their own took 8 us), in the place of the first warp's outputs, which joins its own with them.
-template <int D, int MT, typename T, bool TAIL = false, int W = 4>
+template <int MT, typename T>
 __device__ __forceinline__ void attend(const Params& p) {
-  constexpr int kWarps = W, kThreads = 32 * W, kTile = 16 * W;
-  constexpr int ROWS = 16 * MT, PARTS = W;
+  constexpr int D = 64, ROWS = 16 * MT;
   constexpr int KS = D / 16;        // k16 steps over the dims
   constexpr int NT = D / 8;         // n8 tiles over the dims
   constexpr int VW = D / 32;        // words of a token's V codes a lane holds
   extern __shared__ __align__(16) unsigned char smem[];
   // Q fragments [MT][KS][32 lanes] and the factors of their rows; then, for the join of the
-  // warps, [PARTS][ROWS][D + 4] outputs with their references and sums
+  // warps, [kWarps][ROWS][D + 4] outputs with their references and sums
   uint4* s_q = reinterpret_cast<uint4*>(smem);
   float* s_fac = reinterpret_cast<float*>(s_q + MT * KS * 32);
   float* s_o = s_fac + ROWS;
-  float* s_m = s_o + PARTS * ROWS * (D + 4);
-  float* s_l = s_m + PARTS * ROWS;
-  // TAIL: the window's own references and sums, what a tree's rows see, and its parents (of an odd number
-  // of rows: last)
-  float2* s_ml = reinterpret_cast<float2*>(s_l + PARTS * ROWS);
-  Sees* s_trees = reinterpret_cast<Sees*>(s_ml + ROWS);
-  int32_t* s_parents = reinterpret_cast<int32_t*>(s_trees + TS_MAX_WINDOW);
-  static_assert((MT * KS * 32 * 16 + ROWS * 4 + PARTS * ROWS * (D + 6) * 4) % 8 == 0, "s_ml and s_trees");
+  float* s_m = s_o + kWarps * ROWS * (D + 4);
+  float* s_l = s_m + kWarps * ROWS;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int64_t cta = blockIdx.x;
   int4 desc = make_int4(-1, 0, 0, 0);
   Line<ROWS, kTile> line;
-  bool waited = false;
-  if constexpr (TAIL) {
-    grid_wait();
-    waited = true;
-    if (!line_at<ROWS, kTile>(p, p.starts[cta], line)) {
-      if (tid == 0) p.desc[cta] = desc;
-      return;
-    }
-  } else if (!line_begin<ROWS, kTile, kThreads>(p, kMinTiles, line)) {
+  if (!line_begin<ROWS, kTile, kThreads>(p, kMinTiles, line)) {
     if (tid == 0) p.desc[cta] = desc;
     grid_wait();  // so that this kernel's end is the end of the one before too
     return;
   }
+  bool waited = false;
   Segment sg;
   while (line.next(p, sg)) {
     const Req& r = sg.r;
@@ -91,18 +76,14 @@ __device__ __forceinline__ void attend(const Params& p) {
     // ---- Q: row i of the unit is window row (block*ROWS + i) / group of head kvh*group +
     // the remainder. Each row's factor, then the fragments.
     __syncthreads();  // the previous unit's reads of shared memory are done
-#pragma unroll (TAIL ? 4 : 1)
     for (int i = warp; i < ROWS; i += kWarps) {
       float top = 0.f;
       uint32_t bad = 0;
       if (i < rows) {
-#pragma unroll
-        for (int k = 0; k < D / 64; ++k) {
-          const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(q_row(p, sg, ROWS, i)) + k * 32 + lane);
-          const float2 f = unpack<T>(w);
-          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-          bad |= not_finite<T>(w);
-        }
+        const uint32_t w = reinterpret_cast<const uint32_t*>(q_row(p, sg, ROWS, i))[lane];
+        const float2 f = unpack<T>(w);
+        top = fmaxf(fabsf(f.x), fabsf(f.y));
+        bad = not_finite<T>(w);
       }
       top = warp_max(top);
       // 2^e <= top < 2^(e+1); the row is divided by 2^e (both factors stay normal: by 2^126 above
@@ -112,11 +93,10 @@ __device__ __forceinline__ void attend(const Params& p) {
       if (lane == 0) s_fac[i] = bad ? NAN : __uint_as_float((uint32_t)e << 23);
     }
     __syncthreads();
-#pragma unroll (TAIL ? 4 : 1)
     for (int i = tid; i < MT * KS * 32; i += kThreads) {
       const int l = i & 31, ks = i / 32 % KS, mt = i / 32 / KS, qc = l & 3, qg = l >> 2;
-      // K's lane qc holds dims 16qc .. + 15 of each 64; step k takes dims 4k .. 4k + 3 of them
-      const int dim = ks / 4 * 64 + qc * 16 + ks % 4 * 4;
+      // K's lane qc holds dims 16qc .. + 15; step k takes dims 4k .. 4k + 3 of them
+      const int dim = qc * 16 + ks * 4;
       uint32_t w[4];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -124,7 +104,7 @@ __device__ __forceinline__ void attend(const Params& p) {
         uint2 x = make_uint2(0, 0);
         float inv = 1.f;
         if (row < rows) {
-          x = __ldg(reinterpret_cast<const uint2*>(q_row(p, sg, ROWS, row) + dim * 2));
+          x = *reinterpret_cast<const uint2*>(q_row(p, sg, ROWS, row) + dim * 2);
           inv = __uint_as_float(0x7F000000u - __float_as_uint(s_fac[row]));  // 1 / 2^e
         }
         const float2 u = unpack<T>(x.x), v = unpack<T>(x.y);
@@ -202,9 +182,9 @@ __device__ __forceinline__ void attend(const Params& p) {
     // ---- cached tokens
     const char* kc = static_cast<const char*>(p.c.k) + kvh * p.c.k_head_stride;
     const char* vc = static_cast<const char*>(p.c.v) + kvh * p.c.v_head_stride;
-    const int32_t* table = p.c.page_table + sg.b * p.c.ld_table + r.skip;
+    const int32_t* table = p.c.page_table + sg.b * p.c.ld_table;
     struct Loaded {
-      uint4 k[2][D / 64];
+      uint4 k[2];
       uint32_t v[4][VW];
       float ks, vs;
     };
@@ -221,55 +201,25 @@ __device__ __forceinline__ void attend(const Params& p) {
       for (int n = 0; n < 2; ++n) {
         const bool ok = page >= 0 && tok + n * 8 + g < r.len;
         const char* at = kc + page * p.c.k_page_stride + (int64_t)(slot + n * 8 + g) * p.c.k_token_stride + c * 16;
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) x.k[n][h] = ok ? ldg_stream(at + h * 64) : make_uint4(0, 0, 0, 0);
+        x.k[n] = ok ? ldg_stream(at) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int tt = 2 * c + (i & 1) + (i >> 1) * 8;
         const bool ok = page >= 0 && tok + tt < r.len;
         const char* at = vc + page * p.c.v_page_stride + (int64_t)(slot + tt) * p.c.v_token_stride + g * (D / 8);
-        if constexpr (D == 64) {
-          const uint2 w = ok ? __ldg(reinterpret_cast<const uint2*>(at)) : make_uint2(0, 0);
-          x.v[i][0] = w.x, x.v[i][1] = w.y;
-        } else {
-          const uint4 w = ok ? __ldg(reinterpret_cast<const uint4*>(at)) : make_uint4(0, 0, 0, 0);
-          x.v[i][0] = w.x, x.v[i][1] = w.y, x.v[i][2] = w.z, x.v[i][3] = w.w;
-        }
+        const uint2 w = ok ? __ldg(reinterpret_cast<const uint2*>(at)) : make_uint2(0, 0);
+        x.v[i][0] = w.x, x.v[i][1] = w.y;
       }
       x.ks = x.vs = 1.f;
       if (page >= 0) {
         x.ks = __ldg(p.c.k_scale + (int64_t)page * p.c.heads + kvh);
-        x.vs = __ldg(p.c.v_scale + (int64_t)page * p.c.heads + kvh);  // not looked at before it is needed
+        x.vs = scale_of_v(__ldg(p.c.v_scale + (int64_t)page * p.c.heads + kvh), x.ks);
       }
     };
     Loaded next;
     int32_t page = page_of(t0), page2 = page_of(t0 + 1);
     if (t0 < t1) fetch(t0, page, next);
-    const bool own_here = TAIL && p.a.k_new && t0 == 0;
-    if constexpr (TAIL) {
-      if (own_here) {  // each warp a share of the dims, or of the rows; s_o was read before the sync above
-        const Sees* trees = nullptr;
-        if (p.a.parents) {
-          for (int i = tid; i < r.rows; i += kThreads) s_parents[i] = p.a.parents[r.row0 + i];
-          __syncthreads();
-          for (int i = tid; i < r.rows; i += kThreads) s_trees[i] = tree_sees(s_parents, i);
-          __syncthreads();
-          trees = s_trees;
-        }
-        constexpr int kSlices = W > MT ? W / MT : 1;  // of the dims
-        const int j0 = warp % kSlices * (D / 8 / kSlices), j1 = j0 + D / 8 / kSlices;
-        for (int i16 = warp / kSlices * 16; i16 < rows; i16 += W / kSlices * 16) {
-          if (own_part<D, ROWS, T>(p, sg, i16, j0, j1, trees, s_o, D + 4, s_ml)) {
-            __syncwarp();
-#pragma unroll 1
-            for (int i = i16; i < min(rows, i16 + 16); ++i)
-              own_odd<D, ROWS, T>(p, sg, i, j0 * 8, j1 * 8, trees, s_ml[i].x, s_o + i * (D + 4));
-          }
-        }
-      }
-    }
-    if (own_here) __syncthreads();
     for (int t = t0; t < t1; ++t) {
       Loaded now = next;
       const int32_t page_now = page;
@@ -290,8 +240,8 @@ __device__ __forceinline__ void attend(const Params& p) {
         uint32_t kb[2][2];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const uint4 w4 = now.k[n][ks / 4];
-          const uint32_t w = ks % 4 == 0 ? w4.x : ks % 4 == 1 ? w4.y : ks % 4 == 2 ? w4.z : w4.w;
+          const uint4 w4 = now.k[n];
+          const uint32_t w = ks == 0 ? w4.x : ks == 1 ? w4.y : ks == 2 ? w4.z : w4.w;
           kb[n][0] = e4m3x2_to_f16x2((uint16_t)w);
           kb[n][1] = e4m3x2_to_f16x2((uint16_t)(w >> 16));
         }
@@ -303,7 +253,7 @@ __device__ __forceinline__ void attend(const Params& p) {
           mma16816<__half>(x[mt][1], qa, kb[1][0], kb[1][1]);
         }
       }
-      const float vs = scale_of_v(now.vs, now.ks), lv = __log2f(vs), inv_v = 1.f / vs;
+      const float lv = __log2f(now.vs), inv_v = 1.f / now.vs;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -348,33 +298,17 @@ __device__ __forceinline__ void attend(const Params& p) {
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         const int row = mt * 16 + h * 8 + g;
-        float top = m[mt][h];
-        float* at = s_o + (warp * ROWS + row) * (D + 4);
-        float by = 1.f, own = 0.f;
-        const bool joins = TAIL && own_here && warp == 0;
-        if (joins) {
-          const float2 ml = s_ml[row];
-          top = fmaxf(top, ml.x);
-          by = ex2(m[mt][h] - top);
-          own = ex2(ml.x - top);
-          sum = fmaf(sum, by, ml.y * own);
-        }
         if (c == 0) {
-          s_m[warp * ROWS + row] = top;
+          s_m[warp * ROWS + row] = m[mt][h];
           s_l[warp * ROWS + row] = sum;
         }
+        float* at = s_o + (warp * ROWS + row) * (D + 4);
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int j = 0; j < NT; j += 4) {
-            float4 v = make_float4(o[mt][j][2 * h + e], o[mt][j + 1][2 * h + e], o[mt][j + 2][2 * h + e], o[mt][j + 3][2 * h + e]);
-            float4* to = reinterpret_cast<float4*>(at + (2 * c + e) * (D / 8) + j);
-            if (joins) {
-              const float4 u = *to;
-              v = make_float4(fmaf(v.x, by, u.x * own), fmaf(v.y, by, u.y * own), fmaf(v.z, by, u.z * own), fmaf(v.w, by, u.w * own));
-            }
-            *to = v;
-          }
+          for (int j = 0; j < NT; j += 4)
+            *reinterpret_cast<float4*>(at + (2 * c + e) * (D / 8) + j) =
+                make_float4(o[mt][j][2 * h + e], o[mt][j + 1][2 * h + e], o[mt][j + 2][2 * h + e], o[mt][j + 3][2 * h + e]);
       }
     if (!waited) {  // for the window's own part
       grid_wait();
@@ -388,11 +322,11 @@ __device__ __forceinline__ void attend(const Params& p) {
       const int row = i / (D / 4), d = i % (D / 4) * 4;
       float top = kNone;
 #pragma unroll
-      for (int w = 0; w < PARTS; ++w) top = fmaxf(top, s_m[w * ROWS + row]);
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w * ROWS + row]);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       float sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < PARTS; ++w) {
+      for (int w = 0; w < kWarps; ++w) {
         const float by = ex2(s_m[w * ROWS + row] - top);
         const float4 v = *reinterpret_cast<const float4*>(s_o + (w * ROWS + row) * (D + 4) + d);
         sum = fmaf(by, s_l[w * ROWS + row], sum);
@@ -401,18 +335,12 @@ __device__ __forceinline__ void attend(const Params& p) {
       }
       if (whole) {
         const int64_t at = sg.at(p, ROWS, row);
-        float own, pre;
-        const float by = finish_row(p, r, at, top, sum, own, pre);  // the row's threads write the same lse
+        float own;
+        const float by = finish_row(p, at, top, sum, own);  // the row's threads write the same lse
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (p.own_ml) v = *reinterpret_cast<const float4*>(p.own_o + at * D + d);
-        float2 lo = make_float2(v.x * own, v.y * own), hi = make_float2(v.z * own, v.w * own);
-        if (pre != 0.f) {
-          v = *reinterpret_cast<const float4*>(p.pre_o + at * D + d);
-          add_scaled(lo, pre, make_float2(v.x, v.y));
-          add_scaled(hi, pre, make_float2(v.z, v.w));
-        }
-        const uint2 w = make_uint2(pack<T>(fmaf(acc.x, by, lo.x), fmaf(acc.y, by, lo.y)),
-                                   pack<T>(fmaf(acc.z, by, hi.x), fmaf(acc.w, by, hi.y)));
+        const uint2 w = make_uint2(pack<T>(fmaf(acc.x, by, v.x * own), fmaf(acc.y, by, v.y * own)),
+                                   pack<T>(fmaf(acc.z, by, v.z * own), fmaf(acc.w, by, v.w * own)));
         *reinterpret_cast<uint2*>(static_cast<char*>(p.a.out) + (at * D + d) * 2) = w;
       } else {
         *reinterpret_cast<float4*>(part + row * D + d) = acc;
@@ -438,14 +366,7 @@ __device__ __forceinline__ void attend(const Params& p) {
 template <int MT, typename T>
 __global__ void __launch_bounds__(kThreads) k_window(const __grid_constant__ Params p) {
   grid_launch();
-  attend<64, MT, T, false>(p);
-}
-
-// What is left of each request behind a shared prefix, and its window's own tokens: W warps a CTA.
-template <int D, int MT, typename T, int W>
-__global__ void __launch_bounds__(32 * W) k_tail(const __grid_constant__ Params p) {
-  grid_launch();
-  attend<D, MT, T, true, W>(p);
+  attend<MT, T>(p);
 }
 
 // More than 32 rows a window: blocks of 64 rows, for which K and V are converted half as often, where the
@@ -459,8 +380,8 @@ __global__ void __launch_bounds__(kThreads) k_window_rows(const __grid_constant_
   grid_launch();
   const bool wide = line_length<64, kTile, kThreads>(p) >= (int64_t)kWideTiles * gridDim.x;
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.wide = wide;
-  if (wide) attend<64, 4, T, false>(p);
-  else attend<64, 2, T, false>(p);
+  if (wide) attend<4, T>(p);
+  else attend<2, T>(p);
 }
 
 template <typename T>
@@ -470,9 +391,8 @@ __global__ void __launch_bounds__(128) k_join_rows(const __grid_constant__ Param
   else join_row<64, 32, kTile, T>(p);
 }
 
-constexpr int smem_bytes(int D, int rows, bool tail = false, int warps = 4) {
-  return rows / 16 * (D / 16) * 32 * 16 + rows * 4 + warps * rows * (D + 4) * 4 + warps * rows * 8 +
-         (tail ? TS_MAX_WINDOW * ((int)sizeof(Sees) + 4) + rows * 8 : 0);
+constexpr int smem_bytes(int D, int rows) {
+  return rows / 16 * (D / 16) * 32 * 16 + rows * 4 + kWarps * rows * (D + 4) * 4 + kWarps * rows * 8;
 }
 
 // kernel, join: k_window and k_join, or k_window_rows and k_join_rows, for blocks of at most ROWS rows.
@@ -503,24 +423,7 @@ cudaError_t launch_64(const Params& p, int rows, int sms, cudaStream_t s) {
   }
 }
 
-template <int D, int MT, typename T>
-cudaError_t launch_tail(const Params& p, int sms, cudaStream_t s) {
-  constexpr int W = kTailWarps, bytes = smem_bytes(D, 16 * MT, true, W);
-  cudaError_t e = allow_smem<k_tail<D, MT, T, W>>(bytes);
-  if (e != cudaSuccess) return e;
-  const int grid = sms * kTailCtas;
-  if ((e = launch_after(k_tail<D, MT, T, W>, dim3(grid), 32 * W, bytes, s, p)) != cudaSuccess) return e;
-  if ((int64_t)p.c.max_pages * p.c.page_size <= 16 * W) return cudaSuccess;  // units of one tile are never split
-  return launch_after(k_join<D, 16 * MT, 16 * W, T>, dim3(grid, 4 * MT), 128, 0, s, p);
-}
-
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
-
-}  // namespace
-
-int tail_rows(const WindowParams& p) { return (p.a.total_rows * p.group + p.c.batch - 1) / p.c.batch <= 16 ? 16 : 32; }
-
-namespace {
 
 // The rows of a block: by the average window. head_dim 128, ragged chains of 4 to 20 rows: 162 us
 // with 32, 189 with 64; trees of 256 rows: 416 with 32, 330 with 64. head_dim 64, one row of 4
@@ -532,9 +435,9 @@ int block_rows(const WindowParams& p) {
 }
 
 // Lays the workspace out; returns its bytes.
-size_t lay_out(WindowParams& p, void* ws, int sms, bool tail = false) {
-  const int rows = tail ? tail_rows(p) : block_rows(p), D = p.c.head_dim;
-  const size_t ctas = (size_t)sms * (tail ? kTailCtas : kCtasPerSm);
+size_t lay_out(WindowParams& p, void* ws, int sms) {
+  const int rows = block_rows(p), D = p.c.head_dim;
+  const size_t ctas = (size_t)sms * kCtasPerSm;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     char* at = static_cast<char*>(ws) + off;
@@ -544,7 +447,6 @@ size_t lay_out(WindowParams& p, void* ws, int sms, bool tail = false) {
   p.desc = reinterpret_cast<int4*>(take(ctas * sizeof(int4)));
   p.wide = reinterpret_cast<int32_t*>(take(sizeof(int32_t)));
   p.part = reinterpret_cast<float*>(take(2 * ctas * slot_floats(rows, D) * sizeof(float)));
-  if (tail) return off;
   const size_t n = (size_t)p.a.total_rows * p.a.heads_q;
   // the window's own part: of every row, or (ts_window_tc.cu) of a block a CTA
   p.own_o = reinterpret_cast<float*>(take(std::max(n, (size_t)sms * rows) * D * sizeof(float)));
@@ -553,38 +455,6 @@ size_t lay_out(WindowParams& p, void* ws, int sms, bool tail = false) {
 }
 
 }  // namespace
-
-size_t tail_workspace(int64_t batch, int64_t total_rows, int heads_q, int heads, int head_dim, int sms) {
-  WindowParams p{};
-  p.c.batch = batch;
-  p.c.heads = heads;
-  p.c.head_dim = head_dim;
-  p.a.total_rows = total_rows;
-  p.a.heads_q = heads_q;
-  p.group = heads_q / heads;
-  return lay_out(p, nullptr, sms, true);
-}
-
-WindowParams tail_params(const ts_kv_cache& c, const ts_attn_args& a, void* ws, int sms) {
-  WindowParams p{};
-  p.c = c;
-  p.a = a;
-  p.page_shift = __builtin_ctz((unsigned)c.page_size);
-  p.group = a.heads_q / c.heads;
-  p.scale_log2 = a.sm_scale * kLog2e;
-  lay_out(p, ws, sms, true);
-  return p;
-}
-
-cudaError_t launch_tails(const WindowParams& p, int sms, cudaStream_t s) {
-  const bool bf16 = p.a.dtype == TS_BF16, small = tail_rows(p) == 16;
-  if (p.c.head_dim == 64) {
-    if (small) return bf16 ? launch_tail<64, 1, __nv_bfloat16>(p, sms, s) : launch_tail<64, 1, __half>(p, sms, s);
-    return bf16 ? launch_tail<64, 2, __nv_bfloat16>(p, sms, s) : launch_tail<64, 2, __half>(p, sms, s);
-  }
-  if (small) return bf16 ? launch_tail<128, 1, __nv_bfloat16>(p, sms, s) : launch_tail<128, 1, __half>(p, sms, s);
-  return bf16 ? launch_tail<128, 2, __nv_bfloat16>(p, sms, s) : launch_tail<128, 2, __half>(p, sms, s);
-}
 
 size_t window_workspace(int64_t batch, int64_t total_rows, int heads_q, int heads, int head_dim, int sms) {
   WindowParams p{};

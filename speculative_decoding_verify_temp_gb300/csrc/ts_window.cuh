@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <utility>
 
 #include "../../include/ts_verify.h"
 #include "ts_common.cuh"
@@ -33,10 +34,6 @@ struct WindowParams {
   int32_t* wide;    // blocks of 64 rows (head_dim 64, where the kernel chooses)
   float* own_o;      // [total_rows * heads_q][D] the window's own part: outputs,
   float2* own_ml;    // [total_rows * heads_q] references and sums
-  const int32_t* first;   // [batch] tokens in front that another kernel attended to (whole pages), or NULL
-  const float* pre_o;     // [total_rows * heads_q][D] their part: outputs,
-  const float2* pre_ml;   // references and sums (of the rows of requests with first > 0)
-  const Start* starts;    // [CTAs] their shares (line_starts), or NULL: each finds its own
   uint64_t wait_cycles;  // SM clock cycles that a wait may take (ts_window_tc.cu)
 };
 
@@ -99,8 +96,8 @@ __device__ __forceinline__ uint32_t not_finite<__nv_bfloat16>(uint32_t w) { retu
 struct Req {
   int64_t row0;
   int32_t rows;    // window rows (0: skipped)
-  int32_t skip;    // pages in front that are not attended to here
-  int32_t len;     // cached tokens behind them
+  int32_t len;     // cached tokens
+  int32_t skip;    // pages in front of them that are not attended to here (ts_tail.cu)
   int32_t blocks;  // row blocks
   int32_t tiles;   // of a unit, >= 1
   __device__ __forceinline__ int64_t weight(int heads) const { return rows ? (int64_t)heads * blocks * tiles : 0; }
@@ -109,13 +106,12 @@ struct Req {
 
 // The loads behind a request, apart from what follows from them, so that they can be made early.
 struct RawReq {
-  int32_t row0, row1, len, first;
+  int32_t row0, row1, len;
 };
 
 __device__ __forceinline__ RawReq raw_request(const WindowParams& p, int64_t b) {
-  RawReq r = {0, 0, 0, 0};
+  RawReq r = {0, 0, 0};
   if (b >= p.c.batch) return r;
-  if (p.first) r.first = __ldcg(p.first + b);  // the kernel that plans ahead may run while the one that wrote it ends
   if (p.a.qo_indptr) {
     r.row0 = p.a.qo_indptr[b];
     r.row1 = p.a.qo_indptr[b + 1];
@@ -134,8 +130,7 @@ __device__ __forceinline__ Req request(const WindowParams& p, const RawReq& raw)
   r.row0 = raw.row0;
   const bool fits = raw.row0 >= 0 && raw.row1 <= p.a.total_rows && raw.row1 > raw.row0 && raw.row1 - raw.row0 <= TS_MAX_WINDOW;
   r.rows = fits ? raw.row1 - raw.row0 : 0;
-  r.skip = raw.first >> p.page_shift;
-  r.len = min(max(raw.len, 0), p.c.max_pages << p.page_shift) - raw.first;  // at most 2^30; first is not above it
+  r.len = min(max(raw.len, 0), p.c.max_pages << p.page_shift);  // at most 2^30
   r.blocks = (int)((unsigned)(r.rows * p.group + ROWS - 1) / ROWS);
   r.tiles = max((int)((unsigned)(r.len + TILE - 1) / TILE), 1);
   return r;
@@ -158,7 +153,7 @@ struct Segment {
 template <int ROWS, int TILE, typename P = WindowParams>
 struct Line {
   Req r;
-  RawReq after;  // the request behind it
+  decltype(raw_request(std::declval<const P&>(), 0)) after;  // the request behind it
   int64_t left;
   int32_t b, kvh, block, tile;
   __device__ __forceinline__ bool next(const P& p, Segment& s) {
@@ -192,8 +187,8 @@ struct Line {
 // it up. Returns false for a CTA without work. least_tiles: a CTA takes this many tiles at least, or as
 // many as an average unit has where that is less (14 windows of 8 rows over 4 tokens, head_dim 64:
 // 16 us, 39 with four such units a CTA).
-template <int ROWS, int TILE, int THREADS, typename P>
-__device__ __forceinline__ bool line_begin(const P& p, int least_tiles, Line<ROWS, TILE, P>& line) {
+template <int ROWS, int TILE, int THREADS>
+__device__ __forceinline__ bool line_begin(const WindowParams& p, int least_tiles, Line<ROWS, TILE>& line) {
   static_assert(THREADS % 32 == 0, "whole warps");
   __shared__ int64_t s_scan[THREADS / 32], s_start;
   __shared__ uint32_t s_units[THREADS / 32];  // below 2^28: total_rows * heads_q is below 2^31
@@ -368,33 +363,23 @@ __device__ __forceinline__ float finish_row(const WindowParams& p, int64_t at, f
   return sum != 0.f ? 1.f / sum : 0.f;
 }
 
-// The same, joined with the window's own part if there is one in own_ml, and with the part of the
-// tokens in front if the request has some: their factors come back in own and pre.
-__device__ __forceinline__ float finish_row(const WindowParams& p, const Req& r, int64_t at, float top, float sum, float& own, float& pre) {
-  own = pre = 0.f;
-  const bool in_front = p.pre_ml && r.skip > 0;
-  if (!p.own_ml && !in_front) return finish_row(p, at, top, sum);
-  float2 ml = make_float2(kNone, 0.f), front = ml;
-  if (p.own_ml) ml = p.own_ml[at];
-  if (in_front) front = p.pre_ml[at];
-  const float to = fmaxf(fmaxf(top, ml.x), front.x), by = ex2(top - to);
+// The same, joined with the window's own part if there is one in own_ml: its factor comes back
+// in own.
+__device__ __forceinline__ float finish_row(const WindowParams& p, int64_t at, float top, float sum, float& own) {
+  own = 0.f;
+  if (!p.own_ml) return finish_row(p, at, top, sum);
+  const float2 ml = p.own_ml[at];
+  const float to = fmaxf(top, ml.x), by = ex2(top - to);
   own = ex2(ml.x - to);
-  pre = ex2(front.x - to);
-  const float inv = finish_row(p, at, to, fmaf(front.y, pre, fmaf(sum, by, ml.y * own)));
+  const float inv = finish_row(p, at, to, fmaf(sum, by, ml.y * own));
   own *= inv;
-  pre = in_front ? pre * inv : 0.f;
   return by * inv;
-}
-
-__device__ __forceinline__ void add_scaled(float2& o, float by, float2 v) {
-  o.x = fmaf(v.x, by, o.x);
-  o.y = fmaf(v.y, by, o.y);
 }
 
 // One warp a row of a unit that spans CTAs: the piece of the CTA where it begins (slot
 // 2i + 1), then the first pieces (slots 2j) of the CTAs after it up to the one that ends it.
-template <int D, int ROWS, int TILE, typename T>
-__device__ __forceinline__ void join_row(const WindowParams& p) {
+template <int D, int ROWS, int TILE, typename T, typename P>
+__device__ __forceinline__ void join_row(const P& p) {
   const int first = blockIdx.x, lane = threadIdx.x & 31;
   const int row = blockIdx.y * 4 + (threadIdx.x >> 5);
   const int4 d = p.desc[first];
@@ -431,16 +416,14 @@ __device__ __forceinline__ void join_row(const WindowParams& p) {
   s.kvh = d.y / s.r.blocks;
   s.block = d.y % s.r.blocks;
   const int64_t at = s.at(p, ROWS, row);
-  float own, pre;
-  const float by = finish_row(p, s.r, at, top, sum, own, pre);  // every lane writes the same lse
+  float own;
+  const float by = finish_row(p, at, top, sum, own);  // every lane writes the same lse
 #pragma unroll
   for (int e = 0; e < PER; e += 2) {
     float2 o = make_float2(0.f, 0.f);
     if (p.own_ml) o = *reinterpret_cast<const float2*>(p.own_o + at * D + lane * PER + e);
-    o.x *= own, o.y *= own;
-    if (pre != 0.f) add_scaled(o, pre, *reinterpret_cast<const float2*>(p.pre_o + at * D + lane * PER + e));
     *reinterpret_cast<uint32_t*>(static_cast<char*>(p.a.out) + (at * D + lane * PER + e) * 2) =
-        pack<T>(fmaf(acc[e], by, o.x), fmaf(acc[e + 1], by, o.y));
+        pack<T>(fmaf(acc[e], by, o.x * own), fmaf(acc[e + 1], by, o.y * own));
   }
 }
 
@@ -449,14 +432,6 @@ __global__ void __launch_bounds__(128) k_join(const __grid_constant__ WindowPara
   grid_wait();
   join_row<D, ROWS, TILE, T>(p);
 }
-
-// What is left of the requests behind a shared prefix (ts_window.cu): CTAs of kTailWarps warps, blocks of
-// tail_rows rows; first, pre_o, pre_ml and starts are the caller's.
-constexpr int kTailWarps = 4, kTailCtas = 2, kTailTile = 16 * kTailWarps, kTailLeast = 4;
-int tail_rows(const WindowParams& p);
-size_t tail_workspace(int64_t batch, int64_t total_rows, int heads_q, int heads, int head_dim, int sms);
-WindowParams tail_params(const ts_kv_cache& c, const ts_attn_args& a, void* ws, int sms);
-cudaError_t launch_tails(const WindowParams& p, int sms, cudaStream_t s);
 
 // The tensor map of K or V, a box a page of one head (ts_window_tc.cu); false: not possible.
 bool page_map(CUtensorMap* map, const ts_kv_cache& c, void* base, int64_t page_stride, int64_t head_stride, int64_t token_stride,
@@ -475,6 +450,11 @@ cudaError_t allow_smem(int bytes) {
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
+}
+
+__device__ __forceinline__ void add_scaled(float2& o, float by, float2 v) {
+  o.x = fmaf(v.x, by, o.x);
+  o.y = fmaf(v.y, by, o.y);
 }
 
 // Launches with programmatic stream serialisation: the kernel may start before the one

@@ -114,7 +114,7 @@ struct Shared {
   alignas(16) float delta[kGroups][kCols];  // factors of outputs and sums whose references move
   float peak[kGroups][kCols];               // the rows' largest references so far
   float red[kGroups][4][kCols];
-  float w[kGroups + 2][ROWS];  // a row's factors: the turns', the window's own part, and that of the tokens in front
+  float w[kGroups + 1][ROWS];  // a row's factors: the turns', and the window's own part
   float2 own[ROWS];            // the own part's references and sums
   int32_t at[ROWS];            // a row's index in [total_rows][heads_q]
   int32_t parents[TS_MAX_WINDOW];
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto page_of = [&](const Segment& g, int r) -> int32_t {
         const int i = g.t0 * per_tile + r * 32 + lane;
         if (i >= g.t1 * per_tile || (int64_t)i << p.page_shift >= g.r.len) return -1;
-        const int32_t id = p.c.page_table[g.b * p.c.ld_table + g.r.skip + i];
+        const int32_t id = p.c.page_table[g.b * p.c.ld_table + i];
         return id >= 0 && id < p.c.num_pages ? id : -1;
       };
       auto scales_of = [&](const Segment& g, int32_t page, float& ks, float& vs) {
@@ -626,14 +626,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_sync(kBarAll, kSoftmaxThreads);
       tc_fence_after();
       const bool whole = s.whole();
-      const bool in_front = p.pre_ml && s.t0 == 0 && s.r.skip > 0;  // the first piece takes that part too
       float* part = p.part + (2 * (int64_t)blockIdx.x + (s.t0 == 0 ? 1 : 0)) * slot_floats(ROWS, kD);
       if (tid < s.rows) {
         const int r = tid, c = r % kCols;
         float m[L::turns], sum[L::turns];
         const float2 ml = own ? x.own[r] : make_float2(kNone, 0.f);
-        const float2 front = in_front ? p.pre_ml[x.at[r]] : make_float2(kNone, 0.f);
-        float to = fmaxf(ml.x, front.x);
+        float to = ml.x;
 #pragma unroll
         for (int k = 0; k < L::turns; ++k) {
           const int g = L::split ? 2 * k + r / kCols : k;
@@ -645,8 +643,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float by = ex2(ml.x - to), all = by * ml.y;
         x.w[L::turns][r] = by;
-        const float pre = ex2(front.x - to);
-        all = fmaf(pre, front.y, all);
 #pragma unroll
         for (int k = 0; k < L::turns; ++k) {
           m[k] = ex2(m[k] - to);
@@ -660,7 +656,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           part[ROWS * kD + ROWS + r] = all;
         }
         x.w[L::turns][r] *= by;
-        x.w[L::turns + 1][r] = pre * by;
 #pragma unroll
         for (int k = 0; k < L::turns; ++k) x.w[k][r] = m[k] * by;
       }
@@ -672,12 +667,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         float o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = own && c + e < s.rows ? x.w[L::turns][c + e] * own_o[(c + e) * kD + d] : 0.f;
-        if (in_front) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (c + e < s.rows && x.w[L::turns + 1][c + e] != 0.f)
-              o[e] = fmaf(x.w[L::turns + 1][c + e], p.pre_o[(int64_t)x.at[c + e] * kD + d], o[e]);
-        }
 #pragma unroll 1
         for (int k = 0; k < L::turns; ++k) {
           if (!x.live[L::split ? 2 * k : k]) continue;  // both groups of a turn see the same tokens
@@ -743,9 +732,7 @@ cudaError_t launch(const WindowParams& p, const CUtensorMap& k, const CUtensorMa
   k_window_tc<ROWS, QP, T><<<sms, kThreads, bytes, s>>>(p, k, v);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if ((int64_t)p.c.max_pages * p.c.page_size <= kTile) return cudaSuccess;  // units of one tile are never split
-  WindowParams joined = p;
-  joined.pre_ml = nullptr;  // in the pieces
-  return launch_after(k_join<kD, ROWS, kTile, T>, dim3(sms, ROWS / 4), 128, 0, s, joined);
+  return launch_after(k_join<kD, ROWS, kTile, T>, dim3(sms, ROWS / 4), 128, 0, s, p);
 }
 
 }  // namespace
