@@ -77,12 +77,11 @@ namespace {
 constexpr int kTile = 128;
 constexpr int kRows = 128;   // of a slot
 constexpr int kBlock = 2 * kRows;
-constexpr int kConvert = 4;  // warps that make codes fp16
+constexpr int kConvert = 4;  // warps that make codes fp16: half of them K's, half V's
 constexpr int kThreads = 256 + kConvert * 32 + 128;
 // Registers of a thread: 128 at launch (512 threads), then by role
 constexpr int kSoftmaxRegs = 184, kConvertRegs = 80, kIssueRegs = 64;
 static_assert(256 * kSoftmaxRegs + kConvert * 32 * kConvertRegs + 128 * kIssueRegs <= kThreads * 128, "registers");
-constexpr int kMaxGang = 8;
 constexpr int kMeta = 8;     // tiles whose scales are in shared memory
 constexpr float kHead = 4.f;         // a reference is set this far, in log2, below the largest score
 constexpr float kMostSum = 65504.f;  // of a tile's probabilities, where the reference stays: none is past fp16
@@ -108,10 +107,8 @@ struct Layout {
   static constexpr int col_o = 2 * kTile;            // TMEM: S (and P) of both slots, then O
 };
 
-// Where outputs pass through and the slots meet, in the place of Q: 16 columns, padded, of a slot's rows (each
-// slot's in its own Q; where they meet, in the first's), then references and sums.
-constexpr int kMeetLd = 20, kMeetMl = kRows * kMeetLd * 4;
-static_assert(kMeetMl + 2 * kRows * 8 <= Layout<64>::tile_bytes, "Q's place");
+static_assert(2 * kRows * 8 <= 2 * Layout<64>::tile_bytes && kRows * 64 * 2 == Layout<64>::tile_bytes && kRows * 128 * 2 == Layout<128>::tile_bytes,
+              "Q's place: where the slots meet");
 
 struct Shared {
   uint64_t k_full[4], k_empty[4], v_full[8], v_empty[8], raw_full[6], raw_empty[6], meta_full[kMeta];
@@ -138,10 +135,14 @@ __device__ __forceinline__ void set_regs() {
 struct Share {
   Line<kBlock, kTile, PrefixParams> line;
   int gang, rank;
-  __device__ __forceinline__ bool begin(const PrefixParams& p) {
+  __device__ __forceinline__ static bool any(const PrefixParams& p) {
+    const int g = *p.gang;
+    return blockIdx.x / g < gridDim.x / g && p.starts[blockIdx.x / g].b >= 0;
+  }
+  __device__ __forceinline__ explicit Share(const PrefixParams& p) {
     gang = *p.gang;
     rank = blockIdx.x % gang;
-    return blockIdx.x / gang < gridDim.x / gang && line_at<kBlock, kTile>(p, p.starts[blockIdx.x / gang], line);
+    line_at<kBlock, kTile>(p, p.starts[blockIdx.x / gang], line);
   }
   __device__ __forceinline__ bool next(const PrefixParams& p, Segment& s) {
     while (line.next(p, s)) {
@@ -220,11 +221,11 @@ __device__ __forceinline__ void widen(const uint4& w, uint4& lo, uint4& hi) {
 
 // A warp's 32 rows of Q (rows r0 .. r0 + 31 of `left`; the others zeros) as fp16 into their place: rows of 128
 // bytes in atoms of 64 values, the 16-byte pieces of row r at their place XOR r % 8. Returns what a
-// unit of the products of the lane's row stands for. Four steps of loads are in flight, and the code is kept
+// unit of the products of the lane's row stands for. Eight steps of loads are in flight, and the code is kept
 // small: it runs once a unit, from cold instruction caches (unrolled sixteen times it took 14 us).
 template <int D, typename T>
 __device__ __forceinline__ float load_q(const PrefixParams& p, const Segment& s, int r0, int left, unsigned char* to) {
-  constexpr int kLanes = D / 8, kEach = 32 / kLanes, N = 32 / kEach, kAhead = 4;  // lanes of a row, rows a step, steps
+  constexpr int kLanes = D / 8, kEach = 32 / kLanes, N = 32 / kEach, kAhead = 8;  // lanes of a row, rows a step, steps
   const int lane = threadIdx.x & 31, piece = lane % kLanes, sub = lane / kLanes;
   const int j = s.block * kBlock + r0 + sub;
   int h = j % p.group;
@@ -246,7 +247,7 @@ __device__ __forceinline__ float load_q(const PrefixParams& p, const Segment& s,
       for (; h >= p.group; h -= p.group) at += row;
     }
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k, r += kEach) {
+    for (int k = 0; k < kAhead; ++k, r += kEach) {  // w has to stay in registers
       const uint32_t sign = 0x7FFF7FFFu;
       const uint32_t m = __vmaxu2(__vmaxu2(w[k].x & sign, w[k].y & sign), __vmaxu2(w[k].z & sign, w[k].w & sign));
       uint32_t top = max(m >> 16, m & 0xFFFFu);  // the largest magnitude of the row, as bits
@@ -281,24 +282,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
   int4 desc = make_int4(-1, 0, 0, 0);
   grid_wait();
   grid_launch();  // behind the wait: a CTA of the next kernel reads the plan without one
-  Share line;
-  if (!line.begin(p)) {
+  if (!Share::any(p)) {
     if (tid == 0) p.desc[blockIdx.x] = desc;
     return;
   }
   if (warp == kIssue) tmem_alloc(&x.tmem, 512);
   if (tid == 0) {
     for (int i = 0; i < L::k_stages; ++i) {
-      mbar_init(&x.k_full[i], kConvert);
+      mbar_init(&x.k_full[i], kConvert / 2);
       mbar_init(&x.k_empty[i], 1);
     }
     for (int i = 0; i < L::v_halves; ++i) {
-      mbar_init(&x.v_full[i], kConvert);
+      mbar_init(&x.v_full[i], kConvert / 2);
       mbar_init(&x.v_empty[i], 1);
     }
     for (int i = 0; i < L::units; ++i) {
       mbar_init(&x.raw_full[i], 1);
-      mbar_init(&x.raw_empty[i], kConvert);
+      mbar_init(&x.raw_empty[i], kConvert / 2);
     }
     for (int i = 0; i < kMeta; ++i) mbar_init(&x.meta_full[i], 1);
     for (int i = 0; i < 2; ++i) {
@@ -316,11 +316,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = x.tmem;
-  Segment s{};
-
+  // every role walks the line by itself: what lives through the change of registers is spilled
   if (warp >= kIssue) {
     set_regs<kIssueRegs, false>();
     if (warp == kIssue) {
+      Share line(p);
+      Segment s;
       // ---- the products. Tiles are counted through the CTA's units; tile i is in stage i % k_stages, its
       // halves of V in those of 2 i and 2 i + 1 % v_halves.
       const uint32_t leader = elect_one(), tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -392,7 +393,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
         ++u;
       }
     } else if (warp == kIssue + 1) {
-      // ---- loads: lanes hold a tile's pages and bring them, K and V in turn; page numbers come two
+      Share line(p);
+      Segment s;
+      // ---- loads: lanes hold a tile's pages and bring them, K and V in turn; page numbers come four
       // tiles ahead, scales one.
       struct Tile {
         int32_t page = -1;
@@ -430,9 +433,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
         ks = __ldg(p.c.k_scale + at);
         vs = __ldg(p.c.v_scale + at);
       };
-      Tile now = next_tile();
+      auto to_l2 = [&](const Tile& t) {
+        if (t.page < 0) return;
+        tma_prefetch_4d(&k_map, 0, 0, t.kvh, t.page);
+        tma_prefetch_4d(&v_map, 0, 0, t.kvh, t.page);
+      };
+      // shared memory has room for a tile and a half on its way, which at DRAM's latency is a third of its rate:
+      // the tiles behind are on their way to L2
+      Tile now = next_tile(), then, third, fourth;
       fetch_scales(now);
-      Tile then = next_tile();
       uint32_t i = 0;
 #pragma unroll 1
       while (now.is) {
@@ -460,65 +469,86 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
           for (int k = 0; k < 8 / per_tile; ++k) x.meta[i % kMeta][lane * (8 / per_tile) + k] = g;
         __syncwarp();
         if (lane == 0) mbar_arrive(&x.meta_full[i % kMeta]);
+        if (i == 0) {  // behind the first loads
+          then = next_tile();
+          third = next_tile();
+          fourth = next_tile();
+          to_l2(then);
+          to_l2(third);
+        }
+        to_l2(fourth);
         now = then;
+        then = third;
+        third = fourth;
+        fourth = next_tile();
         fetch_scales(now);
-        if (now.is) then = next_tile();
         ++i;
       }
     }
   } else if (warp >= 8) {
     set_regs<kConvertRegs, false>();
-    // ---- codes to fp16, 16 a step of a thread
-    constexpr int kPer = D / 16, kStep = kConvert * 32 / kPer;  // pieces of a token, tokens a step
-    const int ct = tid - 256, piece = ct % kPer, tok = ct / kPer, atom = piece >> 2;
+    Share line(p);
+    Segment s;
+    // ---- codes to fp16, 16 a step of a thread; half of the warps K, half V, so that neither waits for the other
+    constexpr int kPer = D / 16, kStep = kConvert / 2 * 32 / kPer;  // pieces of a token, tokens a step
+    const bool is_v = warp >= 8 + kConvert / 2;
+    const int ct = tid - 256 - (is_v ? kConvert / 2 * 32 : 0), piece = ct % kPer, tok = ct / kPer, atom = piece >> 2;
     // the second atom's lanes store their halves the other way round: no two at one bank
     const int chunk = (piece & 3) * 2 + (atom & 1);
     const int swizzled = (chunk ^ (tok & 7)) * 16;  // steps are multiples of 8 tokens
-    // n tokens of a unit into an array of rows of 128 bytes
-    auto widen_all = [&](const unsigned char* from, unsigned char* to, int atom_bytes, int n) {
+    // 64 tokens of a unit into an array of rows of 128 bytes; all loads are in flight at once
+    auto widen_half = [&](const unsigned char* from, unsigned char* to, int atom_bytes) {
+      constexpr int N = kTile / 2 / kStep;
       const unsigned char* a = from + tok * D + piece * 16;
       unsigned char* b = to + atom * atom_bytes + tok * 128;
-#pragma unroll 4
-      for (int e = 0; e < n; e += kStep) {
+      uint4 w[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) w[e] = *reinterpret_cast<const uint4*>(a + e * kStep * D);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
         uint4 lo, hi;
-        widen(*reinterpret_cast<const uint4*>(a + e * D), lo, hi);
-        *reinterpret_cast<uint4*>(b + e * 128 + swizzled) = atom & 1 ? hi : lo;
-        *reinterpret_cast<uint4*>(b + e * 128 + (swizzled ^ 16)) = atom & 1 ? lo : hi;
+        widen(w[e], lo, hi);
+        *reinterpret_cast<uint4*>(b + e * kStep * 128 + swizzled) = atom & 1 ? hi : lo;
+        *reinterpret_cast<uint4*>(b + e * kStep * 128 + (swizzled ^ 16)) = atom & 1 ? lo : hi;
       }
-      fence_async_shared();
-      __syncwarp();
     };
     uint32_t i = 0;
 #pragma unroll 1
     while (line.next(p, s)) {
 #pragma unroll 1
       for (int j = s.t0; j < s.t1; ++j, ++i) {
-        uint32_t n = 2 * i, st = n % L::units;
+        const uint32_t n = 2 * i + (is_v ? 1 : 0), st = n % L::units;
+        const unsigned char* raw = sm + L::off_raw + st * L::unit_bytes;
         wait(&x.raw_full[st], n / L::units & 1, &x.stop);
-        const uint32_t k = i % L::k_stages;
-        wait(&x.k_empty[k], (i / L::k_stages & 1) ^ 1, &x.stop);
-        __syncwarp();
-        widen_all(sm + L::off_raw + st * L::unit_bytes, sm + L::off_k + k * L::tile_bytes, L::atom_bytes, kTile);
-        if (lane == 0) {
-          mbar_arrive(&x.k_full[k]);
-          mbar_arrive(&x.raw_empty[st]);
-        }
-        ++n, st = n % L::units;
-        wait(&x.raw_full[st], n / L::units & 1, &x.stop);
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t h = 2 * i + half, v = h % L::v_halves;
-          wait(&x.v_empty[v], (h / L::v_halves & 1) ^ 1, &x.stop);
+        if (!is_v) {
+          const uint32_t k = i % L::k_stages;
+          wait(&x.k_empty[k], (i / L::k_stages & 1) ^ 1, &x.stop);
           __syncwarp();
-          widen_all(sm + L::off_raw + st * L::unit_bytes + half * (L::unit_bytes / 2), sm + L::off_v + v * (L::tile_bytes / 2),
-                    L::atom_bytes / 2, kTile / 2);
-          if (lane == 0) mbar_arrive(&x.v_full[v]);
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half)
+            widen_half(raw + half * (L::unit_bytes / 2), sm + L::off_k + k * L::tile_bytes + half * (L::atom_bytes / 2), L::atom_bytes);
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&x.k_full[k]);
+        } else {
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t h = 2 * i + half, v = h % L::v_halves;
+            wait(&x.v_empty[v], (h / L::v_halves & 1) ^ 1, &x.stop);
+            __syncwarp();
+            widen_half(raw + half * (L::unit_bytes / 2), sm + L::off_v + v * (L::tile_bytes / 2), L::atom_bytes / 2);
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&x.v_full[v]);
+          }
         }
         if (lane == 0) mbar_arrive(&x.raw_empty[st]);
       }
     }
   } else {
     set_regs<kSoftmaxRegs, true>();
+    Share line(p);
+    Segment s;
     // ---- softmax: a thread is a row of its slot
     const int slot = warp >> 2, r = tid & (kRows - 1);
     const uint32_t quarter = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's lanes
@@ -627,30 +657,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
               stored = true;
               break;
             }
-            float all = 0.f, y[2][32];
-            tmem_ld32(my_s, y[0]);
+            float all = 0.f, y[2][16];
+            tmem_ld16(my_s, y[0]);
 #pragma unroll
-            for (int c = 0; c < kTile / 32; ++c) {
+            for (int c = 0; c < kTile / 16; ++c) {
+              const float4 g = meta[c];
+              const f32x2 a = pair(fac * g.x, fac * g.x), b = pair(g.y - m, g.y - m);
               tmem_wait_ld();
-              tmem_tie32(y[c & 1]);
-              if (c + 1 < kTile / 32) tmem_ld32(my_s + (c + 1) * 32, y[(c + 1) & 1]);
+              tmem_tie16(y[c & 1]);
+              if (c + 1 < kTile / 16) tmem_ld16(my_s + (c + 1) * 16, y[(c + 1) & 1]);
+              const float* v = y[c & 1];
+              f32x2 sum[2] = {0, 0};
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float4 g = meta[2 * c + h];
-                const float* v = y[c & 1] + 16 * h;
-                const f32x2 a = pair(fac * g.x, fac * g.x), b = pair(g.y - m, g.y - m);
-                f32x2 sum[2] = {0, 0};
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const float2 z = unpair(fma2(pair(v[2 * e], v[2 * e + 1]), a, b));
-                  const float e0 = ex2(z.x), e1 = ex2(z.y);
-                  sum[e & 1] = add2(sum[e & 1], pair(e0, e1));
-                  w[16 * c + 8 * h + e] = f16x2(e0, e1);
-                }
-                const float2 both = unpair(add2(sum[0], sum[1]));
-                all += both.x + both.y;
-                part = fmaf(both.x + both.y, g.z, part);
+              for (int e = 0; e < 8; ++e) {
+                const float2 z = unpair(fma2(pair(v[2 * e], v[2 * e + 1]), a, b));
+                const float e0 = ex2(z.x), e1 = ex2(z.y);
+                sum[e & 1] = add2(sum[e & 1], pair(e0, e1));
+                w[8 * c + e] = f16x2(e0, e1);
               }
+              const float2 both = unpair(add2(sum[0], sum[1]));
+              all += both.x + both.y;
+              part = fmaf(both.x + both.y, g.z, part);
             }
             may = all > kMostSum || far;
             look = true;
@@ -674,11 +701,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
       tc_fence_after();
       const bool whole = s.whole();
       float* part = p.part + (2 * (int64_t)blockIdx.x + (s.t0 == 0 ? 1 : 0)) * slot_floats(kBlock, D);
-      float* to = whole ? p.pre_o + at * D : part + (int64_t)row * D;
       float by = 1.f;
       if (!wide) {  // the slots meet, when the last scores of both are formed and Q has been read
         bar_sync(1, 256);
-        float2* ml = reinterpret_cast<float2*>(sm + kMeetMl);
+        float2* ml = reinterpret_cast<float2*>(sm);
         ml[slot * kRows + r] = make_float2(m, l);
         bar_sync(1, 256);
         const float2 other = ml[(slot ^ 1) * kRows + r];
@@ -686,53 +712,57 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
         by = live ? ex2(m - top) : 0.f;
         l = fmaf(l, by, other.y * ex2(other.x - top));
         m = top;
+        bar_sync(1, 256);
       }
       if (mine && (wide || slot == 0)) {
         if (whole) p.pre_ml[at] = make_float2(m, l);
         else part[kBlock * D + row] = m, part[kBlock * D + kBlock + row] = l;
       }
-      // 16 columns a step, through the place of Q (each warp its own rows), so that rows are written in runs
-      float4* meet = reinterpret_cast<float4*>(sm) + (wide ? slot * (L::tile_bytes / 16) : 0) + (wide ? warp & 3 : r >> 5) * (32 * kMeetLd / 4);
+      // Outputs pass through the place of Q, half of the columns at a time, so that rows are written in runs: 16
+      // bytes at their place XOR the row. Where the slots meet, each hands the other one half and adds that up.
+      constexpr int kHalf = D / 2, kPieces = kHalf / 4;
+      const int target = mine && (wide || row < s.rows) ? (whole ? (int)at : row) : -1;
+      float* const base = whole ? p.pre_o : part;
+      auto pour = [&](int half, int region, bool add) {
+        float4* place = reinterpret_cast<float4*>(sm + region * L::tile_bytes) + r * kPieces;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 16) {
-        float o[16];
-        if (live) {
-          tmem_ld16(my_o + c, o);
-          tmem_wait_ld();
-          tmem_tie16(o);
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = live ? o[e] * by : 0.f;
-        float4* mine_at = meet + lane * (kMeetLd / 4);
-        if (!wide) {
-          if (slot == 1) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mine_at[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        for (int c = 0; c < kHalf; c += 16) {
+          float o[16];
+          if (live) {
+            tmem_ld16(my_o + half * kHalf + c, o);
+            tmem_wait_ld();
+            tmem_tie16(o);
           }
-          bar_sync(1, 256);
-          if (slot == 0) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float4 y = mine_at[e];
-              o[4 * e] += y.x, o[4 * e + 1] += y.y, o[4 * e + 2] += y.z, o[4 * e + 3] += y.w;
-            }
+          for (int e = 0; e < 4; ++e) {
+            float4* at4 = place + ((c / 4 + e) ^ (r & (kPieces - 1)));
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (add) y = *at4;
+            if (live) y = make_float4(fmaf(o[4 * e], by, y.x), fmaf(o[4 * e + 1], by, y.y), fmaf(o[4 * e + 2], by, y.z), fmaf(o[4 * e + 3], by, y.w));
+            *at4 = y;
           }
         }
-        if (wide || slot == 0) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mine_at[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          __syncwarp();
-          // four lanes a row, eight rows a step
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int rr = k * 8 + (lane >> 2);
-            float* dst = reinterpret_cast<float*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine ? to : nullptr), rr));
-            if (dst) *reinterpret_cast<float4*>(dst + c + (lane & 3) * 4) = meet[rr * (kMeetLd / 4) + (lane & 3)];
-          }
-          __syncwarp();
+      };
+      auto write = [&](int half, int region) {
+        __syncwarp();
+        const float4* place = reinterpret_cast<const float4*>(sm + region * L::tile_bytes) + (r - lane) * kPieces;
+#pragma unroll 4
+        for (int k = lane; k < 32 * kPieces; k += 32) {
+          const int rr = k / kPieces, piece = k % kPieces, to = __shfl_sync(0xffffffffu, target, rr);
+          if (to >= 0) *reinterpret_cast<float4*>(base + (int64_t)to * D + half * kHalf + piece * 4) = place[rr * kPieces + (piece ^ (rr & (kPieces - 1)))];
         }
-        if (!wide) bar_sync(1, 256);
+        __syncwarp();
+      };
+      if (!wide) {
+        pour(slot ^ 1, slot ^ 1, false);
+        bar_sync(1, 256);
       }
+#pragma unroll 1
+      for (int half = wide ? 0 : slot; half < (wide ? 2 : slot + 1); ++half) {
+        pour(half, slot, !wide);
+        write(half, slot);
+      }
+      if (!wide) bar_sync(1, 256);  // before the next unit's Q
       tc_fence_before();
       if (!whole) {
         if (s.t0 == 0) {
@@ -833,7 +863,7 @@ cudaError_t launch(const PrefixParams& p, const TailParams& tail, Start* starts,
   cudaError_t e = allow_smem<k_prefix<D, T>>(bytes);
   if (e != cudaSuccess) return e;
   if ((e = launch_after(k_prefix<D, T>, dim3(sms), kThreads, bytes, s, p, k, v)) != cudaSuccess) return e;
-  return launch_after(k_prefix_join<D>, dim3(sms, kJoinY + 1), kJoinWarps * 32, 0, s, p, tail, sms * kTailCtas, tail_rows(tail), starts);
+  return launch_after(k_prefix_join<D>, dim3(sms, kJoinY + 1), kJoinWarps * 32, 0, s, p, tail, sms * tail_ctas(tail_rows(tail)), tail_rows(tail), starts);
 }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -861,7 +891,7 @@ size_t lay_out(Scratch& x, int64_t batch, int64_t groups, int64_t total_rows, in
   take(x.gang, 1);
   take(x.first, (size_t)batch);
   take(x.starts, (size_t)sms);
-  take(x.tails, (size_t)sms * kTailCtas);
+  take(x.tails, (size_t)sms * tail_ctas(16));
   take(x.pre_o, rows * D);
   take(x.pre_ml, rows);
   take(x.desc, (size_t)sms);

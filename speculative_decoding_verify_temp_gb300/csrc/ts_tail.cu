@@ -8,7 +8,7 @@
 // These are many short units of few rows: time goes into what a unit has to do one after the other (page
 // numbers, their loads, Q, the window's own tokens, the end), so little of it is repeated. A lane looks
 // up the page and the scales of a tile, for 32 tiles at once; K and V go to shared memory by asynchronous
-// copies, kStages tiles ahead, each of the four warps its own 16 tokens of a tile with no barrier between
+// copies, two or three tiles ahead, each of the four warps its own 16 tokens of a tile with no barrier between
 // warps; rows' addresses are worked out once. (The kernel of window attention, which loads a tile ahead
 // into registers, took 54 us where this takes 38: 128 requests of 376 tokens, 8 heads of 128.)
 //
@@ -31,7 +31,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = kTailTile;
-constexpr int kStages = 4;  // tiles on their way or worked on
 constexpr float kSlack = 15.f, kHead = 7.f;
 
 // 16 bytes to shared memory, or zeros.
@@ -44,11 +43,12 @@ __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_grou
 
 template <int D, int MT>
 struct Shape {
+  static constexpr int stages = MT == 1 && D == 128 ? 3 : 4;  // tiles on their way or worked on
   static constexpr int rows = 16 * MT, ks = D / 16, nt = D / 8, ld = D + 4;
   static constexpr int stage = kWarps * 16 * D * 2;  // bytes: K, then V, of each warp
   static constexpr int off_ring = MT * ks * 512;     // Q's fragments before
   // the warps' outputs lie in the place of the ring, which is empty then
-  static constexpr int ring = kStages * stage > kWarps * rows * ld * 4 ? kStages * stage : kWarps * rows * ld * 4;
+  static constexpr int ring = stages * stage > kWarps * rows * ld * 4 ? stages * stage : kWarps * rows * ld * 4;
   static constexpr int off_own = off_ring + ring;
   static constexpr int off_x = off_own + rows * ld * 4;
 };
@@ -67,9 +67,9 @@ template <int D, int MT>
 constexpr int smem_bytes() { return Shape<D, MT>::off_x + (int)sizeof(Shared<MT>); }
 
 template <int D, int MT, typename T>
-__global__ void __launch_bounds__(kThreads) k_tail(const __grid_constant__ TailParams p) {
+__global__ void __launch_bounds__(kThreads, tail_ctas(16 * MT)) k_tail(const __grid_constant__ TailParams p) {
   using S = Shape<D, MT>;
-  constexpr int ROWS = S::rows, KS = S::ks, NT = S::nt, LD = S::ld, PIECES = D / 16;
+  constexpr int kStages = S::stages, ROWS = S::rows, KS = S::ks, NT = S::nt, LD = S::ld, PIECES = D / 16;
   extern __shared__ __align__(16) unsigned char sm[];
   uint4* s_q = reinterpret_cast<uint4*>(sm);
   float* s_o = reinterpret_cast<float*>(sm + S::off_ring);
@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(kThreads) k_tail(const __grid_constant__ TailP
       x.at[tid] = (int)((s.r.row0 + t) * p.a.heads_q + h);
       x.q[tid] = (s.r.row0 + t) * p.a.q_row_stride + (int64_t)h * p.a.q_head_stride;
     }
+    const bool whole = s.whole(), front = s.r.skip > 0 && s.t0 == 0;  // the first piece takes the prefix in too
     const bool own = p.a.k_new && s.t0 == 0;  // the first piece takes the window in
     if (own && p.a.parents)
       for (int i = tid; i < s.r.rows; i += kThreads) x.parents[i] = p.a.parents[s.r.row0 + i];
@@ -170,6 +171,10 @@ __global__ void __launch_bounds__(kThreads) k_tail(const __grid_constant__ TailP
           frag[2] = f16x2(v.x * inv, v.y * inv);
         }
       }
+    }
+    if (front && tid < s.rows * (D / 32)) {  // the prefix's part on its way to L1
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(p.pre_o + (int64_t)x.at[tid / (D / 32)] * D + tid % (D / 32) * 32));
+      if (tid < s.rows) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.pre_ml + x.at[tid]));
     }
     if (own && p.a.parents)
       for (int i = tid; i < s.r.rows; i += kThreads) x.trees[i] = tree_sees(x.parents, i);
@@ -362,7 +367,6 @@ __global__ void __launch_bounds__(kThreads) k_tail(const __grid_constant__ TailP
                 make_float4(o[mt][j][2 * h + e], o[mt][j + 1][2 * h + e], o[mt][j + 2][2 * h + e], o[mt][j + 3][2 * h + e]);
       }
     __syncthreads();
-    const bool whole = s.whole(), front = s.r.skip > 0 && s.t0 == 0;  // the first piece takes the prefix in too
     float* part = p.part + (int64_t)(2 * blockIdx.x + (s.t0 == 0 ? 1 : 0)) * slot_floats(ROWS, D);
     if (tid < s.rows) {
       const float2 none = make_float2(kNone, 0.f), mine = own ? x.own[tid] : none, pre = front ? p.pre_ml[x.at[tid]] : none;
@@ -391,7 +395,7 @@ __global__ void __launch_bounds__(kThreads) k_tail(const __grid_constant__ TailP
       const int row = i / (D / 4), d = i % (D / 4) * 4;
       const int64_t at = x.at[row];
       float4 pre = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (front) pre = __ldcg(reinterpret_cast<const float4*>(p.pre_o + at * D + d));
+      if (front) pre = *reinterpret_cast<const float4*>(p.pre_o + at * D + d);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       auto add = [&](float by, const float4& v) {
         acc.x = fmaf(by, v.x, acc.x), acc.y = fmaf(by, v.y, acc.y);
@@ -429,10 +433,10 @@ __global__ void __launch_bounds__(128) k_tail_join(const __grid_constant__ TailP
 template <int D, int MT, typename T>
 cudaError_t launch(const TailParams& p, int sms, cudaStream_t s) {
   constexpr int bytes = smem_bytes<D, MT>();
-  static_assert(bytes <= 113 * 1024, "two CTAs an SM");
+  static_assert(bytes <= 227 * 1024 / tail_ctas(16 * MT) - 1024, "CTAs an SM");
   cudaError_t e = allow_smem<k_tail<D, MT, T>>(bytes);
   if (e != cudaSuccess) return e;
-  const int grid = sms * kTailCtas;
+  const int grid = sms * tail_ctas(16 * MT);
   if ((e = launch_after(k_tail<D, MT, T>, dim3(grid), kThreads, bytes, s, p)) != cudaSuccess) return e;
   if ((int64_t)p.c.max_pages * p.c.page_size <= kTile) return cudaSuccess;  // units of one tile are never split
   return launch_after(k_tail_join<D, MT, T>, dim3(grid, 4 * MT), 128, 0, s, p);
@@ -441,7 +445,7 @@ cudaError_t launch(const TailParams& p, int sms, cudaStream_t s) {
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 size_t lay_out(TailParams& p, void* ws, int sms) {
-  const size_t ctas = (size_t)sms * kTailCtas;
+  const size_t ctas = (size_t)sms * tail_ctas(tail_rows(p));
   size_t off = 0;
   auto take = [&](auto*& at, size_t n) {
     at = reinterpret_cast<std::remove_reference_t<decltype(at)>>(static_cast<char*>(ws) + off);

@@ -12,7 +12,8 @@ struct TailParams : WindowParams {
   const Start* starts;   // [CTAs] their shares
 };
 
-constexpr int kTailTile = 64, kTailCtas = 2, kTailLeast = 2;  // tokens of a tile; CTAs an SM; least tiles a CTA takes
+constexpr int kTailTile = 64, kTailLeast = 2;  // tokens of a tile; least tiles a CTA takes
+constexpr int tail_ctas(int rows) { return rows == 16 ? 3 : 2; }  // CTAs an SM: registers, and shared memory
 
 int tail_rows(const WindowParams& p);  // of a block
 size_t tail_workspace(int64_t batch, int64_t total_rows, int heads_q, int heads, int head_dim, int sms);
