@@ -47,7 +47,7 @@ struct PrefixParams {
   float scale_log2;
   const int4* groups;  // {first row, rows, shared tokens, first request with a window}
   const int32_t* gang; // CTAs that share tokens
-  const Start* starts; // [gangs]
+  const Start* starts; // [CTAs]
   float* part;         // [2 * CTAs] pieces of kBlock rows: outputs, references, sums
   int4* desc;          // [CTAs] {tail unit's group, its head, rows, 2 * its block | the CTA's first piece ends its unit}
   float* pre_o;
@@ -135,14 +135,12 @@ __device__ __forceinline__ void set_regs() {
 struct Share {
   Line<kBlock, kTile, PrefixParams> line;
   int gang, rank;
-  __device__ __forceinline__ static bool any(const PrefixParams& p) {
-    const int g = *p.gang;
-    return blockIdx.x / g < gridDim.x / g && p.starts[blockIdx.x / g].b >= 0;
-  }
+  __device__ __forceinline__ static bool any(const PrefixParams& p) { return p.starts[blockIdx.x].b >= 0; }
   __device__ __forceinline__ explicit Share(const PrefixParams& p) {
-    gang = *p.gang;
+    const Start at = p.starts[blockIdx.x];
+    gang = at.gang;
     rank = blockIdx.x % gang;
-    line_at<kBlock, kTile>(p, p.starts[blockIdx.x / gang], line);
+    line_at<kBlock, kTile>(p, at, line);
   }
   __device__ __forceinline__ bool next(const PrefixParams& p, Segment& s) {
     while (line.next(p, s)) {
@@ -206,7 +204,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(const __grid_constant__ P
     *gang = 1 << k;
   }
   __syncthreads();
-  line_starts<kBlock, kTile, kPlanThreads>(p, kMinTiles, ctas / *gang, starts);
+  line_starts<kBlock, kTile, kPlanThreads>(p, kMinTiles, ctas, starts, *gang);
 }
 
 // ---- the shared tokens
@@ -221,51 +219,44 @@ __device__ __forceinline__ void widen(const uint4& w, uint4& lo, uint4& hi) {
 
 // A warp's 32 rows of Q (rows r0 .. r0 + 31 of `left`; the others zeros) as fp16 into their place: rows of 128
 // bytes in atoms of 64 values, the 16-byte pieces of row r at their place XOR r % 8. Returns what a
-// unit of the products of the lane's row stands for. Eight steps of loads are in flight, and the code is kept
-// small: it runs once a unit, from cold instruction caches (unrolled sixteen times it took 14 us).
+// unit of the products of the lane's row stands for. The rows come as they are, all at once, by asynchronous
+// copies, and are scaled in place, in loops of little code: this runs once a unit, from cold instruction
+// caches (steps unrolled sixteen times took 14 us, a load a step 10).
 template <int D, typename T>
 __device__ __forceinline__ float load_q(const PrefixParams& p, const Segment& s, int r0, int left, unsigned char* to) {
-  constexpr int kLanes = D / 8, kEach = 32 / kLanes, N = 32 / kEach, kAhead = 8;  // lanes of a row, rows a step, steps
+  constexpr int kLanes = D / 8, kEach = 32 / kLanes, N = 32 / kEach;  // lanes of a row, rows a step, steps
   const int lane = threadIdx.x & 31, piece = lane % kLanes, sub = lane / kLanes;
-  const int j = s.block * kBlock + r0 + sub;
-  int h = j % p.group;
-  const char* at = static_cast<const char*>(p.a.q) + (s.r.row0 + j / p.group) * p.a.q_row_stride + (int64_t)(s.kvh * p.group + h) * p.a.q_head_stride + piece * 16;
-  const int64_t head = p.a.q_head_stride, row = p.a.q_row_stride - p.group * p.a.q_head_stride;
-  left -= sub;
-  int r = (r0 & (kRows - 1)) + sub;
+  const int j = s.block * kBlock + r0 + min(lane, max(left, 1) - 1), t = j / p.group;  // the lane's row
+  const int64_t mine_at = (s.r.row0 + t) * p.a.q_row_stride + (int64_t)(s.kvh * p.group + j - t * p.group) * p.a.q_head_stride;
+  unsigned char* const at = to + (piece >> 3) * Layout<D>::atom_bytes + (r0 & (kRows - 1)) * 128;
+  auto place = [&](int r) { return at + r * 128 + ((piece & 7) ^ (r & 7)) * 16; };
+#pragma unroll 4
+  for (int r = sub; r < 32; r += kEach)
+    copy16(place(r), static_cast<const char*>(p.a.q) + __shfl_sync(0xffffffffu, mine_at, r) + piece * 16, r < left);
+  copies_commit();
+  copies_wait<0>();  // a lane scales what it has copied itself
   float mine = 0.f;
-#pragma unroll 1
-  for (int i = 0; i < N; i += kAhead) {
-    uint4 w[kAhead];
+#pragma unroll 2
+  for (int r = sub; r < 32; r += kEach) {
+    uint4* const here = reinterpret_cast<uint4*>(place(r));
+    const uint4 w = *here;
+    const uint32_t sign = 0x7FFF7FFFu;
+    const uint32_t m = __vmaxu2(__vmaxu2(w.x & sign, w.y & sign), __vmaxu2(w.z & sign, w.w & sign));
+    uint32_t top = max(m >> 16, m & 0xFFFFu);  // the largest magnitude of the row, as bits
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      w[k] = left > 0 ? __ldg(reinterpret_cast<const uint4*>(at)) : make_uint4(0, 0, 0, 0);
-      left -= kEach;
-      h += kEach;
-      at += kEach * head;
-#pragma unroll 1
-      for (; h >= p.group; h -= p.group) at += row;
+    for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // its exponent field as a float; both factors stay normal
+    const int e = min(max((int)(__float_as_uint(unpack<T>(top).x) >> 23), 15), 254);
+    const float by = __uint_as_float((uint32_t)(268 - e) << 23), back = not_finite<T>(top) ? NAN : __uint_as_float((uint32_t)(e - 14) << 23);
+    const float f = __shfl_sync(0xffffffffu, back, lane % kEach * kLanes);  // to the lane whose row it is
+    if (lane / kEach == r / kEach) mine = f;
+    uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float2 v = unpack<T>(x[c]);
+      x[c] = f16x2(v.x * by, v.y * by);
     }
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k, r += kEach) {  // w has to stay in registers
-      const uint32_t sign = 0x7FFF7FFFu;
-      const uint32_t m = __vmaxu2(__vmaxu2(w[k].x & sign, w[k].y & sign), __vmaxu2(w[k].z & sign, w[k].w & sign));
-      uint32_t top = max(m >> 16, m & 0xFFFFu);  // the largest magnitude of the row, as bits
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // its exponent field as a float; both factors stay normal
-      const int e = min(max((int)(__float_as_uint(unpack<T>(top).x) >> 23), 15), 254);
-      const float by = __uint_as_float((uint32_t)(268 - e) << 23), back = not_finite<T>(top) ? NAN : __uint_as_float((uint32_t)(e - 14) << 23);
-      const float f = __shfl_sync(0xffffffffu, back, lane % kEach * kLanes);  // to the lane whose row it is
-      if (lane / kEach == i + k) mine = f;
-      uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float2 v = unpack<T>(x[c]);
-        x[c] = f16x2(v.x * by, v.y * by);
-      }
-      *reinterpret_cast<uint4*>(to + (piece >> 3) * Layout<D>::atom_bytes + r * 128 + ((piece & 7) ^ (r & 7)) * 16) = make_uint4(x[0], x[1], x[2], x[3]);
-    }
+    *here = make_uint4(x[0], x[1], x[2], x[3]);
   }
   return mine;
 }

@@ -33,14 +33,6 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kTile = kTailTile;
 constexpr float kSlack = 15.f, kHead = 7.f;
 
-// 16 bytes to shared memory, or zeros.
-__device__ __forceinline__ void copy16(void* to, const void* from, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(there ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 template <int D, int MT>
 struct Shape {
   static constexpr int stages = MT == 1 && D == 128 ? 3 : 4;  // tiles on their way or worked on

@@ -16,10 +16,11 @@
 
 namespace tsv {
 
-// A share of a line of tiles: `tiles` of them from tile `in` of request b's on (b < 0: none).
+// A share of a line of tiles: `tiles` of them from tile `in` of request b's on (b < 0: none), of as many
+// CTAs as a gang has.
 struct alignas(16) Start {
   int64_t in, tiles;
-  int32_t b, unused[3];
+  int32_t b, gang, unused[2];
 };
 
 struct WindowParams {
@@ -258,9 +259,10 @@ __device__ __forceinline__ int64_t divide(int64_t n, int64_t d) {
   return ((uint64_t)n | (uint64_t)d) >> 32 ? n / d : (int64_t)((uint32_t)n / (uint32_t)d);
 }
 
-// The same for all shares at once, by one CTA, ahead of the kernel whose CTAs begin at them.
+// The same for all shares at once, by one CTA, ahead of the kernel whose CTAs begin at them. gang: so many
+// CTAs beside each other have the same share (the last ones, if they are no gang, none).
 template <int ROWS, int TILE, int THREADS, typename P>
-__device__ __forceinline__ void line_starts(const P& p, int least_tiles, int ctas, Start* starts) {
+__device__ __forceinline__ void line_starts(const P& p, int least_tiles, int ctas, Start* starts, int gang = 1) {
   __shared__ int64_t s_upto[THREADS];  // tiles up to the end of each thread's run of requests
   __shared__ uint32_t s_units;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -293,11 +295,12 @@ __device__ __forceinline__ void line_starts(const P& p, int least_tiles, int cta
   __syncthreads();
   const int64_t all = s_upto[THREADS - 1];
   const int64_t least = all < (int64_t)least_tiles * s_units ? max(divide(all, max(s_units, 1u)), (int64_t)1) : least_tiles;
-  const int64_t share = max(divide(all + ctas - 1, ctas), least);
+  const int gangs = ctas / gang;
+  const int64_t share = max(divide(all + gangs - 1, gangs), least);
 #pragma unroll 1
   for (int i = tid; i < ctas; i += THREADS) {
-    Start s = {0, 0, -1, {}};
-    const int64_t begin = i * share;
+    Start s = {0, 0, -1, gang, {}};
+    const int64_t begin = i / gang * share;  // past all for CTAs behind the last gang
     if (begin < all) {
       int t = 0;  // the first thread whose run ends behind the beginning
 #pragma unroll 1
@@ -310,7 +313,7 @@ __device__ __forceinline__ void line_starts(const P& p, int least_tiles, int cta
         if (begin < at + w) break;
         at += w;
       }
-      s = {begin - at, min(share, all - begin), (int32_t)b, {}};
+      s = {begin - at, min(share, all - begin), (int32_t)b, gang, {}};
     }
     starts[i] = s;
   }
