@@ -81,15 +81,15 @@ const char* ts_last_error_message(void);
  * come from the cluster-staged kernels, bits 8-15 from the renorm row kernel, bits
  * 16-23 from the staged softmax and bits 24-31 from the chain kernel (bit 24: a stage
  * wait gave up; bit 25: a CTA's wait for its own copies in flight ran out) and window
- * attention (bit 27: a wait gave up; that call's outputs are unspecified). The word is
- * sticky until cleared, but it only reports: a later call is not affected by it.
+ * attention (bit 27, shared attention bit 28: a wait gave up; that call's outputs are
+ * unspecified). The word is sticky until cleared, but it only reports: a later call is not affected by it.
  * Returns TS_ERR_TIMEOUT if a wait gave up, TS_ERR_CUDA if the read failed. A
  * diagnostic, not part of the hot path. */
 ts_status ts_device_error(uint32_t* word_host, int clear);
 
 /* Sets how many SM clock cycles a stage wait of the chain kernel (ts_chain_spec_sampling
- * from logits), or a wait of ts_window_attention with head_dim 128, may take before it gives
- * up; 0 restores the default of 2^32 (about 2 s).
+ * from logits), or a wait of ts_window_attention with head_dim 128 or of ts_shared_attention,
+ * may take before it gives up; 0 restores the default of 2^32 (about 2 s).
  * Process-wide; takes effect for calls enqueued afterwards. A CTA whose wait gives up
  * issues no more copies, waits (on the long budget) for the copies it has in flight,
  * and leaves the requests it had not finished with accept_length = 0; their other
@@ -412,11 +412,11 @@ typedef struct ts_shared_args {
  * whole pages; the rest of a request is read for that request. The pages of the shared tokens
  * must be the same in the tables of all of the group's requests (as ts_kv_fork leaves them): they
  * are taken from the first one with a window. With such tables the result is that of
- * ts_window_attention, to the same accuracy and with the same treatment of rows that see nothing, of values
- * that are not finite and of pages outside the pool; q is good to 2^-31 of the largest |q| of its row
- * and head in its products with shared tokens. Workspace:
- * ts_shared_attention_workspace_size bytes of scratch (no zero fill needed) that no other call uses
- * meanwhile. */
+ * ts_window_attention, to the same accuracy (q is good to 2^-25 of the largest |q| of its row and
+ * head; what the smallest probabilities lose is below 2^-11 of their row's sum up to 2^18 shared tokens a CTA) and
+ * with the same treatment of rows that see nothing, of values that are not finite, of scales of V below
+ * 2^-80 and of pages outside the pool. Workspace: ts_shared_attention_workspace_size bytes of scratch (no
+ * zero fill needed) that no other call uses meanwhile. */
 ts_status ts_shared_attention(const ts_shared_args* args, void* workspace, size_t ws_bytes,
                               cudaStream_t stream);
 size_t ts_shared_attention_workspace_size(int64_t batch, int64_t groups, int64_t total_rows,
@@ -534,9 +534,8 @@ typedef struct ts_kv_reserve_args {
  * instead. Pages are given out in request order, the copy first, the lowest free page (of those
  * free before the call) first, each with a count of 1. A request is served if the pages asked for
  * by it and those before it are there, or if it asks for none and keeps none in that way; one that is not
- * served keeps its row, its pages and its length. Its own requests aside, a copied page is not
- * written. Workspace: ts_kv_pages_workspace_size bytes of scratch (no zero fill needed) that no
- * other call uses meanwhile. */
+ * served keeps its row, its pages and its length. Workspace: ts_kv_pages_workspace_size bytes of
+ * scratch (no zero fill needed) that no other call uses meanwhile. */
 ts_status ts_kv_reserve(const ts_kv_reserve_args* args, void* workspace, size_t ws_bytes,
                         cudaStream_t stream);
 

@@ -28,7 +28,8 @@
 // Groups with many rows: CTAs in gangs of up to 8 take the same share of the tokens at the same time, a
 // block of rows each, so that a tile comes from DRAM once for a gang.
 //
-// Every wait is bounded, as in ts_window_tc.cu.
+// Every wait is bounded, as in ts_window_tc.cu: after one ran out no wait waits and no copy is issued, products
+// run on whatever is there (a test of each wait's outcome before them cost 8 %), and the CTA runs to its end.
 #include <stddef.h>
 #include <stdint.h>
 
@@ -224,7 +225,7 @@ __device__ __forceinline__ void widen(const uint4& w, uint4& lo, uint4& hi) {
 // caches (steps unrolled sixteen times took 14 us, a load a step 10).
 template <int D, typename T>
 __device__ __forceinline__ float load_q(const PrefixParams& p, const Segment& s, int r0, int left, unsigned char* to) {
-  constexpr int kLanes = D / 8, kEach = 32 / kLanes, N = 32 / kEach;  // lanes of a row, rows a step, steps
+  constexpr int kLanes = D / 8, kEach = 32 / kLanes;  // lanes of a row, rows a step
   const int lane = threadIdx.x & 31, piece = lane % kLanes, sub = lane / kLanes;
   const int j = s.block * kBlock + r0 + min(lane, max(left, 1) - 1), t = j / p.group;  // the lane's row
   const int64_t mine_at = (s.r.row0 + t) * p.a.q_row_stride + (int64_t)(s.kvh * p.group + j - t * p.group) * p.a.q_head_stride;

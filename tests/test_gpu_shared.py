@@ -168,6 +168,8 @@ CASES = {
                                          (300, [(0, 2), (1, 1), (77, 5)]), (4000, [(10, 7)])], Hq=8, Hkv=4, page=16, outside=3),
     "a group of five heads": dict(groups=[(333, [(50, 3)] * 7), (900, [(1, 1)] * 3)], Hq=15, Hkv=3, page=32, outside=1),
     "long": dict(groups=[(20000, [(100, 2)] * 9)], Hq=8, Hkv=1, page=64),
+    "blocks for eight CTAs side by side": dict(groups=[(1000, [(3, 16)] * 32)], Hq=16, Hkv=4, page=64),
+    "blocks for two": dict(groups=[(700, [(1, 20)] * 32), (300, [(2, 9)] * 30)], Hq=4, Hkv=1, page=16),
     "many units a CTA": dict(groups=[(200 + 16 * i, [(20, 1)] * (1 + i % 4)) for i in range(60)], Hq=16, Hkv=8, page=16),
 }
 
@@ -440,3 +442,76 @@ def test_answers_to_one_prompt(tv, D):
             assert torch.equal(count > 0, torch.arange(pages, device="cuda") < (count > 0).sum())
     tv.kv_free(**cache, refcount=count)
     assert (count == 0).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_requests_and_groups(tv, D):
+    # more groups and requests than the planning CTAs have threads; group sizes from none to nine
+    r = np.random.default_rng(17)
+    groups = [(int(r.integers(0, 90)), [(int(r.integers(0, 40)), int(r.integers(0, 3))) for _ in range(i % 10)]) for i in range(1500)]
+    c = case(17, groups, 2, 1, D, 16)
+    check(c, tv.shared_attention(**c, lse=True))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_what_is_left_may_be_long(tv, D, dtype):
+    # more tiles of its own than a round of page numbers, split over CTAs; short windows and long ones
+    for members in ([(5000, 1), (3, 2)], [(4100, 9)] * 3, [(2100, 40), (64, 5)]):
+        c = case(18, [(200, members)], 8, 2, D, 32, dtype=dtype, mask="tree")
+        check(c, tv.shared_attention(**c, lse=True))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_wait_that_runs_out(tv, D):
+    """With a budget of one cycle waits give up before their copies land: nothing faults or hangs, the
+    call's outputs are unspecified, ts_device_error reports it (bit 28), and the next call is not affected.
+    A wait's first tries take some time of their own: with head_dim 64 every wait may end within it."""
+    c = case(19, [(3000, [(20, 4)] * 50), (1700, [(20, 9)] * 30)], 64, 8, D, 16)
+    want = tv.shared_attention(**c, lse=True)
+    assert tv.device_error() == 0
+    guard = torch.full((c["q"].shape[0] + 2, 64, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    word = 0
+    for _ in range(10):
+        tv.set_wait_cycles(1)
+        try:
+            tv.shared_attention(**c, out=guard[1:-1])
+            torch.cuda.synchronize()
+        finally:
+            tv.set_wait_cycles(0)
+        word |= tv.device_error(clear=True)
+    assert word == 1 << 28 or (D == 64 and word == 0), hex(word)
+    assert (guard[0] == 7.0).all() and (guard[-1] == 7.0).all()
+    got = tv.shared_attention(**c, lse=True)
+    assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
+    assert tv.device_error() == 0
+
+
+def test_rows_that_no_window_owns_and_strided_rows(tv):
+    c = case(20, [(300, [(5, 2), (7, 3)]), (100, [(9, 4)])], 8, 2, 128, 16)
+    ref = reference(c)
+    big = {k: torch.full((12, 2 * c[k].shape[1], 256), 3.0, dtype=torch.bfloat16, device="cuda") for k in ("q", "k_new", "v_new")}
+    x = dict(c)
+    for k in big:
+        big[k][1:10, ::2, 64:192] = c[k]
+        x[k] = big[k][1:11, ::2, 64:192]            # a row behind the last window
+    out = torch.full((10, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    tv.shared_attention(**x, out=out)
+    check(c, dict(out=out[:9], lse=None), ref)
+    assert (out[9] == 7.0).all()
+    # one row of q for all (stride 0)
+    one = dict(c, q=c["q"][:1].expand(9, -1, -1))
+    check(dict(c, q=one["q"].contiguous()), tv.shared_attention(**one, lse=True))
+
+
+def test_two_streams_at_once(tv):
+    a = case(21, [(3000, [(40, 2)] * 20)], 16, 4, 128, 16)
+    b = case(22, [(900, [(10, 5)] * 50)], 8, 2, 64, 32, dtype=torch.float16)
+    want = [tv.shared_attention(**x, lse=True) for x in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[tv.shared_attention(**x, lse=True, stream=s) for x, s in zip((a, b), streams)] for _ in range(10)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for x, y in zip(pair, want):
+            assert torch.equal(x["out"], y["out"]) and torch.equal(x["lse"], y["lse"])
