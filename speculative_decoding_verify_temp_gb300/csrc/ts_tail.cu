@@ -9,8 +9,8 @@
 // numbers, their loads, Q, the window's own tokens, the end), so little of it is repeated. A lane looks
 // up the page and the scales of a tile, for 32 tiles at once; K and V go to shared memory by asynchronous
 // copies, two or three tiles ahead, each of the four warps its own 16 tokens of a tile with no barrier between
-// warps; rows' addresses are worked out once. Measured, 128 requests of 376 tokens and one row of 4 heads a KV
-// head, 8 KV heads of 128: 40 us (96 MB: 2.4 TB/s; window attention's kernel 81, a tile ahead in registers 54);
+// warps; rows' addresses are worked out once. Measured, 100 requests of 382 tokens and one row of 4 heads a KV
+// head, 8 KV heads of 128: 40 us (78 MB: 1.9 TB/s; window attention's kernel 81, a tile ahead in registers 54);
 // 32 requests of 530 tokens and 64 rows: 64 us (81, 98). With 16 rows a block three CTAs an SM (two: 50 us).
 //
 // Products run on mma.m16n8k16 with fp16 operands, the precision is that of ts_window.cu: codes are exact in
