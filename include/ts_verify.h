@@ -486,8 +486,8 @@ ts_status ts_kv_read(const ts_kv_read_args* args, cudaStream_t stream);
  *
  * Results do not depend on timing: pages are given out by number, lowest first. refcount_out may
  * be refcount (in place) or an array apart from it; table_out may be the cache's page_table, with
- * its ld (in place; not for ts_kv_fork), or apart from it. Arrays that overlap otherwise give
- * TS_ERR_INVALID_ARG. Nothing else may use the pool's tables, counts or pages meanwhile. */
+ * its ld (in place; not for ts_kv_fork), or apart from it. int32 arrays and workspaces that
+ * overlap otherwise, where one of them is written, give TS_ERR_INVALID_ARG. Nothing else may use the pool's tables, counts or pages meanwhile. */
 typedef struct ts_kv_fork_args {
   const ts_kv_cache* cache;  /* host struct: the sources */
   const int32_t* sources;    /* [n]: request i of the result continues request sources[i];

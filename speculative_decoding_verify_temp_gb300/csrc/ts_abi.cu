@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <initializer_list>
 
 #include <cuda_runtime.h>
 
@@ -142,6 +143,29 @@ bool overlap(const void* a, int64_t bytes_a, const void* b, int64_t bytes_b, boo
   return x < y + (uintptr_t)bytes_b && y < x + (uintptr_t)bytes_a;
 }
 
+struct Span {
+  const void* at;
+  int64_t bytes;
+};
+
+// What a call on a pool writes: apart from each other and from what it reads. An array that is
+// updated in place is only among the first.
+ts_status check_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    bool clash = false;
+    for (const Span* x = o + 1; x != outs.end(); ++x) clash |= overlap(o->at, o->bytes, x->at, x->bytes, false);
+    for (const Span& x : ins) clash |= overlap(o->at, o->bytes, x.at, x.bytes, false);
+    if (clash) return fail(TS_ERR_INVALID_ARG, "the arrays that a call writes must be apart from each other and from those it reads");
+  }
+  return TS_OK;
+}
+
+Span table_span(const ts_kv_cache& c, const int32_t* t, int64_t ld, int64_t rows) {
+  return {t, c.max_pages ? ((rows - 1) * ld + c.max_pages) * 4 : 0};
+}
+// An input, of no bytes where it is updated in place.
+Span unless_same(const Span& in, const void* out) { return {in.at, in.at == out ? 0 : in.bytes}; }
+
 // refcount and refcount_out of a call on a pool.
 ts_status check_counts(const ts_kv_cache& c, const int32_t* in, int32_t* out) {
   if (c.num_pages > 0 && (!in || !out)) return fail(TS_ERR_INVALID_ARG, "refcount and refcount_out are required");
@@ -154,8 +178,8 @@ ts_status check_counts(const ts_kv_cache& c, const int32_t* in, int32_t* out) {
 ts_status check_table(const ts_kv_cache& c, const int32_t* out, int64_t ld, int64_t rows, bool in_place) {
   if (c.max_pages > 0 && !out) return fail(TS_ERR_INVALID_ARG, "table_out is required");
   if (ld < c.max_pages || ld > (int64_t)1 << 40) return fail(TS_ERR_INVALID_ARG, "ld_out must be >= max_pages");
-  auto bytes = [&](int64_t r, int64_t l) { return c.max_pages ? ((r - 1) * l + c.max_pages) * 4 : 0; };
-  if (overlap(out, bytes(rows, ld), c.page_table, bytes(c.batch, c.ld_table), in_place && (ld == c.ld_table || c.batch == 1)))
+  const Span to = table_span(c, out, ld, rows), from = table_span(c, c.page_table, c.ld_table, c.batch);
+  if (overlap(to.at, to.bytes, from.at, from.bytes, in_place && (ld == c.ld_table || c.batch == 1)))
     return fail(TS_ERR_INVALID_ARG, "table_out must be %sapart from page_table", in_place ? "page_table, with its ld, or " : "");
   return TS_OK;
 }
@@ -800,6 +824,11 @@ ts_status ts_kv_fork(const ts_kv_fork_args* p, cudaStream_t stream) {
   if ((st = check_table(c, p->table_out, p->ld_out, p->n, false)) != TS_OK) return st;
   if (overlap(p->lens_out, p->n * 4, c.seq_lens, c.batch * 4, false) || overlap(p->lens_out, p->n * 4, p->sources, p->n * 4, false))
     return fail(TS_ERR_INVALID_ARG, "lens_out must be apart from seq_lens and sources");
+  const int64_t counts = c.num_pages * 4;
+  if ((st = check_apart({{p->refcount_out, counts}, table_span(c, p->table_out, p->ld_out, p->n), {p->lens_out, p->n * 4}},
+                        {unless_same({p->refcount, counts}, p->refcount_out), table_span(c, c.page_table, c.ld_table, c.batch),
+                         {c.seq_lens, c.batch * 4}, {p->sources, p->n * 4}})) != TS_OK)
+    return st;
   return launched(tsv::launch_kv_fork(c, *p, sm_count(), stream), "fork launch");
 }
 
@@ -807,8 +836,12 @@ ts_status ts_kv_free(const ts_kv_free_args* p, cudaStream_t stream) {
   if (!p) return fail(TS_ERR_INVALID_ARG, "args is NULL");
   ts_status st;
   if ((st = check_cache(p->cache)) != TS_OK) return st;
-  if ((st = check_counts(*p->cache, p->refcount, p->refcount_out)) != TS_OK) return st;
-  return launched(tsv::launch_kv_free(*p->cache, *p, sm_count(), stream), "free launch");
+  const ts_kv_cache& c = *p->cache;
+  if ((st = check_counts(c, p->refcount, p->refcount_out)) != TS_OK) return st;
+  if ((st = check_apart({{p->refcount_out, c.num_pages * 4}},
+                        {table_span(c, c.page_table, c.ld_table, c.batch), {c.seq_lens, c.batch * 4}, {p->release, p->release ? c.batch * 4 : 0}})) != TS_OK)
+    return st;
+  return launched(tsv::launch_kv_free(c, *p, sm_count(), stream), "free launch");
 }
 
 ts_status ts_kv_reserve(const ts_kv_reserve_args* p, void* workspace, size_t ws_bytes, cudaStream_t stream) {
@@ -823,6 +856,13 @@ ts_status ts_kv_reserve(const ts_kv_reserve_args* p, void* workspace, size_t ws_
       overlap(p->reserved, c.batch * 4, p->new_lens, c.batch * 4, false))
     return fail(TS_ERR_INVALID_ARG, "reserved must be apart from seq_lens and new_lens");
   if ((st = check_pages_workspace(c, workspace, ws_bytes)) != TS_OK) return st;
+  const int64_t counts = c.num_pages * 4;
+  if ((st = check_apart({{p->refcount_out, counts}, table_span(c, p->table_out, p->ld_out, c.batch), {p->reserved, c.batch * 4},
+                         {workspace, (int64_t)tsv::pages_workspace(c.batch, c.num_pages)}},
+                        {unless_same({p->refcount, counts}, p->refcount_out),
+                         unless_same(table_span(c, c.page_table, c.ld_table, c.batch), p->table_out), {c.seq_lens, c.batch * 4},
+                         {p->new_lens, c.batch * 4}})) != TS_OK)
+    return st;
   return launched(tsv::launch_kv_reserve(c, *p, workspace, stream), "reserve launch");
 }
 
@@ -835,6 +875,12 @@ ts_status ts_kv_compact(const ts_kv_compact_args* p, void* workspace, size_t ws_
   if ((st = check_counts(c, p->refcount, p->refcount_out)) != TS_OK) return st;
   if ((st = check_table(c, p->table_out, p->ld_out, c.batch, true)) != TS_OK) return st;
   if ((st = check_pages_workspace(c, workspace, ws_bytes)) != TS_OK) return st;
+  const int64_t counts = c.num_pages * 4;
+  if ((st = check_apart({{p->refcount_out, counts}, table_span(c, p->table_out, p->ld_out, c.batch), {p->live, 4},
+                         {workspace, (int64_t)tsv::pages_workspace(c.batch, c.num_pages)}},
+                        {unless_same({p->refcount, counts}, p->refcount_out),
+                         unless_same(table_span(c, c.page_table, c.ld_table, c.batch), p->table_out), {c.seq_lens, c.batch * 4}})) != TS_OK)
+    return st;
   return launched(tsv::launch_kv_compact(c, *p, workspace, sm_count(), stream), "compact launch");
 }
 

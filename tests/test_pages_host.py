@@ -78,6 +78,24 @@ def test_the_rest(lib):  # noqa: F811
         assert getattr(lib, call)(None, *more, None) == 1
 
 
+WS = FAKE << 20  # far from the rest
+
+
+@pytest.mark.parametrize("call,kw", [
+    ("ts_kv_fork", dict(lens_out=C + 44)), ("ts_kv_fork", dict(lens_out=B + 8)),          # 3 rows of 4 entries at C
+    ("ts_kv_fork", dict(table_out=B)), ("ts_kv_fork", dict(table_out=A + 8)),
+    ("ts_kv_fork", dict(refcount=B, refcount_out=FAKE)), ("ts_kv_fork", dict(refcount=B, refcount_out=C, table_out=B)),
+    ("ts_kv_free", dict(refcount_out=A + 4)), ("ts_kv_free", dict(refcount_out=FAKE)),
+    ("ts_kv_reserve", dict(reserved=C + 28)), ("ts_kv_reserve", dict(reserved=B + 36)),
+    ("ts_kv_reserve", dict(table_out=A)), ("ts_kv_reserve", dict(refcount=C, refcount_out=B)),
+    ("ts_kv_reserve", dict(refcount=WS, refcount_out=WS)), ("ts_kv_reserve", dict(new_lens=WS + 64)),
+    ("ts_kv_compact", dict(live=B)), ("ts_kv_compact", dict(live=C + 28)), ("ts_kv_compact", dict(live=FAKE + 4)),
+    ("ts_kv_compact", dict(live=WS)), ("ts_kv_compact", dict(table_out=B + 36)),
+])
+def test_arrays_that_overlap(lib, call, kw):  # noqa: F811
+    refused(lib, call, args(call, **kw), "apart", ws=WS)
+
+
 def test_workspace(lib):  # noqa: F811
     size = lib.ts_kv_pages_workspace_size
     assert 0 < size(1, 0) <= size(1, 10) < size(1, 10 ** 6) < size(1, 2 ** 31 - 1)
