@@ -710,13 +710,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
         if (whole) p.pre_ml[at] = make_float2(m, l);
         else part[kBlock * D + row] = m, part[kBlock * D + kBlock + row] = l;
       }
-      // Outputs pass through the place of Q, half of the columns at a time, so that rows are written in runs: 16
-      // bytes at their place XOR the row. Where the slots meet, each hands the other one half and adds that up.
+      // Outputs pass through the place of Q, half of the columns at a time, so that rows are written in runs. A
+      // row's 16-byte pieces lie where its Q lies, at their place XOR the row: a warp that is done loads the next
+      // unit's Q over its own rows' alone, while its neighbours still write. Where the slots meet, each hands the
+      // other one half and adds that up.
       constexpr int kHalf = D / 2, kPieces = kHalf / 4;
       const int target = mine && (wide || row < s.rows) ? (whole ? (int)at : row) : -1;
       float* const base = whole ? p.pre_o : part;
+      static_assert(kPieces <= 8 * L::atoms, "a row's pieces where its Q is");
+      auto piece_of = [&](int region, int rr, int piece) {
+        return reinterpret_cast<float4*>(sm + region * L::tile_bytes + (piece >> 3) * L::atom_bytes + rr * 128) + ((piece ^ rr) & 7);
+      };
       auto pour = [&](int half, int region, bool add) {
-        float4* place = reinterpret_cast<float4*>(sm + region * L::tile_bytes) + r * kPieces;
 #pragma unroll 1
         for (int c = 0; c < kHalf; c += 16) {
           float o[16];
@@ -727,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float4* at4 = place + ((c / 4 + e) ^ (r & (kPieces - 1)));
+            float4* at4 = piece_of(region, r, c / 4 + e);
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
             if (add) y = *at4;
             if (live) y = make_float4(fmaf(o[4 * e], by, y.x), fmaf(o[4 * e + 1], by, y.y), fmaf(o[4 * e + 2], by, y.z), fmaf(o[4 * e + 3], by, y.w));
@@ -737,11 +742,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
       };
       auto write = [&](int half, int region) {
         __syncwarp();
-        const float4* place = reinterpret_cast<const float4*>(sm + region * L::tile_bytes) + (r - lane) * kPieces;
 #pragma unroll 4
         for (int k = lane; k < 32 * kPieces; k += 32) {
           const int rr = k / kPieces, piece = k % kPieces, to = __shfl_sync(0xffffffffu, target, rr);
-          if (to >= 0) *reinterpret_cast<float4*>(base + (int64_t)to * D + half * kHalf + piece * 4) = place[rr * kPieces + (piece ^ (rr & (kPieces - 1)))];
+          if (to >= 0) *reinterpret_cast<float4*>(base + (int64_t)to * D + half * kHalf + piece * 4) = *piece_of(region, r - lane + rr, piece);
         }
         __syncwarp();
       };
