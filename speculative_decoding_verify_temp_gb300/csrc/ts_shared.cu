@@ -84,6 +84,9 @@ constexpr int kThreads = 256 + kConvert * 32 + 128;
 constexpr int kSoftmaxRegs = 184, kConvertRegs = 80, kIssueRegs = 64;
 static_assert(256 * kSoftmaxRegs + kConvert * 32 * kConvertRegs + 128 * kIssueRegs <= kThreads * 128, "registers");
 constexpr int kMeta = 8;     // tiles whose scales are in shared memory
+// Barriers of K's and V's arrival, in turn: an even number, so that each is K's or V's alone. Who waits for it
+// then sees all of its phases; one that saw every second would take the one before last for the last.
+constexpr int kArrive = 6;
 constexpr float kHead = 4.f;         // a reference is set this far, in log2, below the largest score
 constexpr float kMostSum = 65504.f;  // of a tile's probabilities, where the reference stays: none is past fp16
 constexpr float kMostRef = 65536.f;  // references of at most this size: scores and reference in one operation
@@ -97,6 +100,7 @@ struct Layout {
   static constexpr int k_stages = D == 128 ? 2 : 4;  // tiles of K in fp16
   static constexpr int v_halves = D == 128 ? 3 : 8;  // halves of tiles of V
   static constexpr int units = D == 128 ? 3 : 6;     // tiles of K or V as they come: K, V, K, ...
+  static_assert(kArrive % 2 == 0 && kArrive % units == 0, "a unit's barrier is free when its place is");
   static constexpr int atoms = D / 64;               // of 64 values (128 bytes) a row
   static constexpr int atom_bytes = kTile * 128;     // of Q and K; of a half of V half as many
   static constexpr int tile_bytes = atoms * atom_bytes;
@@ -112,7 +116,7 @@ static_assert(2 * kRows * 8 <= 2 * Layout<64>::tile_bytes && kRows * 64 * 2 == L
               "Q's place: where the slots meet");
 
 struct Shared {
-  uint64_t k_full[4], k_empty[4], v_full[8], v_empty[8], raw_full[6], raw_empty[6], meta_full[kMeta];
+  uint64_t k_full[4], k_empty[4], v_full[8], v_empty[8], raw_full[kArrive], raw_empty[6], meta_full[kMeta];
   uint64_t s_full[2], p_full[2], o_done[2], q_full, q_empty;
   alignas(16) float4 meta[kMeta][8];  // of 16 tokens: K's scale, log2 of V's, 1 / V's, 2 (0: not there; 1: others of the tile are not)
   uint32_t tmem;
@@ -288,10 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
       mbar_init(&x.v_full[i], kConvert / 2);
       mbar_init(&x.v_empty[i], 1);
     }
-    for (int i = 0; i < L::units; ++i) {
-      mbar_init(&x.raw_full[i], 1);
-      mbar_init(&x.raw_empty[i], kConvert / 2);
-    }
+    for (int i = 0; i < kArrive; ++i) mbar_init(&x.raw_full[i], 1);
+    for (int i = 0; i < L::units; ++i) mbar_init(&x.raw_empty[i], kConvert / 2);
     for (int i = 0; i < kMeta; ++i) mbar_init(&x.meta_full[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&x.s_full[i], 1);
@@ -442,11 +444,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
           const uint32_t n = 2 * i + v, st = n % L::units;
           wait(&x.raw_empty[st], (n / L::units & 1) ^ 1, &x.stop);
           if (!__any_sync(0xffffffffu, stopped(&x.stop))) {  // one answer a warp: its lanes meet inside
-            if (lane == 0) mbar_arrive_expect_tx(&x.raw_full[st], L::unit_bytes);
+            if (lane == 0) mbar_arrive_expect_tx(&x.raw_full[n % kArrive], L::unit_bytes);
             __syncwarp();
             if (lane < per_tile)
               tma_load_4d(sm + L::off_raw + st * L::unit_bytes + lane * page_bytes, v ? &v_map : &k_map, 0, 0, now.kvh,
-                          now.page >= 0 ? now.page : outside, &x.raw_full[st]);
+                          now.page >= 0 ? now.page : outside, &x.raw_full[n % kArrive]);
           }
         }
         // the scales' place was last read kMeta tiles ago: the products of later tiles have been issued since
@@ -511,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
       for (int j = s.t0; j < s.t1; ++j, ++i) {
         const uint32_t n = 2 * i + (is_v ? 1 : 0), st = n % L::units;
         const unsigned char* raw = sm + L::off_raw + st * L::unit_bytes;
-        wait(&x.raw_full[st], n / L::units & 1, &x.stop);
+        wait(&x.raw_full[n % kArrive], n / kArrive & 1, &x.stop);
         if (!is_v) {
           const uint32_t k = i % L::k_stages;
           wait(&x.k_empty[k], (i / L::k_stages & 1) ^ 1, &x.stop);

@@ -406,6 +406,34 @@ def test_runs_agree_bit_for_bit(tv):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows,page", [((20,), 128), ((5, 19, 36, 8, 23), 16), ((37,), 64)])
+def test_units_that_follow_each_other(tv, D, rows, page):
+    # several short units a CTA, of 7 x rows rows: warps without rows in the second slot, whole slots, one slot;
+    # a warp that is done with a unit early must not disturb its neighbours, which still write their outputs
+    groups = [(128 + 128 * (i % 5) + page * (i % 3), [(5, rows[i % len(rows)])]) for i in range(120)]
+    c = case(21, groups, 28, 4, D, page)
+    a = tv.shared_attention(**c, lse=True)
+    check(c, a)
+    cold = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")  # more than L2
+    for i in range(100):
+        if i % 4 == 0:
+            cold.fill_(i)
+        b = tv.shared_attention(**c, lse=True)
+        assert torch.equal(a["out"], b["out"]) and torch.equal(a["lse"], b["lse"])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_units_with_pages_of_a_tile(tv, D):
+    # one copy a tile of K or V: these land in any order, and none may be taken for the one before it
+    c = case(22, [(9163, [(5, 10)] * 2), (5826, [(4, 10)] * 2), (30000, [(1, 10)] * 2), (8316, [(5, 3)] * 2)], 28, 4, D, 128)
+    a = tv.shared_attention(**c, lse=True)
+    check(c, a)
+    for _ in range(100):
+        b = tv.shared_attention(**c, lse=True)
+        assert torch.equal(a["out"], b["out"]) and torch.equal(a["lse"], b["lse"])
+
+
+@pytest.mark.parametrize("D", [64, 128])
 def test_answers_to_one_prompt(tv, D):
     """The calls together: a prompt is appended, forked into answers that grow by windows of drafted
     rows of which some are kept; each step's attention is that of window attention."""
