@@ -28,6 +28,10 @@
 // Groups with many rows: CTAs in gangs of up to 8 take the same share of the tokens at the same time, a
 // block of rows each, so that a tile comes from DRAM once for a gang.
 //
+// Measured, 32 windows of 8 rows, 64 query and 8 KV heads of 128, 131071 shared tokens: 842 us, 1305 TFLOP/s,
+// 0.68 of the measured bf16 peak. Bound: a slot's softmax takes 2300 clocks a tile (TMEM loads, 32 exponentials a
+// clock and SM), the products of both slots 2054, and what is left of either is not hidden behind the other.
+//
 // Every wait is bounded, as in ts_window_tc.cu: after one ran out no wait waits and no copy is issued, products
 // run on whatever is there (a test of each wait's outcome before them cost 8 %), and the CTA runs to its end.
 #include <stddef.h>
