@@ -413,7 +413,7 @@ typedef struct ts_shared_args {
  * must be the same in the tables of all of the group's requests (as ts_kv_fork leaves them): they
  * are taken from the first one with a window. With such tables the result is that of
  * ts_window_attention, to the same accuracy (q is good to 2^-25 of the largest |q| of its row and
- * head; what the smallest probabilities lose is below 2^-11 of their row's sum up to 2^18 shared tokens a CTA) and
+ * head; what the smallest probabilities lose is below 2^-11 of their row's sum up to 2^28 shared tokens) and
  * with the same treatment of rows that see nothing, of values that are not finite, of scales of V below
  * 2^-80 and of pages outside the pool. Workspace: ts_shared_attention_workspace_size bytes of scratch (no
  * zero fill needed) that no other call uses meanwhile. */

@@ -15,9 +15,12 @@
 // with S, P and O in TMEM. K and V codes become fp16 (exact) on their way into shared memory,
 // once for the two blocks of 128 rows that a CTA works on; Q is fp16 with a factor a row: a power
 // of two that puts the row's largest magnitude into [2^14, 2^15), so that bf16 values are exact down to
-// 2^-31 of it. P = 2^(x - m) is rounded to fp16 (2^-11), m a reference of the row that is set 2^4 below a
-// score and follows when a tile's sum is past fp16's range: the small ones lose at most 2^-25 each, 2^-11
-// of the row's sum in 2^18 tokens of a CTA. V's scale is in the exponent.
+// 2^-31 of it. P = 2^(x - m) is rounded to fp16 (2^-11), m a reference of the row that is set 2^h below a
+// score and follows when a tile's sum is past fp16's range. V's scale is in the exponent. The small ones lose at
+// most 2^-25 each; h goes by the tokens N of the CTA's share of the unit, log2 N - 13 and 4 at least, so that
+// this is below 2^-12 of the row's sum however many small ones follow a large one (with h = 4 for all, a
+// million of 2^-29 behind one lost 2^-9). At 14 fp16 ends it: 2^-11 in 2^28 tokens. (References that are lowered again
+// where only small ones follow need no such end, but took 961 us in the case below.)
 //
 // Two slots, each 128 rows and 128 threads, a thread a row (no reduction crosses threads): while one
 // slot's scores are made into P, the tensor cores work on the other's products. More than 128 rows
@@ -91,7 +94,7 @@ constexpr int kMeta = 8;     // tiles whose scales are in shared memory
 // Barriers of K's and V's arrival, in turn: an even number, so that each is K's or V's alone. Who waits for it
 // then sees all of its phases; one that saw every second would take the one before last for the last.
 constexpr int kArrive = 6;
-constexpr float kHead = 4.f;         // a reference is set this far, in log2, below the largest score
+constexpr float kLeastHead = 4.f, kMostHead = 14.f;  // how far, in log2, a reference is set below the largest score
 constexpr float kMostSum = 65504.f;  // of a tile's probabilities, where the reference stays: none is past fp16
 constexpr float kMostRef = 65536.f;  // references of at most this size: scores and reference in one operation
 constexpr int kMinTiles = 1;
@@ -606,7 +609,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
                 for (int e = 0; e < 16; ++e) z[e & 3] = e < 4 ? fmaf(y[e], a, g.y) : fmaxf(z[e & 3], fmaf(y[e], a, g.y));
                 top = fmaxf(top, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])));
               }
-              const float to = may && top > m + (kHead + 1.f) ? top - kHead : m, by = ex2(m - to);
+              const float head = fminf(fmaxf((float)(26 - __clz(n)), kLeastHead), kMostHead);  // of 128 n tokens
+              const float to = may && top > m + (head + 1.f) ? top - head : m, by = ex2(m - to);
               const bool moves = to != m;
               m = to;
               if (__any_sync(0xffffffffu, moves) && nth > 0) {

@@ -15,8 +15,9 @@
 //
 // Products run on mma.m16n8k16 with fp16 operands, the precision is that of ts_window.cu: codes are exact in
 // fp16, Q rows are scaled by a power of two to below 2, probabilities are rounded to fp16 relative to a
-// reference that is set 2^7 below the largest score and follows when that is 2^15 above it; V's scale
-// is in the exponent.
+// reference that is set 2^h below the largest score and follows when that is 2^15 above it; V's scale
+// is in the exponent. The small ones lose at most 2^-25 each; h goes by the tokens N of a warp, log2 N - 14 and 7
+// at least, so that this is below 2^-11 of the row's sum (of 2^30 tokens a warp has 2^28).
 #include <stdint.h>
 
 #include <algorithm>
@@ -32,7 +33,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = kTailTile;
-constexpr float kSlack = 15.f, kHead = 7.f;
+constexpr float kSlack = 15.f, kLeastHead = 7.f;
 
 template <int D, int MT>
 struct Shape {
@@ -271,12 +272,13 @@ __global__ void __launch_bounds__(kThreads, tail_ctas(16 * MT)) k_tail(const __g
             move |= z > m[mt][h] + kSlack;
           }
         if (__any_sync(0xffffffffu, move)) {
+          const float head = fmaxf((float)(22 - __clz(s.t1 - s.t0)), kLeastHead);  // of 16 tokens a tile
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               // only where needed: a row's result must not depend on its neighbours'
-              const float to = top[mt][h] > m[mt][h] + kSlack ? top[mt][h] - kHead : m[mt][h];
+              const float to = top[mt][h] > m[mt][h] + kSlack ? top[mt][h] - head : m[mt][h];
               const float by = ex2(m[mt][h] - to);
               m[mt][h] = to;
               l[mt][h] *= by;
