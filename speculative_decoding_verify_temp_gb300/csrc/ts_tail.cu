@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, tail_ctas(16 * MT)) k_tail(const __g
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) add(x.w[w][row], *reinterpret_cast<const float4*>(s_o + (w * ROWS + row) * LD + d));
       if (own) add(x.w[kWarps][row], *reinterpret_cast<const float4*>(s_own + row * LD + d));
-      if (front && x.w[kWarps + 1][row] != 0.f) add(x.w[kWarps + 1][row], pre);
+      if (front) add(x.w[kWarps + 1][row], pre);  // 0 times NaN is NaN
       if (whole)
         *reinterpret_cast<uint2*>(static_cast<char*>(p.a.out) + (at * D + d) * 2) = make_uint2(pack<T>(acc.x, acc.y), pack<T>(acc.z, acc.w));
       else
