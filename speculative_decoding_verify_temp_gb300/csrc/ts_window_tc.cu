@@ -475,7 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // score is too far above its reference, then, from TMEM again, P.
         const bool all_valid = __all_sync(0xffffffffu, valid);
         const f32x2 ks2 = pair(ks, ks), lv2 = pair(lv, lv);
-        // scores less references of rows c .. c + 15
+        // scores less references of rows c .. c + 15: a score is rounded before its reference is subtracted, as the
+        // reference was (in one operation what that rounding dropped would stay, 2^83 where scores are near 2^107)
         auto scores = [&](int c, float* y) {
           tmem_ld16(my_s + c, y);
           tmem_wait_ld();
@@ -484,8 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int r = 0; r < 16; r += 4) {
             const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(&x.neg_m[group][c + r]);
             const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&x.fac[group][c + r]);
-            const float2 a = unpair(fma2(pair(y[r], y[r + 1]), mul2(ks2, f.x), add2(lv2, m.x)));
-            const float2 b = unpair(fma2(pair(y[r + 2], y[r + 3]), mul2(ks2, f.y), add2(lv2, m.y)));
+            const float2 a = unpair(add2(fma2(pair(y[r], y[r + 1]), mul2(ks2, f.x), lv2), m.x));
+            const float2 b = unpair(add2(fma2(pair(y[r + 2], y[r + 3]), mul2(ks2, f.y), lv2), m.y));
             y[r] = a.x, y[r + 1] = a.y, y[r + 2] = b.x, y[r + 3] = b.y;
           }
           if (!all_valid) {
