@@ -484,6 +484,14 @@ ts_status ts_kv_read(const ts_kv_read_args* args, cudaStream_t stream);
  *   ts_kv_free      requests end
  *   ts_kv_compact   the live pages move to the lowest ids, so that the pool can shrink
  *
+ * A step may append less than it reserved room for (drafts that are not accepted). The pages behind
+ * the first ceil(seq_len[b] / page_size) entries are then still the request's: held_lens[b], the largest
+ * `reserved` it was given, says so, and its entries are the first
+ * ceil(max(seq_len[b], held_lens[b]) / page_size) (taken as clamped to [seq_len, max_pages * page_size]).
+ * ts_kv_reserve goes on from them, ts_kv_free releases and ts_kv_compact moves them. Without held_lens
+ * (NULL) such pages are lost to the pool: their entries are overwritten, their counts stay. Pages behind seq_len
+ * must have one holder, as they have where tables come from these calls.
+ *
  * Results do not depend on timing: pages are given out by number, lowest first. refcount_out may
  * be refcount (in place) or an array apart from it; table_out may be the cache's page_table, with
  * its ld (in place; not for ts_kv_fork), or apart from it. int32 arrays and workspaces that
@@ -509,6 +517,7 @@ typedef struct ts_kv_free_args {
   const int32_t* release;    /* [batch]: requests with a value other than 0 end; NULL: all */
   const int32_t* refcount;   /* [num_pages] */
   int32_t* refcount_out;     /* [num_pages]: one less for each entry of an ended request */
+  const int32_t* held_lens;  /* [batch] or NULL (above) */
 } ts_kv_free_args;
 
 /* Tables and lengths are left as they are: an ended request's row names pages that are no longer
@@ -525,9 +534,10 @@ typedef struct ts_kv_reserve_args {
   int64_t ld_out;
   int32_t* reserved;         /* [batch] out: tokens the request has room for: new_lens[b], or
                                 seq_len[b] where the pool had too few pages */
+  const int32_t* held_lens;  /* [batch] or NULL (above) */
 } ts_kv_reserve_args;
 
-/* Request b asks for the pages that new_lens[b] tokens need beyond the ones it has, and, if it grows
+/* Request b asks for the pages that new_lens[b] tokens need beyond the ones it has, and, if it grows (new_lens[b] > seq_len[b])
  * and its last page is partly filled and has more than one holder, for a page to copy that one to
  * (codes of its seq_len % page_size tokens, scales), whose count falls by one. Where the requests
  * of this call that would copy a page are as many as its holders, the last of them keeps it
@@ -547,6 +557,7 @@ typedef struct ts_kv_compact_args {
                                 where an entry names no live page */
   int64_t ld_out;
   int32_t* live;             /* [1] out: n, the pages with a count above 0 */
+  const int32_t* held_lens;  /* [batch] or NULL (above) */
 } ts_kv_compact_args;
 
 /* The k-th lowest live page with an id of n or more moves (codes of K and V, scales, count) to the

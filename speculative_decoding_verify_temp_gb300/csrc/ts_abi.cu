@@ -163,6 +163,8 @@ ts_status check_apart(std::initializer_list<Span> outs, std::initializer_list<Sp
 Span table_span(const ts_kv_cache& c, const int32_t* t, int64_t ld, int64_t rows) {
   return {t, c.max_pages ? ((rows - 1) * ld + c.max_pages) * 4 : 0};
 }
+// A number a request, or NULL.
+Span requests(const ts_kv_cache& c, const int32_t* t) { return {t, t ? c.batch * 4 : 0}; }
 // An input, of no bytes where it is updated in place.
 Span unless_same(const Span& in, const void* out) { return {in.at, in.at == out ? 0 : in.bytes}; }
 
@@ -839,7 +841,7 @@ ts_status ts_kv_free(const ts_kv_free_args* p, cudaStream_t stream) {
   const ts_kv_cache& c = *p->cache;
   if ((st = check_counts(c, p->refcount, p->refcount_out)) != TS_OK) return st;
   if ((st = check_apart({{p->refcount_out, c.num_pages * 4}},
-                        {table_span(c, c.page_table, c.ld_table, c.batch), {c.seq_lens, c.batch * 4}, {p->release, p->release ? c.batch * 4 : 0}})) != TS_OK)
+                        {table_span(c, c.page_table, c.ld_table, c.batch), {c.seq_lens, c.batch * 4}, requests(c, p->release), requests(c, p->held_lens)})) != TS_OK)
     return st;
   return launched(tsv::launch_kv_free(c, *p, sm_count(), stream), "free launch");
 }
@@ -861,7 +863,7 @@ ts_status ts_kv_reserve(const ts_kv_reserve_args* p, void* workspace, size_t ws_
                          {workspace, (int64_t)tsv::pages_workspace(c.batch, c.num_pages)}},
                         {unless_same({p->refcount, counts}, p->refcount_out),
                          unless_same(table_span(c, c.page_table, c.ld_table, c.batch), p->table_out), {c.seq_lens, c.batch * 4},
-                         {p->new_lens, c.batch * 4}})) != TS_OK)
+                         {p->new_lens, c.batch * 4}, requests(c, p->held_lens)})) != TS_OK)
     return st;
   return launched(tsv::launch_kv_reserve(c, *p, workspace, stream), "reserve launch");
 }
@@ -879,7 +881,8 @@ ts_status ts_kv_compact(const ts_kv_compact_args* p, void* workspace, size_t ws_
   if ((st = check_apart({{p->refcount_out, counts}, table_span(c, p->table_out, p->ld_out, c.batch), {p->live, 4},
                          {workspace, (int64_t)tsv::pages_workspace(c.batch, c.num_pages)}},
                         {unless_same({p->refcount, counts}, p->refcount_out),
-                         unless_same(table_span(c, c.page_table, c.ld_table, c.batch), p->table_out), {c.seq_lens, c.batch * 4}})) != TS_OK)
+                         unless_same(table_span(c, c.page_table, c.ld_table, c.batch), p->table_out), {c.seq_lens, c.batch * 4},
+                         requests(c, p->held_lens)})) != TS_OK)
     return st;
   return launched(tsv::launch_kv_compact(c, *p, workspace, sm_count(), stream), "compact launch");
 }

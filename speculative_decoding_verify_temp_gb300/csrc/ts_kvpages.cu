@@ -46,6 +46,7 @@ struct Pool {
   int32_t* table_out;
   int64_t ld_out;
   const int32_t* new_lens;
+  const int32_t* held_lens;  // or null
   int32_t* reserved;
   uint32_t* ask;             // pages a request asks for | kCopies | kKeeps
   int32_t* last;             // its last page, where it copies it (the table may be written in place)
@@ -60,6 +61,10 @@ constexpr uint32_t kCopies = 1u << 30, kKeeps = 1u << 31, kAsk = kCopies - 1;
 
 __device__ __forceinline__ int32_t length(const ts_kv_cache& c, int shift, int64_t b) {
   return min(max(c.seq_lens[b], 0), c.max_pages << shift);  // at most 2^30
+}
+// The tokens that the request's pages have room for.
+__device__ __forceinline__ int32_t room(const ts_kv_cache& c, const int32_t* held, int shift, int64_t b, int32_t len) {
+  return held ? max(len, min(held[b], c.max_pages << shift)) : len;
 }
 __device__ __forceinline__ int32_t entries(int32_t len, int shift) { return (int)(((unsigned)len + (1u << shift) - 1) >> shift); }
 __device__ __forceinline__ bool names(const ts_kv_cache& c, int32_t page) { return page >= 0 && page < c.num_pages; }
@@ -96,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) k_free(ts_kv_cache c, ts_kv_free_arg
   for (int64_t u = blockIdx.x; u < c.batch * columns; u += gridDim.x) {
     const int64_t b = u / columns, first = u % columns * kColumns;
     if (a.release && a.release[b] == 0) continue;
-    const int32_t used = entries(length(c, shift, b), shift);
+    const int32_t used = entries(room(c, a.held_lens, shift, b, length(c, shift, b)), shift);
 #pragma unroll
     for (int k = 0; k < kColumns / kThreads; ++k) {
       const int64_t j = first + k * kThreads + threadIdx.x;
@@ -175,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) k_pool_scan(const __grid_constant__ 
     }
   }
   if (b < p.c.batch && lane == 0) {
-    uint32_t ask = (uint32_t)(entries(want, p.shift) - entries(len, p.shift));
+    uint32_t ask = (uint32_t)max(entries(want, p.shift) - entries(room(p.c, p.held_lens, p.shift, b, len), p.shift), 0);
     if (mine >= 0) {
       const bool keeps = last && sharers >= p.count[mine];
       ask = keeps ? ask | kKeeps : (ask + 1) | kCopies;
@@ -319,9 +324,9 @@ __global__ void __launch_bounds__(kThreads) k_reserve(const __grid_constant__ Po
   const bool served = first + ask <= free || (ask == 0 && !(word & kKeeps));
   copies = copies && served;
   if (part && !copies) return;
-  const int32_t len = length(p.c, p.shift, b), have = entries(len, p.shift);
+  const int32_t len = length(p.c, p.shift, b), have = entries(room(p.c, p.held_lens, p.shift, b, len), p.shift);
   const int32_t want = max(len, min(p.new_lens[b], p.c.max_pages << p.shift));
-  const int32_t need = served ? entries(want, p.shift) : have;
+  const int32_t need = served ? max(entries(want, p.shift), have) : have;
   const int32_t* row = p.c.page_table + b * p.c.ld_table;
   int32_t* out = p.table_out + b * p.ld_out;
   const int32_t from = p.last[b];
@@ -415,7 +420,7 @@ __global__ void __launch_bounds__(kThreads) k_compact(const __grid_constant__ Po
   const int64_t n = *p.live, moves = *p.moves;
   for (int64_t u = blockIdx.x; u < p.c.batch * columns; u += gridDim.x) {
     const int64_t b = u / columns, first = u % columns * kColumns;
-    const int32_t used = entries(length(p.c, p.shift, b), p.shift);
+    const int32_t used = entries(room(p.c, p.held_lens, p.shift, b, length(p.c, p.shift, b)), p.shift);
 #pragma unroll
     for (int k = 0; k < kColumns / kThreads; ++k) {
       const int64_t j = first + k * kThreads + tid;
@@ -526,6 +531,7 @@ cudaError_t launch_kv_free(const ts_kv_cache& c, const ts_kv_free_args& a, int s
 cudaError_t launch_kv_reserve(const ts_kv_cache& c, const ts_kv_reserve_args& a, void* ws, cudaStream_t s) {
   Pool p = pool(c, a.refcount, a.refcount_out, a.table_out, a.ld_out, ws);
   p.new_lens = a.new_lens;
+  p.held_lens = a.held_lens;
   p.reserved = a.reserved;
   k_pool_scan<<<(unsigned)(p.chunks + (c.batch + kWarps - 1) / kWarps), kThreads, 0, s>>>(p);
   const cudaError_t e = cudaGetLastError();
@@ -537,6 +543,7 @@ cudaError_t launch_kv_reserve(const ts_kv_cache& c, const ts_kv_reserve_args& a,
 cudaError_t launch_kv_compact(const ts_kv_cache& c, const ts_kv_compact_args& a, void* ws, int sms, cudaStream_t s) {
   Pool p = pool(c, a.refcount, a.refcount_out, a.table_out, a.ld_out, ws);
   p.live = a.live;
+  p.held_lens = a.held_lens;
   k_pool_scan<<<(unsigned)p.chunks, kThreads, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;

@@ -204,6 +204,7 @@ class KvFreeArgs(ctypes.Structure):
         ("release", ctypes.c_void_p),
         ("refcount", ctypes.c_void_p),
         ("refcount_out", ctypes.c_void_p),
+        ("held_lens", ctypes.c_void_p),
     ]
 
 
@@ -217,6 +218,7 @@ class KvReserveArgs(ctypes.Structure):
         ("table_out", ctypes.c_void_p),
         ("ld_out", ctypes.c_int64),
         ("reserved", ctypes.c_void_p),
+        ("held_lens", ctypes.c_void_p),
     ]
 
 
@@ -229,6 +231,7 @@ class KvCompactArgs(ctypes.Structure):
         ("table_out", ctypes.c_void_p),
         ("ld_out", ctypes.c_int64),
         ("live", ctypes.c_void_p),
+        ("held_lens", ctypes.c_void_p),
     ]
 
 
@@ -866,15 +869,17 @@ def kv_fork(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, *, sources
 
 
 def kv_free(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, *, refcount, release=None,
-            refcount_out=None, stream=None):
+            held_lens=None, refcount_out=None, stream=None):
     """Releases the pages of the requests with release[b] != 0 (int32 [B]; without it: of all):
     each of their entries counts one holder less in refcount (int32 [pages]), in place or into
-    refcount_out, which is returned. Tables and lengths stay as they are."""
+    refcount_out, which is returned. Tables and lengths stay as they are. held_lens: as for
+    kv_reserve."""
     c, device = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)
     count, count_out, refcount_out = _counts(c, refcount, refcount_out)
-    _same_device(device, refcount, refcount_out, release)
+    _same_device(device, refcount, refcount_out, release, held_lens)
     with _on(device, stream) as s:
-        a = KvFreeArgs(ctypes.pointer(c), _int32("release", release, c.batch), count, count_out)
+        a = KvFreeArgs(ctypes.pointer(c), _int32("release", release, c.batch), count, count_out,
+                       _int32("held_lens", held_lens, c.batch))
         st = load().ts_kv_free(a, s)
         if st:
             _check("ts_kv_free", st)
@@ -882,21 +887,24 @@ def kv_free(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, *, refcoun
 
 
 def kv_reserve(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, *, new_lens, refcount,
-               refcount_out=None, page_table_out=None, workspace=None, stream=None):
+               held_lens=None, refcount_out=None, page_table_out=None, workspace=None, stream=None):
     """Room for new_lens (int32 [B]) tokens, ready for kv_append: fresh pages, and a copy of a
     last page that others hold too. refcount and page_table are updated in place, or into
     refcount_out and page_table_out. Returns dict(page_table, refcount, reserved): reserved[b]
-    is new_lens[b], or seq_lens[b] where the pool had too few pages left."""
+    is new_lens[b], or seq_lens[b] where the pool had too few pages left: no more than that
+    may be appended. held_lens (int32 [B]): tokens that requests have pages for already, the
+    largest `reserved` each was given; without it pages behind those of seq_lens are lost."""
     c, device = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)
     count, count_out, refcount_out = _counts(c, refcount, refcount_out)
     table = page_table if page_table_out is None else page_table_out
     ld = _table_out("page_table_out", table, c.batch, c.max_pages)
-    new = _int32("new_lens", new_lens, c.batch)
-    _same_device(device, new_lens, refcount, refcount_out, table, workspace)
+    new, held = _int32("new_lens", new_lens, c.batch), _int32("held_lens", held_lens, c.batch)
+    _same_device(device, new_lens, held_lens, refcount, refcount_out, table, workspace)
     with _on(device, stream) as s:
         reserved = torch.empty((c.batch,), dtype=torch.int32, device=k_cache.device)
         workspace = _pages_workspace(workspace, c, k_cache.device)
-        a = KvReserveArgs(ctypes.pointer(c), new, count, count_out, table.data_ptr(), ld, reserved.data_ptr())
+        a = KvReserveArgs(ctypes.pointer(c), new, count, count_out, table.data_ptr(), ld, reserved.data_ptr(),
+                          held)
         st = load().ts_kv_reserve(a, workspace.data_ptr(), workspace.nbytes, s)
         if st:
             _check("ts_kv_reserve", st)
@@ -904,19 +912,20 @@ def kv_reserve(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, *, new_
 
 
 def kv_compact(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, *, refcount,
-               refcount_out=None, page_table_out=None, workspace=None, stream=None):
+               held_lens=None, refcount_out=None, page_table_out=None, workspace=None, stream=None):
     """Moves the live pages (refcount above 0) to the lowest ids, and the tables with them, in
     place or into refcount_out and page_table_out. Returns dict(page_table, refcount, live):
-    live int32 [1], the number of live pages."""
+    live int32 [1], the number of live pages. held_lens: as for kv_reserve."""
     c, device = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)
     count, count_out, refcount_out = _counts(c, refcount, refcount_out)
     table = page_table if page_table_out is None else page_table_out
     ld = _table_out("page_table_out", table, c.batch, c.max_pages)
-    _same_device(device, refcount, refcount_out, table, workspace)
+    held = _int32("held_lens", held_lens, c.batch)
+    _same_device(device, held_lens, refcount, refcount_out, table, workspace)
     with _on(device, stream) as s:
         live = torch.empty((1,), dtype=torch.int32, device=k_cache.device)
         workspace = _pages_workspace(workspace, c, k_cache.device)
-        a = KvCompactArgs(ctypes.pointer(c), count, count_out, table.data_ptr(), ld, live.data_ptr())
+        a = KvCompactArgs(ctypes.pointer(c), count, count_out, table.data_ptr(), ld, live.data_ptr(), held)
         st = load().ts_kv_compact(a, workspace.data_ptr(), workspace.nbytes, s)
         if st:
             _check("ts_kv_compact", st)
