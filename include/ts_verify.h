@@ -544,7 +544,8 @@ typedef struct ts_kv_reserve_args {
  * instead. Pages are given out in request order, the copy first, the lowest free page (of those
  * free before the call) first, each with a count of 1. A request is served if the pages asked for
  * by it and those before it are there, or if it asks for none and keeps none in that way; one that is not
- * served keeps its row, its pages and its length. Workspace: ts_kv_pages_workspace_size bytes of
+ * served keeps its row, its pages and its length, and nothing may be appended to it: its last page may still
+ * be another's too. Append at most reserved[b] - seq_len[b] rows. Workspace: ts_kv_pages_workspace_size bytes of
  * scratch (no zero fill needed) that no other call uses meanwhile. */
 ts_status ts_kv_reserve(const ts_kv_reserve_args* args, void* workspace, size_t ws_bytes,
                         cudaStream_t stream);
