@@ -492,6 +492,13 @@ ts_status ts_kv_read(const ts_kv_read_args* args, cudaStream_t stream);
  * (NULL) such pages are lost to the pool: their entries are overwritten, their counts stay. Pages behind seq_len
  * must have one holder, as they have where tables come from these calls.
  *
+ * Caches that share tables and counts, as a model's layers do, one pool each: ts_kv_reserve and ts_kv_compact
+ * copy the pages of the cache they are given. Call them once a cache with the same tables, lengths and counts to
+ * read (page_table, held_lens, refcount) and table_out, refcount_out apart from these, for all caches the same: each call
+ * copies its cache's pages and writes the same numbers. In place only the last call may be, or the second would find
+ * a table that is already changed, and copy nothing. ts_kv_fork and ts_kv_free, which touch no page, are
+ * called once for all.
+ *
  * Results do not depend on timing: pages are given out by number, lowest first. refcount_out may
  * be refcount (in place) or an array apart from it; table_out may be the cache's page_table, with
  * its ld (in place; not for ts_kv_fork), or apart from it. int32 arrays and workspaces that

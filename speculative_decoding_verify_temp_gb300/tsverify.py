@@ -893,7 +893,9 @@ def kv_reserve(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, *, new_
     refcount_out and page_table_out. Returns dict(page_table, refcount, reserved): reserved[b]
     is new_lens[b], or seq_lens[b] where the pool had too few pages left: no more than that
     may be appended. held_lens (int32 [B]): tokens that requests have pages for already, the
-    largest `reserved` each was given; without it pages behind those of seq_lens are lost."""
+    largest `reserved` each was given; without it pages behind those of seq_lens are lost.
+    Layers with a pool each under one table: a call a layer, all from the same page_table and
+    refcount into the same page_table_out and refcount_out."""
     c, device = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)
     count, count_out, refcount_out = _counts(c, refcount, refcount_out)
     table = page_table if page_table_out is None else page_table_out
@@ -915,7 +917,7 @@ def kv_compact(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, *, refc
                held_lens=None, refcount_out=None, page_table_out=None, workspace=None, stream=None):
     """Moves the live pages (refcount above 0) to the lowest ids, and the tables with them, in
     place or into refcount_out and page_table_out. Returns dict(page_table, refcount, live):
-    live int32 [1], the number of live pages. held_lens: as for kv_reserve."""
+    live int32 [1], the number of live pages. held_lens, and layers: as for kv_reserve."""
     c, device = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens)
     count, count_out, refcount_out = _counts(c, refcount, refcount_out)
     table = page_table if page_table_out is None else page_table_out

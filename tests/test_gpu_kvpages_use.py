@@ -62,3 +62,57 @@ def test_answers_that_grow_until_the_pool_ends(tv, pages, D):  # noqa: F811
     assert (refused > 0) == (pages == 16)
     tv.kv_free(**cache, held_lens=held, refcount=count)
     assert (count == 0).all()
+
+
+@pytest.mark.parametrize("split", [False, True])
+def test_layers_under_one_table(tv, split):  # noqa: F811
+    """Three layers, a pool each: a step's calls once a layer, from the same tables and counts into the same others
+    (or, split, the last one in place). Every layer reads back what it was given."""
+    H, D, size, pages, layers, n = 2, 64, 16, 60, 3, 4
+    g = torch.Generator("cuda").manual_seed(2)
+    z = torch.zeros((layers, 2, pages, H, size, D), dtype=torch.uint8, device="cuda").view(F8)
+    sc = torch.ones((layers, 2, pages, H), device="cuda")
+    pools = [dict(k_cache=z[i, 0], v_cache=z[i, 1], k_scale=sc[i, 0], v_scale=sc[i, 1]) for i in range(layers)]
+    count, count2 = torch.zeros((2, pages), dtype=torch.int32, device="cuda")
+    table, table2 = torch.full((2, n, 10), -1, dtype=torch.int32, device="cuda")
+    lens = ints([0] * n)
+    want = [[[torch.zeros((0, H, D), device="cuda")] * 2 for _ in range(n)] for _ in range(layers)]
+
+    def each(call, **kw):
+        """The call a layer; the tables and counts are the new ones then."""
+        nonlocal table, table2, count, count2
+        got = []
+        for i, kv in enumerate(pools):
+            out = {} if split and i == layers - 1 else dict(page_table_out=table2, refcount_out=count2)
+            got.append(call(**kv, page_table=table, seq_lens=lens, refcount=count, **kw, **out))
+        assert all(torch.equal(a[k], got[0][k]) for a in got for k in a)
+        if not split:
+            table, table2, count, count2 = table2, table, count2, count
+
+    for step in range(4):
+        grown = ints([37, 0, 0, 0] if step == 0 else [5 + (b + step) % 9 for b in range(n)])
+        each(tv.kv_reserve, new_lens=lens + grown)
+        if step == 2:
+            each(tv.kv_compact, held_lens=lens + grown)
+        ptr = [0] + list(np.cumsum(grown.tolist()))
+        for i, kv in enumerate(pools):
+            x = torch.randint(-7, 8, (2, ptr[-1], H, D), generator=g, device="cuda").half() * 64
+            x[..., 0] = 448  # one scale for all: codes are exact
+            tv.kv_append(x[0], x[1], **kv, page_table=table, seq_lens=lens, qo_indptr=ints(ptr))
+            for b in range(n):
+                want[i][b] = [torch.cat([w, y[ptr[b]:ptr[b + 1]].float()]) for w, y in zip(want[i][b], x)]
+        lens += grown
+        if step == 0:  # all continue the first: the tables and counts once
+            f = tv.kv_fork(**pools[0], page_table=table, seq_lens=lens, sources=ints([0] * n), refcount=count)
+            tv.kv_free(**pools[0], page_table=table, seq_lens=lens, refcount=count)
+            table.copy_(f["page_table"])
+            lens.copy_(f["seq_lens"])
+            want = [[w[0]] * n for w in want]
+        at = [0] + list(np.cumsum(lens.tolist()))
+        for i, kv in enumerate(pools):
+            back = tv.kv_read(**kv, page_table=table, seq_lens=lens, out_indptr=ints(at), total_rows=at[-1], dtype=torch.float32)
+            for b in range(n):
+                for w, name in zip(want[i][b], "kv"):
+                    assert torch.equal(back[name][at[b]:at[b + 1]], w), (step, i, b, name)
+    tv.kv_free(**pools[0], page_table=table, seq_lens=lens, refcount=count)
+    assert (count == 0).all()
