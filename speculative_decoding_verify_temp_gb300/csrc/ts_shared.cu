@@ -859,13 +859,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_co
 }
 
 template <int D, typename T>
-cudaError_t launch(const PrefixParams& p, const TailParams& tail, Start* starts, int sms, cudaStream_t s) {
+cudaError_t launch(const PrefixParams& p, const CUtensorMap& k, const CUtensorMap& v, const TailParams& tail, Start* starts, int sms,
+                   cudaStream_t s) {
   constexpr int bytes = smem_bytes<D>();
-  CUtensorMap k, v;
-  const ts_kv_cache& c = p.c;
-  if (!page_map(&k, c, c.k, c.k_page_stride, c.k_head_stride, c.k_token_stride, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !page_map(&v, c, c.v, c.v_page_stride, c.v_head_stride, c.v_token_stride, CU_TENSOR_MAP_SWIZZLE_NONE))
-    return cudaErrorInvalidValue;
   cudaError_t e = allow_smem<k_prefix<D, T>>(bytes);
   if (e != cudaSuccess) return e;
   if ((e = launch_after(k_prefix<D, T>, dim3(sms), kThreads, bytes, s, p, k, v)) != cudaSuccess) return e;
@@ -947,13 +943,17 @@ cudaError_t launch_shared(const ts_shared_args& sh, void* ws, int sms, uint64_t 
   tail.pre_o = x.pre_o;
   tail.pre_ml = x.pre_ml;
   tail.starts = x.tails;
+  CUtensorMap k, v;  // before anything is launched: a call that fails leaves nothing on the stream
+  if (!page_map(&k, c, c.k, c.k_page_stride, c.k_head_stride, c.k_token_stride, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !page_map(&v, c, c.v, c.v_page_stride, c.v_head_stride, c.v_token_stride, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return encoder_found() ? cudaErrorInvalidValue : cudaErrorNotSupported;
   k_plan<<<1, kPlanThreads, 0, s>>>(p, c, sh, x.groups, x.first, x.gang, x.starts, sms);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (a.dtype == TS_BF16)
-    e = c.head_dim == 128 ? launch<128, __nv_bfloat16>(p, tail, x.tails, sms, s) : launch<64, __nv_bfloat16>(p, tail, x.tails, sms, s);
+    e = c.head_dim == 128 ? launch<128, __nv_bfloat16>(p, k, v, tail, x.tails, sms, s) : launch<64, __nv_bfloat16>(p, k, v, tail, x.tails, sms, s);
   else
-    e = c.head_dim == 128 ? launch<128, __half>(p, tail, x.tails, sms, s) : launch<64, __half>(p, tail, x.tails, sms, s);
+    e = c.head_dim == 128 ? launch<128, __half>(p, k, v, tail, x.tails, sms, s) : launch<64, __half>(p, k, v, tail, x.tails, sms, s);
   return e != cudaSuccess ? e : launch_tail(tail, sms, s);
 }
 
