@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+from tests.test_gpu_kvpages import data, same
 from tests.test_gpu_shared import check, ints, tv  # noqa: F401 (tv: a fixture)
 from tests.window_ref import F8
 
@@ -116,3 +117,33 @@ def test_layers_under_one_table(tv, split):  # noqa: F811
                     assert torch.equal(back[name][at[b]:at[b + 1]], w), (step, i, b, name)
     tv.kv_free(**pools[0], page_table=table, seq_lens=lens, refcount=count)
     assert (count == 0).all()
+
+
+def test_pools_of_their_own_past_32_bits(tv):  # noqa: F811
+    # K and V of 36000 pages of 8 heads x 128 x 128 bytes each, apart, with what differs in every page, head and
+    # of K and V: a copy and a move between pages 4.7 GB apart
+    pages, H, size, D = 36000, 8, 128, 128
+    kv = {}
+    for i, name in enumerate("kv"):
+        x = torch.zeros((pages, H, size, D), dtype=torch.uint8, device="cuda")
+        for p in (pages - 1, pages - 2, 0, 1):
+            x[p] = torch.arange(size * D, device="cuda").view(size, D) % 100 + torch.arange(H, device="cuda")[:, None, None] + 10 * i + p % 5
+        kv[name + "_cache"] = x
+        kv[name + "_scale"] = torch.arange(pages, device="cuda").float()[:, None] + torch.arange(H, device="cuda") / 16 + 0.5 * i
+    cache = dict(kv, page_table=ints([[pages - 1, -1]] * 2), seq_lens=ints([100, 100]))
+    count = torch.ones(pages, dtype=torch.int32, device="cuda")
+    count[pages - 1], count[1] = 2, 0
+    k, v, ks, vs = data(cache)
+    got = tv.kv_reserve(**cache, new_lens=ints([101, 100]), refcount=count)
+    assert got["page_table"][:, 0].tolist() == [1, pages - 1]
+    for x in (k, v):
+        x[1, :, :100] = x[pages - 1, :, :100]
+    for x in (ks, vs):
+        x[1] = x[pages - 1]
+    same(data(cache), [k, v, ks, vs])
+    count[2:pages - 2] = 0
+    got = tv.kv_compact(**cache, refcount=count)  # 0 and 1 stay, the last two come to 2 and 3
+    assert got["live"].item() == 4 and got["page_table"][:, 0].tolist() == [1, 3]
+    for x in (k, v, ks, vs):
+        x[2], x[3] = x[pages - 2], x[pages - 1]
+    same(data(cache), [k, v, ks, vs])
