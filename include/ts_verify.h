@@ -400,8 +400,9 @@ size_t ts_attention_workspace_size(int64_t batch, int64_t total_rows, int32_t he
 typedef struct ts_shared_args {
   const ts_attn_args* attn;     /* host struct: the windows, as for ts_window_attention */
   const int32_t* group_indptr;  /* [groups + 1]: group g is the requests group_indptr[g] ..
-                                   group_indptr[g+1] - 1. Must not decrease; a pair that does not
-                                   fit is no group, and a request in none shares nothing */
+                                   group_indptr[g+1] - 1. Must not decrease (requests that are then
+                                   in two groups: unspecified values); a pair that does not fit is
+                                   no group, and a request in none shares nothing */
   const int32_t* shared_lens;   /* [groups] tokens that the requests of a group have in common */
   int64_t groups;               /* in [1, 65536] */
 } ts_shared_args;
@@ -415,7 +416,8 @@ typedef struct ts_shared_args {
  * ts_window_attention, to the same accuracy (q is good to 2^-25 of the largest |q| of its row and
  * head; what the smallest probabilities lose is below 2^-11 of their row's sum up to 2^28 shared tokens) and
  * with the same treatment of rows that see nothing, of values that are not finite, of scales of V below
- * 2^-80 and of pages outside the pool. Workspace: ts_shared_attention_workspace_size bytes of scratch (no
+ * 2^-80 and of pages outside the pool. It pays where it spares many reads, (requests - groups) * shared tokens *
+ * 2 * heads * head_dim bytes: from some 60 MB (150 MB with one group). Below that ts_window_attention is faster. Workspace: ts_shared_attention_workspace_size bytes of scratch (no
  * zero fill needed) that no other call uses meanwhile. */
 ts_status ts_shared_attention(const ts_shared_args* args, void* workspace, size_t ws_bytes,
                               cudaStream_t stream);

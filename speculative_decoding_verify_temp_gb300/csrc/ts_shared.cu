@@ -5,7 +5,7 @@
 //   k_plan         the groups: rows, shared tokens (whole pages); what each request has left; how
 //                  many CTAs go through the tokens side by side
 //   k_prefix       one persistent CTA an SM: the shared tokens of the groups
-//   k_prefix_join  joins the pieces of units that more than one CTA worked on
+//   k_prefix_join  joins the pieces of units that more than one CTA worked on, and plans the shares of ts_tail.cu
 //
 // The rows of a group's windows, all query heads of a KV head, are one matrix, so the products are
 // proper matrix products: 128 rows of Q are the M = 128 of tcgen05.mma (kind f16),
@@ -31,7 +31,7 @@
 // Groups with many rows: CTAs in gangs of up to 8 take the same share of the tokens at the same time, a
 // block of rows each, so that a tile comes from DRAM once for a gang.
 //
-// Measured, 32 windows of 8 rows, 64 query and 8 KV heads of 128, 131071 shared tokens: 842 us, 1305 TFLOP/s,
+// Measured, 32 windows of 8 rows, 64 query and 8 KV heads of 128, 131071 shared tokens: 832 us, 1321 TFLOP/s,
 // 0.68 of the measured bf16 peak. Bound: a slot's softmax takes 2300 clocks a tile (TMEM loads, 32 exponentials a
 // clock and SM), the products of both slots 2054, and what is left of either is not hidden behind the other.
 //
@@ -807,7 +807,7 @@ template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_constant__ PrefixParams p, const __grid_constant__ TailParams tail,
                                                                  int tail_ctas, int rows, Start* starts) {
   grid_launch();
-  if (blockIdx.y == kJoinY) {  // one CTA, while the prefix is worked on: the shares of the kernel behind this one
+  if (blockIdx.y == kJoinY) {  // one CTA, the last to find room: the shares of the kernel behind this one
     if (blockIdx.x == 0) {
       if (rows == 16) line_starts<16, kTailTile, kJoinWarps * 32>(tail, kTailLeast, tail_ctas, starts);
       else line_starts<32, kTailTile, kJoinWarps * 32>(tail, kTailLeast, tail_ctas, starts);
