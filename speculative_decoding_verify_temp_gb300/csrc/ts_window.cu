@@ -16,9 +16,10 @@
 // products walk the dims and tokens is chosen to fit. Q rows are scaled by a power of two to
 // below 2, where bf16 values are exact in fp16 down to 2^-14 of the row's largest and off by at
 // most 2^-25 of it below. Probabilities are rounded to fp16 (2^-11 relative), relative to a
-// reference m that is set 2^7 below the largest score so far and follows when that is 2^15 above it (no
+// reference m that is set 2^h below the largest score so far and follows when that is 2^15 above it (no
 // rescaling in between): fp16 holds 65504, and at the other end the small ones lose at most
-// 2^-25 each, 2^-11 of the row's sum in 2^21 tokens of a warp (with the largest at 1 it was 2^14 tokens).
+// 2^-25 each. h goes by the tokens N of a warp, log2 N - 14 and 7 at least, so that this is below 2^-11 of the row's
+// sum (with 7 for all it was in 2^21 tokens of a warp, with the largest at 1 in 2^14).
 //
 // V's scale s enters through the exponent: the products take p' = 2^(x + log2 s - m), so the
 // output needs no scale, whatever the blocks' scales; the sum takes p' / s.
@@ -38,7 +39,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16 * kWarps;
 constexpr int kCtasPerSm = 2;
 constexpr float kSlack = 15.f;    // how far, in log2, a score may exceed its row's reference
-constexpr float kHead = 7.f;      // a reference is set this far below the largest score
+constexpr float kLeastHead = 7.f; // a reference is set this far below the largest score, or further
 constexpr int kMinTiles = 4;      // least tiles a CTA takes: pieces of 256 tokens or more
 
 using Params = WindowParams;
@@ -146,12 +147,13 @@ __device__ __forceinline__ void attend(const Params& p) {
           move |= t > m[mt][h] + kSlack;
         }
       if (__any_sync(0xffffffffu, move)) {
+        const float head = fmaxf((float)(22 - __clz(t1 - t0)), kLeastHead);  // of 16 tokens a tile
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             // only where needed: a row's result must not depend on its neighbours'
-            const float to = top[mt][h] > m[mt][h] + kSlack ? top[mt][h] - kHead : m[mt][h];
+            const float to = top[mt][h] > m[mt][h] + kSlack ? top[mt][h] - head : m[mt][h];
             const float by = ex2(m[mt][h] - to);
             m[mt][h] = to;
             l[mt][h] *= by;
