@@ -416,8 +416,9 @@ typedef struct ts_shared_args {
  * ts_window_attention, to the same accuracy (q is good to 2^-25 of the largest |q| of its row and
  * head; what the smallest probabilities lose is below 2^-11 of their row's sum up to 2^28 shared tokens) and
  * with the same treatment of rows that see nothing, of values that are not finite, of scales of V below
- * 2^-80 and of pages outside the pool. It pays where it spares many reads, (requests - groups) * shared tokens *
- * 2 * heads * head_dim bytes: from some 60 MB (150 MB with one group). Below that ts_window_attention is faster. Workspace: ts_shared_attention_workspace_size bytes of scratch (no
+ * 2^-80 and of pages outside the pool. It pays where it spares many reads, (requests - groups) *
+ * shared tokens * 2 * heads * head_dim bytes: from some 60 MB (150 MB with one group). Below that
+ * ts_window_attention is faster. Workspace: ts_shared_attention_workspace_size bytes of scratch (no
  * zero fill needed) that no other call uses meanwhile. */
 ts_status ts_shared_attention(const ts_shared_args* args, void* workspace, size_t ws_bytes,
                               cudaStream_t stream);
@@ -546,9 +547,9 @@ typedef struct ts_kv_reserve_args {
   const int32_t* held_lens;  /* [batch] or NULL (above) */
 } ts_kv_reserve_args;
 
-/* Request b asks for the pages that new_lens[b] tokens need beyond the ones it has, and, if it grows (new_lens[b] > seq_len[b])
- * and its last page is partly filled and has more than one holder, for a page to copy that one to
- * (codes of its seq_len % page_size tokens, scales), whose count falls by one. Where the requests
+/* Request b asks for the pages that new_lens[b] tokens need beyond the ones it has, and, if it grows
+ * (new_lens[b] > seq_len[b]) and the page of its last token is partly filled and has more than one
+ * holder, for a page to copy that one to (codes of its seq_len % page_size tokens, scales), whose count falls by one. Where the requests
  * of this call that would copy a page are as many as its holders, the last of them keeps it
  * instead. Pages are given out in request order, the copy first, the lowest free page (of those
  * free before the call) first, each with a count of 1. A request is served if the pages asked for
